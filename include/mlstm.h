@@ -120,7 +120,9 @@ enum {
   MLSTM_ERR_KERNEL = -8,      /* unknown kernel selector, or an MFMA selector for fp32 */
   MLSTM_ERR_ALIAS = -9,       /* an output overlaps an input or another output */
   MLSTM_ERR_ACTIVATION = -10, /* unknown forget-gate activation */
-  MLSTM_ERR_SCRATCH = -11     /* beyond the allocation-free entry point's fixed workspace */
+  MLSTM_ERR_SCRATCH = -11,    /* beyond the allocation-free entry point's fixed workspace */
+  MLSTM_ERR_HEADS = -12,      /* NH not a multiple of NHK */
+  MLSTM_ERR_NORM = -13        /* unknown norm or gate activation, or eps not a number >= 0 */
 };
 
 /*
@@ -348,6 +350,120 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
                          void* h_out, float* den_out,
                          int64_t B, int64_t NH, int64_t d, int dtype,
                          int forget_activation, void* stream);
+
+/*
+ * The gated delta rule: a matrix memory that corrects what it holds for a key
+ * before it writes, with the same layouts, gate pre-activations and forget
+ * activations as the mLSTM cell above.  Per head, with C (dv x dk, rows by
+ * value), f_t = sigma(f~_t) or exp(f~_t) and a write strength beta_t,
+ *
+ *   C_t = f_t C_{t-1} + beta_t (v_t - f_t C_{t-1} k_t) k_t^T
+ *   h_t = C_t q_t / sqrt(dk)
+ *
+ *   q, k     [B][NHK][T][dk]  dtype
+ *   v, h     [B][NH][T][dv]   dtype; value head n reads key head n / (NH / NHK)
+ *   beta     [B][NH][T]       float32, the strengths themselves
+ *   fgate    [B][NH][T]       float32, the pre-activations f~
+ *   C        [B][NH][dv][dk]  float32
+ *   NHK      a divisor of NH;  dk a multiple of 16 in [16, 512];
+ *   dv       a multiple of 16 in [16, 1024];  T >= 1
+ * k is not normalized here.  The recurrence is stable for
+ * beta |k|^2 <= 2 (unit keys and strengths in (0, 1), as a rule).  A position
+ * with beta = 0 and f = 1 (f~ = +infinity, or 0 with MLSTM_FORGET_EXP) leaves
+ * the memory as it is, which is how a batch is padded.  f~ = -infinity forgets
+ * everything.  Inputs are otherwise finite: NaN and infinities propagate, and
+ * may reach other positions of the same 64.
+ *
+ * All sums, the memory and the products that feed it are float32 (bf16
+ * operands are exact; float32 operands of a matrix product are split into
+ * three bf16 planes), gate sums are float64; for MLSTM_BF16 the operands of h
+ * that are not inputs carry 16 bits, and h is rounded to nearest even.
+ * Results are bitwise reproducible (no atomics, fixed order).
+ */
+
+/*
+ * mlstm_delta_workspace_bytes -- workspace of mlstm_delta_fwd (or, with
+ * backward != 0, of mlstm_delta_bwd) for these sizes; 0 for T = 1 forward, and
+ * for sizes that the call refuses.
+ */
+size_t mlstm_delta_workspace_bytes(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk,
+                                   int64_t dv, int dtype, int backward);
+
+/*
+ * mlstm_delta_fwd -- a whole sequence, in chunks of 64 tokens.
+ *   C_in       in   the memory before the sequence; NULL: zeros
+ *   h          out
+ *   C_out      out  the memory after it; may be C_in (updated in place)
+ *   workspace  mlstm_delta_workspace_bytes bytes of device memory, 256-byte
+ *              aligned, used by this call alone until it has run on `stream`
+ * Tensors 16-byte aligned (beta and fgate 4-byte).  Errors before any device
+ * work.
+ */
+int mlstm_delta_fwd(const void* q, const void* k, const void* v, const float* beta,
+                    const float* fgate, const float* C_in, void* h, float* C_out,
+                    void* workspace, size_t workspace_bytes,
+                    int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk, int64_t dv,
+                    int dtype, int forget_activation, void* stream);
+
+/*
+ * mlstm_delta_step -- one token (generation): q, k [B][NHK][dk], v, h
+ * [B][NH][dv], beta, fgate [B][NH].  C_out may be C_in (updated in place).  No
+ * workspace.  Bound by memory bandwidth: the memory is read and written once.
+ */
+int mlstm_delta_step(const void* q, const void* k, const void* v, const float* beta,
+                     const float* fgate, const float* C_in, float* C_out, void* h,
+                     int64_t B, int64_t NHK, int64_t NH, int64_t dk, int64_t dv,
+                     int dtype, int forget_activation, void* stream);
+
+/*
+ * Block norm: what stands between a cell and the next block, in one pass.  Per
+ * token, with the cell's output p in NH heads of d channels and D = NH d,
+ *
+ *   z = act(g) * w1 * norm(p)    norm over each head's d channels
+ *   r = x + s * z                the residual stream, with its scale
+ *   y = w2 * norm(r)             norm over all D channels: the next block's input
+ *
+ *   p            [B][NH][T][d]   dtype (NH = 1: plain rows of a block's output)
+ *   gate g       [B][NH][T][d]   dtype, or NULL (act(g) = 1)
+ *   residual x   [B][T][D]       dtype, or NULL (0)
+ *   weight w1    [D]             float32
+ *   scale s      [D]             float32, or NULL (1)
+ *   next_weight w2 [D]           float32, or NULL (no y)
+ *   r, y         [B][T][D]       dtype: rows, as a projection reads them
+ *   d a multiple of 8, D <= 8192
+ * norm is (a - mean) / sqrt(var + eps) (MLSTM_NORM_LAYER) or a / sqrt(mean(a^2)
+ * + eps) (MLSTM_NORM_RMS); act is sigma(g) (MLSTM_GATE_SIGMOID) or g sigma(g)
+ * (MLSTM_GATE_SILU).  Everything in between is float32; y is formed from r
+ * before its rounding.  Tensors 16-byte aligned; no output may overlap an
+ * input.  Bitwise reproducible.
+ */
+enum { MLSTM_NORM_LAYER = 0, MLSTM_NORM_RMS = 1 };
+enum { MLSTM_GATE_SIGMOID = 0, MLSTM_GATE_SILU = 1 };
+
+int mlstm_block_norm_fwd(const void* p, const void* gate, const void* residual,
+                         const float* weight, const float* scale, const float* next_weight,
+                         void* r_out, void* y_out,
+                         int64_t B, int64_t NH, int64_t T, int64_t d, int dtype,
+                         int norm, int gate_activation, float eps, void* stream);
+
+/*
+ * mlstm_block_norm_bwd -- its gradients, from dr and dy.
+ *   dr   [B][T][D] dtype, or NULL (0);  dy [B][T][D] dtype, with next_weight only
+ *   dp   out [B][NH][T][d];  dgate, dresidual: out with gate, residual (else NULL)
+ *   dweight [D], dscale [D], dnext_weight [D]: out float32, the last two with
+ *        scale and next_weight (else NULL)
+ *   workspace  mlstm_block_norm_workspace_bytes bytes, 256-byte aligned
+ * Nothing of the forward pass is kept for it: it is formed again from p, gate
+ * and residual, which the gradients need in any case.
+ */
+size_t mlstm_block_norm_workspace_bytes(int64_t B, int64_t NH, int64_t T, int64_t d);
+int mlstm_block_norm_bwd(const void* p, const void* gate, const void* residual,
+                         const float* weight, const float* scale, const float* next_weight,
+                         const void* dr, const void* dy, void* dp, void* dgate, void* dresidual,
+                         float* dweight, float* dscale, float* dnext_weight,
+                         void* workspace, size_t workspace_bytes,
+                         int64_t B, int64_t NH, int64_t T, int64_t d, int dtype,
+                         int norm, int gate_activation, float eps, void* stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* mlstm_strerror(int status);

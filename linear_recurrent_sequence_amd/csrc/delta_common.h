@@ -1,0 +1,117 @@
+// Device pieces shared by the chunked kernels of the gated delta rule.
+//
+// Arithmetic.  The memory is held in float32 and a rounding of it to bf16
+// would be carried from chunk to chunk, so a float32 operand of a matrix
+// product is split into bf16 planes, x = hi + mid + lo (8 bits each, 24 in
+// all: exact up to float32's own spacing), and the product is the sum of the
+// planes' products on the bf16 matrix instruction, float32 accumulation.  A
+// bf16 input needs one plane (three instructions against a float32 operand);
+// two float32 operands take the six products above 2^-24: hh, hm, mh, mm, hl,
+// lh.  Against the float32 matrix instruction, 1/16 of the bf16 one's rate,
+// that is 5.3 and 2.7 times the rate for the same accuracy.
+//
+// Operand order.  A wave owns 16 value columns of a head and keeps its slice
+// of the memory in the accumulators (float32, 16x16 tiles: lane l holds column
+// l % 16 and rows 4 (l / 16) .. + 3).  Rows of a product are free to be
+// permuted, so the left operand's rows are taken in the order `row_of`, which
+// makes the accumulators of two neighbouring tiles the right operand (8
+// consecutive rows 8 (l / 16) .. of 32) of the next product, with no exchange
+// between lanes: the whole chain memory -> X -> memory stays in one wave's
+// registers.  The left operands that a chunk shares between its value columns
+// (the inverse, the scores, the transposed keys) are written once by a kernel
+// over all chunks, in the order in which lanes load them.
+#pragma once
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "delta.h"
+
+namespace mlstm {
+namespace delta {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kC = kDeltaChunk;  // 64 tokens
+
+// the row of a 32-row block that the left operand's row m (0..15) of tile
+// `half` (0, 1) holds: accumulator (half, lane group g, element r) is then row
+// 8 g + 4 half + r
+__device__ __host__ inline int row_of(int half, int m) {
+  return (m >> 2) * 8 + half * 4 + (m & 3);
+}
+
+__device__ inline f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// planes of 8 float32 values
+template <int N>
+struct Planes {
+  bf16x8 p[N];
+};
+template <int N>
+__device__ inline Planes<N> split(f32x8 x) {
+  Planes<N> s;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    s.p[n] = __builtin_convertvector(x, bf16x8);  // to nearest even
+    if (n + 1 < N) x -= __builtin_convertvector(s.p[n], f32x8);
+  }
+  return s;
+}
+__device__ inline f32x8 pair(f32x4 a, f32x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// c += a b over the products of planes above 2^-8 (NA + NB - 1 - ...): with
+// `most` planes kept, products i + j < most; small ones first
+template <int kMost, int NA, int NB>
+__device__ inline f32x4 mma_planes(const Planes<NA>& a, const Planes<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int s = kMost - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j >= 0 && j < NB) c = mma(a.p[i], b.p[j], c);
+    }
+  return c;
+}
+
+// workgroups of one head on one XCD (they are dealt round-robin to the 8
+// XCDs), so that what they share is read into one L2
+__device__ inline void map_head(int64_t wg, int64_t H, int per_head, int64_t& head, int& block) {
+  if ((H & 7) == 0) {
+    const int64_t s = wg >> 3;
+    head = (wg & 7) + 8 * (s / per_head);
+    block = int(s % per_head);
+  } else {
+    head = wg / per_head;
+    block = int(wg % per_head);
+  }
+}
+
+// What the kernel over the chunks leaves for the others.  Counts of bf16
+// elements of one chunk's planes; a plane of a 64 x 64 left operand is stored
+// as [4 row tiles][2 halves of the columns][64 lanes][8], one of a K^T (dk x
+// 64) as [2 ks row tiles][2][64][8], one of K (64 x dk) as [ks][4][64][8],
+// with ks = ceil(dk / 32).
+constexpr int kSquare = kC * kC;
+
+struct Work {
+  __bf16* inv;    // [H][chunks][3] planes of (I + At)^-1
+  __bf16* invT;   // its transpose (backward)
+  __bf16* score;  // [H][chunks][NPP] planes of P
+  __bf16* scoreT; // its transpose (backward)
+  __bf16* keyT;   // [HK][chunks][NPL] planes of K^T
+  __bf16* queryT; // (backward)
+  __bf16* key;    // [HK][chunks][3] planes of K, Q (float32 inputs)
+  __bf16* query;
+  float* decay;   // [H][chunks][3][64]: e^G, e^(G_C - G), beta (0 behind the end)
+};
+
+}  // namespace delta
+}  // namespace mlstm

@@ -3,12 +3,12 @@
 // mLSTM forward pass (xLSTM appendix A.3, Eqs. 79-86: one launch of a tile
 // kernel that scans its own gates, or the gate scan and then a tile kernel),
 // of its backward pass and of the recurrent step.
+#include "abi_common.h"
 #include "mlstm.h"
 #include "mlstm_internal.h"
 
 #include <stdint.h>
 
-#include <initializer_list>
 #include <mutex>
 
 namespace mlstm {
@@ -24,6 +24,10 @@ __device__ __attribute__((aligned(256))) char scratch[MLSTM_NOALLOC_SCRATCH_BYTE
 namespace {
 
 using mlstm::Workspace;
+using mlstm::abi::aligned16;
+using mlstm::abi::check_alias;
+using mlstm::abi::hip_status;
+using mlstm::abi::overlaps;
 
 constexpr int64_t kMaxT = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
@@ -40,35 +44,6 @@ int check_shape(int64_t B, int64_t NH, int64_t T, int64_t d) {
   if (((Tp / 16) * H) > int64_t(0xFFFFFFFF)) return MLSTM_ERR_SHAPE;
   if (d % 16 != 0 || d > kMaxHeadDim) return MLSTM_ERR_HEAD_DIM;
   if (H * Tp > kMaxElems / d) return MLSTM_ERR_SHAPE;
-  return MLSTM_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MLSTM_OK : MLSTM_ERR_HIP; }
-
-// a caller buffer's byte range; a null pointer or an empty range is skipped
-struct Span {
-  const void* p;
-  size_t n;
-};
-
-// MLSTM_ERR_ALIAS if an output overlaps an input or another output (inputs
-// may overlap each other: they are only read).  Runs after every other
-// argument check, on shapes that check_shape has bounded.
-int check_alias(std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
-  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-    if (!o->p || o->n == 0) continue;
-    for (const Span& i : ins)
-      if (i.p && i.n && overlaps(o->p, o->n, i.p, i.n)) return MLSTM_ERR_ALIAS;
-    for (const Span* o2 = outs.begin(); o2 != o; ++o2)
-      if (o2->p && o2->n && overlaps(o->p, o->n, o2->p, o2->n)) return MLSTM_ERR_ALIAS;
-  }
   return MLSTM_OK;
 }
 
@@ -482,7 +457,7 @@ const char* mlstm_strerror(int status) {
     case MLSTM_ERR_NULL: return "a required pointer is NULL";
     case MLSTM_ERR_SHAPE: return "invalid shape: B, NH, T, d must be >= 1 and sizes must not overflow";
     case MLSTM_ERR_DTYPE: return "invalid dtype: expected MLSTM_FP32 or MLSTM_BF16";
-    case MLSTM_ERR_HEAD_DIM: return "unsupported head dimension: d must be a multiple of 16 in [16, 1024] (and <= 512 for the one-wave MFMA kernel)";
+    case MLSTM_ERR_HEAD_DIM: return "unsupported head dimension: d must be a multiple of 16 in [16, 1024] (and <= 512 for the one-wave MFMA kernel and for the delta rule's keys; for the block norm a multiple of 8 with NH * d <= 8192)";
     case MLSTM_ERR_ALIGN: return "misaligned pointer: tensors need 16-byte, workspaces 256-byte alignment";
     case MLSTM_ERR_HIP: return "HIP allocation or kernel launch failed";
     case MLSTM_ERR_WORKSPACE: return "workspace smaller than mlstm_workspace_bytes()";
@@ -490,6 +465,8 @@ const char* mlstm_strerror(int status) {
     case MLSTM_ERR_ALIAS: return "an output overlaps an input it must not alias";
     case MLSTM_ERR_ACTIVATION: return "unknown forget-gate activation";
     case MLSTM_ERR_SCRATCH: return "the problem needs more workspace than the allocation-free entry point's fixed buffer holds (MLSTM_NOALLOC_SCRATCH_BYTES)";
+    case MLSTM_ERR_HEADS: return "the number of value heads must be a multiple of the number of key heads";
+    case MLSTM_ERR_NORM: return "unknown norm or gate activation, or eps is not a number >= 0";
     default: return "unknown status";
   }
 }

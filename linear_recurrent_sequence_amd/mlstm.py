@@ -27,6 +27,8 @@ MLSTM_FP32, MLSTM_BF16 = 0, 1
 KERNELS = {"auto": 0, "mfma": 1, "vector": 2, "mfma_all_tiles": 3, "mfma_single": 4,
            "mfma_wide": 5}
 FORGET_ACTIVATIONS = {"sigmoid": 0, "exp": 1}
+NORMS = {"layer": 0, "rms": 1}
+GATE_ACTIVATIONS = {"sigmoid": 0, "silu": 1}
 
 _lib = None
 
@@ -67,6 +69,19 @@ def load_library():
     lib.mlstm_gate_scan.restype = i32
     lib.mlstm_causal_tiles.argtypes = [vp] * 5 + [f] + [vp] * 2 + [i64] * 4 + [i32, i32, vp]
     lib.mlstm_causal_tiles.restype = i32
+    lib.mlstm_delta_workspace_bytes.argtypes = [i64] * 6 + [i32, i32]
+    lib.mlstm_delta_workspace_bytes.restype = f
+    lib.mlstm_delta_fwd.argtypes = [vp] * 9 + [f] + [i64] * 6 + [i32, i32, vp]
+    lib.mlstm_delta_fwd.restype = i32
+    lib.mlstm_delta_step.argtypes = [vp] * 8 + [i64] * 5 + [i32, i32, vp]
+    lib.mlstm_delta_step.restype = i32
+    fl = ctypes.c_float
+    lib.mlstm_block_norm_fwd.argtypes = [vp] * 8 + [i64] * 4 + [i32] * 3 + [fl, vp]
+    lib.mlstm_block_norm_fwd.restype = i32
+    lib.mlstm_block_norm_workspace_bytes.argtypes = [i64] * 4
+    lib.mlstm_block_norm_workspace_bytes.restype = f
+    lib.mlstm_block_norm_bwd.argtypes = [vp] * 15 + [f] + [i64] * 4 + [i32] * 3 + [fl, vp]
+    lib.mlstm_block_norm_bwd.restype = i32
     lib.mlstm_strerror.argtypes = [i32]
     lib.mlstm_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -389,3 +404,185 @@ def parallel_bwd(q, k, v, igate, fgate, h, m, n, b, dh, forget="sigmoid"):
         raise MlstmError(st, "mlstm_parallel_bwd")
     return dq, dk, dv, dig, dfg
 
+
+
+def _check_delta(q, k, v, beta, fgate, dims):
+    """Checks the gated delta rule's inputs; ``dims`` 4 with a length, 3 for one token."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"q must be a torch.Tensor, got {type(q).__name__}")
+    if not isinstance(v, torch.Tensor):
+        raise TypeError(f"v must be a torch.Tensor, got {type(v).__name__}")
+    form = "T, " if dims == 4 else ""
+    if q.dim() != dims:
+        raise ValueError(f"q must be [B, NHK, {form}dk], got shape {tuple(q.shape)}")
+    if v.dim() != dims:
+        raise ValueError(f"v must be [B, NH, {form}dv], got shape {tuple(v.shape)}")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"q/k/v must be float32 or bfloat16, got {q.dtype}")
+    B, NHK, dk = q.shape[0], q.shape[1], q.shape[-1]
+    NH, dv = v.shape[1], v.shape[-1]
+    T = q.shape[2] if dims == 4 else 1
+    rows = (B, NH, T) if dims == 4 else (B, NH)
+    dev = q.device
+    _require("q", q, q.shape, q.dtype, dev)
+    _require("k", k, q.shape, q.dtype, dev)
+    _require("v", v, (*rows, dv), q.dtype, dev)
+    _require("beta", beta, rows, torch.float32, dev)
+    _require("fgate", fgate, rows, torch.float32, dev)
+    return B, NHK, NH, T, dk, dv
+
+
+def delta_state(B, NH, dk, dv, device):
+    """A fresh memory of the gated delta rule: zeros [B, NH, dv, dk], float32."""
+    return torch.zeros((B, NH, dv, dk), dtype=torch.float32, device=device)
+
+
+def _delta_workspace(lib, sizes, dtype, backward, device):
+    n = lib.mlstm_delta_workspace_bytes(*sizes, dtype, int(backward))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def delta_fwd(q, k, v, beta, fgate, state=None, out_state=None, forget="sigmoid"):
+    """The gated delta rule over a sequence -> (h, new state).
+
+        C_t = f_t C_{t-1} + beta_t (v_t - f_t C_{t-1} k_t) k_t^T,  h_t = C_t q_t / sqrt(dk)
+
+    q, k: [B, NHK, T, dk], v: [B, NH, T, dv] (float32 or bfloat16), NH a
+    multiple of NHK (value head n reads key head n // (NH // NHK)); beta, fgate:
+    [B, NH, T] float32 (write strengths, forget gate pre-activations).
+    ``state``: the memory before the sequence, [B, NH, dv, dk] float32 (zeros by
+    default); ``out_state`` receives the memory after it and may be ``state``;
+    by default a new one is allocated.
+    """
+    lib = load_library()
+    sizes = _check_delta(q, k, v, beta, fgate, 4)
+    B, NHK, NH, T, dk, dv = sizes
+    for name, t in (("state", state), ("out_state", out_state)):
+        if t is not None:
+            _require(name, t, (B, NH, dv, dk), torch.float32, q.device)
+    forget_code, code = _forget_code(forget), _dtype_code(q)
+    with _on(q.device):
+        if out_state is None:
+            out_state = torch.empty((B, NH, dv, dk), dtype=torch.float32, device=q.device)
+        h = torch.empty_like(v)
+        ws = _delta_workspace(lib, sizes, code, False, q.device)
+        st = lib.mlstm_delta_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), fgate.data_ptr(),
+            _ptr(state), h.data_ptr(), out_state.data_ptr(), _ptr(ws),
+            0 if ws is None else ws.numel(), *sizes, code, forget_code, _stream_ptr(q.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_delta_fwd")
+    return h, out_state
+
+
+def delta_step(q, k, v, beta, fgate, state, out_state=None, forget="sigmoid"):
+    """One token of the gated delta rule -> (h, new state).
+
+    q, k: [B, NHK, dk], v: [B, NH, dv]; beta, fgate: [B, NH]; ``state`` as for
+    ``delta_fwd``, updated in place unless ``out_state`` is given.
+    """
+    lib = load_library()
+    B, NHK, NH, _, dk, dv = _check_delta(q, k, v, beta, fgate, 3)
+    if out_state is None:
+        out_state = state
+    _require("state", state, (B, NH, dv, dk), torch.float32, q.device)
+    _require("out_state", out_state, (B, NH, dv, dk), torch.float32, q.device)
+    h = torch.empty_like(v)
+    with _on(q.device):
+        st = lib.mlstm_delta_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), fgate.data_ptr(),
+            state.data_ptr(), out_state.data_ptr(), h.data_ptr(), B, NHK, NH, dk, dv,
+            _dtype_code(q), _forget_code(forget), _stream_ptr(q.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_delta_step")
+    return h, out_state
+
+
+def _check_block_norm(p, weight, gate, residual, scale, next_weight, norm, activation):
+    if not isinstance(p, torch.Tensor):
+        raise TypeError(f"p must be a torch.Tensor, got {type(p).__name__}")
+    if p.dim() != 4:
+        raise ValueError(f"p must be [B, NH, T, d], got shape {tuple(p.shape)}")
+    if p.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"p must be float32 or bfloat16, got {p.dtype}")
+    B, NH, T, d = p.shape
+    dev, D = p.device, NH * d
+    _require("p", p, p.shape, p.dtype, dev)
+    _require("weight", weight, (D,), torch.float32, dev)
+    if gate is not None:
+        _require("gate", gate, p.shape, p.dtype, dev)
+    if residual is not None:
+        _require("residual", residual, (B, T, D), p.dtype, dev)
+    for name, t in (("scale", scale), ("next_weight", next_weight)):
+        if t is not None:
+            _require(name, t, (D,), torch.float32, dev)
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {tuple(NORMS)}, got {norm!r}")
+    if activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(GATE_ACTIVATIONS)}, got {activation!r}")
+    return B, NH, T, d
+
+
+def block_norm_fwd(p, weight, gate=None, residual=None, scale=None, next_weight=None,
+                   norm="layer", activation="sigmoid", eps=1e-5):
+    """The norms, gate and scaled residual between a cell and the next block -> (r, y).
+
+        z = act(gate) * weight * norm(p),  r = residual + scale * z,  y = next_weight * norm(r)
+
+    p, gate: [B, NH, T, d] (a cell's output by heads, each normed over its d
+    channels; NH = 1 for plain rows); residual, r, y: [B, T, NH * d] rows, all
+    float32 or all bfloat16; weight, scale, next_weight: [NH * d] float32.  What
+    is None is left out (y is None without next_weight).  norm: "layer" or
+    "rms"; activation of the gate: "sigmoid" or "silu".
+    """
+    lib = load_library()
+    B, NH, T, d = _check_block_norm(p, weight, gate, residual, scale, next_weight, norm,
+                                    activation)
+    r = torch.empty((B, T, NH * d), dtype=p.dtype, device=p.device)
+    y = None if next_weight is None else torch.empty_like(r)
+    with _on(p.device):
+        st = lib.mlstm_block_norm_fwd(
+            p.data_ptr(), _ptr(gate), _ptr(residual), weight.data_ptr(), _ptr(scale),
+            _ptr(next_weight), r.data_ptr(), _ptr(y), B, NH, T, d, _dtype_code(p), NORMS[norm],
+            GATE_ACTIVATIONS[activation], eps, _stream_ptr(p.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_block_norm_fwd")
+    return r, y
+
+
+def block_norm_bwd(p, weight, dr, dy, gate=None, residual=None, scale=None, next_weight=None,
+                   norm="layer", activation="sigmoid", eps=1e-5):
+    """Gradients of ``block_norm_fwd`` given dr and dy (either may be None; dy
+    comes with next_weight) -> a dict with "dp", "dweight" and, for the inputs
+    that are given, "dgate", "dresidual", "dscale", "dnext_weight"."""
+    lib = load_library()
+    B, NH, T, d = _check_block_norm(p, weight, gate, residual, scale, next_weight, norm,
+                                    activation)
+    rows = (B, T, NH * d)
+    if dr is not None:
+        _require("dr", dr, rows, p.dtype, p.device)
+    if (dy is None) != (next_weight is None):
+        raise ValueError("dy and next_weight are given together or not at all")
+    if dy is not None:
+        _require("dy", dy, rows, p.dtype, p.device)
+    g = {"dp": torch.empty_like(p), "dweight": torch.empty_like(weight)}
+    for name, t in (("dgate", gate), ("dresidual", residual), ("dscale", scale),
+                    ("dnext_weight", next_weight)):
+        if t is not None:
+            g[name] = torch.empty_like(t)
+    ws = torch.empty(lib.mlstm_block_norm_workspace_bytes(B, NH, T, d), dtype=torch.uint8,
+                     device=p.device)
+    with _on(p.device):
+        st = lib.mlstm_block_norm_bwd(
+            p.data_ptr(), _ptr(gate), _ptr(residual), weight.data_ptr(), _ptr(scale),
+            _ptr(next_weight), _ptr(dr), _ptr(dy), g["dp"].data_ptr(), _ptr(g.get("dgate")),
+            _ptr(g.get("dresidual")), g["dweight"].data_ptr(), _ptr(g.get("dscale")),
+            _ptr(g.get("dnext_weight")), ws.data_ptr(), ws.numel(), B, NH, T, d, _dtype_code(p),
+            NORMS[norm], GATE_ACTIVATIONS[activation], eps, _stream_ptr(p.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_block_norm_bwd")
+    return g
