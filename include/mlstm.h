@@ -406,6 +406,28 @@ int mlstm_delta_fwd(const void* q, const void* k, const void* v, const float* be
                     int dtype, int forget_activation, void* stream);
 
 /*
+ * mlstm_delta_bwd -- gradients of mlstm_delta_fwd.
+ *   C_in            in   the memory before the sequence, or NULL (zeros)
+ *   dh              in   dL/dh, [B][NH][T][dv] dtype
+ *   dC_in           in   dL/dC after the sequence, or NULL (zeros)
+ *   dq, dk, dv      out  dtype; dq and dk are summed over the value heads that
+ *                        share a key head
+ *   dbeta, dfgate   out  [B][NH][T] float32
+ *   dC_out          out  dL/dC before the sequence, or NULL
+ *   workspace       mlstm_delta_workspace_bytes(..., 1) bytes, 256-byte aligned:
+ *                   chiefly the memory and its gradient at every 64th token
+ *                   (8 dk dv bytes per head and chunk)
+ * The forward pass is formed again; nothing of it is kept.  No output may
+ * overlap an input.
+ */
+int mlstm_delta_bwd(const void* q, const void* k, const void* v, const float* beta,
+                    const float* fgate, const float* C_in, const void* dh, const float* dC_in,
+                    void* dq, void* dk, void* dv, float* dbeta, float* dfgate, float* dC_out,
+                    void* workspace, size_t workspace_bytes,
+                    int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk_dim,
+                    int64_t dv_dim, int dtype, int forget_activation, void* stream);
+
+/*
  * mlstm_delta_step -- one token (generation): q, k [B][NHK][dk], v, h
  * [B][NH][dv], beta, fgate [B][NH].  C_out may be C_in (updated in place).  No
  * workspace.  Bound by memory bandwidth: the memory is read and written once.

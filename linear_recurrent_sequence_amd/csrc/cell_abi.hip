@@ -109,7 +109,7 @@ size_t mlstm_delta_workspace_bytes(int64_t B, int64_t NHK, int64_t NH, int64_t T
                                    int64_t dv, int dtype, int backward) {
   if (check_delta(B, NHK, NH, T, dk, dv, dtype) != MLSTM_OK) return 0;
   const DeltaShape s = delta_shape(B, NHK, NH, T, dk, dv, dtype, MLSTM_FORGET_SIGMOID);
-  if (backward) return 0;
+  if (backward) return mlstm::delta_bwd_workspace_bytes(s);
   return T == 1 ? 0 : mlstm::delta_fwd_workspace_bytes(s);
 }
 
@@ -148,6 +148,36 @@ int mlstm_delta_step(const void* q, const void* k, const void* v, const float* b
   if (!C_in) return MLSTM_ERR_NULL;
   return mlstm_delta_fwd(q, k, v, beta, fgate, C_in, h, C_out, nullptr, 0, B, NHK, NH, 1, dk, dv,
                          dtype, forget_activation, stream);
+}
+
+int mlstm_delta_bwd(const void* q, const void* k, const void* v, const float* beta,
+                    const float* fgate, const float* C_in, const void* dh, const float* dC_in,
+                    void* dq, void* dk, void* dv, float* dbeta, float* dfgate, float* dC_out,
+                    void* workspace, size_t workspace_bytes, int64_t B, int64_t NHK, int64_t NH,
+                    int64_t T, int64_t dk_dim, int64_t dv_dim, int dtype, int forget_activation,
+                    void* stream) {
+  int st = check_delta(B, NHK, NH, T, dk_dim, dv_dim, dtype);
+  if (st != MLSTM_OK) return st;
+  if (!known_forget(forget_activation)) return MLSTM_ERR_ACTIVATION;
+  st = check_given({q, k, v, beta, fgate, dh, dq, dk, dv, dbeta, dfgate, workspace});
+  if (st != MLSTM_OK) return st;
+  st = check_aligned({q, k, v, C_in, dh, dC_in, dq, dk, dv, dC_out});
+  if (st != MLSTM_OK) return st;
+  if (!aligned4(beta) || !aligned4(fgate) || !aligned4(dbeta) || !aligned4(dfgate) ||
+      !aligned256(workspace))
+    return MLSTM_ERR_ALIGN;
+  const DeltaShape s = delta_shape(B, NHK, NH, T, dk_dim, dv_dim, dtype, forget_activation);
+  const size_t need = mlstm::delta_bwd_workspace_bytes(s);
+  if (workspace_bytes < need) return MLSTM_ERR_WORKSPACE;
+  const DeltaBytes n = delta_bytes(s);
+  st = check_alias({{q, n.qk}, {k, n.qk}, {v, n.vh}, {beta, n.gate}, {fgate, n.gate},
+                    {C_in, n.C}, {dh, n.vh}, {dC_in, n.C}},
+                   {{dq, n.qk}, {dk, n.qk}, {dv, n.vh}, {dbeta, n.gate}, {dfgate, n.gate},
+                    {dC_out, n.C}, {workspace, need}});
+  if (st != MLSTM_OK) return st;
+  const mlstm::DeltaGrads g = {dh, dC_in, dq, dk, dv, dbeta, dfgate, dC_out};
+  return hip_status(mlstm::launch_delta_bwd(s, q, k, v, beta, fgate, C_in, g, workspace,
+                                            static_cast<hipStream_t>(stream)));
 }
 
 int mlstm_block_norm_fwd(const void* p, const void* gate, const void* residual,

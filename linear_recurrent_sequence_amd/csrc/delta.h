@@ -28,4 +28,16 @@ hipError_t launch_delta_fwd(const DeltaShape& s, const void* q, const void* k, c
                             const float* beta, const float* fgate, const float* C_in, void* h,
                             float* C_out, void* workspace, hipStream_t stream);
 
+struct DeltaGrads {
+  const void* dh;      // [B][NH][T][dv]
+  const float* dC_in;  // gradient of the memory after the sequence, or NULL (zeros)
+  void *dq, *dk, *dv;
+  float *dbeta, *dfgate;
+  float* dC_out;       // gradient of the memory before it, or NULL
+};
+size_t delta_bwd_workspace_bytes(const DeltaShape& s);
+hipError_t launch_delta_bwd(const DeltaShape& s, const void* q, const void* k, const void* v,
+                            const float* beta, const float* fgate, const float* C_in,
+                            const DeltaGrads& d, void* workspace, hipStream_t stream);
+
 }  // namespace mlstm

@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "delta.h"
 
 namespace mlstm {
@@ -81,6 +83,74 @@ __device__ inline f32x4 mma_planes(const Planes<NA>& a, const Planes<NB>& b, f32
   return c;
 }
 
+__device__ inline float load_elem(const float* p) { return *p; }
+__device__ inline float load_elem(const __hip_bfloat16* p) { return __bfloat162float(*p); }
+__device__ inline void store_elem(float* p, float x) { *p = x; }
+__device__ inline void store_elem(__hip_bfloat16* p, float x) { *p = __float2bfloat16(x); }
+
+__device__ inline float exp2_once(double x) { return __builtin_amdgcn_exp2f(float(x)); }
+
+// log sigma(x) = min(x, 0) - log1p(exp(-|x|)) in float64.  -inf (an infinite
+// or overflowing pre-activation: f = 0) is held at -1e4, whose exponential is
+// 0 too, so that differences of sums stay numbers.
+__device__ inline double log_forget(float x, int exp_forget) {
+  const double v = double(x);
+  const double f = exp_forget ? v : fmin(v, 0.0) - log1p(exp(-fabs(v)));
+  return f < -1e4 ? -1e4 : f;  // NaN stays
+}
+
+// A chunk's log2-decay sums, one token per lane (inclusive, float64).
+__device__ inline double chunk_decay(const float* fgate, int lane, int valid, int exp_forget) {
+  double s = lane < valid ? log_forget(fgate[lane], exp_forget) : 0.0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double left = __shfl_up(s, o, 64);
+    if (lane >= o) s += left;
+  }
+  return s * 1.4426950408889634;
+}
+
+// planes of 8 neighbouring elements of a row; zeros where off
+template <int N>
+__device__ inline Planes<N> load_row(const void* x, int64_t at, bool on);
+template <>
+__device__ inline Planes<1> load_row<1>(const void* x, int64_t at, bool on) {
+  Planes<1> s;
+  s.p[0] = bf16x8{};
+  if (on) s.p[0] = *reinterpret_cast<const bf16x8*>(static_cast<const __bf16*>(x) + at);
+  return s;
+}
+template <>
+__device__ inline Planes<3> load_row<3>(const void* x, int64_t at, bool on) {
+  f32x8 v = {};
+  if (on) v = *reinterpret_cast<const f32x8*>(static_cast<const float*>(x) + at);
+  return split<3>(v);
+}
+
+// the planes of a left operand in load order
+template <int N>
+__device__ inline Planes<N> load_frag(const __bf16* base, int64_t plane, int frag, int lane) {
+  Planes<N> s;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    s.p[n] = *reinterpret_cast<const bf16x8*>(base + n * plane + (int64_t(frag) * 64 + lane) * 8);
+  return s;
+}
+
+// sum over the 16 lanes of a row (every lane gets it), by DPP: lane i with
+// i ^ 1, i ^ 2, 7 - i (of 8) and 15 - i
+__device__ inline float row_sum(float x) {
+  auto dpp = [](float v, auto ctrl) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x += dpp(x, std::integral_constant<int, 0xB1>{});
+  x += dpp(x, std::integral_constant<int, 0x4E>{});
+  x += dpp(x, std::integral_constant<int, 0x141>{});
+  x += dpp(x, std::integral_constant<int, 0x140>{});
+  return x;
+}
+
 // workgroups of one head on one XCD (they are dealt round-robin to the 8
 // XCDs), so that what they share is read into one L2
 __device__ inline void map_head(int64_t wg, int64_t H, int per_head, int64_t& head, int& block) {
@@ -111,6 +181,17 @@ struct Work {
   __bf16* key;    // [HK][chunks][3] planes of K, Q (float32 inputs)
   __bf16* query;
   float* decay;   // [H][chunks][3][64]: e^G, e^(G_C - G), beta (0 behind the end)
+};
+
+// What the backward keeps between its passes.
+struct Saved {
+  float* S;     // [H][chunks][dv][dk] memory at each chunk's start
+  float* Z;     // [H][chunks][dv][dk] its gradient at each chunk's end
+  float* X;     // [H][T][dv]
+  float* dR;    // [H][T][dv] (bf16 inputs: dV is rounded)
+  float* part;  // [H][chunks][dv / 16][3][64] parts of the gates' gradients
+  float* dq;    // [HK][T][dk] sums over value heads (several to a key head)
+  float* dk;
 };
 
 }  // namespace delta

@@ -23,21 +23,6 @@ namespace {
 
 constexpr int kWaves = 4;  // value tiles of 16 per workgroup
 
-__device__ inline float load_elem(const float* p) { return *p; }
-__device__ inline float load_elem(const __hip_bfloat16* p) { return __bfloat162float(*p); }
-__device__ inline void store_elem(float* p, float x) { *p = x; }
-__device__ inline void store_elem(__hip_bfloat16* p, float x) { *p = __float2bfloat16(x); }
-
-// the planes of a left operand in load order
-template <int N>
-__device__ inline Planes<N> load_frag(const __bf16* base, int64_t plane, int frag, int lane) {
-  Planes<N> s;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    s.p[n] = *reinterpret_cast<const bf16x8*>(base + n * plane + (int64_t(frag) * 64 + lane) * 8);
-  return s;
-}
-
 // T: element type of q, k, v, h.  KS: 32-column blocks of dk.
 template <typename T, int KS>
 __global__ __launch_bounds__(64 * kWaves) void delta_fwd_kernel(

@@ -17,6 +17,7 @@ inline int key_blocks(int64_t dk) {
 
 struct Layout {
   Work ws;
+  Saved sv;
   int ks;
   size_t bytes;
 };
@@ -48,6 +49,19 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.ws.scoreT = planes(H * npp * square);
   }
   l.ws.decay = reinterpret_cast<float*>(take(H * 3 * kC * sizeof(float)));
+  if (backward) {
+    auto floats = [&](size_t n) { return reinterpret_cast<float*>(take(n * sizeof(float))); };
+    const size_t state = size_t(s.dk * s.dv), rows = size_t(s.B * s.T);
+    l.sv.S = floats(H * state);
+    l.sv.Z = floats(H * state);
+    l.sv.X = floats(rows * size_t(s.NH * s.dv));
+    if (s.is_bf16) l.sv.dR = floats(rows * size_t(s.NH * s.dv));
+    l.sv.part = floats(H * size_t(s.dv / 16) * 3 * kC);
+    if (s.NH != s.NHK) {
+      l.sv.dq = floats(rows * size_t(s.NHK * s.dk));
+      l.sv.dk = floats(rows * size_t(s.NHK * s.dk));
+    }
+  }
   return l;
 }
 

@@ -25,33 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPitch = kC + 1;  // floats between rows in LDS
 
-// log sigma(x) = min(x, 0) - log1p(exp(-|x|)) in float64.  -inf (an infinite
-// or overflowing pre-activation: f = 0) is held at -1e4, whose exponential is
-// 0 too, so that differences of sums stay numbers.
-__device__ inline double log_forget(float x, int exp_forget) {
-  const double v = double(x);
-  const double f = exp_forget ? v : fmin(v, 0.0) - log1p(exp(-fabs(v)));
-  return f < -1e4 ? -1e4 : f;  // NaN stays
-}
-
-__device__ inline float exp2_once(double x) { return __builtin_amdgcn_exp2f(float(x)); }
-
-template <int NPL>
-__device__ inline Planes<NPL> load_row(const void* x, int64_t at, bool on);
-template <>
-__device__ inline Planes<1> load_row<1>(const void* x, int64_t at, bool on) {
-  Planes<1> s;
-  s.p[0] = bf16x8{};
-  if (on) s.p[0] = *reinterpret_cast<const bf16x8*>(static_cast<const __bf16*>(x) + at);
-  return s;
-}
-template <>
-__device__ inline Planes<3> load_row<3>(const void* x, int64_t at, bool on) {
-  f32x8 v = {};
-  if (on) v = *reinterpret_cast<const f32x8*>(static_cast<const float*>(x) + at);
-  return split<3>(v);
-}
-
 __device__ inline f32x4 mma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
@@ -142,14 +115,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(
 
   if (w == 0) {
     const bool on = lane < valid;
-    double s = on ? log_forget(fgate[head * T + tok0 + lane], exp_forget) : 0.0;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double left = __shfl_up(s, o, 64);
-      if (lane >= o) s += left;
-    }
+    const double s = chunk_decay(fgate + head * T + tok0, lane, valid, exp_forget);
     const float b = on ? beta[head * T + tok0 + lane] : 0.0f;
-    s *= 1.4426950408889634;  // to base 2
     G[lane] = s;
     bt[lane] = b;
     float* v = ws.decay + at * 3 * kC;

@@ -73,6 +73,8 @@ def load_library():
     lib.mlstm_delta_workspace_bytes.restype = f
     lib.mlstm_delta_fwd.argtypes = [vp] * 9 + [f] + [i64] * 6 + [i32, i32, vp]
     lib.mlstm_delta_fwd.restype = i32
+    lib.mlstm_delta_bwd.argtypes = [vp] * 15 + [f] + [i64] * 6 + [i32, i32, vp]
+    lib.mlstm_delta_bwd.restype = i32
     lib.mlstm_delta_step.argtypes = [vp] * 8 + [i64] * 5 + [i32, i32, vp]
     lib.mlstm_delta_step.restype = i32
     fl = ctypes.c_float
@@ -477,6 +479,35 @@ def delta_fwd(q, k, v, beta, fgate, state=None, out_state=None, forget="sigmoid"
     if st != 0:
         raise MlstmError(st, "mlstm_delta_fwd")
     return h, out_state
+
+
+def delta_bwd(q, k, v, beta, fgate, dh, state=None, dstate=None, forget="sigmoid"):
+    """Gradients of ``delta_fwd`` given dh = dL/dh and ``dstate`` = dL/d(new
+    state) (zeros by default) -> (dq, dk, dv, dbeta, dfgate, d(state)).
+
+    q, k, v, beta, fgate, ``state``: as given to ``delta_fwd``.
+    """
+    lib = load_library()
+    sizes = _check_delta(q, k, v, beta, fgate, 4)
+    B, NHK, NH, T, dk, dv = sizes
+    _require("dh", dh, v.shape, v.dtype, q.device)
+    for name, t in (("state", state), ("dstate", dstate)):
+        if t is not None:
+            _require(name, t, (B, NH, dv, dk), torch.float32, q.device)
+    forget_code, code = _forget_code(forget), _dtype_code(q)
+    with _on(q.device):
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        db, df = torch.empty_like(beta), torch.empty_like(fgate)
+        dC = torch.empty((B, NH, dv, dk), dtype=torch.float32, device=q.device)
+        ws = _delta_workspace(lib, sizes, code, True, q.device)
+        st = lib.mlstm_delta_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(), fgate.data_ptr(),
+            _ptr(state), dh.data_ptr(), _ptr(dstate), dq.data_ptr(), dk_.data_ptr(),
+            dv_.data_ptr(), db.data_ptr(), df.data_ptr(), dC.data_ptr(), _ptr(ws),
+            0 if ws is None else ws.numel(), *sizes, code, forget_code, _stream_ptr(q.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_delta_bwd")
+    return dq, dk_, dv_, db, df, dC
 
 
 def delta_step(q, k, v, beta, fgate, state, out_state=None, forget="sigmoid"):
