@@ -408,6 +408,16 @@ def parallel_bwd(q, k, v, igate, fgate, h, m, n, b, dh, forget="sigmoid"):
 
 
 
+def _require_all(named, device):
+    """_require for each (name, tensor, shape, dtype); devices last, so that a
+    malformed tensor is named first."""
+    for name, t, shape, dtype in named:
+        _require(name, t, shape, dtype)
+    for name, t, _, _ in named:
+        if t.device != device or device.type != "cuda":
+            _require_device(name, t, device)
+
+
 def _check_delta(q, k, v, beta, fgate, dims):
     """Checks the gated delta rule's inputs; ``dims`` 4 with a length, 3 for one token."""
     if not isinstance(q, torch.Tensor):
@@ -425,12 +435,9 @@ def _check_delta(q, k, v, beta, fgate, dims):
     NH, dv = v.shape[1], v.shape[-1]
     T = q.shape[2] if dims == 4 else 1
     rows = (B, NH, T) if dims == 4 else (B, NH)
-    dev = q.device
-    _require("q", q, q.shape, q.dtype, dev)
-    _require("k", k, q.shape, q.dtype, dev)
-    _require("v", v, (*rows, dv), q.dtype, dev)
-    _require("beta", beta, rows, torch.float32, dev)
-    _require("fgate", fgate, rows, torch.float32, dev)
+    _require_all((("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
+                  ("v", v, (*rows, dv), q.dtype), ("beta", beta, rows, torch.float32),
+                  ("fgate", fgate, rows, torch.float32)), q.device)
     return B, NHK, NH, T, dk, dv
 
 
@@ -541,16 +548,16 @@ def _check_block_norm(p, weight, gate, residual, scale, next_weight, norm, activ
     if p.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"p must be float32 or bfloat16, got {p.dtype}")
     B, NH, T, d = p.shape
-    dev, D = p.device, NH * d
-    _require("p", p, p.shape, p.dtype, dev)
-    _require("weight", weight, (D,), torch.float32, dev)
+    D = NH * d
+    named = [("p", p, p.shape, p.dtype), ("weight", weight, (D,), torch.float32)]
     if gate is not None:
-        _require("gate", gate, p.shape, p.dtype, dev)
+        named.append(("gate", gate, p.shape, p.dtype))
     if residual is not None:
-        _require("residual", residual, (B, T, D), p.dtype, dev)
+        named.append(("residual", residual, (B, T, D), p.dtype))
     for name, t in (("scale", scale), ("next_weight", next_weight)):
         if t is not None:
-            _require(name, t, (D,), torch.float32, dev)
+            named.append((name, t, (D,), torch.float32))
+    _require_all(named, p.device)
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {tuple(NORMS)}, got {norm!r}")
     if activation not in GATE_ACTIVATIONS:

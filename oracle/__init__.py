@@ -38,6 +38,10 @@ Parity status of each function (what pins it, in ``tests/test_oracle_pins.py``):
   closed form of F, finite differences of the backward).
 * ``output_gate``          pinned: sigma(0) = 1/2 and sigma(-x) = 1 - sigma(x)
   closed forms (Eq. 78).
+
+``delta`` evaluates the gated delta rule and the block norm the same way, from
+their definitions; its gradients are pinned by central differences and its
+forward by closed forms (``tests/test_cells_cpu.py``).
 """
 
 from .mlstm import (  # noqa: F401
@@ -56,3 +60,4 @@ from .mlstm import (  # noqa: F401
     output_gate,
     backward_stabilized,
 )
+from .delta import block_norm, delta_backward, delta_forward  # noqa: F401
