@@ -55,13 +55,30 @@ template <int N>
 struct Planes {
   bf16x8 p[N];
 };
+// two values to bf16, to nearest even, the first in the low half (one
+// instruction; the compiler's own, since it has to see that a result of the
+// matrix unit is read)
+__device__ inline unsigned to_bf16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
 template <int N>
 __device__ inline Planes<N> split(f32x8 x) {
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   Planes<N> s;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    s.p[n] = __builtin_convertvector(x, bf16x8);  // to nearest even
-    if (n + 1 < N) x -= __builtin_convertvector(s.p[n], f32x8);
+    u32x4 u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] = to_bf16(x[2 * e], x[2 * e + 1]);
+      if (n + 1 < N) {
+        x[2 * e] -= __uint_as_float(u[e] << 16);
+        x[2 * e + 1] -= __uint_as_float(u[e] & 0xFFFF0000u);
+      }
+    }
+    s.p[n] = __builtin_bit_cast(bf16x8, u);
   }
   return s;
 }
@@ -149,6 +166,18 @@ __device__ inline float row_sum(float x) {
   x += dpp(x, std::integral_constant<int, 0x141>{});
   x += dpp(x, std::integral_constant<int, 0x140>{});
   return x;
+}
+
+// The products of planes i + j < kMost, small ones first, as one list: f(i, j)
+// for each, so that a caller can run one product over independent accumulators
+// before the next one (a dependent matrix instruction waits for the last).
+template <int kMost, int NA, int NB, typename F>
+__device__ inline void each_product(F&& f) {
+#pragma unroll
+  for (int s = kMost - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) f(i, s - i);
 }
 
 // workgroups of one head on one XCD (they are dealt round-robin to the 8

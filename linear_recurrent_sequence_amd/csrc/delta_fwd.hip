@@ -38,6 +38,9 @@ struct Stages {
   static constexpr int kRow = 16 * kWaves * int(sizeof(T));  // bytes of a token's values
   static constexpr int kValue = kC * kRow;                   // of a chunk's
   static constexpr int kValueCopies = kValue / kFrag / kWaves;
+  // at most a chunk ahead: the values and decays of two chunks have room
+  static constexpr int kMost = kBf16 ? 6 : 4, kAhead = n < kMost ? n : kMost;
+  static constexpr int kSlots = kAhead + 1;
   static constexpr int kShared = kSlots * kSlot + 2 * (kValue + kFrag);
 
   // copies of each wave in a stage
@@ -61,7 +64,7 @@ struct Stages {
 
 // T: element type of q, k, v, h.  KS: 32-column blocks of dk.
 template <typename T, int KS>
-__global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel(
+__global__ __launch_bounds__(128 * kWaves, 1) void delta_fwd_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const float* C_in,
     Work ws, T* __restrict__ h, float* C_out, int64_t T_len, int chunks, int64_t H, int NH,
     int NHK, int dk, int dv, int per_head, float scale) {
@@ -69,27 +72,18 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
   constexpr int NPL = St::NPL, NPP = St::NPP;
   constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
   __shared__ __attribute__((aligned(1024))) char lds[St::kShared];
-  char* const values = lds + kSlots * St::kSlot;
+  char* const values = lds + St::kSlots * St::kSlot;
   char* const decays = values + 2 * St::kValue;
   int64_t head;
   int block;
   map_head(blockIdx.x, H, per_head, head, block);
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // waves 0-3 compute, waves 4-7 copy for them
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % kWaves;
   const int col = (block * kWaves + w) * 16 + m;  // value column
-  const bool mine = col < dv;  // whole waves; the others help with the copies
+  const bool mine = col < dv;  // whole waves; the others keep the barriers company
   const int64_t khead = head / NH * NHK + head % NH / (NH / NHK);
   const unsigned lds0 = tilecommon::lds_addr(lds);
-
-  // tile 2 t + p, element r: memory row t * 32 + 8 g + 4 p + r
-  f32x4 S[2 * KS];
-#pragma unroll
-  for (int i = 0; i < 2 * KS; ++i) {
-    const int row = (i >> 1) * 32 + 8 * g + 4 * (i & 1);
-    S[i] = f32x4{};
-    if (C_in && mine && row < dk)
-      S[i] = *reinterpret_cast<const f32x4*>(C_in + (head * dv + col) * dk + row);
-  }
 
   // this wave's copies of stage s of a chunk into a slot
   const unsigned krow = ((w >> 1) * 32 + row_of(w & 1, m)) * dk * 2;  // row tile w (bf16)
@@ -101,7 +95,7 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
     const int valid = T_len - tok0 < kC ? int(T_len - tok0) : kC;
     const unsigned dst = lds0 + slot * St::kSlot, lane16 = lane * 16;
     if constexpr (s == 0) {
-      const unsigned to = lds0 + kSlots * St::kSlot + (chunk & 1) * St::kValue;
+      const unsigned to = lds0 + St::kSlots * St::kSlot + (chunk & 1) * St::kValue;
       const i32x4 from = tilecommon::rsrc_words(v + (head * T_len + tok0) * dv,
                                                 int64_t(valid) * dv * sizeof(T));
       constexpr int kLanes = St::kRow / 16;  // of a token
@@ -114,7 +108,7 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
                   0, to + (w * St::kValueCopies + j) * kFrag);
       }
       copy_frag(tilecommon::rsrc_words(ws.decay + at * 3 * kC, 3 * kC * 4), lane16, 0,
-                lds0 + kSlots * St::kSlot + 2 * St::kValue + (chunk & 1) * kFrag);
+                lds0 + St::kSlots * St::kSlot + 2 * St::kValue + (chunk & 1) * kFrag);
     }
     if constexpr (s < St::nKQ) {
       // wave w: row tile w of K and of Q
@@ -160,15 +154,37 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
     }
   };
 
+  if (wave >= kWaves) {
+    static_for<St::kAhead>(
+        [&](auto s) { issue(std::integral_constant<int, s % St::n>{}, s / St::n, s); });
+    int slot = St::kAhead;
+    for (int chunk = 0; chunk < chunks; ++chunk)
+      static_for<St::n>([&](auto stage) {
+        constexpr int s = decltype(stage)::value, next = s + St::kAhead;
+        stage_barrier<St::in_flight(s)>();
+        issue(std::integral_constant<int, next % St::n>{}, chunk + next / St::n, slot);
+        slot = slot + 1 == St::kSlots ? 0 : slot + 1;
+      });
+    // no copy may be in flight into LDS that another workgroup gets
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return;
+  }
+
+  // tile 2 t + p, element r: memory row t * 32 + 8 g + 4 p + r
+  f32x4 S[2 * KS];
+#pragma unroll
+  for (int i = 0; i < 2 * KS; ++i) {
+    const int row = (i >> 1) * 32 + 8 * g + 4 * (i & 1);
+    S[i] = f32x4{};
+    if (C_in && mine && row < dk)
+      S[i] = *reinterpret_cast<const f32x4*>(C_in + (head * dv + col) * dk + row);
+  }
+
   int read = 0;  // the slot of the stage at hand
-  static_for<kAhead>([&](auto s) { issue(std::integral_constant<int, s % St::n>{}, s / St::n, s); });
-  auto enter = [&](auto stage, int chunk) {
-    constexpr int s = decltype(stage)::value, next = s + kAhead;
-    stage_barrier<St::in_flight(s)>();
-    issue(std::integral_constant<int, next % St::n>{}, chunk + next / St::n,
-          read == 0 ? kSlots - 1 : read - 1);
+  auto enter = [&]() {
+    join_barrier();
     const char* slot = lds + read * St::kSlot;
-    read = read + 1 == kSlots ? 0 : read + 1;
+    read = read + 1 == St::kSlots ? 0 : read + 1;
     return slot;
   };
 
@@ -182,16 +198,24 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
     f32x4 ks[4] = {}, qs[4] = {};
     static_for<St::nKQ>([&](auto stage) {
       constexpr int s = decltype(stage)::value;
-      const char* slot = enter(stage, chunk);
+      const char* slot = enter();
 #pragma unroll
       for (int t = s * St::kT; t < KS && t < (s + 1) * St::kT; ++t) {
         const Planes<3> b = split<3>(pair(S[2 * t], S[2 * t + 1]));
         const char* at = slot + (t - s * St::kT) * 2 * NPL * 4 * kFrag;
+        Planes<NPL> kf[4], qf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[i] = mma_planes<3>(lds_frag<NPL>(at, i, 4, lane), b, ks[i]);
-          qs[i] = mma_planes<NPP>(lds_frag<NPL>(at, NPL * 4 + i, 4, lane), b, qs[i]);
-        }
+        for (int i = 0; i < 4; ++i) kf[i] = lds_frag<NPL>(at, i, 4, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(at, NPL * 4 + i, 4, lane);
+        each_product<3, NPL, 3>([&](int x, int y) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ks[i] = mma(kf[i].p[x], b.p[y], ks[i]);
+        });
+        each_product<NPP, NPL, 3>([&](int x, int y) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qs[i] = mma(qf[i].p[x], b.p[y], qs[i]);
+        });
       }
     });
 
@@ -211,29 +235,16 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
     // X, then U = beta X
     f32x4 U[4] = {};
     {
-      const char* slot = enter(std::integral_constant<int, St::kInv>{}, chunk);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Planes<3> b = split<3>(pair(R[2 * s], R[2 * s + 1]));
-#pragma unroll
-        for (int i = 2 * s; i < 4; ++i)  // lower triangular
-          U[i] = mma_planes<3>(lds_frag<3>(slot, i < 2 ? i : 2 * i + s - 2, 6, lane), b, U[i]);
-      }
+      const char* slot = enter();
+      low_product<3>(slot, R, U, lane);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       U[i] *= *reinterpret_cast<const f32x4*>(decay + 2 * kC + (i >> 1) * 32 + 8 * g + 4 * (i & 1));
     // h = e^G Q^ S + P U
     {
-      const char* slot = enter(std::integral_constant<int, St::kScore>{}, chunk);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Planes<NPP> b = split<NPP>(pair(U[2 * s], U[2 * s + 1]));
-#pragma unroll
-        for (int i = 2 * s; i < 4; ++i)
-          qs[i] =
-              mma_planes<NPP>(lds_frag<NPP>(slot, i < 2 ? i : 2 * i + s - 2, 6, lane), b, qs[i]);
-      }
+      const char* slot = enter();
+      low_product<NPP>(slot, U, qs, lane);
       if (mine)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -252,18 +263,28 @@ __global__ __launch_bounds__(64 * kWaves, KS <= 8 ? 2 : 1) void delta_fwd_kernel
     const Planes<3> u0 = split<3>(pair(U[0], U[1])), u1 = split<3>(pair(U[2], U[3]));
     static_for<St::nKT>([&](auto stage) {
       constexpr int j = decltype(stage)::value;
-      const char* slot = enter(std::integral_constant<int, St::kKeyT + j>{}, chunk);
+      const char* slot = enter();
+      constexpr int i0 = j * St::kI, n = 2 * KS - i0 < St::kI ? 2 * KS - i0 : St::kI;
 #pragma unroll
-      for (int i = j * St::kI; i < 2 * KS && i < (j + 1) * St::kI; ++i) {
-        const int f = (i - j * St::kI) * 2;
-        S[i] *= e_all;
-        S[i] = mma_planes<3>(lds_frag<NPL>(slot, f, St::kI * 2, lane), u0, S[i]);
-        S[i] = mma_planes<3>(lds_frag<NPL>(slot, f + 1, St::kI * 2, lane), u1, S[i]);
+      for (int i = i0; i < i0 + n; ++i) S[i] *= e_all;
+      // four tiles at a time
+#pragma unroll
+      for (int f = 0; f < n; f += 4) {
+        Planes<NPL> a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4 && f + i < n; ++i) {
+          a[i] = lds_frag<NPL>(slot, 2 * (f + i), St::kI * 2, lane);
+          b[i] = lds_frag<NPL>(slot, 2 * (f + i) + 1, St::kI * 2, lane);
+        }
+        each_product<3, NPL, 3>([&](int x, int y) {
+#pragma unroll
+          for (int i = 0; i < 4 && f + i < n; ++i) S[i0 + f + i] = mma(a[i].p[x], u0.p[y], S[i0 + f + i]);
+#pragma unroll
+          for (int i = 0; i < 4 && f + i < n; ++i) S[i0 + f + i] = mma(b[i].p[x], u1.p[y], S[i0 + f + i]);
+        });
       }
     });
   }
-  // no copy may be in flight into LDS that another workgroup gets
-  stage_barrier<0>();
   if (mine)
 #pragma unroll
     for (int i = 0; i < 2 * KS; ++i) {
@@ -277,7 +298,7 @@ hipError_t launch(const DeltaShape& s, const void* q, const void* k, const void*
                   const float* C_in, const Work& ws, void* h, float* C_out, hipStream_t stream) {
   const int chunks = int((s.T + kC - 1) / kC);
   const int per_head = int((s.dv + 16 * kWaves - 1) / (16 * kWaves));
-  delta_fwd_kernel<T, KS><<<unsigned(s.B * s.NH * per_head), 64 * kWaves, 0, stream>>>(
+  delta_fwd_kernel<T, KS><<<unsigned(s.B * s.NH * per_head), 128 * kWaves, 0, stream>>>(
       static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), C_in, ws,
       static_cast<T*>(h), C_out, s.T, chunks, s.B * s.NH, int(s.NH), int(s.NHK), int(s.dk),
       int(s.dv), per_head, 1.0f / sqrtf(float(s.dk)));
