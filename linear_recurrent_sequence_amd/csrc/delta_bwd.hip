@@ -603,9 +603,7 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
     e = chains<T, KS>(a, C_in, d.dC_in, dv, d.dC_out, stream);      \
     break
   switch (l.ks) {
-    MLSTM_CHAINS(1);
     MLSTM_CHAINS(2);
-    MLSTM_CHAINS(3);
     MLSTM_CHAINS(4);
     MLSTM_CHAINS(6);
     MLSTM_CHAINS(8);

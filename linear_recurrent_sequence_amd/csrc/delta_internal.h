@@ -7,10 +7,11 @@
 namespace mlstm {
 namespace delta {
 
-// The 32-column blocks of dk that the kernels are built for.
+// The 32-column blocks of dk that the kernels are built for (even: two waves
+// share them).
 inline int key_blocks(int64_t dk) {
   const int n = int((dk + 31) / 32);
-  for (int ks : {1, 2, 3, 4, 6, 8, 12, 16})
+  for (int ks : {2, 4, 6, 8, 12, 16})
     if (n <= ks) return ks;
   return 0;
 }
