@@ -26,259 +26,329 @@
 // that the float32 gradients (beta, gates, memory) come from has float32
 // accuracy (three bf16 planes); for bf16 inputs the products that only dq and
 // dk take carry two planes per operand (16 bits), dq and dk being rounded to 8.
-#include "delta_common.h"
+#include "delta_chain.h"
 #include "delta_internal.h"
 
 namespace mlstm {
 namespace delta {
 namespace {
 
-constexpr int kWaves = 4;
+// The stages of a chunk: P^T, K by blocks for both halves of the memory's rows,
+// (I + At)^-T, then Q^T and K^T by row tiles.
+template <typename T, int KS>
+struct Stages {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k and dh
+  static constexpr int kT = kBf16 ? 2 : 1;   // 32-column blocks of K for each half
+  static constexpr int kI = kBf16 ? 4 : 2;   // row tiles of Q^T or K^T for each half
+  static constexpr int nK = (KS / 2 + kT - 1) / kT, nT = (KS + kI - 1) / kI;
+  static constexpr int kInv = 1 + nK, kQueryT = kInv + 1, kKeyT = kQueryT + nT, n = kKeyT + nT;
+  static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
+  static constexpr int kMost = kBf16 ? 4 : 2, kAhead = n < kMost ? n : kMost;
+  static constexpr int kSlots = kAhead + 1;
+  static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
+                       kPartAt = kDecayAt + 2 * kFrag, kShared = kPartAt + kWaves * kPart;
 
-// the position of accumulator (tile i, lane group g, element 0)
-__device__ inline int acc_row(int i, int g) { return (i >> 1) * 32 + 8 * g + 4 * (i & 1); }
-
-template <typename T>
-struct Chain {
-  const T *q, *k, *v, *dh;
-  Work ws;
-  Saved sv;
-  int64_t T_len, H;
-  int chunks, NH, NHK, dk, dv, per_head, tiles;
-  float scale;
+  static constexpr int blocks_of(int s) {  // of K, for each half
+    return KS / 2 - (s - 1) * kT < kT ? KS / 2 - (s - 1) * kT : kT;
+  }
+  static constexpr int tiles_of(int j) { return KS - j * kI < kI ? KS - j * kI : kI; }
+  static constexpr int copies(int s) {
+    s %= n;
+    if (s == 0) return Copier::square_copies(3) + Values<T>::kCopies + 1;
+    if (s < kInv) return 2 * NPL * blocks_of(s);
+    if (s == kInv) return Copier::square_copies(3);
+    return tiles_of((s - kQueryT) % nT) * NPL;
+  }
+  static constexpr int in_flight(int s) {
+    int k = 0;
+    for (int j = 1; j < kAhead; ++j) k += copies(s + j);
+    return k;
+  }
 };
-
-// left operand tile i, columns t * 32 + 8 g ..: rows of q or k (bf16, those
-// behind the end repeat the last: their results are dropped), or their planes
-template <typename T, int KS>
-__device__ inline auto key_frag(const Chain<T>& a, const T* x, const __bf16* planes,
-                                int64_t khead, int64_t chunk, int valid, int t, int i, int lane) {
-  const int g = lane >> 4, m = lane & 15;
-  if constexpr (sizeof(T) == 2) {
-    const int tok = (i >> 1) * 32 + row_of(i & 1, m), c = t * 32 + g * 8;
-    return load_row<1>(
-        x, (khead * a.T_len + chunk * kC + (tok < valid ? tok : valid - 1)) * a.dk + c, c < a.dk);
-  } else {
-    constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
-    return load_frag<3>(planes + (khead * a.chunks + chunk) * 3 * kPlane, kPlane, t * 4 + i, lane);
-  }
-}
-
-// The memory once more: S at each chunk's start, X, and the part e^G dh . (S^T q^)
-// of dG that each 16 value columns give.
-template <typename T, int KS>
-__global__ __launch_bounds__(64 * kWaves) void delta_again_kernel(Chain<T> a, const float* C_in) {
-  constexpr int NPL = sizeof(T) == 2 ? 1 : 3;
-  constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
-  int64_t head;
-  int block;
-  map_head(blockIdx.x, a.H, a.per_head, head, block);
-  const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-  const int tile = block * kWaves + (threadIdx.x >> 6), col = tile * 16 + m;
-  if (col >= a.dv) return;  // whole waves; no barrier follows
-  const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
-
-  f32x4 S[2 * KS];
-#pragma unroll
-  for (int i = 0; i < 2 * KS; ++i) {
-    S[i] = f32x4{};
-    if (C_in && acc_row(i, g) < a.dk)
-      S[i] = *reinterpret_cast<const f32x4*>(C_in + (head * a.dv + col) * a.dk + acc_row(i, g));
-  }
-  for (int chunk = 0; chunk < a.chunks; ++chunk) {
-    const int64_t at = head * a.chunks + chunk, kat = khead * a.chunks + chunk;
-    const int64_t tok0 = int64_t(chunk) * kC;
-    const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
-    const float* decay = a.ws.decay + at * 3 * kC;
-#pragma unroll
-    for (int i = 0; i < 2 * KS; ++i)
-      if (acc_row(i, g) < a.dk)
-        *reinterpret_cast<f32x4*>(a.sv.S + (at * a.dv + col) * a.dk + acc_row(i, g)) = S[i];
-
-    f32x4 ks[4] = {}, qs[4] = {};
-#pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      const Planes<3> s = split<3>(pair(S[2 * t], S[2 * t + 1]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ks[i] = mma_planes<3>(
-            key_frag<T, KS>(a, a.k, a.ws.key, khead, chunk, valid, t, i, lane), s, ks[i]);
-        qs[i] = mma_planes<3>(
-            key_frag<T, KS>(a, a.q, a.ws.query, khead, chunk, valid, t, i, lane), s, qs[i]);
-      }
-    }
-    f32x4 R[4], U[4] = {};
-    float* part = a.sv.part + (at * a.tiles + tile) * 3 * kC;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = acc_row(i, g);
-      const f32x4 e = *reinterpret_cast<const f32x4*>(decay + tok);
-      f32x4 s;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        R[i][r] = 0.0f;
-        float x = 0.0f;
-        if (tok + r < valid) {
-          const int64_t from = (head * a.T_len + tok0 + tok + r) * a.dv + col;
-          R[i][r] = load_elem(a.v + from) - e[r] * ks[i][r];
-          x = load_elem(a.dh + from) * (a.scale * e[r] * qs[i][r]);
-        }
-        s[r] = row_sum(x);
-      }
-      if (m == 0) *reinterpret_cast<f32x4*>(part + tok) = s;
-    }
-    const __bf16* inv = a.ws.inv + at * 3 * kSquare;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Planes<3> b = split<3>(pair(R[2 * s], R[2 * s + 1]));
-#pragma unroll
-      for (int i = 2 * s; i < 4; ++i)
-        U[i] = mma_planes<3>(load_frag<3>(inv, kSquare, i * 2 + s, lane), b, U[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = acc_row(i, g);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (tok + r < valid) a.sv.X[(head * a.T_len + tok0 + tok + r) * a.dv + col] = U[i][r];
-      U[i] *= *reinterpret_cast<const f32x4*>(decay + 2 * kC + tok) *
-              *reinterpret_cast<const f32x4*>(decay + kC + tok);
-    }
-    const float e_all = decay[kC - 1];
-    const Planes<3> u0 = split<3>(pair(U[0], U[1])), u1 = split<3>(pair(U[2], U[3]));
-    const __bf16* keyT = a.ws.keyT + kat * NPL * kPlane;
-#pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) {
-      S[i] *= e_all;
-      S[i] = mma_planes<3>(load_frag<NPL>(keyT, kPlane, i * 2, lane), u0, S[i]);
-      S[i] = mma_planes<3>(load_frag<NPL>(keyT, kPlane, i * 2 + 1, lane), u1, S[i]);
-    }
-  }
-}
 
 // The memory's gradient backward: Z at each chunk's end, dR (and dV), and the
 // parts X . (e^(G_C - G) Z^T k) and dR . (V - X) that each 16 columns give.
+// Built as the forward is (delta_fwd.hip): the operands are upper triangular
+// here, so the first half's wave takes what the second's does there.
 template <typename T, int KS>
-__global__ __launch_bounds__(64 * kWaves) void delta_back_kernel(Chain<T> a, const float* dC_in,
-                                                                 T* dv_out, float* dC_out) {
-  constexpr int NPL = sizeof(T) == 2 ? 1 : 3;
+__global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const float* dC_in,
+                                                              T* dv_out, float* dC_out) {
+  using St = Stages<T, KS>;
+  using V = Values<T>;
+  constexpr int NPL = St::NPL;
   constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
+  __shared__ __attribute__((aligned(1024))) char lds[St::kShared];
   int64_t head;
   int block;
   map_head(blockIdx.x, a.H, a.per_head, head, block);
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
-  const int tile = block * kWaves + (threadIdx.x >> 6), col = tile * 16 + m;
-  if (col >= a.dv) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
+  const int chunks = a.chunks, dk = a.dk, dv = a.dv;
 
-  f32x4 Z[2 * KS];
+  if (wave >= kChainWaves) {
+    const Copier cp = {wave - kChainWaves, lane, tilecommon::lds_addr(lds)};
+    // `turn` counts chunks from the last one
+    auto issue = [&](auto stage, int turn, int slot) {
+      constexpr int s = decltype(stage)::value;
+      const int side = turn & 1, chunk = turn < chunks ? chunks - 1 - turn : 0;
+      const int64_t at = head * chunks + chunk, kat = khead * chunks + chunk;
+      const int64_t tok0 = int64_t(chunk) * kC;
+      const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
+      const unsigned dst = slot * St::kSlot;
+      if constexpr (s == 0) {
+        cp.values(a.dh, (head * a.T_len + tok0) * dv, valid, dv, block * 16 * kWaves,
+                  St::kValueAt + side * V::kBytes);
+        cp.decay(a.ws.decay + at * 3 * kC, St::kDecayAt + side * kFrag);
+        cp.template square<3, false>(a.ws.scoreT + at * 3 * kSquare, dst);
+      } else if constexpr (s < St::kInv) {
 #pragma unroll
-  for (int i = 0; i < 2 * KS; ++i) {
-    Z[i] = f32x4{};
-    if (dC_in && acc_row(i, g) < a.dk)
-      Z[i] = *reinterpret_cast<const f32x4*>(dC_in + (head * a.dv + col) * a.dk + acc_row(i, g));
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < St::blocks_of(s); ++j) {
+            const int t = half * (KS / 2) + (s - 1) * St::kT + j;
+            if constexpr (St::kBf16) {
+              cp.rows(a.k, (khead * a.T_len + tok0) * dk, valid, dk, t,
+                      dst + (half * 2 + j) * 4 * kFrag);
+            } else {
+#pragma unroll
+              for (int p = 0; p < NPL; ++p)
+                cp.frag(a.ws.key + (kat * NPL + p) * kPlane, kPlane * 2, t * 4 + cp.w,
+                        dst + ((half * NPL + p) * 4 + cp.w) * kFrag);
+            }
+          }
+      } else if constexpr (s == St::kInv) {
+        cp.template square<3, false>(a.ws.invT + at * 3 * kSquare, dst);
+      } else {
+        constexpr int j = (s - St::kQueryT) % St::nT;
+        cp.template transposed<NPL, KS, St::kI>(
+            (s < St::kKeyT ? a.ws.queryT : a.ws.keyT) + kat * NPL * kPlane, j * St::kI,
+            St::tiles_of(j), dst);
+      }
+    };
+    static_for<St::kAhead>(
+        [&](auto s) { issue(std::integral_constant<int, s % St::n>{}, s / St::n, s); });
+    int slot = St::kAhead;
+    for (int turn = 0; turn < chunks; ++turn)
+      static_for<St::n>([&](auto stage) {
+        constexpr int s = decltype(stage)::value, next = s + St::kAhead;
+        stage_barrier<St::in_flight(s)>();
+        issue(std::integral_constant<int, next % St::n>{}, turn + next / St::n, slot);
+        slot = slot + 1 == St::kSlots ? 0 : slot + 1;
+        if constexpr (s == St::kQueryT) {  // dV is where dh was
+          const int64_t tok0 = int64_t(chunks - 1 - turn) * kC;
+          cp.store_values(lds + St::kValueAt + (turn & 1) * V::kBytes, dv_out,
+                          (head * a.T_len + tok0) * dv,
+                          a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC, dv,
+                          block * 16 * kWaves);
+        }
+      });
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return;
   }
-  for (int chunk = a.chunks - 1; chunk >= 0; --chunk) {
-    const int64_t at = head * a.chunks + chunk, kat = khead * a.chunks + chunk;
-    const int64_t tok0 = int64_t(chunk) * kC;
-    const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
-    const float* decay = a.ws.decay + at * 3 * kC;
-#pragma unroll
-    for (int i = 0; i < 2 * KS; ++i)
-      if (acc_row(i, g) < a.dk)
-        *reinterpret_cast<f32x4*>(a.sv.Z + (at * a.dv + col) * a.dk + acc_row(i, g)) = Z[i];
 
-    // K Z
-    f32x4 kz[4] = {};
+  const int tile = wave % kWaves, half = wave / kWaves;
+  const int col = (block * kWaves + tile) * 16 + m;
+  const bool mine = col < dv;
+  const int first_row = half * KS * 16;
+  f32x4 Z[KS];
 #pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      const Planes<3> s = split<3>(pair(Z[2 * t], Z[2 * t + 1]));
+  for (int i = 0; i < KS; ++i) {
+    const int row = first_row + acc_row(i, g);
+    Z[i] = f32x4{};
+    if (dC_in && mine && row < dk)
+      Z[i] = *reinterpret_cast<const f32x4*>(dC_in + (head * dv + col) * dk + row);
+  }
+  // K Z of all tokens to the first half's wave, of tokens 32-63 to the
+  // second's; then each one's dR to the other
+  f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * kPart) + lane;
+  f32x4* const to_second = to_first + 4 * 64;
+  int read = 0;
+  auto enter = [&]() {
+    join_barrier();
+    const char* slot = lds + read * St::kSlot;
+    read = read + 1 == St::kSlots ? 0 : read + 1;
+    return slot;
+  };
+
+  for (int turn = 0; turn < chunks; ++turn) {
+    const int chunk = chunks - 1 - turn;
+    const int64_t at = head * chunks + chunk, tok0 = int64_t(chunk) * kC;
+    const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
+    const float* decay = reinterpret_cast<const float*>(lds + St::kDecayAt + (turn & 1) * kFrag);
+    char* value = lds + St::kValueAt + (turn & 1) * V::kBytes;
+    auto value_of = [&](int tok) {
+      return reinterpret_cast<T*>(value + V::at(tok)) + tile * 16 + m;
+    };
+    auto at_tile = [&](int what, int i) {
+      return *reinterpret_cast<const f32x4*>(decay + what * kC + acc_row(i, g));
+    };
+    // of values: this wave's tokens are rows + (4 i + r) dv + mine0
+    const int64_t rows = (head * a.T_len + tok0) * dv;
+    const unsigned mine0 = (32 * half + 8 * g) * dv + col;
+    if (mine) {
+      float* const end = a.sv.Z + (at * dv + col) * dk + first_row + 8 * g;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const int row = first_row + acc_row(i, g);
+        if (row < dk) *reinterpret_cast<f32x4*>(end + (row - first_row - 8 * g)) = Z[i];
+      }
+    }
+    // P^T dh: of this wave's tokens, and for the first half of the others too
+    f32x4 dh[4], dU[4] = {};
+    {
+      const char* slot = enter();
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        kz[i] = mma_planes<3>(
-            key_frag<T, KS>(a, a.k, a.ws.key, khead, chunk, valid, t, i, lane), s, kz[i]);
-    }
-    f32x4 dh[4], X[4], pred[4];
-    float* part = a.sv.part + (at * a.tiles + tile) * 3 * kC;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = acc_row(i, g);
-      const f32x4 e = *reinterpret_cast<const f32x4*>(decay + kC + tok);
-      f32x4 s;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        dh[i][r] = X[i][r] = pred[i][r] = 0.0f;
-        kz[i][r] = tok + r < valid ? kz[i][r] * e[r] : 0.0f;
-        if (tok + r < valid) {
-          const int64_t from = (head * a.T_len + tok0 + tok + r) * a.dv + col;
-          dh[i][r] = load_elem(a.dh + from);
-          X[i][r] = a.sv.X[from];
-          pred[i][r] = load_elem(a.v + from) - X[i][r];
+        for (int r = 0; r < 4; ++r) {
+          const int tok = acc_row(i, g) + r;
+          const float x = load_elem(value_of(tok));
+          dh[i][r] = tok < valid ? x : 0.0f;
         }
-        s[r] = row_sum(X[i][r] * kz[i][r]);
-      }
-      if (m == 0) *reinterpret_cast<f32x4*>(part + kC + tok) = s;
+      const Planes<NPL> h0 = split<NPL>(pair(dh[0], dh[1])), h1 = split<NPL>(pair(dh[2], dh[3]));
+      add_square<3, false>(slot, lane, kHighSecond, h1, h1, dU[2], dU[3]);
+      if (half == 0) add_square<3, true>(slot, lane, kHighFirst, h0, h1, dU[0], dU[1]);
     }
-    // dU = P^T dh + e^(G_C - G) K Z  (upper triangular), times beta
-    const __bf16* scoreT = a.ws.scoreT + at * 3 * kSquare;
+    // this wave's tokens of X and V - X
+    f32x4 X[2] = {}, pred[2] = {};
+    if (mine)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Planes<NPL> b = split<NPL>(pair(dh[2 * s], dh[2 * s + 1]));
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 2 * s + 2; ++i)
-        kz[i] = mma_planes<3>(load_frag<3>(scoreT, kSquare, i * 2 + s, lane), b, kz[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      kz[i] *= *reinterpret_cast<const f32x4*>(decay + 2 * kC + acc_row(i, g));
-    // dR
-    f32x4 dR[4] = {};
-    const __bf16* invT = a.ws.invT + at * 3 * kSquare;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Planes<3> b = split<3>(pair(kz[2 * s], kz[2 * s + 1]));
-#pragma unroll
-      for (int i = 0; i < 2 * s + 2; ++i)
-        dR[i] = mma_planes<3>(load_frag<3>(invT, kSquare, i * 2 + s, lane), b, dR[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = acc_row(i, g);
-      const f32x4 e = *reinterpret_cast<const f32x4*>(decay + tok);
-      f32x4 s;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[r] = row_sum(dR[i][r] * pred[i][r]);
-        if (tok + r < valid) {
-          const int64_t to = (head * a.T_len + tok0 + tok + r) * a.dv + col;
-          store_elem(dv_out + to, dR[i][r]);
-          if (sizeof(T) == 2) a.sv.dR[to] = dR[i][r];
+        for (int r = 0; r < 4; ++r) {
+          const int tok = acc_row(2 * half + i, g) + r;
+          if (tok < valid) {
+            X[i][r] = elem(a.sv.X + rows + (4 * i + r) * dv, mine0);
+            pred[i][r] = load_elem(&elem(a.v + rows + (4 * i + r) * dv, mine0)) - X[i][r];
+          }
         }
-        dR[i][r] *= -e[r];
-        dh[i][r] *= a.scale * e[r];
+    // K Z over this half's rows
+    f32x4 kz[4] = {};
+    static_for<St::nK>([&](auto stage) {
+      constexpr int s = decltype(stage)::value, nb = St::blocks_of(s + 1);
+      const char* slot = enter() + half * (St::kBf16 ? 8 : NPL * 4) * kFrag;
+#pragma unroll
+      for (int j = 0; j < nb; ++j) {
+        Planes<NPL> kf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kf[i] = lds_frag<NPL>(slot, j * 4 + i, 4, lane);
+        const int t = s * St::kT + j;
+        const Planes<3> b = split<3>(pair(Z[2 * t], Z[2 * t + 1]));
+        each_product<3, NPL, 3>([&](int x, int y) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kz[i] = mma(kf[i].p[x], b.p[y], kz[i]);
+        });
       }
-      if (m == 0) *reinterpret_cast<f32x4*>(part + 2 * kC + tok) = s;
+    });
+    if (half == 0) {
+      to_second[0] = kz[2];
+      to_second[64] = kz[3];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to_first[i * 64] = kz[i];
+    }
+    // dU, and dR = (I + At)^-T (beta dU) of this wave's tokens
+    f32x4 dR[4], own[2] = {};
+    float* const part = a.sv.part + (at * a.tiles + block * kWaves + tile) * 3 * kC;
+    {
+      const char* slot = enter();
+      // e^(G_C - G) K Z, nothing behind the end
+      auto whole = [&](int i, f32x4 other) {
+        f32x4 x = (kz[i] + other) * at_tile(1, i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = acc_row(i, g) + r < valid ? x[r] : 0.0f;
+        return x;
+      };
+      auto write_part = [&](int what, int i, f32x4 x, f32x4 y) {
+        f32x4 s;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[r] = row_sum(x[r] * y[r]);
+        if (mine && m == 0)
+          elem4(part, what * kC + acc_row(2 * half + i, g)) = s;
+      };
+      if (half == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 x = whole(i, to_first[i * 64]);
+          if (i < 2) write_part(1, i, X[i], x);
+          dU[i] = (dU[i] + x) * at_tile(2, i);
+        }
+        add_square<3, true>(slot, lane, kHighFirst, split<3>(pair(dU[0], dU[1])),
+                            split<3>(pair(dU[2], dU[3])), own[0], own[1]);
+        to_first[0] = own[0];
+        to_first[64] = own[1];
+      } else {
+#pragma unroll
+        for (int i = 2; i < 4; ++i) {
+          const f32x4 x = whole(i, to_second[(i - 2) * 64]);
+          write_part(1, i - 2, X[i - 2], x);
+          dU[i] = (dU[i] + x) * at_tile(2, i);
+        }
+        const Planes<3> b = split<3>(pair(dU[2], dU[3]));
+        add_square<3, false>(slot, lane, kHighSecond, b, b, own[0], own[1]);
+        to_second[0] = own[0];
+        to_second[64] = own[1];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        write_part(2, i, own[i], pred[i]);
+        const int tok = acc_row(2 * half + i, g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // the other wave has read dh (before this stage's barrier)
+          store_elem(value_of(tok + r), own[i][r]);
+          if (sizeof(T) == 2 && mine && tok + r < valid)
+            elem(a.sv.dR + rows + (4 * i + r) * dv, mine0) = own[i][r];
+        }
+      }
     }
     // Z at the chunk's start
+    const char* slot = enter();
+    if (half == 0) {
+      dR[0] = own[0];
+      dR[1] = own[1];
+      dR[2] = to_second[0];
+      dR[3] = to_second[64];
+    } else {
+      dR[0] = to_first[0];
+      dR[1] = to_first[64];
+      dR[2] = own[0];
+      dR[3] = own[1];
+    }
     const float e_all = decay[kC - 1];
-    const Planes<3> r0 = split<3>(pair(dR[0], dR[1])), r1 = split<3>(pair(dR[2], dR[3]));
-    const Planes<3> h0 = split<3>(pair(dh[0], dh[1])), h1 = split<3>(pair(dh[2], dh[3]));
-    const __bf16* keyT = a.ws.keyT + kat * NPL * kPlane;
-    const __bf16* queryT = a.ws.queryT + kat * NPL * kPlane;
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) {
-      Z[i] *= e_all;
-      Z[i] = mma_planes<3>(load_frag<NPL>(queryT, kPlane, i * 2, lane), h0, Z[i]);
-      Z[i] = mma_planes<3>(load_frag<NPL>(queryT, kPlane, i * 2 + 1, lane), h1, Z[i]);
-      Z[i] = mma_planes<3>(load_frag<NPL>(keyT, kPlane, i * 2, lane), r0, Z[i]);
-      Z[i] = mma_planes<3>(load_frag<NPL>(keyT, kPlane, i * 2 + 1, lane), r1, Z[i]);
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 e = at_tile(0, i);
+      dR[i] *= -e;
+      dh[i] *= a.scale * e;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) Z[i] *= e_all;
+    {
+      const Planes<3> u0 = split<3>(pair(dh[0], dh[1])), u1 = split<3>(pair(dh[2], dh[3]));
+      static_for<St::nT>([&](auto stage) {
+        constexpr int j = decltype(stage)::value;
+        if (j > 0) slot = enter();
+        add_transposed<NPL, St::tiles_of(j), St::kI>(slot, half, u0, u1, Z + j * St::kI, lane);
+      });
+    }
+    {
+      const Planes<3> u0 = split<3>(pair(dR[0], dR[1])), u1 = split<3>(pair(dR[2], dR[3]));
+      static_for<St::nT>([&](auto stage) {
+        constexpr int j = decltype(stage)::value;
+        slot = enter();
+        add_transposed<NPL, St::tiles_of(j), St::kI>(slot, half, u0, u1, Z + j * St::kI, lane);
+      });
     }
   }
-  if (dC_out)
+  if (dC_out && mine)
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i)
-      if (acc_row(i, g) < a.dk)
-        *reinterpret_cast<f32x4*>(dC_out + (head * a.dv + col) * a.dk + acc_row(i, g)) = Z[i];
+    for (int i = 0; i < KS; ++i) {
+      const int row = first_row + acc_row(i, g);
+      if (row < dk) *reinterpret_cast<f32x4*>(dC_out + (head * dv + col) * dk + row) = Z[i];
+    }
 }
 
 // planes of 8 neighbouring float32 values, scaled; zeros where off
@@ -574,49 +644,35 @@ __global__ __launch_bounds__(64 * kWaves) void delta_grads_kernel(Grads<T> a) {
   }
 }
 
-template <typename T, int KS>
-hipError_t chains(const Chain<T>& a, const float* C_in, const float* dC_in, T* dv, float* dC_out,
-                  hipStream_t stream) {
-  const unsigned grid = unsigned(a.H * a.per_head);
-  delta_again_kernel<T, KS><<<grid, 64 * kWaves, 0, stream>>>(a, C_in);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  delta_back_kernel<T, KS><<<grid, 64 * kWaves, 0, stream>>>(a, dC_in, dv, dC_out);
-  return hipGetLastError();
-}
-
 template <typename T>
 hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, const void* q,
                     const void* k, const void* v, const float* fgate, const float* C_in,
                     hipStream_t stream) {
-  const int chunks = int((s.T + kC - 1) / kC), tiles = int(s.dv / 16);
-  const int per_head = (tiles + kWaves - 1) / kWaves;
-  const float scale = 1.0f / sqrtf(float(s.dk));
-  const Chain<T> a = {static_cast<const T*>(q), static_cast<const T*>(k),
-                      static_cast<const T*>(v), static_cast<const T*>(d.dh), l.ws, l.sv, s.T,
-                      s.B * s.NH, chunks, int(s.NH), int(s.NHK), int(s.dk), int(s.dv), per_head,
-                      tiles, scale};
-  T* dv = static_cast<T*>(d.dv);
-  hipError_t e = hipErrorInvalidValue;
-#define MLSTM_CHAINS(KS)                                            \
-  case KS:                                                          \
-    e = chains<T, KS>(a, C_in, d.dC_in, dv, d.dC_out, stream);      \
+  hipError_t e = launch_again(s, l, q, k, v, d.dh, C_in, stream);
+  if (e != hipSuccess) return e;
+  const Chain<T> a = chain<T>(s, l, q, k, v, d.dh);
+#define MLSTM_BACK(KS)                                                                   \
+  case KS:                                                                               \
+    delta_back_kernel<T, KS><<<unsigned(a.H * a.per_head), kThreads, 0, stream>>>(       \
+        a, d.dC_in, static_cast<T*>(d.dv), d.dC_out);                                    \
     break
   switch (l.ks) {
-    MLSTM_CHAINS(2);
-    MLSTM_CHAINS(4);
-    MLSTM_CHAINS(6);
-    MLSTM_CHAINS(8);
-    MLSTM_CHAINS(12);
-    MLSTM_CHAINS(16);
+    MLSTM_BACK(2);
+    MLSTM_BACK(4);
+    MLSTM_BACK(6);
+    MLSTM_BACK(8);
+    MLSTM_BACK(12);
+    MLSTM_BACK(16);
+    default: return hipErrorInvalidValue;
   }
-#undef MLSTM_CHAINS
+#undef MLSTM_BACK
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const float* dR = sizeof(T) == 2 ? l.sv.dR : static_cast<const float*>(d.dv);
   const Grads<T> b = {a.q, a.k, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
-                      static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, chunks, int(s.NH),
-                      int(s.NHK), int(s.dk), int(s.dv), l.ks, tiles, int(s.exp_forget), scale};
-  delta_grads_kernel<T><<<unsigned(s.B * s.NHK * chunks), 64 * kWaves, 0, stream>>>(b);
+                      static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
+                      a.dv, l.ks, a.tiles, int(s.exp_forget), a.scale};
+  delta_grads_kernel<T><<<unsigned(s.B * s.NHK * a.chunks), 64 * kWaves, 0, stream>>>(b);
   return hipGetLastError();
 }
 

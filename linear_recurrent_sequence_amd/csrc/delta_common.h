@@ -154,6 +154,18 @@ __device__ inline Planes<N> load_frag(const __bf16* base, int64_t plane, int fra
   return s;
 }
 
+// x[i] with the same x in all lanes: the address is a scalar base and a 32-bit
+// offset, one register instead of a pair for each access
+template <typename T>
+__device__ inline T& elem(T* x, unsigned i) {
+  return *reinterpret_cast<T*>(
+      reinterpret_cast<std::conditional_t<std::is_const<T>::value, const char, char>*>(x) +
+      i * unsigned(sizeof(T)));
+}
+__device__ inline f32x4& elem4(float* x, unsigned i) {
+  return *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(x) + i * 4u);
+}
+
 // sum over the 16 lanes of a row (every lane gets it), by DPP: lane i with
 // i ^ 1, i ^ 2, 7 - i (of 8) and 15 - i
 __device__ inline float row_sum(float x) {

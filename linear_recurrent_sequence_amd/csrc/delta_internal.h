@@ -66,6 +66,30 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
   return l;
 }
 
+// What a chain kernel takes.
+template <typename T>
+struct Chain {
+  const T *q, *k, *v, *dh;
+  Work ws;
+  Saved sv;
+  int64_t T_len, H;
+  int chunks, NH, NHK, dk, dv, tiles, per_head;
+  float scale;
+};
+template <typename T>
+Chain<T> chain(const DeltaShape& s, const Layout& l, const void* q, const void* k, const void* v,
+               const void* dh) {
+  const int tiles = int(s.dv / 16);
+  return {static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+          static_cast<const T*>(dh), l.ws, l.sv, s.T, s.B * s.NH, int((s.T + kC - 1) / kC),
+          int(s.NH), int(s.NHK), int(s.dk), int(s.dv), tiles, (tiles + 3) / 4,
+          1.0f / sqrtf(float(s.dk))};
+}
+
+// the memory once more for the backward (Saved::S, X and the first of part)
+hipError_t launch_again(const DeltaShape& s, const Layout& l, const void* q, const void* k,
+                        const void* v, const void* dh, const float* C_in, hipStream_t stream);
+
 // ks: the 32-column blocks that the kernels are built for, >= ceil(dk / 32)
 hipError_t launch_prep(const DeltaShape& s, const void* q, const void* k, const float* beta,
                        const float* fgate, const Work& ws, int ks, bool backward,
