@@ -366,7 +366,8 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
  *   fgate    [B][NH][T]       float32, the pre-activations f~
  *   C        [B][NH][dv][dk]  float32
  *   NHK      a divisor of NH;  dk a multiple of 16 in [16, 512];
- *   dv       a multiple of 16 in [16, 1024];  T >= 1
+ *   dv       a multiple of 16 in [16, 1024];  T >= 1;  fewer than 2^18 heads
+ *            B NH, and 2^22 chunks B NH ceil(T / 64)
  * k is not normalized here.  The recurrence is stable for
  * beta |k|^2 <= 2 (unit keys and strengths in (0, 1), as a rule).  A position
  * with beta = 0 and f = 1 (f~ = +infinity, or 0 with MLSTM_FORGET_EXP) leaves

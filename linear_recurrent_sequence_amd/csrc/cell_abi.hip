@@ -20,6 +20,8 @@ using mlstm::abi::overlaps;
 
 constexpr int64_t kMaxT = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
+constexpr int64_t kMaxDeltaHeads = (int64_t(1) << 18) - 1;
+constexpr int64_t kMaxDeltaChunks = (int64_t(1) << 22) - 1;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
@@ -42,10 +44,9 @@ int check_delta(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk, int64
       dv > mlstm::kDeltaMaxValueDim)
     return MLSTM_ERR_HEAD_DIM;
   const int64_t H = B * NH, chunks = (T + mlstm::kDeltaChunk - 1) / mlstm::kDeltaChunk;
-  // grids are one-dimensional: a workgroup per head and chunk, and at most
-  // dv / 16 <= 64 per head
-  if (H > kMaxGrid / 64 || H > kMaxGrid / chunks) return MLSTM_ERR_SHAPE;
-  if (H * chunks > kMaxElems / (64 * 1024)) return MLSTM_ERR_SHAPE;
+  // a launch takes fewer than 2^32 threads: at most 64 workgroups of 256 to a
+  // head, or 4 to a head's chunk
+  if (H > kMaxDeltaHeads || H > kMaxDeltaChunks / chunks) return MLSTM_ERR_SHAPE;
   return MLSTM_OK;
 }
 

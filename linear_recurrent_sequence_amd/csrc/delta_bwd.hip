@@ -18,11 +18,11 @@
 // (V_j - X_j is what the memory predicted for token j), and dlog f is the sum
 // of dG from its token to the chunk's end, so no sum is longer than a chunk.
 //
-// Four passes: the terms that all columns share (delta_prep.hip), the memory
-// forward once more (its start and X of every chunk are kept, float32), the
-// gradient of the memory backward (Z and dR kept), and, over all chunks at
-// once, the gradients of q, k, beta and the gates.  The two chains hold 16
-// value columns per wave in the accumulators, as the forward does.  Everything
+// Six passes: the terms that all columns share (delta_prep.hip), the memory
+// forward once more (delta_fwd.hip; its start and X of every chunk are kept,
+// float32), the gradient of the memory backward (Z and dR kept), and, over all
+// chunks at once, the pairs of tokens, the gradients of q and k, and those of
+// beta and the gates.  Everything
 // that the float32 gradients (beta, gates, memory) come from has float32
 // accuracy (three bf16 planes); for bf16 inputs the products that only dq and
 // dk take carry two planes per operand (16 bits), dq and dk being rounded to 8.
@@ -187,14 +187,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     // of values: this wave's tokens are rows + (4 i + r) dv + mine0
     const int64_t rows = (head * a.T_len + tok0) * dv;
     const unsigned mine0 = (32 * half + 8 * g) * dv + col;
-    if (mine) {
-      float* const end = a.sv.Z + (at * dv + col) * dk + first_row + 8 * g;
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const int row = first_row + acc_row(i, g);
-        if (row < dk) *reinterpret_cast<f32x4*>(end + (row - first_row - 8 * g)) = Z[i];
-      }
-    }
+    if (mine) store_state(a.sv.Z + at * dk * dv, Z, first_row, dk, dv, col, lane);
     // P^T dh: of this wave's tokens, and for the first half of the others too
     f32x4 dh[4], dU[4] = {};
     {
@@ -296,12 +289,10 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
         write_part(2, i, own[i], pred[i]);
         const int tok = acc_row(2 * half + i, g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          // the other wave has read dh (before this stage's barrier)
+        for (int r = 0; r < 4; ++r)  // the other wave has read dh (before this stage's barrier)
           store_elem(value_of(tok + r), own[i][r]);
-          if (sizeof(T) == 2 && mine && tok + r < valid)
-            elem(a.sv.dR + rows + (4 * i + r) * dv, mine0) = own[i][r];
-        }
+        if (sizeof(T) == 2 && mine)
+          store_tokens(a.sv.dR + rows, own[i], tok, valid, dv, col, lane);
       }
     }
     // Z at the chunk's start
@@ -351,13 +342,34 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     }
 }
 
-// planes of 8 neighbouring float32 values, scaled; zeros where off
+// planes of 8 neighbouring values
 template <int N>
-__device__ inline Planes<N> load_scaled(const float* x, int64_t at, float by, bool on) {
-  f32x8 v = {};
-  if (on) v = *reinterpret_cast<const f32x8*>(x + at) * by;
-  return split<N>(v);
+__device__ inline Planes<N> to_planes(const f32x8& x) {
+  return split<N>(x);
 }
+template <int N>
+__device__ inline Planes<N> to_planes(const bf16x8& x) {
+  Planes<N> s = {};
+  s.p[0] = x;
+  return s;
+}
+template <typename T>
+struct Eight {
+  using type = f32x8;
+};
+template <>
+struct Eight<__hip_bfloat16> {
+  using type = bf16x8;
+};
+template <typename T>
+__device__ inline typename Eight<T>::type load8(const T* x, int64_t at, bool on) {
+  typename Eight<T>::type v = {};
+  if (on) v = *reinterpret_cast<const typename Eight<T>::type*>(x + at);
+  return v;
+}
+
+constexpr int kGradThreads = 256;
+constexpr int kPitch = kC + 1;
 
 template <typename T>
 struct Grads {
@@ -369,278 +381,330 @@ struct Grads {
   T *dq, *dk;
   float *dbeta, *dfgate;
   int64_t T_len;
-  int chunks, NH, NHK, dk_dim, dv, ks, tiles, exp_forget;
+  int chunks, NH, NHK, dk_dim, dv, ks, tiles, groups, exp_forget;
   float scale;
 };
 
-constexpr int kPitch = kC + 1;
-
 // writes N planes of m (or its transpose) in load order
 template <int N, bool kTranspose>
-__device__ inline void write_planes(const float (*m)[kPitch], __bf16* to) {
-  for (int i = threadIdx.x; i < kSquare / 8; i += 64 * kWaves) {
+__device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* to) {
+  for (int i = threadIdx.x; i < kSquare / 8; i += kGradThreads) {
     const int lane = i & 63, frag = i >> 6;
     const int row = (frag >> 2) * 32 + row_of((frag >> 1) & 1, lane & 15);
     const int col = (frag & 1) * 32 + (lane >> 4) * 8;
     f32x8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = kTranspose ? m[col + e][row] : m[row][col + e];
+    for (int e = 0; e < 8; ++e) v[e] = by * (kTranspose ? m[col + e][row] : m[row][col + e]);
     const Planes<N> s = split<N>(v);
 #pragma unroll
     for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(to + n * kSquare + i * 8) = s.p[n];
   }
 }
 
-// The gradients of q, k, beta and the gates: one workgroup per key head and
-// chunk, its value heads one after the other.
+// The 64 x 64 matrices of a head's chunk: B, B^T / sqrt(dk) and -(N + N^T) in
+// planes for delta_grads_kernel, and what they give to dG and dbeta.
 template <typename T>
-__global__ __launch_bounds__(64 * kWaves) void delta_grads_kernel(Grads<T> a) {
+__global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
   constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k, dh
-  constexpr int NPD = kBf16 ? 2 : 3;  // planes of what only dq and dk take
+  constexpr int NPL = kBf16 ? 1 : 3, NPD = kBf16 ? 2 : 3;
   __shared__ double G[kC];
-  __shared__ float e0[kC], e1[kC], bt[kC], row_g[kC], col_g[kWaves][kC], col_b[kWaves][kC];
-  __shared__ float inner[kWaves], mat[kC][kPitch];
-  __shared__ __attribute__((aligned(16))) __bf16 planes[3][NPD * kSquare];  // B, B^T, -(N + N^T)
+  __shared__ float bt[kC], row_g[kC], col_g[kWaves][kC], col_b[kWaves][kC];
+  __shared__ float mat[kC][kPitch];
   const int chunk = blockIdx.x % a.chunks;
-  const int64_t khead = blockIdx.x / a.chunks;
-  const int group = a.NH / a.NHK;
+  const int64_t head = blockIdx.x / a.chunks, at = blockIdx.x;
+  const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
   const int64_t tok0 = int64_t(chunk) * kC;
   const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+  const int64_t krow0 = khead * a.T_len + tok0, row0 = head * a.T_len + tok0;
+  if (w == 0) {
+    G[lane] = chunk_decay(a.fgate + row0, lane, valid, a.exp_forget);
+    bt[lane] = a.ws.decay[at * 3 * kC + 2 * kC + lane];
+  }
+  // rows 16 w ..: dh . X, dR . X, k . k, q . k
+  f32x4 hx[4] = {}, rx[4] = {}, kk[4] = {}, qk[4] = {};
+  const bool r_on = 16 * w + m < valid;
+  for (int s = 0; s < a.dv; s += 32) {
+    const int c = s + g * 8;
+    const bool c_on = c < a.dv;
+    const Planes<NPL> h =
+        to_planes<NPL>(load8(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on));
+    const Planes<3> r = to_planes<3>(load8(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+        const Planes<3> x = to_planes<3>(
+            load8(a.sv.X, (row0 + 16 * j + m) * a.dv + c, c_on && 16 * j + m < valid));
+        hx[j] = mma_planes<3>(h, x, hx[j]);
+        rx[j] = mma_planes<3>(r, x, rx[j]);
+      }
+  }
+  for (int t = 0; t < a.dk_dim; t += 32) {
+    const int c = t + g * 8;
+    const bool c_on = c < a.dk_dim;
+    const Planes<NPL> qa =
+        to_planes<NPL>(load8(a.q, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on));
+    const Planes<NPL> ka =
+        to_planes<NPL>(load8(a.k, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= w) {
+        const Planes<NPL> kb = to_planes<NPL>(
+            load8(a.k, (krow0 + 16 * j + m) * a.dk_dim + c, c_on && 16 * j + m < valid));
+        kk[j] = mma_planes<NPL>(ka, kb, kk[j]);
+        qk[j] = mma_planes<NPL>(qa, kb, qk[j]);
+      }
+  }
+  __syncthreads();
+  f32x4 rows = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float cg = 0.0f, cb = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r, c = 16 * j + m;
+      const float d = c <= row ? exp2_once(G[row] - G[c]) : 0.0f, b = bt[c];
+      const float p = d * qk[j][r] * a.scale;
+      mat[row][c] = c <= row ? d * b * hx[j][r] : 0.0f;
+      float n = 0.0f;
+      if (c <= row) cb += p * hx[j][r];
+      if (c < row) {
+        n = d * b * rx[j][r];
+        cb -= d * rx[j][r] * kk[j][r];
+        rows[r] += p * b * hx[j][r];
+        cg += n * kk[j][r] - p * b * hx[j][r];
+      }
+      rx[j][r] = n;
+    }
+    cg += __shfl_xor(cg, 16, 64);
+    cg += __shfl_xor(cg, 32, 64);
+    cb += __shfl_xor(cb, 16, 64);
+    cb += __shfl_xor(cb, 32, 64);
+    if (g == 0) {
+      col_g[w][16 * j + m] = cg;
+      col_b[w][16 * j + m] = cb;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float s = row_sum(rows[r]);
+    if (m == 0) row_g[16 * w + 4 * g + r] = s;
+  }
+  __syncthreads();
+  __bf16* const out = a.sv.pairs + at * 3 * NPD * kSquare;
+  write_planes<NPD, false>(mat, 1.0f, out);
+  write_planes<NPD, true>(mat, a.scale, out + NPD * kSquare);
+  if (w == 0) {
+    float cg = row_g[lane], cb = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      cg += col_g[i][lane];
+      cb += col_b[i][lane];
+    }
+    a.sv.gates[at * 2 * kC + lane] = cg;
+    a.sv.gates[at * 2 * kC + kC + lane] = cb;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * w + 4 * g + r, c = 16 * j + m;
+      if (c < row) mat[row][c] = mat[c][row] = -rx[j][r];
+      if (c == row) mat[row][c] = 0.0f;
+    }
+  __syncthreads();
+  write_planes<NPD, false>(mat, 1.0f, out + 2 * NPD * kSquare);
+}
+
+// The gradients of q and k: a workgroup takes a key head's chunk and 128
+// columns of dk, a wave 32 of them, for the value heads one after the other.
+// The contraction over dv runs 32 at a time: wave i splits token tile i of dh,
+// dR and X into planes in LDS (two buffers, one barrier), and each wave the
+// columns of S and Z that it alone needs; the next 32 are loaded meanwhile.
+template <typename T>
+__global__ __launch_bounds__(kGradThreads) void delta_grads_kernel(Grads<T> a) {
+  constexpr bool kBf16 = sizeof(T) == 2;
+  constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k, dh
+  constexpr int NPD = kBf16 ? 2 : 3;  // planes of what only dq and dk take
+  constexpr int kSet = NPL + 2 * NPD;
+  __shared__ __attribute__((aligned(16))) char lds[2][4][kSet][kFrag];
+  __shared__ float e0[kC], inner[kWaves];
+  const int64_t id = blockIdx.x / a.groups;
+  const int chunk = id % a.chunks, blk = int(blockIdx.x % a.groups) * kWaves;
+  const int64_t khead = id / a.chunks;
+  const int group = a.NH / a.NHK;
+  const int64_t tok0 = int64_t(chunk) * kC;
+  const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, m = lane & 15;
   const int64_t krow0 = khead * a.T_len + tok0;
   const int64_t plane = int64_t(a.ks) * 32 * kC;
+  const int col0 = (blk + w) * 32;  // this wave's columns
+  const int tok = (w >> 1) * 32 + row_of(w & 1, m);  // token tile w
+  f32x4 dq[4][2] = {}, dk[4][2] = {};
 
   for (int hh = 0; hh < group; ++hh) {
     const int64_t head = khead / a.NHK * a.NH + khead % a.NHK * group + hh;
     const int64_t at = head * a.chunks + chunk, row0 = head * a.T_len + tok0;
+    const float* decay = a.ws.decay + at * 3 * kC;
     __syncthreads();
-    if (w == 0) {
-      const float* decay = a.ws.decay + at * 3 * kC;
-      G[lane] = chunk_decay(a.fgate + row0, lane, valid, a.exp_forget);
-      e0[lane] = decay[lane];
-      e1[lane] = decay[kC + lane];
-      bt[lane] = decay[2 * kC + lane];
-    }
-    // rows 16 w ..: dh . X, dR . X, k . k, q . k
-    f32x4 hx[4] = {}, rx[4] = {}, kk[4] = {}, qk[4] = {};
-    const bool r_on = 16 * w + m < valid;
-    for (int s = 0; s < a.dv; s += 32) {
-      const int c = s + g * 8;
-      const bool c_on = c < a.dv;
-      const Planes<NPL> h = load_row<NPL>(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
-      const Planes<3> r = load_row<3>(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          const Planes<3> x =
-              load_row<3>(a.sv.X, (row0 + 16 * j + m) * a.dv + c, c_on && 16 * j + m < valid);
-          hx[j] = mma_planes<3>(h, x, hx[j]);
-          rx[j] = mma_planes<3>(r, x, rx[j]);
-        }
-    }
-    for (int t = 0; t < a.dk_dim; t += 32) {
-      const int c = t + g * 8;
-      const bool c_on = c < a.dk_dim;
-      const Planes<NPL> qa = load_row<NPL>(a.q, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on);
-      const Planes<NPL> ka = load_row<NPL>(a.k, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          const Planes<NPL> kb = load_row<NPL>(a.k, (krow0 + 16 * j + m) * a.dk_dim + c,
-                                               c_on && 16 * j + m < valid);
-          kk[j] = mma_planes<NPL>(ka, kb, kk[j]);
-          qk[j] = mma_planes<NPL>(qa, kb, qk[j]);
-        }
-    }
-    __syncthreads();
-    f32x4 rows = {};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float cg = 0.0f, cb = 0.0f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r, c = 16 * j + m;
-        const float d = c <= row ? exp2_once(G[row] - G[c]) : 0.0f, b = bt[c];
-        const float p = d * qk[j][r] * a.scale;
-        mat[row][c] = c <= row ? d * b * hx[j][r] : 0.0f;
-        float n = 0.0f;
-        if (c <= row) cb += p * hx[j][r];
-        if (c < row) {
-          n = d * b * rx[j][r];
-          cb -= d * rx[j][r] * kk[j][r];
-          rows[r] += p * b * hx[j][r];
-          cg += n * kk[j][r] - p * b * hx[j][r];
-        }
-        rx[j][r] = n;
-      }
-      cg += __shfl_xor(cg, 16, 64);
-      cg += __shfl_xor(cg, 32, 64);
-      cb += __shfl_xor(cb, 16, 64);
-      cb += __shfl_xor(cb, 32, 64);
-      if (g == 0) {
-        col_g[w][16 * j + m] = cg;
-        col_b[w][16 * j + m] = cb;
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float s = row_sum(rows[r]);
-      if (m == 0) row_g[16 * w + 4 * g + r] = s;
-    }
-    __syncthreads();
-    write_planes<NPD, false>(mat, planes[0]);
-    write_planes<NPD, true>(mat, planes[1]);
-    __syncthreads();
-    // -(N + N^T): the strict lower part by its owners, then the upper by theirs
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * w + 4 * g + r, c = 16 * j + m;
-        if (c < row) mat[row][c] = mat[c][row] = -rx[j][r];
-        if (c == row) mat[row][c] = 0.0f;
-      }
-    __syncthreads();
-    write_planes<NPD, false>(mat, planes[2]);
-    __syncthreads();
-
-    // 32 columns of dq and dk at a time per wave
+    if (w == 0) e0[lane] = decay[lane];
+    const float by_r = -decay[tok], by_x = decay[kC + tok] * decay[2 * kC + tok];
     float dot = 0.0f;
-    for (int blk = w; blk * 32 < a.dk_dim; blk += kWaves) {
-      f32x4 dq[4][2] = {}, dk[4][2] = {};
-      for (int s = 0; s < a.dv; s += 32) {
-        Planes<NPD> S[2], Z[2];
+    typename Eight<T>::type dh;
+    f32x8 dR, X, S[2], Z[2];
+    auto load = [&](int s) {
+      const int c = s + g * 8;
+      const bool on = tok < valid && c < a.dv;
+      const int64_t from = (row0 + tok) * a.dv + c;
+      dh = load8(a.dh, from, on);
+      dR = load8(a.dR, from, on);
+      X = load8(a.sv.X, from, on);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int kc = col0 + row_of(p, m);
+        const bool k_on = kc < a.dk_dim && c < a.dv;
+        const int64_t k_from = (at * a.dk_dim + kc) * a.dv + c;
+        S[p] = load8(a.sv.S, k_from, k_on);
+        Z[p] = load8(a.sv.Z, k_from, k_on);
+      }
+    };
+    load(0);
+    f32x4 own[4][2] = {};  // dh S^T of this value head
+    for (int s = 0, side = 0; s < a.dv; s += 32, side ^= 1) {
+      {
+        const Planes<NPL> h = to_planes<NPL>(dh);
+        const Planes<NPD> r = split<NPD>(dR * by_r), x = split<NPD>(X * by_x);
+        auto put = [&](int n, bf16x8 v) {
+          *reinterpret_cast<bf16x8*>(&lds[side][w][n][lane * 16]) = v;
+        };
+#pragma unroll
+        for (int n = 0; n < NPL; ++n) put(n, h.p[n]);
+#pragma unroll
+        for (int n = 0; n < NPD; ++n) {
+          put(NPL + n, r.p[n]);
+          put(NPL + NPD + n, x.p[n]);
+        }
+      }
+      Planes<NPD> Sp[2], Zp[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += S[p][e] * Z[p][e];
+        Sp[p] = split<NPD>(S[p]);
+        Zp[p] = split<NPD>(Z[p]);
+      }
+      __syncthreads();
+      load(s + 32);  // nothing behind the last column
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Planes<NPL> h = lds_frag<NPL>(lds[side][i][0], 0, 1, lane);
+        const Planes<NPD> r = lds_frag<NPD>(lds[side][i][NPL], 0, 1, lane);
+        const Planes<NPD> x = lds_frag<NPD>(lds[side][i][NPL + NPD], 0, 1, lane);
+        each_product<NPD, NPL, NPD>([&](int y, int z) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) own[i][p] = mma(h.p[y], Sp[p].p[z], own[i][p]);
+        });
+        each_product<NPD, NPD, NPD>([&](int y, int z) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) dk[i][p] = mma(r.p[y], Sp[p].p[z], dk[i][p]);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) dk[i][p] = mma(x.p[y], Zp[p].p[z], dk[i][p]);
+        });
+      }
+    }
+    // e^G dh S^T + B K, B^T Q^ - (N + N^T) K
+    const __bf16* pairs = a.sv.pairs + at * 3 * NPD * kSquare;
+    const __bf16* keyT = a.ws.keyT + (khead * a.chunks + chunk) * NPL * plane;
+    const __bf16* queryT = a.ws.queryT + (khead * a.chunks + chunk) * NPL * plane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float e = e0[acc_row(i, g) + r];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) dq[i][p][r] += e * own[i][p][r];
+      }
+    if (col0 < a.dk_dim)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Planes<NPL> kf[2], qf[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const int kc = blk * 32 + row_of(p, m);
-          f32x8 x = {}, z = {};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int vr = s + g * 8 + e;
-            if (vr < a.dv && kc < a.dk_dim) {
-              x[e] = a.sv.S[(at * a.dv + vr) * a.dk_dim + kc];
-              z[e] = a.sv.Z[(at * a.dv + vr) * a.dk_dim + kc];
-            }
-            dot += x[e] * z[e];
-          }
-          S[p] = split<NPD>(x);
-          Z[p] = split<NPD>(z);
+          kf[p] = load_frag<NPL>(keyT, plane, ((blk + w) * 2 + p) * 2 + s, lane);
+          qf[p] = load_frag<NPL>(queryT, plane, ((blk + w) * 2 + p) * 2 + s, lane);
         }
-        const int c = s + g * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tok = (i >> 1) * 32 + row_of(i & 1, m);
-          const bool on = tok < valid && c < a.dv;
-          const int64_t from = (row0 + tok) * a.dv + c;
-          const Planes<NPL> h = load_row<NPL>(a.dh, from, on);
-          const Planes<NPD> r = load_scaled<NPD>(a.dR, from, -e0[tok], on);
-          const Planes<NPD> x = load_scaled<NPD>(a.sv.X, from, e1[tok] * bt[tok], on);
+          const int f = i * 2 + s;
+          auto add = [&](int which, const Planes<NPL>(&b)[2], f32x4(&c)[2]) {
+            const Planes<NPD> x =
+                load_frag<NPD>(pairs + which * NPD * kSquare, kSquare, f, lane);
+            each_product<NPD, NPD, NPL>([&](int y, int z) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            dq[i][p] = mma_planes<NPD>(h, S[p], dq[i][p]);
-            dk[i][p] = mma_planes<NPD>(r, S[p], dk[i][p]);
-            dk[i][p] = mma_planes<NPD>(x, Z[p], dk[i][p]);
-          }
+              for (int p = 0; p < 2; ++p) c[p] = mma(x.p[y], b[p].p[z], c[p]);
+            });
+          };
+          if (i >= 2 * s) add(0, kf, dq[i]);  // lower triangular
+          if (i < 2 * s + 2) add(1, qf, dk[i]);
+          add(2, kf, dk[i]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = e0[acc_row(i, g) + r];
-          dq[i][0][r] *= e;
-          dq[i][1][r] *= e;
-        }
-      const __bf16* keyT = a.ws.keyT + (khead * a.chunks + chunk) * NPL * plane;
-      const __bf16* queryT = a.ws.queryT + (khead * a.chunks + chunk) * NPL * plane;
-      f32x4 bq[4][2] = {};
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int frag = (blk * 2 + p) * 2 + s;
-          const Planes<NPL> kf = load_frag<NPL>(keyT, plane, frag, lane);
-          const Planes<NPL> qf = load_frag<NPL>(queryT, plane, frag, lane);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int f = i * 2 + s;
-            if (i >= 2 * s)  // B is lower triangular
-              dq[i][p] =
-                  mma_planes<NPD>(load_frag<NPD>(planes[0], kSquare, f, lane), kf, dq[i][p]);
-            if (i < 2 * s + 2)
-              bq[i][p] =
-                  mma_planes<NPD>(load_frag<NPD>(planes[1], kSquare, f, lane), qf, bq[i][p]);
-            dk[i][p] =
-                mma_planes<NPD>(load_frag<NPD>(planes[2], kSquare, f, lane), kf, dk[i][p]);
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int tok = acc_row(i, g) + r, kc = blk * 32 + row_of(p, m);
-            if (tok >= valid || kc >= a.dk_dim) continue;
-            const int64_t to = (krow0 + tok) * a.dk_dim + kc;
-            float x = a.scale * dq[i][p][r], y = dk[i][p][r] + a.scale * bq[i][p][r];
-            // value heads of one key head: summed in float32, by this thread
-            if (hh > 0) {
-              x += a.sv.dq[to];
-              y += a.sv.dk[to];
-            }
-            if (hh + 1 < group) {
-              a.sv.dq[to] = x;
-              a.sv.dk[to] = y;
-            } else {
-              store_elem(a.dq + to, x);
-              store_elem(a.dk + to, y);
-            }
-          }
-    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o, 64);
     if (lane == 0) inner[w] = dot;
     __syncthreads();
-    if (w == 0) {
-      double dg = 0.0;
-      float t1 = 0.0f, t3 = 0.0f, t2 = 0.0f;
-      const float* part = a.sv.part + at * a.tiles * 3 * kC;
-      for (int i = 0; i < a.tiles; ++i) {
-        t1 += part[i * 3 * kC + lane];
-        t3 += part[i * 3 * kC + kC + lane];
-        t2 += part[i * 3 * kC + 2 * kC + lane];
-      }
-      float cg = 0.0f, cb = 0.0f;
+    if (threadIdx.x == 0)
+      a.sv.inner[at * a.groups + blk / kWaves] = (inner[0] + inner[1]) + (inner[2] + inner[3]);
+  }
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
-        cg += col_g[i][lane];
-        cb += col_b[i][lane];
-      }
-      const double s3 = double(bt[lane]) * t3;
-      dg = double(t1) + row_g[lane] + cg - t2 - s3;
-      // to the chunk's end: the tokens' writes and what the memory keeps
-      double all = s3;
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o, 64);
-      if (lane == 63)
-        dg += all + double(e0[63]) * ((double(inner[0]) + inner[1]) + (double(inner[2]) + inner[3]));
-      // sums from each token to the end
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double right = __shfl_down(dg, o, 64);
-        if (lane + o < 64) dg += right;
+      for (int r = 0; r < 4; ++r) {
+        const int t = acc_row(i, g) + r, kc = col0 + row_of(p, m);
+        if (t >= valid || kc >= a.dk_dim) continue;
+        store_elem(a.dq + (krow0 + t) * a.dk_dim + kc, a.scale * dq[i][p][r]);
+        store_elem(a.dk + (krow0 + t) * a.dk_dim + kc, dk[i][p][r]);
       }
-      if (lane < valid) {
-        const float x = a.fgate[row0 + lane];
-        // d log sigma(x) = sigma(-x), from e^-|x|
-        const double t = exp(-fabs(double(x)));
-        a.dfgate[row0 + lane] =
-            float(a.exp_forget ? dg : dg * ((x >= 0.0f ? t : 1.0) / (1.0 + t)));
-        a.dbeta[row0 + lane] = cb + t3;
-      }
-    }
+}
+
+// The gradients of beta and of the gates: a wave per head and chunk.
+template <typename T>
+__global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
+  const int chunk = blockIdx.x % a.chunks, lane = threadIdx.x;
+  const int64_t head = blockIdx.x / a.chunks, at = blockIdx.x;
+  const int64_t row0 = head * a.T_len + int64_t(chunk) * kC;
+  const int valid = a.T_len - int64_t(chunk) * kC < kC ? int(a.T_len - int64_t(chunk) * kC) : kC;
+  float t1 = 0.0f, t3 = 0.0f, t2 = 0.0f;
+  const float* part = a.sv.part + at * a.tiles * 3 * kC;
+  for (int i = 0; i < a.tiles; ++i) {
+    t1 += part[i * 3 * kC + lane];
+    t3 += part[i * 3 * kC + kC + lane];
+    t2 += part[i * 3 * kC + 2 * kC + lane];
+  }
+  const float* decay = a.ws.decay + at * 3 * kC;
+  const double s3 = double(decay[2 * kC + lane]) * t3;
+  double dg = double(t1) + a.sv.gates[at * 2 * kC + lane] - t2 - s3;
+  // to the chunk's end: the tokens' writes and what the memory keeps
+  double all = s3, kept = 0.0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o, 64);
+  for (int i = 0; i < a.groups; ++i) kept += a.sv.inner[at * a.groups + i];
+  if (lane == 63) dg += all + double(decay[kC - 1]) * kept;
+  // sums from each token to the end
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double right = __shfl_down(dg, o, 64);
+    if (lane + o < 64) dg += right;
+  }
+  if (lane < valid) {
+    const float x = a.fgate[row0 + lane];
+    // d log sigma(x) = sigma(-x), from e^-|x|
+    const double t = exp(-fabs(double(x)));
+    a.dfgate[row0 + lane] = float(a.exp_forget ? dg : dg * ((x >= 0.0f ? t : 1.0) / (1.0 + t)));
+    a.dbeta[row0 + lane] = a.sv.gates[at * 2 * kC + kC + lane] + t3;
   }
 }
 
@@ -669,10 +733,17 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const float* dR = sizeof(T) == 2 ? l.sv.dR : static_cast<const float*>(d.dv);
+  const int groups = int((s.dk + 127) / 128);
   const Grads<T> b = {a.q, a.k, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
                       static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
-                      a.dv, l.ks, a.tiles, int(s.exp_forget), a.scale};
-  delta_grads_kernel<T><<<unsigned(s.B * s.NHK * a.chunks), 64 * kWaves, 0, stream>>>(b);
+                      a.dv, l.ks, a.tiles, groups, int(s.exp_forget), a.scale};
+  const unsigned each = unsigned(a.H * a.chunks);
+  delta_pairs_kernel<T><<<each, kGradThreads, 0, stream>>>(b);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  delta_grads_kernel<T>
+      <<<unsigned(s.B * s.NHK * a.chunks * groups), kGradThreads, 0, stream>>>(b);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  delta_gates_kernel<T><<<each, 64, 0, stream>>>(b);
   return hipGetLastError();
 }
 

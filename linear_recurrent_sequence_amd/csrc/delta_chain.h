@@ -90,6 +90,29 @@ struct Values {
 // memory row from the half's first on.
 __device__ inline int acc_row(int i, int g) { return (i >> 1) * 32 + 8 * g + 4 * (i & 1); }
 
+// The memory's slice of a wave (KS tiles from row first_row on, one value column
+// per lane) to x [dk][dv], and 4 tokens of a value column per lane to x
+// [T][dv]: transposed over quads of lanes, so that a lane stores 16 bytes and 16
+// lanes four runs of 64.
+template <int KS>
+__device__ inline void store_state(float* x, const f32x4 (&S)[KS], int first_row, int dk, int dv,
+                                   int col, int lane) {
+  const int row = first_row + acc_row(0, lane >> 4) + (lane & 3);
+  float* const to = x + int64_t(row) * dv + (col & ~3);
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const int more = acc_row(i, 0);
+    const f32x4 y = quad_transpose(S[i], lane);
+    if (row + more < dk) *reinterpret_cast<f32x4*>(to + more * dv) = y;
+  }
+}
+__device__ inline void store_tokens(float* x, f32x4 y, int tok, int valid, int dv, int col,
+                                    int lane) {
+  y = quad_transpose(y, lane);
+  tok += lane & 3;
+  if (tok < valid) elem4(x, tok * dv + (col & ~3)) = y;
+}
+
 // One copying wave's view: w of kWaves.
 struct Copier {
   int w, lane;

@@ -166,6 +166,25 @@ __device__ inline f32x4& elem4(float* x, unsigned i) {
   return *reinterpret_cast<f32x4*>(reinterpret_cast<char*>(x) + i * 4u);
 }
 
+// Transposes 4 registers over each 4 neighbouring lanes: lane j of a quad gets
+// x[j] of its lanes 0 .. 3.
+__device__ inline f32x4 quad_transpose(f32x4 x, int lane) {
+  auto swap = [](float& a, float& b, bool odd, auto ctrl) {
+    const float out = odd ? a : b;
+    const float in = __int_as_float(__builtin_amdgcn_update_dpp(
+        0, __float_as_int(out), decltype(ctrl)::value, 0xF, 0xF, true));
+    a = odd ? in : a;
+    b = odd ? b : in;
+  };
+  float a = x[0], b = x[1], c = x[2], d = x[3];
+  const bool odd = lane & 1, high = lane & 2;
+  swap(a, b, odd, std::integral_constant<int, 0xB1>{});  // lane ^ 1
+  swap(c, d, odd, std::integral_constant<int, 0xB1>{});
+  swap(a, c, high, std::integral_constant<int, 0x4E>{});  // lane ^ 2
+  swap(b, d, high, std::integral_constant<int, 0x4E>{});
+  return f32x4{a, b, c, d};
+}
+
 // sum over the 16 lanes of a row (every lane gets it), by DPP: lane i with
 // i ^ 1, i ^ 2, 7 - i (of 8) and 15 - i
 __device__ inline float row_sum(float x) {
@@ -226,13 +245,14 @@ struct Work {
 
 // What the backward keeps between its passes.
 struct Saved {
-  float* S;     // [H][chunks][dv][dk] memory at each chunk's start
-  float* Z;     // [H][chunks][dv][dk] its gradient at each chunk's end
+  float* S;     // [H][chunks][dk][dv] memory at each chunk's start
+  float* Z;     // [H][chunks][dk][dv] its gradient at each chunk's end
   float* X;     // [H][T][dv]
   float* dR;    // [H][T][dv] (bf16 inputs: dV is rounded)
   float* part;  // [H][chunks][dv / 16][3][64] parts of the gates' gradients
-  float* dq;    // [HK][T][dk] sums over value heads (several to a key head)
-  float* dk;
+  __bf16* pairs;  // [H][chunks][3][NPD] planes of B, B^T / sqrt(dk), -(N + N^T)
+  float* gates;   // [H][chunks][2][64] what the pairs of tokens give to dG, dbeta
+  float* inner;   // [H][chunks][blocks of 128 dk] parts of <S, Z>
 };
 
 }  // namespace delta

@@ -192,12 +192,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
             const int tok = acc_row(2 * half + i, g) + r;
             if (tok < valid) dh[i][r] = load_elem(&elem(a.dh + rows + (4 * i + r) * dv, own));
           }
-        float* const start = a.sv.S + (at * dv + col) * dk + first_row + 8 * g;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const int row = first_row + acc_row(i, g);
-          if (row < dk) *reinterpret_cast<f32x4*>(start + (row - first_row - 8 * g)) = S[i];
-        }
+        store_state(a.sv.S + at * dk * dv, S, first_row, dk, dv, col, lane);
       }
     }
 
@@ -282,13 +277,10 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = acc_row(2 * half + i, g);
+        if (mine) store_tokens(a.sv.X + rows, x[i], tok, valid, dv, col, lane);
         f32x4 s;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          s[r] = row_sum(dh[i][r] * hs[i][r]);
-          if (mine && tok + r < valid)
-            elem(a.sv.X + rows + (4 * i + r) * dv, own) = x[i][r];
-        }
+        for (int r = 0; r < 4; ++r) s[r] = row_sum(dh[i][r] * hs[i][r]);
         if (mine && m == 0)
           elem4(a.sv.part + (at * a.tiles + block * kWaves + tile) * 3 * kC, tok) = s;
       }

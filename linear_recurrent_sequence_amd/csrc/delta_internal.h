@@ -58,10 +58,10 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.sv.X = floats(rows * size_t(s.NH * s.dv));
     if (s.is_bf16) l.sv.dR = floats(rows * size_t(s.NH * s.dv));
     l.sv.part = floats(H * size_t(s.dv / 16) * 3 * kC);
-    if (s.NH != s.NHK) {
-      l.sv.dq = floats(rows * size_t(s.NHK * s.dk));
-      l.sv.dk = floats(rows * size_t(s.NHK * s.dk));
-    }
+    const size_t npd = s.is_bf16 ? 2 : 3;
+    l.sv.pairs = planes(H * 3 * npd * square);
+    l.sv.gates = floats(H * 2 * kC);
+    l.sv.inner = floats(H * size_t((s.dk + 127) / 128));
   }
   return l;
 }
