@@ -51,20 +51,34 @@ struct Geometry {
   int rows_per_wg;
 };
 
-__device__ inline void load8(const float* p, float* x) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// 8 neighbouring elements as they lie in memory
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+};
+template <>
+struct Raw<__hip_bfloat16> {
+  uint4 a;
+};
+template <typename T>
+__device__ inline Raw<T> raw8(const T* p) {
+  return *reinterpret_cast<const Raw<T>*>(p);
 }
-__device__ inline void load8(const __hip_bfloat16* p, float* x) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const unsigned u[4] = {a.x, a.y, a.z, a.w};
+__device__ inline void floats(const Raw<float>& r, float* x) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+__device__ inline void floats(const Raw<__hip_bfloat16>& r, float* x) {
+  const unsigned u[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
+__device__ inline void load8(const float* p, float* x) { floats(raw8(p), x); }
 __device__ inline void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -76,16 +90,34 @@ __device__ inline void store8(__hip_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
 }
 
+// Butterflies in registers: x plus that of lane ^ 1, ^ 2 (quads), the mirrored
+// lane of 8 and of 16 (whose halves are equal by then), lane ^ 16, lane ^ 32.
+template <int kCtrl>
+__device__ inline float plus_dpp(float x) {
+  return x + __int_as_float(
+                 __builtin_amdgcn_update_dpp(0, __float_as_int(x), kCtrl, 0xF, 0xF, true));
+}
+__device__ inline float plus_16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float plus_32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 // sum over the 2^shift lanes of a head (every lane gets it)
 __device__ inline float head_sum(float x, int shift) {
-  for (int o = 0; o < shift; ++o) x += __shfl_xor(x, 1 << o, 64);
+  if (shift > 0) x = plus_dpp<0xB1>(x);
+  if (shift > 1) x = plus_dpp<0x4E>(x);
+  if (shift > 2) x = plus_dpp<0x141>(x);
+  if (shift > 3) x = plus_dpp<0x140>(x);
+  if (shift > 4) x = plus_16(x);
+  if (shift > 5) x = plus_32(x);
   return x;
 }
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-  return x;
-}
+__device__ inline float wave_sum(float x) { return head_sum(x, 6); }
 
 // mean and sum of squares about it of `n` values, joined with another set's
 struct Moments {
@@ -127,6 +159,66 @@ struct Lane {
     }
     count = wave_sum(mine);
     head_count = head_sum(in_head, g.lane_shift);
+  }
+};
+
+// A wave's rows one after the other: (b, t) by addition, no division per row.
+struct Rows {
+  int64_t row, b, t, step, step_b, step_t;
+
+  __device__ Rows(const Geometry& g, int sub) {
+    step = int64_t(gridDim.x) * g.rows_per_wg;
+    step_b = step / g.T;
+    step_t = step % g.T;
+    row = int64_t(blockIdx.x) * g.rows_per_wg + sub;
+    b = row / g.T;
+    t = row % g.T;
+  }
+  __device__ void next(const Geometry& g) {
+    row += step;
+    b += step_b;
+    t += step_t;
+    if (t >= g.T) t -= g.T, ++b;
+  }
+  __device__ bool live(const Geometry& g) const { return row < g.rows; }
+  // of p and gate, before the head's offset
+  __device__ int64_t base(const Geometry& g) const { return (b * g.NH * g.T + t) * g.d; }
+};
+
+// A wave's inputs of one row, zeros where off (and behind the end).
+template <typename T, int VPL, int NP>
+struct Inputs {
+  Raw<T> p[VPL * NP], g[VPL * NP], x[VPL * NP];
+
+  __device__ void load(const Geometry& geo, const Lane<VPL, NP>& L, const T* from_p,
+                       const T* gate, const T* residual, const Rows& rows) {
+    const int64_t base = rows.base(geo);
+#pragma unroll
+    for (int c = 0; c < VPL * NP; ++c) {
+      p[c] = g[c] = x[c] = Raw<T>{};
+      if (!L.on[c] || !rows.live(geo)) continue;
+      const int64_t at = base + L.head_off[c / VPL] + L.channel[c];
+      p[c] = raw8(from_p + at);
+      if (gate) g[c] = raw8(gate + at);
+      if (residual) x[c] = raw8(residual + rows.row * geo.D + L.column[c]);
+    }
+  }
+};
+template <typename T, int NC>
+struct RowGrads {
+  Raw<T> r[NC], y[NC];
+
+  template <typename L>
+  __device__ void load(const Geometry& geo, const L& lane, const T* dr, const T* dy,
+                       const Rows& rows) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      r[c] = y[c] = Raw<T>{};
+      if (!lane.on[c] || !rows.live(geo)) continue;
+      const int64_t at = rows.row * geo.D + lane.column[c];
+      if (dr) r[c] = raw8(dr + at);
+      if (dy) y[c] = raw8(dy + at);
+    }
   }
 };
 
@@ -241,7 +333,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
     T* __restrict__ r_out, T* __restrict__ y_out, float eps, int silu) {
   constexpr int NC = VPL * NP;
   __shared__ Shared sh;
-  const int all = threadIdx.x >> 6, sub = all / g.waves_per_row;
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = all / g.waves_per_row;
   const int wave = all % g.waves_per_row, wave0 = sub * g.waves_per_row;
   const Lane<VPL, NP> L(g, wave, threadIdx.x & 63);
   float w1[NC][kVec], sc[NC][kVec], w2[NC][kVec];
@@ -257,25 +349,26 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
       if (next_weight) load8(next_weight + L.column[c], w2[c]);
     }
   int parity = 0;
+  constexpr bool kAhead = NC <= 2;  // where registers allow it
+  Rows next(g, sub);
+  Inputs<T, VPL, NP> now;
+  if (kAhead) now.load(g, L, p, gate, residual, next);
+  // the same number of turns for all of a workgroup's rows: they share barriers
   for (int64_t first = int64_t(blockIdx.x) * g.rows_per_wg; first < g.rows;
-       first += int64_t(gridDim.x) * g.rows_per_wg, parity ^= 1) {
-    const bool live = first + sub < g.rows;
-    const int64_t row = live ? first + sub : g.rows - 1;  // keeps the barriers company
-    const int64_t b = row / g.T, t = row % g.T;
-    const int64_t base = (b * g.NH * g.T + t) * g.d;
+       first += next.step, parity ^= 1) {
+    if (!kAhead) now.load(g, L, p, gate, residual, next);
+    const bool live = next.live(g);
+    const int64_t row = next.row;
+    next.next(g);
     float z[NC][kVec], gt[NC][kVec], r[NC][kVec];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) z[c][e] = gt[c][e] = r[c][e] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (L.on[c]) {
-        const int64_t at = base + L.head_off[c / VPL] + L.channel[c];
-        load8(p + at, z[c]);
-        if (gate) load8(gate + at, gt[c]);
-        if (residual) load8(residual + row * g.D + L.column[c], r[c]);
-      }
+    for (int c = 0; c < NC; ++c) {
+      floats(now.p[c], z[c]);
+      floats(now.g[c], gt[c]);
+      floats(now.x[c], r[c]);
+    }
+    // the next row is on its way while this one is worked on
+    if (kAhead) now.load(g, L, p, gate, residual, next);
     float inv1[NP];
     head_norms<kLayer, VPL, NP>(g, L, z, inv1, eps, sh.head[parity], wave0, all);
 #pragma unroll
@@ -317,7 +410,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     int silu) {
   constexpr int NC = VPL * NP;
   __shared__ Shared sh;
-  const int all = threadIdx.x >> 6, sub = all / g.waves_per_row;
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = all / g.waves_per_row;
   const int wave = all % g.waves_per_row, wave0 = sub * g.waves_per_row;
   const Lane<VPL, NP> L(g, wave, threadIdx.x & 63);
   float w1[NC][kVec], sc[NC][kVec], w2[NC][kVec];
@@ -338,28 +431,38 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     }
   const float inv_d = 1.0f / float(g.d), inv_D = 1.0f / float(g.D);
   int parity = 0;
+  const T* const x_in = next_weight ? residual : nullptr;  // only r needs it
+  const T* const dy_in = next_weight ? dy : nullptr;
+  constexpr bool kAhead = NC == 1;
+  Rows next(g, sub);
+  Inputs<T, VPL, NP> now;
+  RowGrads<T, NC> grads;
+  if (kAhead) {
+    now.load(g, L, p, gate, x_in, next);
+    grads.load(g, L, dr, dy_in, next);
+  }
   for (int64_t first = int64_t(blockIdx.x) * g.rows_per_wg; first < g.rows;
-       first += int64_t(gridDim.x) * g.rows_per_wg, parity ^= 1) {
-    const bool live = first + sub < g.rows;
-    const int64_t row = live ? first + sub : g.rows - 1;
-    const int64_t b = row / g.T, t = row % g.T;
-    const int64_t base = (b * g.NH * g.T + t) * g.d;
+       first += next.step, parity ^= 1) {
+    if (!kAhead) {
+      now.load(g, L, p, gate, x_in, next);
+      grads.load(g, L, dr, dy_in, next);
+    }
+    const bool live = next.live(g);
+    const int64_t row = next.row, base = next.base(g);
+    next.next(g);
     float n1[NC][kVec], gt[NC][kVec], r[NC][kVec], gr[NC][kVec], gy[NC][kVec];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) n1[c][e] = gt[c][e] = r[c][e] = gr[c][e] = gy[c][e] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (L.on[c]) {
-        const int64_t at = base + L.head_off[c / VPL] + L.channel[c];
-        const int64_t rat = row * g.D + L.column[c];
-        load8(p + at, n1[c]);
-        if (gate) load8(gate + at, gt[c]);
-        if (residual && next_weight) load8(residual + rat, r[c]);
-        if (dr) load8(dr + rat, gr[c]);
-        if (next_weight) load8(dy + rat, gy[c]);
-      }
+    for (int c = 0; c < NC; ++c) {
+      floats(now.p[c], n1[c]);
+      floats(now.g[c], gt[c]);
+      floats(now.x[c], r[c]);
+      floats(grads.r[c], gr[c]);
+      floats(grads.y[c], gy[c]);
+    }
+    if (kAhead) {
+      now.load(g, L, p, gate, x_in, next);
+      grads.load(g, L, dr, dy_in, next);
+    }
     float inv1[NP];
     head_norms<kLayer, VPL, NP>(g, L, n1, inv1, eps, sh.head[parity], wave0, all);
     // act(g) in gt's place needs the sigmoid again for its slope: keep that
@@ -458,24 +561,26 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     }
 }
 
-// Sums of the partials over the workgroups: 64 columns and 4 shares of the
+// Sums of the partials over the workgroups: 64 columns and 16 shares of the
 // partials to a workgroup, each share in order, then the shares in order.
-__global__ __launch_bounds__(256) void block_norm_weights_kernel(const float* __restrict__ partials,
-                                                                 float* dweight, float* dscale,
-                                                                 float* dnext_weight, int n,
-                                                                 int D) {
-  __shared__ float part[4][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), share = threadIdx.x >> 6;
+constexpr int kShares = 16;
+__global__ __launch_bounds__(64 * kShares) void block_norm_weights_kernel(
+    const float* __restrict__ partials, float* dweight, float* dscale, float* dnext_weight, int n,
+    int D) {
+  __shared__ float part[kShares][64];
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
   float* out = blockIdx.y == 0 ? dweight : blockIdx.y == 1 ? dscale : dnext_weight;
   if (!out) return;  // the same for the whole workgroup
   float s = 0.0f;
   if (col < D)
-    for (int i = share; i < n; i += 4) s += partials[(int64_t(i) * 3 + blockIdx.y) * D + col];
-  part[share][threadIdx.x & 63] = s;
+#pragma unroll 4
+    for (int i = share; i < n; i += kShares) s += partials[(int64_t(i) * 3 + blockIdx.y) * D + col];
+  part[share][lane] = s;
   __syncthreads();
-  if (share == 0 && col < D)
-    out[col] = ((part[0][threadIdx.x] + part[1][threadIdx.x]) + part[2][threadIdx.x]) +
-               part[3][threadIdx.x];
+  if (share == 0 && col < D) {
+    for (int i = 1; i < kShares; ++i) s += part[i][lane];
+    out[col] = s;
+  }
 }
 
 struct Shape {
@@ -553,7 +658,7 @@ hipError_t bwd(const Shape& s, const BlockNorm& a, const BlockNormGrads& d, floa
           static_cast<T*>(d.dgate), static_cast<T*>(d.dresidual), partials, a.eps, int(a.silu));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  block_norm_weights_kernel<<<dim3((g.D + 63) / 64, 3), 256, 0, stream>>>(
+  block_norm_weights_kernel<<<dim3((g.D + 63) / 64, 3), 64 * kShares, 0, stream>>>(
       partials, d.dweight, a.scale ? d.dscale : nullptr, a.next_weight ? d.dnext_weight : nullptr,
       int(grid) * g.rows_per_wg, g.D);
   return hipGetLastError();
