@@ -323,7 +323,25 @@ __device__ inline float2 row_norm(const float (*r)[kVec], const bool* on, float 
   return make_float2(m.mean, inverse<kLayer>(m, eps));
 }
 
-__device__ inline float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// sigma(x) and sigma(-x) from e^-|x|: neither overflows nor cancels.  For bf16
+// the exponential and the reciprocal are the hardware's (an exponent of x log2 e
+// rounded once, 2^-24 |x|, and 1 ulp): far below the output's rounding, and a
+// third of the instructions, which bounded the pass.
+struct Sigmoid {
+  float plus, minus;
+};
+template <typename T>
+__device__ inline Sigmoid sigmoid(float x) {
+  float t, s;
+  if (sizeof(T) == 2) {
+    t = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(x));
+    s = __builtin_amdgcn_rcpf(1.0f + t);
+  } else {
+    t = expf(-fabsf(x));
+    s = 1.0f / (1.0f + t);
+  }
+  return x >= 0.0f ? Sigmoid{s, t * s} : Sigmoid{t * s, s};
+}
 
 template <typename T, bool kLayer, int VPL, int NP>
 __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
@@ -349,7 +367,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
       if (next_weight) load8(next_weight + L.column[c], w2[c]);
     }
   int parity = 0;
-  constexpr bool kAhead = NC <= 2;  // where registers allow it
+  constexpr bool kAhead = NC <= 2;  // where registers allow it (two rows ahead gain nothing)
   Rows next(g, sub);
   Inputs<T, VPL, NP> now;
   if (kAhead) now.load(g, L, p, gate, residual, next);
@@ -377,7 +395,7 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
       for (int e = 0; e < kVec; ++e) {
         float v = z[c][e] * w1[c][e];
         if (gate) {
-          const float sg = sigmoid(gt[c][e]);
+          const float sg = sigmoid<T>(gt[c][e]).plus;
           v *= silu ? gt[c][e] * sg : sg;
         }
         // off: 0 by a select, since a weight or gate of 0 times it is not 0 for infinities
@@ -398,10 +416,11 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
   }
 }
 
-// Weight gradients of one workgroup's rows go to partials[blockIdx.x][3][D]
-// (dw1, ds, dw2).
+// The weight gradients of one workgroup's rows go to partials[...][2][D]: a =
+// sum_rows dr' act(g) n1 (dw1 = s a and ds = w1 a, both constant in a column)
+// and dw2.  The weights stay in LDS: with them in registers fewer waves fit.
 template <typename T, bool kLayer, int VPL, int NP>
-__global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
+__global__ __launch_bounds__(kMaxWaves * 64, VPL * NP == 1 ? (sizeof(T) == 2 ? 4 : 3) : 2) void block_norm_bwd_kernel(
     Geometry g, const T* __restrict__ p, const T* __restrict__ gate,
     const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ scale, const float* __restrict__ next_weight,
@@ -413,21 +432,40 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = all / g.waves_per_row;
   const int wave = all % g.waves_per_row, wave0 = sub * g.waves_per_row;
   const Lane<VPL, NP> L(g, wave, threadIdx.x & 63);
-  float w1[NC][kVec], sc[NC][kVec], w2[NC][kVec];
-  float dw1[NC][kVec], dsc[NC][kVec], dw2[NC][kVec];
+  float da[NC][kVec], dw2[NC][kVec];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      w1[c][e] = w2[c][e] = dw1[c][e] = dsc[c][e] = dw2[c][e] = 0.0f;
-      sc[c][e] = 1.0f;
+    for (int e = 0; e < kVec; ++e) da[c][e] = dw2[c][e] = 0.0f;
+  // w1, s and w2 (`what` 0 - 2) of a lane's channels: with one vector per lane
+  // from LDS, written and read by the same lane (12 KiB a wave); with more they
+  // would not fit, and come from the cache
+  constexpr bool kHeld = NC == 1;
+  extern __shared__ __attribute__((aligned(16))) float weights[];
+  auto cached = [&](int what, int c, float* w) {
+    const float* from = what == 0 ? weight : what == 1 ? scale : next_weight;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) w[e] = what == 1 ? 1.0f : 0.0f;
+    if (from && L.on[c]) load8(from + L.column[c], w);
+  };
+  auto held = [&](int what, int c, float* w) {
+    if (!kHeld) return cached(what, c, w);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 x = *reinterpret_cast<const float4*>(
+          weights + ((what * 2 + q) * blockDim.x + threadIdx.x) * 4);
+      w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
     }
+  };
+  if (kHeld)
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
-    if (L.on[c]) {
-      load8(weight + L.column[c], w1[c]);
-      if (scale) load8(scale + L.column[c], sc[c]);
-      if (next_weight) load8(next_weight + L.column[c], w2[c]);
+    for (int what = 0; what < 3; ++what) {
+      float w[kVec];
+      cached(what, 0, w);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float4*>(weights + ((what * 2 + q) * blockDim.x + threadIdx.x) * 4) =
+            make_float4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     }
   const float inv_d = 1.0f / float(g.d), inv_D = 1.0f / float(g.D);
   int parity = 0;
@@ -465,38 +503,47 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     }
     float inv1[NP];
     head_norms<kLayer, VPL, NP>(g, L, n1, inv1, eps, sh.head[parity], wave0, all);
-    // act(g) in gt's place needs the sigmoid again for its slope: keep that
+    // act(g), and its slope in g's place
     float act[NC][kVec];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
+      float w1[kVec], sc[kVec];
+      if (next_weight) {
+        held(0, c, w1);
+        held(1, c, sc);
+      }
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         float a = 1.0f, slope = 0.0f;
         if (gate) {
-          const float sg = sigmoid(gt[c][e]), x = gt[c][e];
-          a = silu ? x * sg : sg;
-          // sg (1 - sg) as sg sigma(-x): no cancellation for large x
-          slope = silu ? sg * (1.0f + x * sigmoid(-x)) : sg * sigmoid(-x);
+          const float x = gt[c][e];
+          const Sigmoid sg = sigmoid<T>(x);
+          a = silu ? x * sg.plus : sg.plus;
+          slope = silu ? sg.plus * (1.0f + x * sg.minus) : sg.plus * sg.minus;
         }
         act[c][e] = a;
         gt[c][e] = slope;
-        if (next_weight) r[c][e] = L.on[c] ? r[c][e] + sc[c][e] * (n1[c][e] * w1[c][e] * a) : 0.0f;
+        if (next_weight) r[c][e] = L.on[c] ? r[c][e] + sc[e] * (n1[c][e] * w1[e] * a) : 0.0f;
       }
+    }
     if (next_weight) {
       const float2 m = row_norm<kLayer, NC>(r, L.on, L.count, eps, sh.row[parity], wave0, all,
                                             g.waves_per_row);
       float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (L.on[c])
+        if (L.on[c]) {
+          float w2[kVec];
+          held(2, c, w2);
 #pragma unroll
           for (int e = 0; e < kVec; ++e) {
             r[c][e] = (r[c][e] - m.x) * m.y;  // n2
             if (live) dw2[c][e] += gy[c][e] * r[c][e];
-            gy[c][e] *= w2[c][e];
+            gy[c][e] *= w2[e];
             s.x += gy[c][e] * r[c][e];
             s.y += gy[c][e];
           }
+        }
       s = add_waves(make_float2(wave_sum(s.x), wave_sum(s.y)), sh.row_grad[parity], wave0, all,
                     g.waves_per_row);
       s.x *= inv_D;
@@ -511,15 +558,15 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     for (int c = 0; c < NC; ++c) {
       if (!L.on[c]) continue;
       if (residual && live) store8(dresidual + row * g.D + L.column[c], gr[c]);
-      float dg[kVec];
+      float dg[kVec], w1[kVec], sc[kVec];
+      held(0, c, w1);
+      held(1, c, sc);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        const float u = n1[c][e] * act[c][e];
-        if (live) dsc[c][e] += gr[c][e] * (u * w1[c][e]);
-        const float dz = gr[c][e] * sc[c][e];
-        if (live) dw1[c][e] += dz * u;
-        dg[e] = dz * w1[c][e] * n1[c][e] * gt[c][e];
-        gr[c][e] = dz * w1[c][e] * act[c][e];
+        if (live) da[c][e] += gr[c][e] * (n1[c][e] * act[c][e]);
+        const float dz = gr[c][e] * sc[e] * w1[e];
+        dg[e] = dz * n1[c][e] * gt[c][e];
+        gr[c][e] = dz * act[c][e];
       }
       if (gate && live) store8(dgate + base + L.head_off[c / VPL] + L.channel[c], dg);
     }
@@ -551,13 +598,12 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
     }
   }
   // several rows of a workgroup side by side write a partial each
-  float* out = partials + (int64_t(blockIdx.x) * g.rows_per_wg + sub) * 3 * g.D;
+  float* out = partials + (int64_t(blockIdx.x) * g.rows_per_wg + sub) * 2 * g.D;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
     if (L.on[c]) {
-      store8(out + L.column[c], dw1[c]);
-      if (scale) store8(out + g.D + L.column[c], dsc[c]);
-      if (next_weight) store8(out + 2 * g.D + L.column[c], dw2[c]);
+      store8(out + L.column[c], da[c]);
+      if (next_weight) store8(out + g.D + L.column[c], dw2[c]);
     }
 }
 
@@ -565,21 +611,26 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_bwd_kernel(
 // partials to a workgroup, each share in order, then the shares in order.
 constexpr int kShares = 16;
 __global__ __launch_bounds__(64 * kShares) void block_norm_weights_kernel(
-    const float* __restrict__ partials, float* dweight, float* dscale, float* dnext_weight, int n,
+    const float* __restrict__ partials, const float* __restrict__ weight,
+    const float* __restrict__ scale, float* dweight, float* dscale, float* dnext_weight, int n,
     int D) {
   __shared__ float part[kShares][64];
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-  float* out = blockIdx.y == 0 ? dweight : blockIdx.y == 1 ? dscale : dnext_weight;
-  if (!out) return;  // the same for the whole workgroup
+  if (blockIdx.y == 1 && !dnext_weight) return;  // the same for the whole workgroup
   float s = 0.0f;
   if (col < D)
 #pragma unroll 4
-    for (int i = share; i < n; i += kShares) s += partials[(int64_t(i) * 3 + blockIdx.y) * D + col];
+    for (int i = share; i < n; i += kShares) s += partials[(int64_t(i) * 2 + blockIdx.y) * D + col];
   part[share][lane] = s;
   __syncthreads();
   if (share == 0 && col < D) {
     for (int i = 1; i < kShares; ++i) s += part[i][lane];
-    out[col] = s;
+    if (blockIdx.y == 1) {
+      dnext_weight[col] = s;
+    } else {
+      dweight[col] = scale ? scale[col] * s : s;
+      if (dscale) dscale[col] = weight[col] * s;
+    }
   }
 }
 
@@ -625,20 +676,32 @@ Shape shape_of(int64_t B, int64_t NH, int64_t T, int64_t d) {
   return s;
 }
 
-// Workgroups: enough to fill the card, few enough that the weights are read
-// seldom and (backward) that the partials stay small beside the rows.
-unsigned grid_of(const Geometry& g, int64_t most_waves) {
+// Workgroups: as many as the card holds at once (the waves that a CU has
+// registers for, by vectors per lane: a second round of workgroups would leave
+// part of it idle), and no more than there are rows.
+constexpr int kCUs = 256;
+unsigned grid_of(const Geometry& g, int waves) {
   const int64_t need = (g.rows + g.rows_per_wg - 1) / g.rows_per_wg;
-  const int64_t most = most_waves / (g.waves_per_row * g.rows_per_wg);
+  const int64_t most = kCUs * (waves / (g.waves_per_row * g.rows_per_wg));
   return unsigned(need < most ? need : most);
 }
-constexpr int64_t kFwdWaves = 256 * 32, kBwdWaves = 256 * 8;
+unsigned fwd_grid(const Geometry& g, int vectors) {
+  return grid_of(g, vectors == 1 ? 20 : vectors == 2 ? 12 : 8);
+}
+// backward: a workgroup's partials are worth about a row's traffic, so from two
+// workgroups per CU on each takes at least four rows
+unsigned bwd_grid(const Geometry& g, int vectors) {
+  const unsigned most = grid_of(g, vectors == 1 ? 16 : 8);
+  const int64_t four = (g.rows + 4 * g.rows_per_wg - 1) / (4 * g.rows_per_wg);
+  const int64_t n = four > 2 * kCUs ? four : 2 * kCUs;
+  return n < most ? unsigned(n) : most;
+}
 
 template <typename T, bool kLayer, int VPL, int NP>
 hipError_t fwd(const Shape& s, const BlockNorm& a, void* r, void* y, hipStream_t stream) {
   const Geometry& g = s.g;
   block_norm_fwd_kernel<T, kLayer, VPL, NP>
-      <<<grid_of(g, kFwdWaves), 64 * g.waves_per_row * g.rows_per_wg, 0, stream>>>(
+      <<<fwd_grid(g, VPL * NP), 64 * g.waves_per_row * g.rows_per_wg, 0, stream>>>(
           g, static_cast<const T*>(a.p), static_cast<const T*>(a.gate),
           static_cast<const T*>(a.residual), a.weight, a.scale, a.next_weight,
           static_cast<T*>(r), static_cast<T*>(y), a.eps, int(a.silu));
@@ -649,17 +712,18 @@ template <typename T, bool kLayer, int VPL, int NP>
 hipError_t bwd(const Shape& s, const BlockNorm& a, const BlockNormGrads& d, float* partials,
                hipStream_t stream) {
   const Geometry& g = s.g;
-  const unsigned grid = grid_of(g, kBwdWaves);
+  const unsigned grid = bwd_grid(g, VPL * NP);
+  const unsigned threads = 64 * g.waves_per_row * g.rows_per_wg;
   block_norm_bwd_kernel<T, kLayer, VPL, NP>
-      <<<grid, 64 * g.waves_per_row * g.rows_per_wg, 0, stream>>>(
+      <<<grid, threads, VPL * NP == 1 ? threads * 3 * kVec * sizeof(float) : 0, stream>>>(
           g, static_cast<const T*>(a.p), static_cast<const T*>(a.gate),
           static_cast<const T*>(a.residual), a.weight, a.scale, a.next_weight,
           static_cast<const T*>(d.dr), static_cast<const T*>(d.dy), static_cast<T*>(d.dp),
           static_cast<T*>(d.dgate), static_cast<T*>(d.dresidual), partials, a.eps, int(a.silu));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  block_norm_weights_kernel<<<dim3((g.D + 63) / 64, 3), 64 * kShares, 0, stream>>>(
-      partials, d.dweight, a.scale ? d.dscale : nullptr, a.next_weight ? d.dnext_weight : nullptr,
+  block_norm_weights_kernel<<<dim3((g.D + 63) / 64, 2), 64 * kShares, 0, stream>>>(
+      partials, a.weight, a.scale, d.dweight, a.scale ? d.dscale : nullptr, a.next_weight ? d.dnext_weight : nullptr,
       int(grid) * g.rows_per_wg, g.D);
   return hipGetLastError();
 }
@@ -712,7 +776,7 @@ struct Bwd {
 
 size_t block_norm_partial_bytes(int64_t B, int64_t NH, int64_t T, int64_t d) {
   const Shape s = shape_of(B, NH, T, d);
-  return size_t(grid_of(s.g, kBwdWaves)) * s.g.rows_per_wg * 3 * s.g.D * sizeof(float);
+  return size_t(bwd_grid(s.g, s.vpl * s.np)) * s.g.rows_per_wg * 2 * s.g.D * sizeof(float);
 }
 
 hipError_t launch_block_norm_fwd(const BlockNorm& a, void* r_out, void* y_out,
