@@ -56,11 +56,6 @@ __device__ inline void join_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The (row tile, half) pairs of a lower triangular 64 x 64 left operand that
-// are not zero, as indexes 2 i + s; of an upper triangular one likewise.
-__device__ inline int low_pair(int n) { return n < 2 ? 2 * n : n + 2; }   // 0 2 4 5 6 7
-__device__ inline int high_pair(int n) { return n < 4 ? n : 2 * n - 3; }  // 0 1 2 3 5 7
-
 template <int N>
 __device__ inline Planes<N> lds_frag(const char* slot, int first, int step, int lane) {
   Planes<N> s;

@@ -46,6 +46,11 @@ __device__ __host__ inline int row_of(int half, int m) {
   return (m >> 2) * 8 + half * 4 + (m & 3);
 }
 
+// The (row tile, half) pairs of a lower triangular 64 x 64 left operand that
+// are not zero, as indexes 2 i + s; of an upper triangular one likewise.
+__device__ inline int low_pair(int n) { return n < 2 ? 2 * n : n + 2; }   // 0 2 4 5 6 7
+__device__ inline int high_pair(int n) { return n < 4 ? n : 2 * n - 3; }  // 0 1 2 3 5 7
+
 __device__ inline f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }

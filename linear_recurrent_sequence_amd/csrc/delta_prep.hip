@@ -23,16 +23,18 @@ namespace delta {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPitch = kC + 1;  // floats between rows in LDS
+constexpr int kPitch = kC + 4;  // floats between rows in LDS: 16-byte rows, columns without conflicts
 
 __device__ inline f32x4 mma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
 // one 16 x 16 tile of C = A B over n columns of A, from LDS (rows kPitch apart)
-__device__ inline f32x4 tile_product(const float* a, const float* b, int n, int lane) {
+template <int n>
+__device__ inline f32x4 tile_product(const float* a, const float* b, int lane) {
   f32x4 c = {};
   const int m = lane & 15, g = lane >> 4;
+#pragma unroll
   for (int k = 0; k < n; k += 4) c = mma_f32(a[m * kPitch + k + g], b[(k + g) * kPitch + m], c);
   return c;
 }
@@ -41,68 +43,79 @@ __device__ inline void store_tile(float* to, f32x4 c, float sign, int lane) {
   for (int r = 0; r < 4; ++r) to[((lane >> 4) * 4 + r) * kPitch + (lane & 15)] = sign * c[r];
 }
 
-// Writes NP planes of the 64 x 64 matrix in LDS (or its transpose) in load order.
+// Writes NP planes of the lower triangular 64 x 64 matrix in LDS (or of its
+// transpose) in load order: the six (row tile, half) pairs that hold something.
 template <int NP, bool kTranspose>
 __device__ inline void write_square(const float (*m)[kPitch], __bf16* to) {
-  for (int i = threadIdx.x; i < kSquare / 8; i += kThreads) {
-    const int lane = i & 63, frag = i >> 6;  // frag: [row tile][half]
+  for (int i = threadIdx.x; i < 6 * 64; i += kThreads) {
+    const int lane = i & 63;
+    const int frag = kTranspose ? high_pair(i >> 6) : low_pair(i >> 6);  // 2 * row tile + half
     const int row = (frag >> 2) * 32 + row_of((frag >> 1) & 1, lane & 15);
     const int col = (frag & 1) * 32 + (lane >> 4) * 8;
     f32x8 v;
+    if constexpr (kTranspose) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = kTranspose ? m[col + e][row] : m[row][col + e];
+      for (int e = 0; e < 8; ++e) v[e] = col + e >= row ? m[col + e][row] : 0.0f;
+    } else {
+      v = pair(*reinterpret_cast<const f32x4*>(&m[row][col]),
+               *reinterpret_cast<const f32x4*>(&m[row][col + 4]));
+    }
     const Planes<NP> s = split<NP>(v);
 #pragma unroll
     for (int n = 0; n < NP; ++n)
-      *reinterpret_cast<bf16x8*>(to + n * kSquare + int64_t(i) * 8) = s.p[n];
+      *reinterpret_cast<bf16x8*>(to + n * kSquare + (frag * 64 + lane) * 8) = s.p[n];
   }
 }
 
 // Writes the planes of a tensor's chunk X (64 x dk) as it is, transposed, or
-// both (what is NULL is left out).  `tile` holds 64 tokens of 32 columns at a time.
+// both (what is NULL is left out).  The transpose is a product with columns of
+// the identity, which is exact: the accumulators of two token tiles hold 8
+// neighbouring tokens of a column in one lane, as K^T's left operand needs them.
 template <int NPL>
 __device__ inline void write_rows(const void* x, int64_t row0, int valid, int dk, int ks,
-                                  __bf16* natural, __bf16* transposed, float (*tile)[kPitch]) {
+                                  __bf16* natural, __bf16* transposed) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, m = lane & 15;
-  for (int t = 0; t < ks; ++t) {
-    // wave w: tokens of row tile w, 8 columns per lane
-    const int tok = (w >> 1) * 32 + row_of(w & 1, m), col = t * 32 + g * 8;
-    const bool on = tok < valid && col < dk;
-    const Planes<NPL> s = load_row<NPL>(x, (row0 + tok) * dk + col, on);
-    if (natural)
+  const int64_t plane = int64_t(ks) * 32 * kC;
+  bf16x8 one[2];
 #pragma unroll
-      for (int n = 0; n < NPL; ++n)
-        *reinterpret_cast<bf16x8*>(natural + int64_t(n) * ks * 32 * kC +
-                                   (int64_t(t * 4 + w) * 64 + lane) * 8) = s.p[n];
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      one[half][e] = static_cast<__bf16>(8 * g + e == row_of(half, m) ? 1.0f : 0.0f);
+  const int s = w & 1;  // half of the tokens
+  for (int t = w >> 1; t < ks; t += 2) {
+    Planes<NPL> f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tok = s * 32 + row_of(i, m), col = t * 32 + g * 8;
+      f[i] = load_row<NPL>(x, (row0 + tok) * dk + col, tok < valid && col < dk);
+      if (natural)
+#pragma unroll
+        for (int n = 0; n < NPL; ++n)
+          *reinterpret_cast<bf16x8*>(natural + n * plane +
+                                     (int64_t(t * 4 + 2 * s + i) * 64 + lane) * 8) = f[i].p[n];
+    }
     if (!transposed) continue;
-    // the sum of the planes is the value again
-    f32x8 v = __builtin_convertvector(s.p[NPL - 1], f32x8);
-#pragma unroll
-    for (int n = NPL - 2; n >= 0; --n) v += __builtin_convertvector(s.p[n], f32x8);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) tile[g * 8 + e][tok] = v[e];
-    __syncthreads();
-    // wave w: row tile 2 t + (w >> 1) of the transpose, half w & 1 of the tokens
-    const int half = w >> 1, row = row_of(half, m), tok0 = (w & 1) * 32 + g * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[row][tok0 + e];
-    const Planes<NPL> u = split<NPL>(v);
 #pragma unroll
     for (int n = 0; n < NPL; ++n)
-      *reinterpret_cast<bf16x8*>(transposed + int64_t(n) * ks * 32 * kC +
-                                 (int64_t((2 * t + half) * 2 + (w & 1)) * 64 + lane) * 8) = u.p[n];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const f32x4 a = mma(f[0].p[n], one[half], f32x4{}), b = mma(f[1].p[n], one[half], f32x4{});
+        *reinterpret_cast<bf16x8*>(transposed + n * plane +
+                                   (int64_t((2 * t + half) * 2 + s) * 64 + lane) * 8) =
+            split<1>(pair(a, b)).p[0];
+      }
   }
 }
 
 template <int NPL, bool kBackward>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(
+__global__ __launch_bounds__(kThreads, NPL == 1 ? 6 : 4) void delta_prep_kernel(
     const void* __restrict__ q, const void* __restrict__ k, const float* __restrict__ beta,
     const float* __restrict__ fgate, Work ws, int64_t T, int chunks, int NH, int NHK, int dk,
     int ks, float scale, int exp_forget) {
   __shared__ double G[kC];
   __shared__ float bt[kC];
-  __shared__ float A[kC][kPitch], S[kC][kPitch], tmp[32][kPitch];
+  __shared__ __attribute__((aligned(16))) float A[kC][kPitch];
   const int64_t head = blockIdx.x / chunks;
   const int chunk = blockIdx.x % chunks;
   const int64_t at = head * chunks + chunk;
@@ -110,7 +123,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(
   const int64_t khead = head / NH * NHK + head % NH / group;
   const int64_t tok0 = int64_t(chunk) * kC;
   const int valid = T - tok0 < kC ? int(T - tok0) : kC;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t row0 = khead * T + tok0;
 
   if (w == 0) {
@@ -126,6 +140,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(
   }
   // wave w: rows 16 w .. of the scores
   f32x4 kk[4] = {}, qk[4] = {};
+#pragma unroll 2
   for (int t = 0; t < ks; ++t) {
     const int col = t * 32 + g * 8;
     const bool c_on = col < dk;
@@ -136,12 +151,21 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(
     for (int j = 0; j < 4; ++j)
       if (j <= w) {
         const Planes<NPL> kb =
-            load_row<NPL>(k, (row0 + 16 * j + m) * dk + col, c_on && 16 * j + m < valid);
+            j == w ? ka
+                   : load_row<NPL>(k, (row0 + 16 * j + m) * dk + col, c_on && 16 * j + m < valid);
         kk[j] = mma_planes<NPL>(ka, kb, kk[j]);
         qk[j] = mma_planes<NPL>(qa, kb, qk[j]);
       }
   }
+  if (head % group == 0) {  // NH is a multiple of the group: one head per key head
+    const int64_t kat = (khead * chunks + chunk) * NPL * int64_t(ks) * 32 * kC;
+    write_rows<NPL>(k, row0, valid, dk, ks, NPL == 3 ? ws.key + kat : nullptr, ws.keyT + kat);
+    if (NPL == 3 || kBackward)
+      write_rows<NPL>(q, row0, valid, dk, ks, NPL == 3 ? ws.query + kat : nullptr,
+                      kBackward ? ws.queryT + kat : nullptr);
+  }
   __syncthreads();
+  // P to memory through the one matrix in LDS, then At into its place
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -149,56 +173,65 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(
       const int row = 16 * w + 4 * g + r, c = 16 * j + m;
       // above the diagonal by a select: no product with what is there
       const float e = c <= row ? exp2_once(G[row] - G[c]) : 0.0f;
-      A[row][c] = c < row ? e * kk[j][r] * bt[c] : 0.0f;
-      S[row][c] = c <= row ? e * qk[j][r] * scale : 0.0f;
+      A[row][c] = c <= row ? e * qk[j][r] * scale : 0.0f;
+      kk[j][r] = c < row ? e * kk[j][r] * bt[c] : 0.0f;
     }
   __syncthreads();
   constexpr int NPP = NPL == 1 && !kBackward ? 2 : 3;
-  write_square<NPP, false>(S, ws.score + at * NPP * kSquare);
-  if (kBackward) write_square<NPP, true>(S, ws.scoreT + at * NPP * kSquare);
+  write_square<NPP, false>(A, ws.score + at * NPP * kSquare);
+  if (kBackward) write_square<NPP, true>(A, ws.scoreT + at * NPP * kSquare);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) A[16 * w + 4 * g + r][16 * j + m] = kk[j][r];
+  __syncthreads();
 
   // 16 x 16 blocks on the diagonal: lane m holds column m of the inverse
   if (lane < 16) {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == m ? 1.0f : 0.0f;
+      float row[16];
 #pragma unroll
-      for (int j = 0; j < i; ++j) s -= A[16 * w + i][16 * w + j] * x[j];
-      x[i] = s;
+      for (int j = 0; j < i; j += 4)
+        *reinterpret_cast<f32x4*>(row + j) =
+            *reinterpret_cast<const f32x4*>(&A[16 * w + i][16 * w + j]);
+      float s = i == m ? 1.0f : 0.0f, s1 = 0.0f;  // two chains of additions
+#pragma unroll
+      for (int j = 0; j < i; ++j)
+        if (j & 1)
+          s1 -= row[j] * x[j];
+        else
+          s -= row[j] * x[j];
+      x[i] = s + s1;
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) A[16 * w + i][16 * w + m] = x[i];
   }
   __syncthreads();
-  // blocks (1, 0) and (3, 2), by waves 0 and 1
+  // blocks (1, 0) and (3, 2), by waves 0 and 1; the upper right block, which
+  // nobody reads, takes the first product of each
+  float(*tmp)[kPitch] = reinterpret_cast<float(*)[kPitch]>(&A[0][32]);
   if (w < 2)
-    store_tile(&tmp[16 * w][0], tile_product(&A[32 * w + 16][32 * w], &A[32 * w][32 * w], 16, lane),
+    store_tile(&tmp[16 * w][0], tile_product<16>(&A[32 * w + 16][32 * w], &A[32 * w][32 * w], lane),
                1.0f, lane);
   __syncthreads();
   if (w < 2)
     store_tile(&A[32 * w + 16][32 * w],
-               tile_product(&A[32 * w + 16][32 * w + 16], &tmp[16 * w][0], 16, lane), -1.0f, lane);
+               tile_product<16>(&A[32 * w + 16][32 * w + 16], &tmp[16 * w][0], lane), -1.0f, lane);
   __syncthreads();
   // the lower left 32 x 32 block, a 16 x 16 tile per wave
   {
     const int i = 16 * (w >> 1), j = 16 * (w & 1);
-    store_tile(&tmp[i][j], tile_product(&A[32 + i][0], &A[0][j], 32, lane), 1.0f, lane);
+    store_tile(&tmp[i][j], tile_product<32>(&A[32 + i][0], &A[0][j], lane), 1.0f, lane);
     __syncthreads();
-    const f32x4 c = tile_product(&A[32 + i][32], &tmp[0][j], 32, lane);
-    __syncthreads();
-    store_tile(&A[32 + i][j], c, -1.0f, lane);
+    const f32x4 c = tile_product<32>(&A[32 + i][32], &tmp[0][j], lane);
+    store_tile(&A[32 + i][j], c, -1.0f, lane);  // no wave reads this block any more
   }
   __syncthreads();
   write_square<3, false>(A, ws.inv + at * 3 * kSquare);
   if (kBackward) write_square<3, true>(A, ws.invT + at * 3 * kSquare);
-  if (head % group == 0) {  // NH is a multiple of the group: one head per key head
-    const int64_t n = int64_t(ks) * 32 * kC, kat = (khead * chunks + chunk) * NPL * n;
-    write_rows<NPL>(k, row0, valid, dk, ks, NPL == 3 ? ws.key + kat : nullptr, ws.keyT + kat, S);
-    if (NPL == 3 || kBackward)
-      write_rows<NPL>(q, row0, valid, dk, ks, NPL == 3 ? ws.query + kat : nullptr,
-                      kBackward ? ws.queryT + kat : nullptr, S);
-  }
 }
 
 }  // namespace

@@ -409,17 +409,26 @@ def parallel_bwd(q, k, v, igate, fgate, h, m, n, b, dh, forget="sigmoid"):
 
 
 def _require_all(named, device):
-    """_require for each (name, tensor, shape, dtype); devices last, so that a
-    malformed tensor is named first."""
+    """_require for each (name, tensor, shape, dtype), all on ``device``, a GPU.
+    The common case in one pass (a call's host time is that of a small kernel);
+    on failure the messages of _require, devices last, so that a malformed
+    tensor is named first."""
+    if device.type == "cuda":
+        for _, t, shape, dtype in named:
+            if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+                    and t.device == device and t.is_contiguous()):
+                break
+        else:
+            return
     for name, t, shape, dtype in named:
         _require(name, t, shape, dtype)
     for name, t, _, _ in named:
-        if t.device != device or device.type != "cuda":
-            _require_device(name, t, device)
+        _require_device(name, t, device)
 
 
-def _check_delta(q, k, v, beta, fgate, dims):
-    """Checks the gated delta rule's inputs; ``dims`` 4 with a length, 3 for one token."""
+def _check_delta(q, k, v, beta, fgate, dims, dh=None, **states):
+    """Checks the gated delta rule's tensors (``states``: memories, None where
+    they are left out); ``dims`` 4 with a length, 3 for one token."""
     if not isinstance(q, torch.Tensor):
         raise TypeError(f"q must be a torch.Tensor, got {type(q).__name__}")
     if not isinstance(v, torch.Tensor):
@@ -435,9 +444,15 @@ def _check_delta(q, k, v, beta, fgate, dims):
     NH, dv = v.shape[1], v.shape[-1]
     T = q.shape[2] if dims == 4 else 1
     rows = (B, NH, T) if dims == 4 else (B, NH)
-    _require_all((("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
-                  ("v", v, (*rows, dv), q.dtype), ("beta", beta, rows, torch.float32),
-                  ("fgate", fgate, rows, torch.float32)), q.device)
+    named = [("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype),
+             ("v", v, (*rows, dv), q.dtype), ("beta", beta, rows, torch.float32),
+             ("fgate", fgate, rows, torch.float32)]
+    if dh is not None:
+        named.append(("dh", dh, v.shape, v.dtype))
+    for name, t in states.items():
+        if t is not None:
+            named.append((name, t, (B, NH, dv, dk), torch.float32))
+    _require_all(named, q.device)
     return B, NHK, NH, T, dk, dv
 
 
@@ -468,11 +483,8 @@ def delta_fwd(q, k, v, beta, fgate, state=None, out_state=None, forget="sigmoid"
     by default a new one is allocated.
     """
     lib = load_library()
-    sizes = _check_delta(q, k, v, beta, fgate, 4)
+    sizes = _check_delta(q, k, v, beta, fgate, 4, state=state, out_state=out_state)
     B, NHK, NH, T, dk, dv = sizes
-    for name, t in (("state", state), ("out_state", out_state)):
-        if t is not None:
-            _require(name, t, (B, NH, dv, dk), torch.float32, q.device)
     forget_code, code = _forget_code(forget), _dtype_code(q)
     with _on(q.device):
         if out_state is None:
@@ -495,12 +507,10 @@ def delta_bwd(q, k, v, beta, fgate, dh, state=None, dstate=None, forget="sigmoid
     q, k, v, beta, fgate, ``state``: as given to ``delta_fwd``.
     """
     lib = load_library()
-    sizes = _check_delta(q, k, v, beta, fgate, 4)
+    if not isinstance(dh, torch.Tensor):
+        raise TypeError(f"dh must be a torch.Tensor, got {type(dh).__name__}")
+    sizes = _check_delta(q, k, v, beta, fgate, 4, dh=dh, state=state, dstate=dstate)
     B, NHK, NH, T, dk, dv = sizes
-    _require("dh", dh, v.shape, v.dtype, q.device)
-    for name, t in (("state", state), ("dstate", dstate)):
-        if t is not None:
-            _require(name, t, (B, NH, dv, dk), torch.float32, q.device)
     forget_code, code = _forget_code(forget), _dtype_code(q)
     with _on(q.device):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -524,11 +534,12 @@ def delta_step(q, k, v, beta, fgate, state, out_state=None, forget="sigmoid"):
     ``delta_fwd``, updated in place unless ``out_state`` is given.
     """
     lib = load_library()
-    B, NHK, NH, _, dk, dv = _check_delta(q, k, v, beta, fgate, 3)
+    if not isinstance(state, torch.Tensor):
+        raise TypeError(f"state must be a torch.Tensor, got {type(state).__name__}")
+    B, NHK, NH, _, dk, dv = _check_delta(q, k, v, beta, fgate, 3, state=state,
+                                         out_state=out_state)
     if out_state is None:
         out_state = state
-    _require("state", state, (B, NH, dv, dk), torch.float32, q.device)
-    _require("out_state", out_state, (B, NH, dv, dk), torch.float32, q.device)
     h = torch.empty_like(v)
     with _on(q.device):
         st = lib.mlstm_delta_step(
@@ -540,7 +551,8 @@ def delta_step(q, k, v, beta, fgate, state, out_state=None, forget="sigmoid"):
     return h, out_state
 
 
-def _check_block_norm(p, weight, gate, residual, scale, next_weight, norm, activation):
+def _check_block_norm(p, weight, gate, residual, scale, next_weight, norm, activation, dr=None,
+                      dy=None):
     if not isinstance(p, torch.Tensor):
         raise TypeError(f"p must be a torch.Tensor, got {type(p).__name__}")
     if p.dim() != 4:
@@ -557,6 +569,9 @@ def _check_block_norm(p, weight, gate, residual, scale, next_weight, norm, activ
     for name, t in (("scale", scale), ("next_weight", next_weight)):
         if t is not None:
             named.append((name, t, (D,), torch.float32))
+    for name, t in (("dr", dr), ("dy", dy)):
+        if t is not None:
+            named.append((name, t, (B, T, D), p.dtype))
     _require_all(named, p.device)
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {tuple(NORMS)}, got {norm!r}")
@@ -599,14 +614,9 @@ def block_norm_bwd(p, weight, dr, dy, gate=None, residual=None, scale=None, next
     that are given, "dgate", "dresidual", "dscale", "dnext_weight"."""
     lib = load_library()
     B, NH, T, d = _check_block_norm(p, weight, gate, residual, scale, next_weight, norm,
-                                    activation)
-    rows = (B, T, NH * d)
-    if dr is not None:
-        _require("dr", dr, rows, p.dtype, p.device)
+                                    activation, dr, dy)
     if (dy is None) != (next_weight is None):
         raise ValueError("dy and next_weight are given together or not at all")
-    if dy is not None:
-        _require("dy", dy, rows, p.dtype, p.device)
     g = {"dp": torch.empty_like(p), "dweight": torch.empty_like(weight)}
     for name, t in (("dgate", gate), ("dresidual", residual), ("dscale", scale),
                     ("dnext_weight", next_weight)):
