@@ -44,10 +44,17 @@ struct Stages {
   static constexpr int nK = (KS / 2 + kT - 1) / kT, nT = (KS + kI - 1) / kI;
   static constexpr int kInv = 1 + nK, kQueryT = kInv + 1, kKeyT = kQueryT + nT, n = kKeyT + nT;
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
-  static constexpr int kMost = kBf16 ? 4 : 2, kAhead = n < kMost ? n : kMost;
+  // bf16: X and V come through LDS, with the inverse (a wave that stores and then
+  // loads waits for its stores); one buffer each, so less than a chunk ahead
+  static constexpr bool kStaged = kBf16;
+  static constexpr int kMost = kBf16 ? 3 : 2;
+  static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
   static constexpr int kSlots = kAhead + 1;
+  static constexpr int kPart = 6 * kFrag;  // a value tile's sums between its two waves
   static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
-                       kPartAt = kDecayAt + 2 * kFrag, kShared = kPartAt + kWaves * kPart;
+                       kPartAt = kDecayAt + 2 * kFrag, kXAt = kPartAt + kWaves * kPart,
+                       kVAt = kXAt + (kStaged ? Values<float>::kBytes : 0),
+                       kShared = kVAt + (kStaged ? Values<T>::kBytes : 0);
 
   static constexpr int blocks_of(int s) {  // of K, for each half
     return KS / 2 - (s - 1) * kT < kT ? KS / 2 - (s - 1) * kT : kT;
@@ -57,7 +64,9 @@ struct Stages {
     s %= n;
     if (s == 0) return Copier::square_copies(3) + Values<T>::kCopies + 1;
     if (s < kInv) return 2 * NPL * blocks_of(s);
-    if (s == kInv) return Copier::square_copies(3);
+    if (s == kInv)
+      return Copier::square_copies(3) +
+             (kStaged ? Values<float>::kCopies + Values<T>::kCopies : 0);
     return tiles_of((s - kQueryT) % nT) * NPL;
   }
   static constexpr int in_flight(int s) {
@@ -119,6 +128,12 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
             }
           }
       } else if constexpr (s == St::kInv) {
+        if constexpr (St::kStaged) {
+          const int64_t from = (head * a.T_len + tok0) * dv;
+          cp.values(static_cast<const float*>(a.sv.X), from, valid, dv, block * 16 * kWaves,
+                    St::kXAt);
+          cp.values(a.v, from, valid, dv, block * 16 * kWaves, St::kVAt);
+        }
         cp.template square<3, false>(a.ws.invT + at * 3 * kSquare, dst);
       } else {
         constexpr int j = (s - St::kQueryT) % St::nT;
@@ -162,8 +177,9 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
   }
   // K Z of all tokens to the first half's wave, of tokens 32-63 to the
   // second's; then each one's dR to the other
-  f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * kPart) + lane;
+  f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;
   f32x4* const to_second = to_first + 4 * 64;
+  const unsigned state_off = state_offset(dv, col, lane);
   int read = 0;
   auto enter = [&]() {
     join_barrier();
@@ -178,16 +194,14 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
     const float* decay = reinterpret_cast<const float*>(lds + St::kDecayAt + (turn & 1) * kFrag);
     char* value = lds + St::kValueAt + (turn & 1) * V::kBytes;
-    auto value_of = [&](int tok) {
-      return reinterpret_cast<T*>(value + V::at(tok)) + tile * 16 + m;
-    };
+    char* const my_value = value + V::lane_at(g) + (tile * 16 + m) * sizeof(T);
+    auto value_of = [&](int i, int r) { return reinterpret_cast<T*>(my_value + V::acc_at(i, r)); };
     auto at_tile = [&](int what, int i) {
       return *reinterpret_cast<const f32x4*>(decay + what * kC + acc_row(i, g));
     };
     // of values: this wave's tokens are rows + (4 i + r) dv + mine0
     const int64_t rows = (head * a.T_len + tok0) * dv;
     const unsigned mine0 = (32 * half + 8 * g) * dv + col;
-    if (mine) store_state(a.sv.Z + at * dk * dv, Z, first_row, dk, dv, col, lane);
     // P^T dh: of this wave's tokens, and for the first half of the others too
     f32x4 dh[4], dU[4] = {};
     {
@@ -197,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int tok = acc_row(i, g) + r;
-          const float x = load_elem(value_of(tok));
+          const float x = load_elem(value_of(i, r));
           dh[i][r] = tok < valid ? x : 0.0f;
         }
       const Planes<NPL> h0 = split<NPL>(pair(dh[0], dh[1])), h1 = split<NPL>(pair(dh[2], dh[3]));
@@ -206,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     }
     // this wave's tokens of X and V - X
     f32x4 X[2] = {}, pred[2] = {};
-    if (mine)
+    if (!St::kStaged && mine)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -229,6 +243,9 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
         for (int i = 0; i < 4; ++i) kf[i] = lds_frag<NPL>(slot, j * 4 + i, 4, lane);
         const int t = s * St::kT + j;
         const Planes<3> b = split<3>(pair(Z[2 * t], Z[2 * t + 1]));
+        if (mine)
+          store_rows(a.sv.Z + (at * dk + first_row + 32 * t) * dv, Z[2 * t], Z[2 * t + 1],
+                     state_off, dk - first_row - 32 * t, dv, lane);
         each_product<3, NPL, 3>([&](int x, int y) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) kz[i] = mma(kf[i].p[x], b.p[y], kz[i]);
@@ -247,6 +264,19 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     float* const part = a.sv.part + (at * a.tiles + block * kWaves + tile) * 3 * kC;
     {
       const char* slot = enter();
+      if constexpr (St::kStaged)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {  // zeros behind the end
+            using F = Values<float>;
+            X[i][r] = *reinterpret_cast<const float*>(lds + St::kXAt + F::lane_at(g) +
+                                                      (tile * 16 + m) * 4 +
+                                                      half * F::acc_at(2, 0) + F::acc_at(i, r));
+            pred[i][r] = load_elem(reinterpret_cast<const T*>(
+                             lds + St::kVAt + V::lane_at(g) + (tile * 16 + m) * sizeof(T) +
+                             half * V::acc_at(2, 0) + V::acc_at(i, r))) - X[i][r];
+          }
       // e^(G_C - G) K Z, nothing behind the end
       auto whole = [&](int i, f32x4 other) {
         f32x4 x = (kz[i] + other) * at_tile(1, i);
@@ -290,7 +320,8 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
         const int tok = acc_row(2 * half + i, g);
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // the other wave has read dh (before this stage's barrier)
-          store_elem(value_of(tok + r), own[i][r]);
+          store_elem(reinterpret_cast<T*>(my_value + half * V::acc_at(2, 0) + V::acc_at(i, r)),
+                     own[i][r]);
         if (sizeof(T) == 2 && mine)
           store_tokens(a.sv.dR + rows, own[i], tok, valid, dv, col, lane);
       }

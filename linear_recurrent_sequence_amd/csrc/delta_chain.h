@@ -68,7 +68,6 @@ __device__ inline Planes<N> lds_frag(const char* slot, int first, int step, int 
 constexpr int kWaves = 4;                              // value tiles, and copying waves
 constexpr int kChainWaves = 2 * kWaves;                // two to a value tile
 constexpr int kThreads = 64 * (kChainWaves + kWaves);
-constexpr int kPart = 10 * kFrag;  // a value tile's sums between its two waves
 
 // A chunk's values (64 tokens of the workgroup's 64 columns) in LDS.
 template <typename T>
@@ -79,27 +78,32 @@ struct Values {
   static constexpr int kCopies = kC * kRow / kFrag / kWaves;  // of each copying wave
   static constexpr int kLanes = kRow / 16;                    // of a token
   static __device__ int at(int tok) { return tok * kRow + (tok >> 3) * kPad; }
+  // of token acc_row(i, g) + r: a lane's base and a constant
+  static __device__ int lane_at(int g) { return g * (8 * kRow + kPad); }
+  static constexpr int acc_at(int i, int r) {
+    return (i >> 1) * (32 * kRow + 4 * kPad) + (4 * (i & 1) + r) * kRow;
+  }
 };
 
 // The position of accumulator (tile i, lane group g, element 0): a token, or a
 // memory row from the half's first on.
 __device__ inline int acc_row(int i, int g) { return (i >> 1) * 32 + 8 * g + 4 * (i & 1); }
 
-// The memory's slice of a wave (KS tiles from row first_row on, one value column
-// per lane) to x [dk][dv], and 4 tokens of a value column per lane to x
+// Two tiles (32 rows from `row` on) of a wave's slice of the memory, one value
+// column per lane, to x [dk][dv], and 4 tokens of a value column per lane to x
 // [T][dv]: transposed over quads of lanes, so that a lane stores 16 bytes and 16
-// lanes four runs of 64.
-template <int KS>
-__device__ inline void store_state(float* x, const f32x4 (&S)[KS], int first_row, int dk, int dv,
-                                   int col, int lane) {
-  const int row = first_row + acc_row(0, lane >> 4) + (lane & 3);
-  float* const to = x + int64_t(row) * dv + (col & ~3);
-#pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    const int more = acc_row(i, 0);
-    const f32x4 y = quad_transpose(S[i], lane);
-    if (row + more < dk) *reinterpret_cast<f32x4*>(to + more * dv) = y;
-  }
+// lanes four runs of 64.  The memory goes out two tiles to a stage.
+// x: from row `row` on; off: state_offset; more: dk - row.
+__device__ inline unsigned state_offset(int dv, int col, int lane) {
+  return (8 * (lane >> 4) + (lane & 3)) * dv + (col & ~3);
+}
+__device__ inline void store_rows(float* x, f32x4 s0, f32x4 s1, unsigned off, int more, int dv,
+                                  int lane) {
+  const int row = 8 * (lane >> 4) + (lane & 3);
+  s0 = quad_transpose(s0, lane);
+  if (row < more) elem4(x, off) = s0;
+  s1 = quad_transpose(s1, lane);
+  if (row + 4 < more) elem4(x + 4 * dv, off) = s1;
 }
 __device__ inline void store_tokens(float* x, f32x4 y, int tok, int valid, int dv, int col,
                                     int lane) {

@@ -35,11 +35,18 @@ struct Stages {
   static constexpr int kInv = nKQ, kScore = nKQ + 1, kKeyT = nKQ + (kAgain ? 1 : 2),
                        n = kKeyT + nKT;
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
-  // at most a chunk ahead: the values and decays of two chunks have room
-  static constexpr int kMost = kBf16 ? 4 : 2, kAhead = n < kMost ? n : kMost;
+  // kAgain with bf16: dh comes through LDS too, with the inverse (a wave that
+  // stores and then loads waits for its stores); one buffer, so less than a
+  // chunk ahead.  Otherwise at most a chunk ahead: the values and decays of two
+  // chunks have room.
+  static constexpr bool kStaged = kAgain && kBf16;
+  static constexpr int kMost = kStaged ? 3 : kBf16 ? 4 : 2;
+  static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
+  static constexpr int kPart = 10 * kFrag;  // a value tile's sums between its two waves
   static constexpr int kSlots = kAhead + 1;
   static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
-                       kPartAt = kDecayAt + 2 * kFrag, kShared = kPartAt + kWaves * kPart;
+                       kPartAt = kDecayAt + 2 * kFrag, kDhAt = kPartAt + kWaves * kPart,
+                       kShared = kDhAt + (kStaged ? Values<T>::kBytes : 0);
 
   static constexpr int tiles_of(int s) {  // of K^T, for each half
     return KS - (s - kKeyT) * kI < kI ? KS - (s - kKeyT) * kI : kI;
@@ -48,7 +55,7 @@ struct Stages {
   static constexpr int copies(int s) {
     s %= n;
     if (s < nKQ) return (kBf16 ? 4 : 6) + (s == 0 ? Values<T>::kCopies + 1 : 0);
-    if (s == kInv) return Copier::square_copies(3);
+    if (s == kInv) return Copier::square_copies(3) + (kStaged ? Values<T>::kCopies : 0);
     if (s < kKeyT) return Copier::square_copies(NPP);
     return tiles_of(s) * NPL;
   }
@@ -111,6 +118,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
           }
         }
       } else if constexpr (s == St::kInv) {
+        if constexpr (St::kStaged)
+          cp.values(a.dh, (head * a.T_len + tok0) * dv, valid, dv, block * 16 * kWaves, St::kDhAt);
         cp.template square<3, true>(a.ws.inv + at * 3 * kSquare, dst);
       } else if constexpr (s < St::kKeyT) {
         cp.template square<NPP, true>(a.ws.score + at * NPP * kSquare, dst);
@@ -157,8 +166,10 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
   // the second's: K S of all, Q S of tokens 32-63 (six).  What a wave has read
   // it overwrites with its X, for the other one.
-  f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * kPart) + lane;
+  f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;
   f32x4* const to_second = to_first + 4 * 64;
+
+  const unsigned state_off = state_offset(dv, col, lane);
 
   int read = 0;  // the slot of the stage at hand
   auto enter = [&]() {
@@ -173,9 +184,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
     const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
     const float* decay = reinterpret_cast<const float*>(lds + St::kDecayAt + (chunk & 1) * kFrag);
     char* value = lds + St::kValueAt + (chunk & 1) * V::kBytes;
-    auto value_of = [&](int tok) {
-      return reinterpret_cast<T*>(value + V::at(tok)) + tile * 16 + m;
-    };
+    char* const my_value = value + V::lane_at(g) + (tile * 16 + m) * sizeof(T);
+    auto value_of = [&](int i, int r) { return reinterpret_cast<T*>(my_value + V::acc_at(i, r)); };
     auto at_tile = [&](int what, int i) {
       return *reinterpret_cast<const f32x4*>(decay + what * kC + acc_row(i, g));
     };
@@ -183,8 +193,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
     const int64_t rows = (head * a.T_len + tok0) * dv;
     const unsigned own = (32 * half + 8 * g) * dv + col;
     f32x4 dh[2] = {};
-    if constexpr (kAgain) {
-      if (mine) {
+    if constexpr (kAgain && !St::kStaged)
+      if (mine)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -192,9 +202,6 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
             const int tok = acc_row(2 * half + i, g) + r;
             if (tok < valid) dh[i][r] = load_elem(&elem(a.dh + rows + (4 * i + r) * dv, own));
           }
-        store_state(a.sv.S + at * dk * dv, S, first_row, dk, dv, col, lane);
-      }
-    }
 
     // K S and Q S over this half's rows
     f32x4 ks[4] = {}, qs[4] = {};
@@ -204,10 +211,13 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
       const char* slot = enter() + half * (St::kBf16 ? 8 : NPL * 4) * kFrag;
 #pragma unroll
       for (int i = 0; i < 4; ++i) kf[i] = lds_frag<NPL>(slot, i, 4, lane);
-      if constexpr (St::kBf16)
+      if constexpr (St::kBf16 && !kAgain)
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, 4 + i, 4, lane);
       const Planes<3> b = split<3>(pair(S[2 * t], S[2 * t + 1]));
+      if (kAgain && mine)
+        store_rows(a.sv.S + (at * dk + first_row + 32 * t) * dv, S[2 * t], S[2 * t + 1], state_off,
+                   dk - first_row - 32 * t, dv, lane);
       each_product<3, NPL, 3>([&](int x, int y) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) ks[i] = mma(kf[i].p[x], b.p[y], ks[i]);
@@ -216,6 +226,10 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
         slot = enter() + half * NPL * 4 * kFrag;
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, i, 4, lane);
+      } else if constexpr (kAgain) {
+        asm volatile("" ::: "memory");  // not before: registers are short
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, 4 + i, 4, lane);
       }
       each_product<NPP, NPL, 3>([&](int x, int y) {
 #pragma unroll
@@ -241,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
       f32x4 R;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float x = load_elem(value_of(tok + r)) - e[r] * ks[r];
+        const float x = load_elem(value_of(i, r)) - e[r] * ks[r];
         R[r] = tok + r < valid ? x : 0.0f;  // behind the end: nothing, whatever the memory holds
       }
       return R;
@@ -280,7 +294,13 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
         if (mine) store_tokens(a.sv.X + rows, x[i], tok, valid, dv, col, lane);
         f32x4 s;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[r] = row_sum(dh[i][r] * hs[i][r]);
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (St::kStaged)  // zeros behind the end
+            dh[i][r] = load_elem(reinterpret_cast<const T*>(
+                lds + St::kDhAt + V::lane_at(g) + (tile * 16 + m) * sizeof(T) +
+                half * V::acc_at(2, 0) + V::acc_at(i, r)));
+          s[r] = row_sum(dh[i][r] * hs[i][r]);
+        }
         if (mine && m == 0)
           elem4(a.sv.part + (at * a.tiles + block * kWaves + tile) * 3 * kC, tok) = s;
       }
@@ -308,11 +328,12 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
         add_square<NPP, true>(slot, lane, kLowSecond, b0, split<NPP>(pair(U[2], U[3])), hs[0],
                               hs[1]);
       // to where the values were; the copying waves store it
+      char* const my_half = my_value + half * V::acc_at(2, 0);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          store_elem(value_of(acc_row(2 * half + i, g) + r), hs[i][r]);
+          store_elem(reinterpret_cast<T*>(my_half + V::acc_at(i, r)), hs[i][r]);
       slot = nullptr;
     }
     // S = e^(G_C) S + K^T (e^(G_C - G) U)
