@@ -22,17 +22,22 @@ namespace mlstm {
 namespace delta {
 namespace {
 
+// What a pass over the chunks is for: h and the memory, the memory once more for
+// the backward (no scores, no h), or what a segment of the sequence makes of a
+// memory (no Q either).
+enum Pass { kForward, kAgainPass, kMapPass };
+
 // The stages of a chunk.  A stage of K and Q (float32: of K, then of Q) and one
-// of K^T serve both halves of the memory's rows (KS tiles each).  kAgain: the
-// memory once more for the backward, with no scores and no h.
-template <typename T, int KS, bool kAgain>
+// of K^T serve both halves of the memory's rows (KS tiles each).
+template <typename T, int KS, Pass kPass>
 struct Stages {
+  static constexpr bool kAgain = kPass == kAgainPass, kMap = kPass == kMapPass;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPL = kBf16 ? 1 : 3;             // planes of q and k
   static constexpr int NPP = kBf16 && !kAgain ? 2 : 3;  // of P, and of S and U where h is formed
   static constexpr int kI = kBf16 ? 4 : 2;              // row tiles of K^T for each half
-  static constexpr int nKQ = kBf16 ? KS / 2 : KS, nKT = (KS + kI - 1) / kI;
-  static constexpr int kInv = nKQ, kScore = nKQ + 1, kKeyT = nKQ + (kAgain ? 1 : 2),
+  static constexpr int nKQ = kBf16 || kMap ? KS / 2 : KS, nKT = (KS + kI - 1) / kI;
+  static constexpr int kInv = nKQ, kScore = nKQ + 1, kKeyT = nKQ + (kPass == kForward ? 2 : 1),
                        n = kKeyT + nKT;
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
   // kAgain with bf16: dh comes through LDS too, with the inverse (a wave that
@@ -54,7 +59,7 @@ struct Stages {
   // copies of each copying wave in a stage
   static constexpr int copies(int s) {
     s %= n;
-    if (s < nKQ) return (kBf16 ? 4 : 6) + (s == 0 ? Values<T>::kCopies + 1 : 0);
+    if (s < nKQ) return (!kBf16 ? 6 : kMap ? 2 : 4) + (s == 0 ? Values<T>::kCopies + 1 : 0);
     if (s == kInv) return Copier::square_copies(3) + (kStaged ? Values<T>::kCopies : 0);
     if (s < kKeyT) return Copier::square_copies(NPP);
     return tiles_of(s) * NPL;
@@ -67,21 +72,36 @@ struct Stages {
 };
 
 // T: element type of q, k, v, h.  KS: 32-column blocks of dk (even).
-template <typename T, int KS, bool kAgain>
-__global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const float* C_in, T* h,
+//
+// A sequence may be cut into segments (Segments): each is a workgroup's own, from
+// chunk first to chunk last.  The forward takes the memory before a segment from
+// `seg.maps`; the map pass writes there what a segment makes of zero (segment 0:
+// of C_in) with its values, and of each unit vector without them (value columns
+// dv .. dv + dk).
+template <typename T, int KS, Pass kPass>
+__global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segments seg,
+                                                             const float* C_in, T* h,
                                                              float* C_out) {
-  using St = Stages<T, KS, kAgain>;
+  using St = Stages<T, KS, kPass>;
   using V = Values<T>;
+  constexpr bool kAgain = St::kAgain, kMap = St::kMap;
   constexpr int NPL = St::NPL, NPP = St::NPP;
   constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
   __shared__ __attribute__((aligned(1024))) char lds[St::kShared];
   int64_t head;
   int block;
-  map_head(blockIdx.x, a.H, a.per_head, head, block);
+  map_head(blockIdx.x, a.H, a.per_head * seg.n_of(kMap), head, block);
+  const int segment = block / a.per_head;
+  block %= a.per_head;
+  const int columns = kMap ? a.dv + a.dk : a.dv;
+  // segment 0 starts from a memory that is known
+  if (kMap && segment == 0 && block * 16 * kWaves >= a.dv) return;  // the whole workgroup
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
-  const int chunks = a.chunks, dk = a.dk, dv = a.dv;
+  const int first = segment * seg.chunks;
+  const int chunks = first + seg.chunks < a.chunks ? first + seg.chunks : a.chunks;
+  const int dk = a.dk, dv = a.dv;
 
   if (wave >= kChainWaves) {
     // ------------------------------------------------------ the copying waves
@@ -92,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
       // behind the last chunk: its data again, into the buffers of the one after
       const int side = chunk & 1;
       chunk = chunk < chunks ? chunk : chunks - 1;
-      const int64_t at = head * chunks + chunk, kat = khead * chunks + chunk;
+      const int64_t at = head * a.chunks + chunk, kat = khead * a.chunks + chunk;
       const int64_t tok0 = int64_t(chunk) * kC;
       const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
       const unsigned dst = slot * St::kSlot;
@@ -108,12 +128,12 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
             const int t = half * (KS / 2) + s;
             const int64_t from = (khead * a.T_len + tok0) * dk;
             cp.rows(a.k, from, valid, dk, t, dst + half * 8 * kFrag);
-            cp.rows(a.q, from, valid, dk, t, dst + (half * 8 + 4) * kFrag);
+            if (!kMap) cp.rows(a.q, from, valid, dk, t, dst + (half * 8 + 4) * kFrag);
           } else {
-            const int t = half * (KS / 2) + s / 2;
+            const int t = half * (KS / 2) + (kMap ? s : s / 2);
 #pragma unroll
             for (int p = 0; p < NPL; ++p)
-              cp.frag((s % 2 ? a.ws.query : a.ws.key) + (kat * NPL + p) * kPlane, kPlane * 2,
+              cp.frag((!kMap && s % 2 ? a.ws.query : a.ws.key) + (kat * NPL + p) * kPlane, kPlane * 2,
                       t * 4 + cp.w, dst + ((half * NPL + p) * 4 + cp.w) * kFrag);
           }
         }
@@ -129,15 +149,15 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
       }
     };
     static_for<St::kAhead>(
-        [&](auto s) { issue(std::integral_constant<int, s % St::n>{}, s / St::n, s); });
+        [&](auto s) { issue(std::integral_constant<int, s % St::n>{}, first + s / St::n, s); });
     int slot = St::kAhead;
-    for (int chunk = 0; chunk < chunks; ++chunk)
+    for (int chunk = first; chunk < chunks; ++chunk)
       static_for<St::n>([&](auto stage) {
         constexpr int s = decltype(stage)::value, next = s + St::kAhead;
         stage_barrier<St::in_flight(s)>();
         issue(std::integral_constant<int, next % St::n>{}, chunk + next / St::n, slot);
         slot = slot + 1 == St::kSlots ? 0 : slot + 1;
-        if constexpr (s == St::kKeyT && !kAgain) {  // h is where the chunk's values were
+        if constexpr (s == St::kKeyT && kPass == kForward) {  // h is where the chunk's values were
           const int64_t tok0 = int64_t(chunk) * kC;
           cp.store_values(lds + St::kValueAt + (chunk & 1) * V::kBytes, h,
                           (head * a.T_len + tok0) * dv,
@@ -153,15 +173,21 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
   // ---------------------------------------------------------- the chain's waves
   const int tile = wave % kWaves, half = wave / kWaves;
   const int col = (block * kWaves + tile) * 16 + m;  // value column
-  const bool mine = col < dv;  // whole waves; the others keep the barriers company
+  const bool mine = col < columns;  // whole waves; the others keep the barriers company
   const int first_row = half * KS * 16;
+  const float* const from = kMap || segment == 0 ? C_in : seg.before(head, segment, dk, dv);
   f32x4 S[KS];
 #pragma unroll
   for (int i = 0; i < KS; ++i) {
     const int row = first_row + acc_row(i, g);
     S[i] = f32x4{};
-    if (C_in && mine && row < dk)
-      S[i] = *reinterpret_cast<const f32x4*>(C_in + (head * dv + col) * dk + row);
+    if (kMap && col >= dv) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = row + r == col - dv ? 1.0f : 0.0f;
+    } else if (from && mine && row < dk && (!kMap || segment == 0)) {
+      S[i] = *reinterpret_cast<const f32x4*>(
+          from + (int64_t(segment == 0 ? head : 0) * dv + col) * dk + row);
+    }
   }
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
   // the second's: K S of all, Q S of tokens 32-63 (six).  What a wave has read
@@ -179,8 +205,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
     return slot;
   };
 
-  for (int chunk = 0; chunk < chunks; ++chunk) {
-    const int64_t at = head * chunks + chunk, tok0 = int64_t(chunk) * kC;
+  for (int chunk = first; chunk < chunks; ++chunk) {
+    const int64_t at = head * a.chunks + chunk, tok0 = int64_t(chunk) * kC;
     const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
     const float* decay = reinterpret_cast<const float*>(lds + St::kDecayAt + (chunk & 1) * kFrag);
     char* value = lds + St::kValueAt + (chunk & 1) * V::kBytes;
@@ -211,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
       const char* slot = enter() + half * (St::kBf16 ? 8 : NPL * 4) * kFrag;
 #pragma unroll
       for (int i = 0; i < 4; ++i) kf[i] = lds_frag<NPL>(slot, i, 4, lane);
-      if constexpr (St::kBf16 && !kAgain)
+      if constexpr (St::kBf16 && kPass == kForward)
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, 4 + i, 4, lane);
       const Planes<3> b = split<3>(pair(S[2 * t], S[2 * t + 1]));
@@ -222,7 +248,9 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
 #pragma unroll
         for (int i = 0; i < 4; ++i) ks[i] = mma(kf[i].p[x], b.p[y], ks[i]);
       });
-      if constexpr (!St::kBf16) {
+      if constexpr (kMap) {
+        return;
+      } else if constexpr (!St::kBf16) {
         slot = enter() + half * NPL * 4 * kFrag;
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, i, 4, lane);
@@ -319,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) U[i] *= at_tile(2, i);
-    if constexpr (!kAgain) {
+    if constexpr (kPass == kForward) {
       // h = e^G Q^ S + P U, for this wave's tokens
       const Planes<NPP> b0 = split<NPP>(pair(U[0], U[1]));
       if (half == 0)
@@ -345,37 +373,136 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, const f
     for (int i = 0; i < KS; ++i) S[i] *= e_all;
     static_for<St::nKT>([&](auto stage) {
       constexpr int j = decltype(stage)::value;
-      if (!kAgain || j > 0) slot = enter();
+      if (kPass == kForward || j > 0) slot = enter();
       add_transposed<NPL, St::tiles_of(St::kKeyT + j), St::kI>(slot, half, u0, u1,
                                                                S + j * St::kI, lane);
     });
   }
-  if (C_out && mine)
+  // the memory after the segment: the caller's, or the map pass's
+  float* to = nullptr;
+  if (kMap) to = seg.after(head, segment, dk, dv);
+  if (kPass == kForward && chunks == a.chunks) to = C_out + head * dv * dk;
+  if (to && mine)
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       const int row = first_row + acc_row(i, g);
-      if (row < dk) *reinterpret_cast<f32x4*>(C_out + (head * dv + col) * dk + row) = S[i];
+      if (row < dk) *reinterpret_cast<f32x4*>(to + int64_t(col) * dk + row) = S[i];
     }
 }
 
-template <typename T, int KS, bool kAgain>
+// The memories before segments 2 ..: S' = Phi S + B, one segment after the other,
+// Phi and B as the map pass left them (S' takes B's place).  A workgroup has 8
+// value columns; a thread has two of 256 rows and an eighth of the sum over Phi's
+// columns, so that what it reads of S from LDS serves two rows.  First it copies
+// C_in, which the forward's last segment may overwrite before its first has read
+// it.
+constexpr int kJoinCols = 8, kJoinLanes = 128, kJoinRows = 2 * kJoinLanes, kJoinShares = kJoinCols,
+              kJoinMax = int(kDeltaMaxKeyDim) / kJoinRows;
+constexpr int kJoinAhead = 16;  // loads on their way at a time
+template <int kMax>  // blocks of rows
+__global__ __launch_bounds__(kJoinLanes * kJoinShares) void delta_join_kernel(Segments seg,
+                                                                              const float* C_in,
+                                                                              int dk, int dv) {
+  __shared__ __attribute__((aligned(16))) float S[kDeltaMaxKeyDim][kJoinCols];
+  __shared__ float part[kJoinShares][kJoinCols][kJoinRows];
+  const int64_t head = blockIdx.x / (dv / kJoinCols);
+  const int col0 = int(blockIdx.x % (dv / kJoinCols)) * kJoinCols;
+  const int r0 = threadIdx.x % kJoinLanes, share = threadIdx.x / kJoinLanes;
+  const int n = dk / kJoinShares;  // dk is a multiple of 16
+  if (C_in)
+    for (int i = threadIdx.x; i < kJoinCols * dk; i += kJoinLanes * kJoinShares)
+      seg.start[(head * dv + col0) * dk + i] = C_in[(head * dv + col0) * dk + i];
+  for (int i = threadIdx.x; i < kJoinCols * dk; i += kJoinLanes * kJoinShares)
+    S[i % dk][i / dk] = seg.after(head, 0, dk, dv)[int64_t(col0 + i / dk) * dk + i % dk];
+  __syncthreads();
+  for (int j = 1; j + 1 < seg.n; ++j) {
+    float* const map = seg.after(head, j, dk, dv);
+    float x[kMax][2][kJoinCols], B[kMax][2];
+#pragma unroll
+    for (int p = 0; p < kMax; ++p)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = p * kJoinRows + q * kJoinLanes + r0;
+        B[p][q] = r < dk ? map[int64_t(col0 + share) * dk + r] : 0.0f;
+      }
+#pragma unroll
+    for (int p = 0; p < kMax; ++p) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < kJoinCols; ++c) x[p][i][c] = 0.0f;
+      const int r = p * kJoinRows + r0;
+      if (r >= dk) continue;
+      const int more = r + kJoinLanes < dk ? kJoinLanes : 0;  // without a second row: the first
+      for (int k = 0; k < n; k += kJoinAhead) {
+        const float* const from = map + int64_t(dv + share * n + k) * dk + r;
+        float phi[kJoinAhead][2];  // all on their way before one is used
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) {
+          phi[i][0] = k + i < n ? from[i * dk] : 0.0f;
+          phi[i][1] = k + i < n ? from[i * dk + more] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+          if (k + i < n) {
+            float s[kJoinCols];
+#pragma unroll
+            for (int c = 0; c < kJoinCols; ++c) s[c] = S[share * n + k + i][c];
+#pragma unroll
+            for (int c = 0; c < kJoinCols; ++c) {
+              x[p][0][c] += phi[i][0] * s[c];
+              x[p][1][c] += phi[i][1] * s[c];
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < kMax; ++p) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kJoinCols; ++c) {
+        part[share][c][r0] = x[p][0][c];
+        part[share][c][r0 + kJoinLanes] = x[p][1][c];
+      }
+      __syncthreads();
+      // every share has read S: its next value, two rows of column `share` each
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int r = p * kJoinRows + q * kJoinLanes + r0;
+        if (r >= dk) continue;
+        float y = B[p][q];
+#pragma unroll
+        for (int t = 0; t < kJoinShares; ++t) y += part[t][share][q * kJoinLanes + r0];
+        map[int64_t(col0 + share) * dk + r] = y;
+        S[r][share] = y;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int KS, Pass kPass>
 hipError_t launch(const DeltaShape& s, const Layout& l, const void* q, const void* k, const void* v,
                   const void* dh, const float* C_in, void* h, float* C_out, hipStream_t stream) {
-  const Chain<T> a = chain<T>(s, l, q, k, v, dh);
-  delta_fwd_kernel<T, KS, kAgain><<<unsigned(a.H * a.per_head), kThreads, 0, stream>>>(
-      a, C_in, static_cast<T*>(h), C_out);
+  Chain<T> a = chain<T>(s, l, q, k, v, dh);
+  Segments seg = l.seg;
+  if (kPass == kAgainPass) seg = {1, a.chunks, nullptr, nullptr};
+  if (kPass == kMapPass) a.per_head = int((s.dv + s.dk + 63) / 64);
+  const unsigned grid = unsigned(a.H * a.per_head * seg.n_of(kPass == kMapPass));
+  delta_fwd_kernel<T, KS, kPass><<<grid, kThreads, 0, stream>>>(a, seg, C_in, static_cast<T*>(h),
+                                                                C_out);
   return hipGetLastError();
 }
 
-template <bool kAgain>
+template <Pass kPass>
 hipError_t dispatch(const DeltaShape& s, const Layout& l, const void* q, const void* k,
                     const void* v, const void* dh, const float* C_in, void* h, float* C_out,
                     hipStream_t stream) {
-#define MLSTM_FWD(KS)                                                                          \
-  case KS:                                                                                     \
-    return s.is_bf16                                                                           \
-               ? launch<__hip_bfloat16, KS, kAgain>(s, l, q, k, v, dh, C_in, h, C_out, stream) \
-               : launch<float, KS, kAgain>(s, l, q, k, v, dh, C_in, h, C_out, stream)
+#define MLSTM_FWD(KS)                                                                         \
+  case KS:                                                                                    \
+    return s.is_bf16                                                                          \
+               ? launch<__hip_bfloat16, KS, kPass>(s, l, q, k, v, dh, C_in, h, C_out, stream) \
+               : launch<float, KS, kPass>(s, l, q, k, v, dh, C_in, h, C_out, stream)
   switch (l.ks) {
     MLSTM_FWD(2);
     MLSTM_FWD(4);
@@ -392,7 +519,7 @@ hipError_t dispatch(const DeltaShape& s, const Layout& l, const void* q, const v
 
 hipError_t launch_again(const DeltaShape& s, const Layout& l, const void* q, const void* k,
                         const void* v, const void* dh, const float* C_in, hipStream_t stream) {
-  return dispatch<true>(s, l, q, k, v, dh, C_in, nullptr, nullptr, stream);
+  return dispatch<kAgainPass>(s, l, q, k, v, dh, C_in, nullptr, nullptr, stream);
 }
 
 }  // namespace delta
@@ -405,9 +532,19 @@ hipError_t launch_delta_fwd(const DeltaShape& s, const void* q, const void* k, c
                             const float* beta, const float* fgate, const float* C_in, void* h,
                             float* C_out, void* workspace, hipStream_t stream) {
   const Layout l = layout(s, false, workspace);
-  const hipError_t e = launch_prep(s, q, k, beta, fgate, l.ws, l.ks, false, stream);
+  hipError_t e = launch_prep(s, q, k, beta, fgate, l.ws, l.ks, false, stream);
   if (e != hipSuccess) return e;
-  return dispatch<false>(s, l, q, k, v, nullptr, C_in, h, C_out, stream);
+  if (l.seg.n > 1) {
+    e = dispatch<kMapPass>(s, l, q, k, v, nullptr, C_in, nullptr, nullptr, stream);
+    if (e != hipSuccess) return e;
+    const auto join =
+        s.dk <= kJoinRows ? delta_join_kernel<1> : delta_join_kernel<kJoinMax>;
+    join<<<unsigned(s.B * s.NH * (s.dv / kJoinCols)), kJoinLanes * kJoinShares, 0, stream>>>(
+        l.seg, C_in, int(s.dk), int(s.dv));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (C_in) C_in = l.seg.start;
+  }
+  return dispatch<kForward>(s, l, q, k, v, nullptr, C_in, h, C_out, stream);
 }
 
 }  // namespace mlstm

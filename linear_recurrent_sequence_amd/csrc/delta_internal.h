@@ -16,9 +16,54 @@ inline int key_blocks(int64_t dk) {
   return 0;
 }
 
+// A sequence cut into n segments of `chunks` chunks (the last one shorter).
+struct Segments {
+  int n, chunks;
+  float* maps;   // [H][n - 1][dv + dk][dk]: the memory after each (see delta_fwd_kernel)
+  float* start;  // [H][dv][dk]: the memory before the first
+
+  __host__ __device__ int n_of(bool map) const { return map ? n - 1 : n; }
+  __device__ float* after(int64_t head, int segment, int dk, int dv) const {
+    return maps + ((head * (n - 1) + segment) * (dv + dk)) * int64_t(dk);
+  }
+  __device__ const float* before(int64_t head, int segment, int dk, int dv) const {
+    return after(head, segment - 1, dk, dv);
+  }
+};
+
+// How many segments.  The chains of a sequence's chunks run one workgroup to a
+// CU, so where heads times value columns leave CUs idle, a longer sequence is cut
+// and each segment's effect on a memory taken first: (dv + dk) / dv times the
+// work, but segments side by side.  In units of a chunk's time (4.5 us at dk =
+// 128), from the rounds of workgroups that each pass takes, 0.8 for a chunk of the
+// map pass, three for joining a segment at dk = 256 and four for the launches; taken
+// if a fifth is won.  8 heads of 256 x 16384 in bf16: 1334 us in one piece.
+inline Segments segments_of(const DeltaShape& s) {
+  constexpr int64_t kCUs = 256;
+  const int64_t chunks = (s.T + kC - 1) / kC, H = s.B * s.NH;
+  auto rounds = [&](int64_t wgs) { return (wgs + kCUs - 1) / kCUs; };
+  const int64_t per_head = (s.dv + 63) / 64, mapped = (s.dv + s.dk + 63) / 64;
+  Segments best = {1, int(chunks), nullptr, nullptr};
+  double least = 0.8 * double(chunks * rounds(H * per_head));
+  for (int64_t n = 2; n <= 16 && n * 4 <= chunks; ++n) {
+    const int64_t len = (chunks + n - 1) / n;
+    if ((chunks + len - 1) / len != n) continue;  // as few segments of that length do
+    const double join = 3.0 * double(s.dk) * double(s.dk) / 65536.0;
+    const double t = double(len) * (0.8 * double(rounds(H * mapped * (n - 1))) +
+                                    double(rounds(H * per_head * n))) +
+                     double(n) * join + 4.0;
+    if (t < least) {
+      least = t;
+      best = {int(n), int(len), nullptr, nullptr};
+    }
+  }
+  return best;
+}
+
 struct Layout {
   Work ws;
   Saved sv;
+  Segments seg;
   int ks;
   size_t bytes;
 };
@@ -50,6 +95,13 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.ws.scoreT = planes(H * npp * square);
   }
   l.ws.decay = reinterpret_cast<float*>(take(H * 3 * kC * sizeof(float)));
+  l.seg = segments_of(s);
+  if (!backward && l.seg.n > 1) {
+    const size_t heads = size_t(s.B * s.NH), dk = size_t(s.dk), dv = size_t(s.dv);
+    l.seg.maps = reinterpret_cast<float*>(
+        take(heads * size_t(l.seg.n - 1) * (dv + dk) * dk * sizeof(float)));
+    l.seg.start = reinterpret_cast<float*>(take(heads * dv * dk * sizeof(float)));
+  }
   if (backward) {
     auto floats = [&](size_t n) { return reinterpret_cast<float*>(take(n * sizeof(float))); };
     const size_t state = size_t(s.dk * s.dv), rows = size_t(s.B * s.T);

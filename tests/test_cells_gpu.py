@@ -269,6 +269,26 @@ def test_delta_in_two_calls(dtype):
         close("C", C2, Cr)
 
 
+@pytest.mark.parametrize("NHK,NH,T,dk,dv,dtype,forget", [
+    (1, 1, 1500, 64, 64, BF, "sigmoid"), (1, 2, 2113, 48, 80, FP, "exp"),
+    (1, 1, 1600, 272, 16, BF, "exp"), (2, 4, 3001, 112, 96, BF, "sigmoid"),
+    (1, 1, 2048, 512, 32, FP, "sigmoid"), (1, 1, 4160, 16, 144, FP, "sigmoid")])
+def test_delta_long_sequences_in_segments(NHK, NH, T, dk, dv, dtype, forget):
+    """Few heads and many chunks: the sequence is cut into segments.  In place
+    too, where the last segment writes what the first one starts from."""
+    args, C0, _, _ = inputs(1, NHK, NH, T, dk, dv, dtype, 15, forget, fmean=6.0)
+    hr, Cr = oracle_of(args, C0, forget)
+    h, C = mlstm.delta_fwd(*args, state=C0, forget=forget)
+    close("h", h, hr)
+    close("C", C, Cr)
+    kept = C0.clone()
+    h2, _ = mlstm.delta_fwd(*args, state=kept, out_state=kept, forget=forget)
+    assert torch.equal(h2, h) and torch.equal(kept, C)
+    h0, C1 = mlstm.delta_fwd(*args, forget=forget)
+    zero, _ = mlstm.delta_fwd(*args, state=torch.zeros_like(C0), forget=forget)
+    assert torch.equal(h0, zero)
+
+
 def test_delta_keeps_heads_and_earlier_chunks_apart():
     """A NaN at one token reaches neither other heads nor earlier chunks."""
     args, C0, _, _ = inputs(2, 2, 4, 200, 32, 32, BF, 9)
