@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
     }
   }
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
-  // the second's: K S of all, Q S of tokens 32-63 (six).  What a wave has read
+  // the second's: V - e^G K S of all, Q S of tokens 32-63 (six).  What a wave has read
   // it overwrites with its X, for the other one.
   f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;
   f32x4* const to_second = to_first + 4 * 64;
@@ -264,9 +264,17 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
         for (int i = 0; i < 4; ++i) qs[i] = mma(qf[i].p[x], b.p[y], qs[i]);
       });
     });
+    // R = V - e^G K S, from the sum of the halves: the first half's wave takes the
+    // values, so that the second's, which has more to do below, has less here
+    f32x4 R[4];
     if (half == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to_second[i * 64] = ks[i];
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 e = at_tile(0, i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[i][r] = load_elem(value_of(i, r)) - e[r] * ks[i][r];
+        to_second[i * 64] = R[i];
+      }
       to_second[4 * 64] = qs[2];
       to_second[5 * 64] = qs[3];
     } else {
@@ -275,25 +283,19 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
       to_first[2 * 64] = qs[0];
       to_first[3 * 64] = qs[1];
     }
-
-    // R = V - e^G K S of token tile i, from the sum of the halves
-    auto rest = [&](int i, f32x4 ks) {
-      const int tok = acc_row(i, g);
-      const f32x4 e = at_tile(0, i);
-      f32x4 R;
+    auto whole = [&](int i, f32x4 part, f32x4 ks) {
+      f32x4 x = part - at_tile(0, i) * ks;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float x = load_elem(value_of(i, r)) - e[r] * ks[r];
-        R[r] = tok + r < valid ? x : 0.0f;  // behind the end: nothing, whatever the memory holds
-      }
-      return R;
+      for (int r = 0; r < 4; ++r)  // behind the end: nothing, whatever the memory holds
+        x[r] = acc_row(i, g) + r < valid ? x[r] : 0.0f;
+      return x;
     };
     // X (first half: tokens 0-31, second: 32-63), exchanged; then U = beta X
     f32x4 U[4], x[2] = {}, hs[2];
     {
       const char* slot = enter();
       if (half == 0) {
-        const f32x4 r0 = rest(0, ks[0] + to_first[0]), r1 = rest(1, ks[1] + to_first[64]);
+        const f32x4 r0 = whole(0, R[0], to_first[0]), r1 = whole(1, R[1], to_first[64]);
         hs[0] = qs[0] + to_first[2 * 64];
         hs[1] = qs[1] + to_first[3 * 64];
         const Planes<3> b = split<3>(pair(r0, r1));
@@ -301,9 +303,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
         to_first[0] = x[0];
         to_first[64] = x[1];
       } else {
-        f32x4 R[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) R[i] = rest(i, ks[i] + to_second[i * 64]);
+        for (int i = 0; i < 4; ++i) R[i] = whole(i, to_second[i * 64], ks[i]);
         hs[0] = qs[2] + to_second[4 * 64];
         hs[1] = qs[3] + to_second[5 * 64];
         add_square<3, true>(slot, lane, kLowSecond, split<3>(pair(R[0], R[1])),
