@@ -174,7 +174,7 @@ struct Copier {
       const int f = j * kWaves + w < 6 * NP ? j * kWaves + w : 6 * NP - 1;
       copy_frag(r, lane16(),
                 f / 6 * (kSquare * 2) + (kLow ? low_pair(f % 6) : high_pair(f % 6)) * kFrag,
-                lds0 + to + (j * kWaves + w) * kFrag);
+                lds0 + to + f * kFrag);  // the last one more than once, where they do not divide
     }
   }
   static constexpr int square_copies(int np) { return (6 * np + kWaves - 1) / kWaves; }

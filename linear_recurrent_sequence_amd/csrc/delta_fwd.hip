@@ -39,7 +39,7 @@ struct Stages {
   static constexpr int nKQ = kBf16 || kMap ? KS / 2 : KS, nKT = (KS + kI - 1) / kI;
   static constexpr int kInv = nKQ, kScore = nKQ + 1, kKeyT = nKQ + (kPass == kForward ? 2 : 1),
                        n = kKeyT + nKT;
-  static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
+  static constexpr int kSlot = (kBf16 ? 18 : 24) * kFrag;
   // kAgain with bf16: dh comes through LDS too, with the inverse (a wave that
   // stores and then loads waits for its stores); one buffer, so less than a
   // chunk ahead.  Otherwise at most a chunk ahead: the values and decays of two
@@ -47,7 +47,9 @@ struct Stages {
   static constexpr bool kStaged = kAgain && kBf16;
   static constexpr int kMost = kStaged ? 3 : kBf16 ? 4 : 2;
   static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
-  static constexpr int kPart = 10 * kFrag;  // a value tile's sums between its two waves
+  // between a value tile's two waves: to the first (K S and Q S of tokens 0-31,
+  // then U's planes) and to the second
+  static constexpr int kToFirst = 4 > 3 + NPP ? 4 : 3 + NPP, kPart = (kToFirst + 6) * kFrag;
   static constexpr int kSlots = kAhead + 1;
   static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
                        kPartAt = kDecayAt + 2 * kFrag, kDhAt = kPartAt + kWaves * kPart,
@@ -191,9 +193,9 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
   }
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
   // the second's: V - e^G K S of all, Q S of tokens 32-63 (six).  What a wave has read
-  // it overwrites with its X, for the other one.
+  // it overwrites with planes of its U, for the other one.
   f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;
-  f32x4* const to_second = to_first + 4 * 64;
+  f32x4* const to_second = to_first + St::kToFirst * 64;
 
   const unsigned state_off = state_offset(dv, col, lane);
 
@@ -290,8 +292,9 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
         x[r] = acc_row(i, g) + r < valid ? x[r] : 0.0f;
       return x;
     };
-    // X (first half: tokens 0-31, second: 32-63), exchanged; then U = beta X
-    f32x4 U[4], x[2] = {}, hs[2];
+    // X (first half: tokens 0-31, second: 32-63) and U = beta X; the planes that
+    // the other wave takes of it go through LDS
+    f32x4 x[2] = {}, hs[2];
     {
       const char* slot = enter();
       if (half == 0) {
@@ -300,8 +303,6 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
         hs[1] = qs[1] + to_first[3 * 64];
         const Planes<3> b = split<3>(pair(r0, r1));
         add_square<3, false>(slot, lane, kLowFirst, b, b, x[0], x[1]);
-        to_first[0] = x[0];
-        to_first[64] = x[1];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) R[i] = whole(i, to_second[i * 64], ks[i]);
@@ -309,12 +310,23 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
         hs[1] = qs[3] + to_second[5 * 64];
         add_square<3, true>(slot, lane, kLowSecond, split<3>(pair(R[0], R[1])),
                             split<3>(pair(R[2], R[3])), x[0], x[1]);
-        to_second[0] = x[0];
-        to_second[64] = x[1];
       }
       hs[0] *= a.scale * at_tile(0, 2 * half);
       hs[1] *= a.scale * at_tile(0, 2 * half + 1);
     }
+    const f32x4 own_u[2] = {x[0] * at_tile(2, 2 * half), x[1] * at_tile(2, 2 * half + 1)};
+    // of U for h, of e^(G_C - G) U for the memory
+    Planes<NPP> for_h;
+    if (kPass == kForward) for_h = split<NPP>(pair(own_u[0], own_u[1]));
+    const Planes<3> for_s = split<3>(
+        pair(own_u[0] * at_tile(1, 2 * half), own_u[1] * at_tile(1, 2 * half + 1)));
+    asm volatile("" ::: "memory");  // what lies there has been read, as another type
+    bf16x8* const out = reinterpret_cast<bf16x8*>(half == 0 ? to_first : to_second);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) out[n * 64] = for_s.p[n];
+    if (kPass == kForward && half == 0)
+#pragma unroll
+      for (int n = 0; n < NPP; ++n) out[(3 + n) * 64] = for_h.p[n];
     if constexpr (kAgain) {
       // X, and e^G dh . (S^T q^) summed over the tile's columns
 #pragma unroll
@@ -335,27 +347,17 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
       }
     }
     const char* slot = enter();
-    if (half == 0) {
-      U[0] = x[0];
-      U[1] = x[1];
-      U[2] = to_second[0];
-      U[3] = to_second[64];
-    } else {
-      U[0] = to_first[0];
-      U[1] = to_first[64];
-      U[2] = x[0];
-      U[3] = x[1];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) U[i] *= at_tile(2, i);
+    const bf16x8* const in = reinterpret_cast<const bf16x8*>(half == 0 ? to_second : to_first);
     if constexpr (kPass == kForward) {
       // h = e^G Q^ S + P U, for this wave's tokens
-      const Planes<NPP> b0 = split<NPP>(pair(U[0], U[1]));
-      if (half == 0)
-        add_square<NPP, false>(slot, lane, kLowFirst, b0, b0, hs[0], hs[1]);
-      else
-        add_square<NPP, true>(slot, lane, kLowSecond, b0, split<NPP>(pair(U[2], U[3])), hs[0],
-                              hs[1]);
+      if (half == 0) {
+        add_square<NPP, false>(slot, lane, kLowFirst, for_h, for_h, hs[0], hs[1]);
+      } else {
+        Planes<NPP> other;
+#pragma unroll
+        for (int n = 0; n < NPP; ++n) other.p[n] = in[(3 + n) * 64];
+        add_square<NPP, true>(slot, lane, kLowSecond, other, for_h, hs[0], hs[1]);
+      }
       // to where the values were; the copying waves store it
       char* const my_half = my_value + half * V::acc_at(2, 0);
 #pragma unroll
@@ -367,9 +369,9 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
     }
     // S = e^(G_C) S + K^T (e^(G_C - G) U)
     const float e_all = decay[kC - 1];
+    Planes<3> u0 = for_s, u1 = for_s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) U[i] *= at_tile(1, i);
-    const Planes<3> u0 = split<3>(pair(U[0], U[1])), u1 = split<3>(pair(U[2], U[3]));
+    for (int n = 0; n < 3; ++n) (half == 0 ? u1 : u0).p[n] = in[n * 64];
 #pragma unroll
     for (int i = 0; i < KS; ++i) S[i] *= e_all;
     static_for<St::nKT>([&](auto stage) {
