@@ -446,7 +446,8 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
   const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
   const int64_t tok0 = int64_t(chunk) * kC;
   const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, m = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t krow0 = khead * a.T_len + tok0, row0 = head * a.T_len + tok0;
   if (w == 0) {
     G[lane] = chunk_decay(a.fgate + row0, lane, valid, a.exp_forget);
@@ -455,36 +456,64 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
   // rows 16 w ..: dh . X, dR . X, k . k, q . k
   f32x4 hx[4] = {}, rx[4] = {}, kk[4] = {}, qk[4] = {};
   const bool r_on = 16 * w + m < valid;
-  for (int s = 0; s < a.dv; s += 32) {
-    const int c = s + g * 8;
-    const bool c_on = c < a.dv;
-    const Planes<NPL> h =
-        to_planes<NPL>(load8(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on));
-    const Planes<3> r = to_planes<3>(load8(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on));
+  // the next 32 columns are on their way while these are worked on
+  {
+    typename Eight<T>::type h;
+    f32x8 r, x[4];
+    auto load = [&](int s) {
+      const int c = s + g * 8;
+      const bool c_on = c < a.dv;
+      h = load8(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
+      r = load8(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
-        const Planes<3> x = to_planes<3>(
-            load8(a.sv.X, (row0 + 16 * j + m) * a.dv + c, c_on && 16 * j + m < valid));
-        hx[j] = mma_planes<3>(h, x, hx[j]);
-        rx[j] = mma_planes<3>(r, x, rx[j]);
-      }
+      for (int j = 0; j < 4; ++j)
+        if (j <= w)
+          x[j] = load8(a.sv.X, (row0 + 16 * j + m) * a.dv + c, c_on && 16 * j + m < valid);
+    };
+    load(0);
+    for (int s = 0; s < a.dv; s += 32) {
+      const Planes<NPL> hp = to_planes<NPL>(h);
+      const Planes<3> rp = to_planes<3>(r);
+      f32x8 now[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) now[j] = x[j];
+      load(s + 32);  // nothing behind the last column
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          const Planes<3> xp = to_planes<3>(now[j]);
+          hx[j] = mma_planes<3>(hp, xp, hx[j]);
+          rx[j] = mma_planes<3>(rp, xp, rx[j]);
+        }
+    }
   }
-  for (int t = 0; t < a.dk_dim; t += 32) {
-    const int c = t + g * 8;
-    const bool c_on = c < a.dk_dim;
-    const Planes<NPL> qa =
-        to_planes<NPL>(load8(a.q, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on));
-    const Planes<NPL> ka =
-        to_planes<NPL>(load8(a.k, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on));
+  {
+    typename Eight<T>::type q, k[4];
+    auto load = [&](int t) {
+      const int c = t + g * 8;
+      const bool c_on = c < a.dk_dim;
+      q = load8(a.q, (krow0 + 16 * w + m) * a.dk_dim + c, c_on && r_on);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
-        const Planes<NPL> kb = to_planes<NPL>(
-            load8(a.k, (krow0 + 16 * j + m) * a.dk_dim + c, c_on && 16 * j + m < valid));
-        kk[j] = mma_planes<NPL>(ka, kb, kk[j]);
-        qk[j] = mma_planes<NPL>(qa, kb, qk[j]);
-      }
+      for (int j = 0; j < 4; ++j)
+        if (j <= w)
+          k[j] = load8(a.k, (krow0 + 16 * j + m) * a.dk_dim + c, c_on && 16 * j + m < valid);
+    };
+    load(0);
+    for (int t = 0; t < a.dk_dim; t += 32) {
+      const Planes<NPL> qa = to_planes<NPL>(q);
+      Planes<NPL> kb[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) kb[j] = to_planes<NPL>(k[j]);
+      const Planes<NPL> ka = w == 0 ? kb[0] : w == 1 ? kb[1] : w == 2 ? kb[2] : kb[3];
+      load(t + 32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j <= w) {
+          kk[j] = mma_planes<NPL>(ka, kb[j], kk[j]);
+          qk[j] = mma_planes<NPL>(qa, kb[j], qk[j]);
+        }
+    }
   }
   __syncthreads();
   f32x4 rows = {};
@@ -710,6 +739,7 @@ __global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
   const int valid = a.T_len - int64_t(chunk) * kC < kC ? int(a.T_len - int64_t(chunk) * kC) : kC;
   float t1 = 0.0f, t3 = 0.0f, t2 = 0.0f;
   const float* part = a.sv.part + at * a.tiles * 3 * kC;
+#pragma unroll 8
   for (int i = 0; i < a.tiles; ++i) {
     t1 += part[i * 3 * kC + lane];
     t3 += part[i * 3 * kC + kC + lane];
