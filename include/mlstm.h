@@ -1,5 +1,6 @@
 /*
- * mlstm.h -- C ABI of the MI355X (gfx950) stabilized parallel mLSTM forward pass.
+ * mlstm.h -- C ABI of the MI355X (gfx950) stabilized parallel mLSTM forward pass,
+ * and, further down, of the gated delta rule and the block norm.
  *
  * The operation is the stabilized parallel forward pass of the mLSTM cell of
  * "xLSTM: Extended Long Short-Term Memory", Appendix A.3: the parallel form
@@ -397,6 +398,9 @@ size_t mlstm_delta_workspace_bytes(int64_t B, int64_t NHK, int64_t NH, int64_t T
  *   C_out      out  the memory after it; may be C_in (updated in place)
  *   workspace  mlstm_delta_workspace_bytes bytes of device memory, 256-byte
  *              aligned, used by this call alone until it has run on `stream`
+ * Where few heads leave the card idle a long sequence is cut into segments that
+ * run side by side (each one's effect on a memory is taken first), so a position's
+ * result may differ in its last bits from that of a shorter call.
  * Tensors 16-byte aligned (beta and fgate 4-byte).  Errors before any device
  * work.
  */
@@ -457,8 +461,9 @@ int mlstm_delta_step(const void* q, const void* k, const void* v, const float* b
  * norm is (a - mean) / sqrt(var + eps) (MLSTM_NORM_LAYER) or a / sqrt(mean(a^2)
  * + eps) (MLSTM_NORM_RMS); act is sigma(g) (MLSTM_GATE_SIGMOID) or g sigma(g)
  * (MLSTM_GATE_SILU).  Everything in between is float32; y is formed from r
- * before its rounding.  Tensors 16-byte aligned; no output may overlap an
- * input.  Bitwise reproducible.
+ * before its rounding.  Inputs finite: a NaN or an infinity stays in its row (and
+ * in the weights' gradients).  With eps = 0 a row without spread gives NaN.
+ * Tensors 16-byte aligned; no output may overlap an input.  Bitwise reproducible.
  */
 enum { MLSTM_NORM_LAYER = 0, MLSTM_NORM_RMS = 1 };
 enum { MLSTM_GATE_SIGMOID = 0, MLSTM_GATE_SILU = 1 };

@@ -1,4 +1,5 @@
-"""MI355X (gfx950) implementation of the stabilized parallel mLSTM forward pass.
+"""MI355X (gfx950) implementation of the stabilized parallel mLSTM forward pass,
+and beside it the gated delta rule and the block norm.
 
 The compute lives in a C-ABI shared library (``libmlstm.so``, HIP kernels for
 gfx950, declared in ``include/mlstm.h``); ``linear_recurrent_sequence_amd.mlstm``

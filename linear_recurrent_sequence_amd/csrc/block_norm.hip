@@ -30,6 +30,15 @@
 // zero loses nothing.  The weight gradients are summed per workgroup in
 // registers, then over the workgroups in a fixed order by a second kernel: no
 // atomics, results are bitwise reproducible.
+//
+// Measured (bf16, layer norm, gate and residual): forward on 8 x 2048 rows of
+// 4 x 384 67 us, 51 us being a copy's time for the same bytes; 4 x 2048 rows of
+// 8 x 512 95 us (67); backward there 176 us and 6 us for the weights' sums (108).
+// What is left is the vector work of a row beside its loads: about 280
+// instructions per 8 channels forward and 600 backward.  The next row is loaded
+// while one is worked on (two rows ahead gain nothing); with divisions by T per
+// row, sums through LDS shuffles and the precise exponential the same took 96 us
+// and 324 us.
 #include "block_norm.h"
 
 #include <hip/hip_bf16.h>
@@ -420,7 +429,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
 // sum_rows dr' act(g) n1 (dw1 = s a and ds = w1 a, both constant in a column)
 // and dw2.  The weights stay in LDS: with them in registers fewer waves fit.
 template <typename T, bool kLayer, int VPL, int NP>
-__global__ __launch_bounds__(kMaxWaves * 64, VPL * NP == 1 ? (sizeof(T) == 2 ? 4 : 3) : 2) void block_norm_bwd_kernel(
+__global__ __launch_bounds__(kMaxWaves * 64, VPL * NP == 1 ? (sizeof(T) == 2 ? 4 : 3)
+                                                                 : 2) void block_norm_bwd_kernel(
     Geometry g, const T* __restrict__ p, const T* __restrict__ gate,
     const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ scale, const float* __restrict__ next_weight,

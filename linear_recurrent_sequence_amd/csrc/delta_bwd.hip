@@ -22,10 +22,19 @@
 // forward once more (delta_fwd.hip; its start and X of every chunk are kept,
 // float32), the gradient of the memory backward (Z and dR kept), and, over all
 // chunks at once, the pairs of tokens, the gradients of q and k, and those of
-// beta and the gates.  Everything
-// that the float32 gradients (beta, gates, memory) come from has float32
-// accuracy (three bf16 planes); for bf16 inputs the products that only dq and
-// dk take carry two planes per operand (16 bits), dq and dk being rounded to 8.
+// beta and the gates.  Everything that the float32 gradients (beta, gates, memory)
+// come from has float32 accuracy (three bf16 planes); for bf16 inputs the products
+// that only dq and dk take carry two planes per operand (16 bits), dq and dk being
+// rounded to 8.
+//
+// What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
+// chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
+// bf16: chunk terms 84 us, memory again 465, its gradient 465, pairs 120, key
+// gradients 460, gates 9; the 1.2 GB of memories alone are 240 us each way at a
+// copy's rate.  Stored all at once at a chunk's start the memories stood 7 us in
+// the way of each chunk; and a chain's wave that loads from memory waits for its
+// own stores first, so V, X and dh come through LDS (bf16), which took the chains
+// from 630 to 460 us.
 #include "delta_chain.h"
 #include "delta_internal.h"
 

@@ -11,10 +11,23 @@
 // h_t = C_t q_t / sqrt(dk), 64 steps at a time.  Two waves hold the memory of 16
 // value columns in their accumulators, half of its rows each, and go through
 // the chunks of their head; they add their parts of K S and Q S, and take half
-// of the tokens' rows of X and h each, through LDS.  The four products of a chunk run on the bf16 matrix instruction with float32
-// operands as sums of bf16 planes (delta_common.h).  What is rounded to fewer
-// bits: for bf16 inputs the operands of h alone (S, U and P to 16 bits; h is
-// then rounded to 8), never what the memory takes in.
+// of the tokens' rows of X and h each, through LDS.  The four products of a
+// chunk run on the bf16 matrix instruction with float32 operands as sums of bf16
+// planes (delta_common.h).  What is rounded to fewer bits: for bf16 inputs the
+// operands of h alone (S, U and P to 16 bits; h is then rounded to 8), never what
+// the memory takes in.
+//
+// What bounds it: the chain.  A chunk of 128 wide heads takes a workgroup 4.5 us
+// (about 8700 cycles) whatever runs beside it; of these a SIMD's vector unit is
+// busy 47 %, its matrix unit 33 %, the CU's LDS 32 %, and the five barriers and
+// the chain's own latencies are the rest.  8 x 16 heads of 128 x 2048 in bf16:
+// 145 us for this kernel and 88 us for delta_prep.hip, 58 us being what a copy of
+// the inputs and outputs takes.  Measured on the way there: one wave to a value
+// tile that loads its operands from memory 750 us; through an LDS ring 195 us;
+// with copying waves of its own 138 us, and no less with two waves to a tile, which
+// take 317 -> 248 us on 8 x 4 heads of 384 x 2048, where one wave's registers
+// spilled.  Slots enough for a whole chunk ahead change nothing there (197 us with
+// 7, 195 with 3, before the copying waves).
 #include "delta_chain.h"
 #include "delta_internal.h"
 

