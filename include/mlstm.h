@@ -368,7 +368,8 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
  *   C        [B][NH][dv][dk]  float32
  *   NHK      a divisor of NH;  dk a multiple of 16 in [16, 512];
  *   dv       a multiple of 16 in [16, 1024];  T >= 1;  fewer than 2^18 heads
- *            B NH, and 2^22 chunks B NH ceil(T / 64)
+ *            B NH, and 2^22 chunks B NH ceil(T / 64) (one token: fewer than 2^24
+ *            value columns in sixteens, B NH dv / 16)
  * k is not normalized here.  The recurrence is stable for
  * beta |k|^2 <= 2 (unit keys and strengths in (0, 1), as a rule).  A position
  * with beta = 0 and f = 1 (f~ = +infinity, or 0 with MLSTM_FORGET_EXP) leaves

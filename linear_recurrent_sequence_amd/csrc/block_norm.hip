@@ -429,8 +429,8 @@ __global__ __launch_bounds__(kMaxWaves * 64) void block_norm_fwd_kernel(
 // sum_rows dr' act(g) n1 (dw1 = s a and ds = w1 a, both constant in a column)
 // and dw2.  The weights stay in LDS: with them in registers fewer waves fit.
 template <typename T, bool kLayer, int VPL, int NP>
-__global__ __launch_bounds__(kMaxWaves * 64, VPL * NP == 1 ? (sizeof(T) == 2 ? 4 : 3)
-                                                                 : 2) void block_norm_bwd_kernel(
+__global__ __launch_bounds__(
+    kMaxWaves * 64, VPL * NP > 1 ? 2 : sizeof(T) == 2 ? 4 : 3) void block_norm_bwd_kernel(
     Geometry g, const T* __restrict__ p, const T* __restrict__ gate,
     const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ scale, const float* __restrict__ next_weight,
@@ -733,8 +733,8 @@ hipError_t bwd(const Shape& s, const BlockNorm& a, const BlockNormGrads& d, floa
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   block_norm_weights_kernel<<<dim3((g.D + 63) / 64, 2), 64 * kShares, 0, stream>>>(
-      partials, a.weight, a.scale, d.dweight, a.scale ? d.dscale : nullptr, a.next_weight ? d.dnext_weight : nullptr,
-      int(grid) * g.rows_per_wg, g.D);
+      partials, a.weight, a.scale, d.dweight, a.scale ? d.dscale : nullptr,
+      a.next_weight ? d.dnext_weight : nullptr, int(grid) * g.rows_per_wg, g.D);
   return hipGetLastError();
 }
 

@@ -20,6 +20,10 @@ using mlstm::abi::overlaps;
 
 constexpr int64_t kMaxT = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
+// a launch takes fewer than 2^32 threads: a token's workgroups of 256 have at
+// least 16 value columns, a sequence has at most 16 of 768 to a head and 4 of 256
+// to a head's chunk
+constexpr int64_t kMaxTokenTiles = (int64_t(1) << 24) - 1;
 constexpr int64_t kMaxDeltaHeads = (int64_t(1) << 18) - 1;
 constexpr int64_t kMaxDeltaChunks = (int64_t(1) << 22) - 1;
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
@@ -34,8 +38,9 @@ int check_common(int64_t B, int64_t NH, int64_t T, int dtype) {
   return MLSTM_OK;
 }
 
-int check_delta(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk, int64_t dv,
-                int dtype) {
+// one_token: T = 1 forward, the step kernel's
+int check_delta(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk, int64_t dv, int dtype,
+                bool one_token) {
   const int st = check_common(B, NH, T, dtype);
   if (st != MLSTM_OK) return st;
   if (NHK < 1 || dk < 1 || dv < 1) return MLSTM_ERR_SHAPE;
@@ -44,9 +49,9 @@ int check_delta(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk, int64
       dv > mlstm::kDeltaMaxValueDim)
     return MLSTM_ERR_HEAD_DIM;
   const int64_t H = B * NH, chunks = (T + mlstm::kDeltaChunk - 1) / mlstm::kDeltaChunk;
-  // a launch takes fewer than 2^32 threads: at most 64 workgroups of 256 to a
-  // head, or 4 to a head's chunk
-  if (H > kMaxDeltaHeads || H > kMaxDeltaChunks / chunks) return MLSTM_ERR_SHAPE;
+  if (one_token ? H > kMaxTokenTiles / (dv / 16)
+                : H > kMaxDeltaHeads || H > kMaxDeltaChunks / chunks)
+    return MLSTM_ERR_SHAPE;
   return MLSTM_OK;
 }
 
@@ -108,7 +113,7 @@ extern "C" {
 
 size_t mlstm_delta_workspace_bytes(int64_t B, int64_t NHK, int64_t NH, int64_t T, int64_t dk,
                                    int64_t dv, int dtype, int backward) {
-  if (check_delta(B, NHK, NH, T, dk, dv, dtype) != MLSTM_OK) return 0;
+  if (check_delta(B, NHK, NH, T, dk, dv, dtype, T == 1 && !backward) != MLSTM_OK) return 0;
   const DeltaShape s = delta_shape(B, NHK, NH, T, dk, dv, dtype, MLSTM_FORGET_SIGMOID);
   if (backward) return mlstm::delta_bwd_workspace_bytes(s);
   return T == 1 ? 0 : mlstm::delta_fwd_workspace_bytes(s);
@@ -118,7 +123,7 @@ int mlstm_delta_fwd(const void* q, const void* k, const void* v, const float* be
                     const float* fgate, const float* C_in, void* h, float* C_out, void* workspace,
                     size_t workspace_bytes, int64_t B, int64_t NHK, int64_t NH, int64_t T,
                     int64_t dk, int64_t dv, int dtype, int forget_activation, void* stream) {
-  int st = check_delta(B, NHK, NH, T, dk, dv, dtype);
+  int st = check_delta(B, NHK, NH, T, dk, dv, dtype, T == 1);
   if (st != MLSTM_OK) return st;
   if (!known_forget(forget_activation)) return MLSTM_ERR_ACTIVATION;
   if ((st = check_given({q, k, v, beta, fgate, h, C_out})) != MLSTM_OK) return st;
@@ -157,7 +162,7 @@ int mlstm_delta_bwd(const void* q, const void* k, const void* v, const float* be
                     void* workspace, size_t workspace_bytes, int64_t B, int64_t NHK, int64_t NH,
                     int64_t T, int64_t dk_dim, int64_t dv_dim, int dtype, int forget_activation,
                     void* stream) {
-  int st = check_delta(B, NHK, NH, T, dk_dim, dv_dim, dtype);
+  int st = check_delta(B, NHK, NH, T, dk_dim, dv_dim, dtype, false);
   if (st != MLSTM_OK) return st;
   if (!known_forget(forget_activation)) return MLSTM_ERR_ACTIVATION;
   st = check_given({q, k, v, beta, fgate, dh, dq, dk, dv, dbeta, dfgate, workspace});

@@ -592,7 +592,8 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
 // dR and X into planes in LDS (two buffers, one barrier), and each wave the
 // columns of S and Z that it alone needs; the next 32 are loaded meanwhile.
 template <typename T>
-__global__ __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 2 : 1) void delta_grads_kernel(Grads<T> a) {
+__global__ __launch_bounds__(kGradThreads,
+                             sizeof(T) == 2 ? 2 : 1) void delta_grads_kernel(Grads<T> a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k, dh
   constexpr int NPD = kBf16 ? 2 : 3;  // planes of what only dq and dk take

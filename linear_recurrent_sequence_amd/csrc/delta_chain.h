@@ -224,7 +224,8 @@ __device__ inline void add_square(const char* slot, int lane, const int (&frag)[
   for (int i = NP - 1; i >= 0; --i) {
     bf16x8 a[4];
 #pragma unroll
-    for (int n = 0; n < (kBoth ? 4 : 2); ++n) a[n] = lds_frag<1>(slot, i * 6 + frag[n], 0, lane).p[0];
+    for (int n = 0; n < (kBoth ? 4 : 2); ++n)
+      a[n] = lds_frag<1>(slot, i * 6 + frag[n], 0, lane).p[0];
 #pragma unroll
     for (int j = NX - 1; j >= 0; --j)
       if (i + j < NP) {

@@ -50,7 +50,7 @@ struct Stages {
   static constexpr int NPP = kBf16 && !kAgain ? 2 : 3;  // of P, and of S and U where h is formed
   static constexpr int kI = kBf16 ? 4 : 2;              // row tiles of K^T for each half
   static constexpr int nKQ = kBf16 || kMap ? KS / 2 : KS, nKT = (KS + kI - 1) / kI;
-  static constexpr int kInv = nKQ, kScore = nKQ + 1, kKeyT = nKQ + (kPass == kForward ? 2 : 1),
+  static constexpr int kInv = nKQ, kKeyT = nKQ + (kPass == kForward ? 2 : 1),
                        n = kKeyT + nKT;
   static constexpr int kSlot = (kBf16 ? 18 : 24) * kFrag;
   // kAgain with bf16: dh comes through LDS too, with the inverse (a wave that
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(kThreads) void delta_fwd_kernel(Chain<T> a, Segment
             const int t = half * (KS / 2) + (kMap ? s : s / 2);
 #pragma unroll
             for (int p = 0; p < NPL; ++p)
-              cp.frag((!kMap && s % 2 ? a.ws.query : a.ws.key) + (kat * NPL + p) * kPlane, kPlane * 2,
-                      t * 4 + cp.w, dst + ((half * NPL + p) * 4 + cp.w) * kFrag);
+              cp.frag((!kMap && s % 2 ? a.ws.query : a.ws.key) + (kat * NPL + p) * kPlane,
+                      kPlane * 2, t * 4 + cp.w, dst + ((half * NPL + p) * 4 + cp.w) * kFrag);
           }
         }
       } else if constexpr (s == St::kInv) {

@@ -128,7 +128,7 @@ SIZES = [(dict(B=0), -2), (dict(NH=0), -2), (dict(NHK=0), -2), (dict(ddk=0), -2)
 
 @needs_lib
 @pytest.mark.parametrize("case,status", SIZES + [
-    (dict(T=0), -2), (dict(T=1 << 40), -2), (dict(T=1 << 30, B=64), -2),
+    (dict(T=0), -2), (dict(T=1 << 40), -2), (dict(T=1 << 30, B=64), -2), (dict(B=1 << 16), -2),
     (dict(q=0), -1), (dict(C_out=0), -1), (dict(h=0), -1), (dict(ws=0), -1), (dict(beta=0), -1),
     (dict(q=F[0] + 8), -5), (dict(beta=F[3] + 2), -5), (dict(ws=F[8] + 128), -5),
     (dict(C_in=F[5] + 4), -5), (dict(nws=100), -7),
@@ -151,8 +151,8 @@ def test_delta_bwd_rejects_before_device_work(case, status):
 
 @needs_lib
 @pytest.mark.parametrize("case,status", SIZES + [
-    (dict(C_in=0), -1), (dict(h=0), -1), (dict(v=F[2] + 2), -5), (dict(C_out=F[5] + 64), -9),
-    (dict(h=F[0]), -9)])
+    (dict(B=1 << 18, NH=32), -2), (dict(C_in=0), -1), (dict(h=0), -1), (dict(v=F[2] + 2), -5),
+    (dict(C_out=F[5] + 64), -9), (dict(h=F[0]), -9)])
 def test_delta_step_rejects_before_device_work(case, status):
     assert _call("mlstm_delta_step", STEP, DELTA, case) == status
 

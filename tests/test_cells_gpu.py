@@ -340,6 +340,25 @@ def test_delta_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_delta_step_of_more_heads_than_a_sequence_may_have():
+    """2^18 heads: one token is given no chunks, and takes them."""
+    B, NH, dk, dv = 1 << 17, 2, 16, 16
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    rand = lambda *shape: torch.randn(shape, device=DEV, generator=gen)  # noqa: E731
+    k = torch.nn.functional.normalize(rand(B, 1, dk), dim=-1).to(BF)
+    args = rand(B, 1, dk).to(BF), k, rand(B, NH, dv).to(BF), rand(B, NH).sigmoid(), rand(B, NH) + 3
+    C0 = rand(B, NH, dv, dk)
+    h, C = mlstm.delta_step(*args, C0, out_state=torch.empty_like(C0))
+    pick = torch.tensor([0, 1, 65535, 65536, B - 1], device=DEV)
+    hr, Cr = oracle_of([x[pick].unsqueeze(2) for x in args], C0[pick])
+    close("h", h[pick], hr[:, :, 0])
+    close("C", C[pick], Cr)
+    h2, C2 = mlstm.delta_fwd(*(x.unsqueeze(2) for x in args), state=C0)
+    assert torch.equal(h2[:, :, 0], h) and torch.equal(C2, C)
+    with pytest.raises(mlstm.MlstmError):
+        mlstm.delta_fwd(*(x.unsqueeze(2).repeat_interleave(2, 2) for x in args))
+
+
 def test_delta_on_other_streams_and_in_graphs():
     """Two calls at once on two streams, and captured forward and backward passes
     replayed with new inputs and eager work in between, against eager calls."""
