@@ -19,13 +19,14 @@
 // of dG from its token to the chunk's end, so no sum is longer than a chunk.
 //
 // Six passes: the terms that all columns share (delta_prep.hip), the memory
-// forward once more (delta_fwd.hip; its start and X of every chunk are kept,
+// forward once more (delta_forward.h; its start and X of every chunk are kept,
 // float32), the gradient of the memory backward (Z and dR kept), and, over all
-// chunks at once, the pairs of tokens, the gradients of q and k, and those of
-// beta and the gates.  Everything that the float32 gradients (beta, gates, memory)
-// come from has float32 accuracy (three bf16 planes); for bf16 inputs the products
-// that only dq and dk take carry two planes per operand (16 bits), dq and dk being
-// rounded to 8.
+// chunks at once, the pairs of tokens, the gradients of q and k, and those of beta
+// and the gates.  The two chains need each other only for sums of X with Z^T k
+// and run in one launch where the card holds both (side_by_side).  Everything that
+// the float32 gradients (beta, gates, memory) come from has float32 accuracy (three
+// bf16 planes); for bf16 inputs the products that only dq and dk take carry two
+// planes per operand (16 bits), dq and dk being rounded to 8.
 //
 // What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
 // chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
@@ -35,8 +36,7 @@
 // the way of each chunk; and a chain's wave that loads from memory waits for its
 // own stores first, so V, X and dh come through LDS (bf16), which took the chains
 // from 630 to 460 us.
-#include "delta_chain.h"
-#include "delta_internal.h"
+#include "delta_forward.h"
 
 namespace mlstm {
 namespace delta {
@@ -44,8 +44,9 @@ namespace {
 
 // The stages of a chunk: P^T, K by blocks for both halves of the memory's rows,
 // (I + At)^-T, then Q^T and K^T by row tiles.
-template <typename T, int KS>
-struct Stages {
+// kApart: it runs beside the memory's pass, without X (and V).
+template <typename T, int KS, bool kApart>
+struct BackStages {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k and dh
   static constexpr int kT = kBf16 ? 2 : 1;   // 32-column blocks of K for each half
@@ -55,7 +56,7 @@ struct Stages {
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
   // bf16: X and V come through LDS, with the inverse (a wave that stores and then
   // loads waits for its stores); one buffer each, so less than a chunk ahead
-  static constexpr bool kStaged = kBf16;
+  static constexpr bool kStaged = kBf16 && !kApart;
   static constexpr int kMost = kBf16 ? 3 : 2;
   static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
   static constexpr int kSlots = kAhead + 1;
@@ -86,20 +87,20 @@ struct Stages {
 };
 
 // The memory's gradient backward: Z at each chunk's end, dR (and dV), and the
-// parts X . (e^(G_C - G) Z^T k) and dR . (V - X) that each 16 columns give.
+// parts X . (e^(G_C - G) Z^T k) and dR . (V - X) that each 16 columns give (kApart:
+// e^(G_C - G) Z^T k itself, from which delta_pairs_kernel forms them).
 // Built as the forward is (delta_fwd.hip): the operands are upper triangular
 // here, so the first half's wave takes what the second's does there.
-template <typename T, int KS>
-__global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const float* dC_in,
-                                                              T* dv_out, float* dC_out) {
-  using St = Stages<T, KS>;
+template <typename T, int KS, bool kApart>
+__device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_out, float* dC_out,
+                                  int64_t wg, char* lds) {
+  using St = BackStages<T, KS, kApart>;
   using V = Values<T>;
   constexpr int NPL = St::NPL;
   constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
-  __shared__ __attribute__((aligned(1024))) char lds[St::kShared];
   int64_t head;
   int block;
-  map_head(blockIdx.x, a.H, a.per_head, head, block);
+  map_head(wg, a.H, a.per_head, head, block);
   const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t khead = head / a.NH * a.NHK + head % a.NH / (a.NH / a.NHK);
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     }
     // this wave's tokens of X and V - X
     f32x4 X[2] = {}, pred[2] = {};
-    if (!St::kStaged && mine)
+    if (!kApart && !St::kStaged && mine)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -300,11 +301,17 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
         if (mine && m == 0)
           elem4(part, what * kC + acc_row(2 * half + i, g)) = s;
       };
+      auto keep = [&](int i, f32x4 x) {
+        if constexpr (!kApart)
+          write_part(1, i, X[i], x);
+        else if (mine)
+          store_tokens(a.sv.KZ + rows, x, acc_row(2 * half + i, g), valid, dv, col, lane);
+      };
       if (half == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const f32x4 x = whole(i, to_first[i * 64]);
-          if (i < 2) write_part(1, i, X[i], x);
+          if (i < 2) keep(i, x);
           dU[i] = (dU[i] + x) * at_tile(2, i);
         }
         add_square<3, true>(slot, lane, kHighFirst, split<3>(pair(dU[0], dU[1])),
@@ -315,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
 #pragma unroll
         for (int i = 2; i < 4; ++i) {
           const f32x4 x = whole(i, to_second[(i - 2) * 64]);
-          write_part(1, i - 2, X[i - 2], x);
+          keep(i - 2, x);
           dU[i] = (dU[i] + x) * at_tile(2, i);
         }
         const Planes<3> b = split<3>(pair(dU[2], dU[3]));
@@ -325,7 +332,7 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        write_part(2, i, own[i], pred[i]);
+        if (!kApart) write_part(2, i, own[i], pred[i]);
         const int tok = acc_row(2 * half + i, g);
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // the other wave has read dh (before this stage's barrier)
@@ -382,6 +389,25 @@ __global__ __launch_bounds__(kThreads) void delta_back_kernel(Chain<T> a, const 
     }
 }
 
+// The two chains: one after the other, or (kBoth) side by side, one in the first
+// half of the workgroups.
+enum Chains { kMemory, kGradient, kBoth };
+
+template <typename T, int KS, Chains kWhich>
+__global__ __launch_bounds__(kThreads) void delta_chains_kernel(Chain<T> a, const float* C_in,
+                                                                const float* dC_in, T* dv_out,
+                                                                float* dC_out) {
+  constexpr int kAgain = ForwardStages<T, KS, kAgainPass>::kShared,
+                kBack = BackStages<T, KS, kWhich == kBoth>::kShared;
+  __shared__ __attribute__((aligned(1024))) char
+      lds[kWhich == kMemory ? kAgain : kWhich == kGradient || kBack > kAgain ? kBack : kAgain];
+  const int64_t first = kWhich == kBoth ? a.H * a.per_head : 0, wg = blockIdx.x;
+  if (kWhich == kMemory || wg < first)
+    forward_chain<T, KS, kAgainPass>(a, Segments{}, C_in, nullptr, nullptr, wg, lds);
+  else
+    back_chain<T, KS, kWhich == kBoth>(a, dC_in, dv_out, dC_out, wg - first, lds);
+}
+
 // planes of 8 neighbouring values
 template <int N>
 __device__ inline Planes<N> to_planes(const f32x8& x) {
@@ -413,7 +439,7 @@ constexpr int kPitch = kC + 1;
 
 template <typename T>
 struct Grads {
-  const T *q, *k, *dh;
+  const T *q, *k, *v, *dh;
   const float* fgate;
   const float* dR;
   Work ws;
@@ -421,7 +447,7 @@ struct Grads {
   T *dq, *dk;
   float *dbeta, *dfgate;
   int64_t T_len;
-  int chunks, NH, NHK, dk_dim, dv, ks, tiles, groups, exp_forget;
+  int chunks, NH, NHK, dk_dim, dv, ks, tiles, groups, exp_forget, apart;
   float scale;
 };
 
@@ -442,8 +468,9 @@ __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* 
 }
 
 // The 64 x 64 matrices of a head's chunk: B, B^T / sqrt(dk) and -(N + N^T) in
-// planes for delta_grads_kernel, and what they give to dG and dbeta.
-template <typename T>
+// planes for delta_grads_kernel, and what they give to dG and dbeta.  kApart: also
+// X . (e^(G_C - G) Z^T k) and dR . (V - X), for the one tile of Saved::part.
+template <typename T, bool kApart>
 __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int NPL = kBf16 ? 1 : 3, NPD = kBf16 ? 2 : 3;
@@ -467,13 +494,18 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
   const bool r_on = 16 * w + m < valid;
   // the next 32 columns are on their way while these are worked on
   {
-    typename Eight<T>::type h;
-    f32x8 r, x[4];
+    typename Eight<T>::type h, v;
+    f32x8 r, x[4], z;
+    float xz = 0.0f, rv = 0.0f;
     auto load = [&](int s) {
       const int c = s + g * 8;
       const bool c_on = c < a.dv;
       h = load8(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
       r = load8(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
+      if (kApart) {
+        v = load8(a.v, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
+        z = load8(a.sv.KZ, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w)
@@ -486,6 +518,14 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
       f32x8 now[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) now[j] = x[j];
+      if (kApart) {
+        const f32x8 own = w == 0 ? x[0] : w == 1 ? x[1] : w == 2 ? x[2] : x[3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          xz += own[e] * z[e];
+          rv += r[e] * (float(v[e]) - own[e]);
+        }
+      }
       load(s + 32);  // nothing behind the last column
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -494,6 +534,18 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
           hx[j] = mma_planes<3>(hp, xp, hx[j]);
           rx[j] = mma_planes<3>(rp, xp, rx[j]);
         }
+    }
+    if (kApart) {  // over the lane groups' columns
+#pragma unroll
+      for (int o = 16; o < 64; o <<= 1) {
+        xz += __shfl_xor(xz, o, 64);
+        rv += __shfl_xor(rv, o, 64);
+      }
+      float* const part = a.sv.part + at * a.tiles * 3 * kC + 16 * w + m;
+      if (g == 0) {
+        part[kC] = xz;
+        part[2 * kC] = rv;
+      }
     }
   }
   {
@@ -752,6 +804,7 @@ __global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
 #pragma unroll 8
   for (int i = 0; i < a.tiles; ++i) {
     t1 += part[i * 3 * kC + lane];
+    if (a.apart && i > 0) continue;
     t3 += part[i * 3 * kC + kC + lane];
     t2 += part[i * 3 * kC + 2 * kC + lane];
   }
@@ -783,33 +836,47 @@ template <typename T>
 hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, const void* q,
                     const void* k, const void* v, const float* fgate, const float* C_in,
                     hipStream_t stream) {
-  hipError_t e = launch_again(s, l, q, k, v, d.dh, C_in, stream);
-  if (e != hipSuccess) return e;
   const Chain<T> a = chain<T>(s, l, q, k, v, d.dh);
-#define MLSTM_BACK(KS)                                                                   \
-  case KS:                                                                               \
-    delta_back_kernel<T, KS><<<unsigned(a.H * a.per_head), kThreads, 0, stream>>>(       \
-        a, d.dC_in, static_cast<T*>(d.dv), d.dC_out);                                    \
+  const unsigned wgs = unsigned(a.H * a.per_head);
+  hipError_t e = hipSuccess;
+  auto run = [&](auto blocks, auto which) {
+    constexpr int KS = decltype(blocks)::value;
+    constexpr Chains kWhich = decltype(which)::value;
+    delta_chains_kernel<T, KS, kWhich><<<kWhich == kBoth ? 2 * wgs : wgs, kThreads, 0, stream>>>(
+        a, C_in, d.dC_in, static_cast<T*>(d.dv), d.dC_out);
+    return hipGetLastError();
+  };
+  auto chains = [&](auto blocks) {
+    if (l.side_by_side) return run(blocks, std::integral_constant<Chains, kBoth>{});
+    const hipError_t first = run(blocks, std::integral_constant<Chains, kMemory>{});
+    return first != hipSuccess ? first
+                               : run(blocks, std::integral_constant<Chains, kGradient>{});
+  };
+#define MLSTM_CHAINS(KS)                            \
+  case KS:                                          \
+    e = chains(std::integral_constant<int, KS>{});  \
     break
   switch (l.ks) {
-    MLSTM_BACK(2);
-    MLSTM_BACK(4);
-    MLSTM_BACK(6);
-    MLSTM_BACK(8);
-    MLSTM_BACK(12);
-    MLSTM_BACK(16);
+    MLSTM_CHAINS(2);
+    MLSTM_CHAINS(4);
+    MLSTM_CHAINS(6);
+    MLSTM_CHAINS(8);
+    MLSTM_CHAINS(12);
+    MLSTM_CHAINS(16);
     default: return hipErrorInvalidValue;
   }
-#undef MLSTM_BACK
-  e = hipGetLastError();
+#undef MLSTM_CHAINS
   if (e != hipSuccess) return e;
   const float* dR = sizeof(T) == 2 ? l.sv.dR : static_cast<const float*>(d.dv);
   const int groups = int((s.dk + 127) / 128);
-  const Grads<T> b = {a.q, a.k, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
+  const Grads<T> b = {a.q, a.k, a.v, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
                       static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
-                      a.dv, l.ks, a.tiles, groups, int(s.exp_forget), a.scale};
+                      a.dv, l.ks, a.tiles, groups, int(s.exp_forget), int(l.side_by_side), a.scale};
   const unsigned each = unsigned(a.H * a.chunks);
-  delta_pairs_kernel<T><<<each, kGradThreads, 0, stream>>>(b);
+  if (l.side_by_side)
+    delta_pairs_kernel<T, true><<<each, kGradThreads, 0, stream>>>(b);
+  else
+    delta_pairs_kernel<T, false><<<each, kGradThreads, 0, stream>>>(b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   delta_grads_kernel<T>
       <<<unsigned(s.B * s.NHK * a.chunks * groups), kGradThreads, 0, stream>>>(b);

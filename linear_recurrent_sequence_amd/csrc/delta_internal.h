@@ -16,6 +16,8 @@ inline int key_blocks(int64_t dk) {
   return 0;
 }
 
+constexpr int64_t kCUs = 256;
+
 // A sequence cut into n segments of `chunks` chunks (the last one shorter).
 struct Segments {
   int n, chunks;
@@ -41,7 +43,6 @@ struct Segments {
 // piece; in eight segments 297 us for the map pass, 47 to join and 205 for the
 // forward.
 inline Segments segments_of(const DeltaShape& s) {
-  constexpr int64_t kCUs = 256;
   const int64_t chunks = (s.T + kC - 1) / kC, H = s.B * s.NH;
   auto rounds = [&](int64_t wgs) { return (wgs + kCUs - 1) / kCUs; };
   const int64_t per_head = (s.dv + 63) / 64, mapped = (s.dv + s.dk + 63) / 64;
@@ -62,11 +63,25 @@ inline Segments segments_of(const DeltaShape& s) {
   return best;
 }
 
+// Whether the backward's two chains, the memory once more and its gradient, run
+// in one launch (delta_pairs_kernel then forms what needs both): where that
+// saves a tenth of the rounds of workgroups: up to 128 of them, and some numbers
+// above.  The whole backward pass, one after the other and side by side: 4 x 4
+// heads of 384 x 2048 (96 workgroups) in bf16 1049 and 786 us, 12 x 4 of 384 x
+// 1024 (288) 1319 and 1182, 2 x 16 of 128 x 2048 (64) in float32 982 and 627.
+// With as many rounds either way it is apart: X and V then need not be read again.
+inline bool side_by_side(const DeltaShape& s) {
+  const int64_t wgs = s.B * s.NH * ((s.dv + 63) / 64);
+  const int64_t apart = 2 * ((wgs + kCUs - 1) / kCUs), together = (2 * wgs + kCUs - 1) / kCUs;
+  return 10 * (apart - together) >= apart;
+}
+
 struct Layout {
   Work ws;
   Saved sv;
   Segments seg;
   int ks;
+  bool side_by_side;  // the backward's chains
   size_t bytes;
 };
 
@@ -111,6 +126,8 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.sv.Z = floats(H * state);
     l.sv.X = floats(rows * size_t(s.NH * s.dv));
     if (s.is_bf16) l.sv.dR = floats(rows * size_t(s.NH * s.dv));
+    l.side_by_side = side_by_side(s);
+    if (l.side_by_side) l.sv.KZ = floats(rows * size_t(s.NH * s.dv));
     l.sv.part = floats(H * size_t(s.dv / 16) * 3 * kC);
     const size_t npd = s.is_bf16 ? 2 : 3;
     l.sv.pairs = planes(H * 3 * npd * square);
@@ -139,10 +156,6 @@ Chain<T> chain(const DeltaShape& s, const Layout& l, const void* q, const void* 
           int(s.NH), int(s.NHK), int(s.dk), int(s.dv), tiles, (tiles + 3) / 4,
           1.0f / sqrtf(float(s.dk))};
 }
-
-// the memory once more for the backward (Saved::S, X and the first of part)
-hipError_t launch_again(const DeltaShape& s, const Layout& l, const void* q, const void* k,
-                        const void* v, const void* dh, const float* C_in, hipStream_t stream);
 
 // ks: the 32-column blocks that the kernels are built for, >= ceil(dk / 32)
 hipError_t launch_prep(const DeltaShape& s, const void* q, const void* k, const float* beta,

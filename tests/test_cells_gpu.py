@@ -128,6 +128,15 @@ def test_delta_backward(B, NHK, NH, T, dk, dv, dtype, forget, with_state):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+# the chains of the backward run one after the other where side by side takes no
+# fewer rounds of workgroups: 129 to 256 of them
+@pytest.mark.parametrize("B,NHK,NH,T,dk,dv,dtype,forget", [
+    (2, 5, 35, 131, 32, 80, BF, "sigmoid"), (9, 2, 16, 66, 16, 16, FP, "exp"),
+    (1, 3, 33, 65, 112, 272, BF, "exp"), (1, 33, 33, 67, 48, 272, FP, "sigmoid")])
+def test_delta_backward_of_many_heads(B, NHK, NH, T, dk, dv, dtype, forget):
+    test_delta_backward(B, NHK, NH, T, dk, dv, dtype, forget, True)
+
+
 @pytest.mark.parametrize("NHK,NH,dk,dv,dtype,forget", [
     (4, 4, 64, 64, BF, "sigmoid"), (1, 3, 16, 48, FP, "exp"), (2, 2, 272, 80, FP, "sigmoid"),
     (1, 2, 512, 1024, BF, "exp"), (1, 1, 80, 16, BF, "sigmoid"), (2, 4, 128, 128, BF, "sigmoid")])
