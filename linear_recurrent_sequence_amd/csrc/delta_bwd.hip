@@ -30,9 +30,8 @@
 //
 // What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
 // chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
-// bf16: chunk terms 84 us, memory again 465, its gradient 465, pairs 120, key
-// gradients 460, gates 9; the 1.2 GB of memories alone are 240 us each way at a
-// copy's rate.  Stored all at once at a chunk's start the memories stood 7 us in
+// bf16: chunk terms 85 us, the chains 440 and 465, pairs 120, key gradients 420,
+// gates 9; the 1.2 GB of memories alone are 240 us each way at a copy's rate.  Stored all at once at a chunk's start the memories stood 7 us in
 // the way of each chunk; and a chain's wave that loads from memory waits for its
 // own stores first, so V, X and dh come through LDS (bf16), which took the chains
 // from 630 to 460 us.
@@ -434,6 +433,13 @@ __device__ inline typename Eight<T>::type load8(const T* x, int64_t at, bool on)
   return v;
 }
 
+template <typename T>
+__device__ inline typename Eight<T>::type load8(const T* x, unsigned at, bool on) {
+  typename Eight<T>::type v = {};
+  if (on) v = *reinterpret_cast<const typename Eight<T>::type*>(&elem(x, at));
+  return v;
+}
+
 constexpr int kGradThreads = 256;
 constexpr int kPitch = kC + 1;
 
@@ -447,7 +453,7 @@ struct Grads {
   T *dq, *dk;
   float *dbeta, *dfgate;
   int64_t T_len;
-  int chunks, NH, NHK, dk_dim, dv, ks, tiles, groups, exp_forget, apart;
+  int chunks, NH, NHK, dk_dim, dv, ks, tiles, groups, exp_forget;
   float scale;
 };
 
@@ -471,7 +477,7 @@ __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* 
 // planes for delta_grads_kernel, and what they give to dG and dbeta.  kApart: also
 // X . (e^(G_C - G) Z^T k) and dR . (V - X), for the one tile of Saved::part.
 template <typename T, bool kApart>
-__global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
+__global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a) {
   constexpr bool kBf16 = sizeof(T) == 2;
   constexpr int NPL = kBf16 ? 1 : 3, NPD = kBf16 ? 2 : 3;
   __shared__ double G[kC];
@@ -566,7 +572,10 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) kb[j] = to_planes<NPL>(k[j]);
-      const Planes<NPL> ka = w == 0 ? kb[0] : w == 1 ? kb[1] : w == 2 ? kb[2] : kb[3];
+      Planes<NPL> ka;  // a plane at a time: a choice of structures goes through memory
+#pragma unroll
+      for (int n = 0; n < NPL; ++n)
+        ka.p[n] = w == 0 ? kb[0].p[n] : w == 1 ? kb[1].p[n] : w == 2 ? kb[2].p[n] : kb[3].p[n];
       load(t + 32);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -643,7 +652,10 @@ __global__ __launch_bounds__(kGradThreads) void delta_pairs_kernel(Grads<T> a) {
 // The contraction over dv runs 32 at a time: wave i splits token tile i of dh,
 // dR and X into planes in LDS (two buffers, one barrier), and each wave the
 // columns of S and Z that it alone needs; the next 32 are loaded meanwhile.
-template <typename T>
+// Registers are what is short: kShared only where value heads share a key head,
+// since dq then lives through the loop (460 us on the layer above; without, and
+// with 32-bit offsets, nothing spills: 420).
+template <typename T, bool kShared>
 __global__ __launch_bounds__(kGradThreads,
                              sizeof(T) == 2 ? 2 : 1) void delta_grads_kernel(Grads<T> a) {
   constexpr bool kBf16 = sizeof(T) == 2;
@@ -655,7 +667,7 @@ __global__ __launch_bounds__(kGradThreads,
   const int64_t id = blockIdx.x / a.groups;
   const int chunk = id % a.chunks, blk = int(blockIdx.x % a.groups) * kWaves;
   const int64_t khead = id / a.chunks;
-  const int group = a.NH / a.NHK;
+  const int group = kShared ? a.NH / a.NHK : 1;
   const int64_t tok0 = int64_t(chunk) * kC;
   const int valid = a.T_len - tok0 < kC ? int(a.T_len - tok0) : kC;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, m = lane & 15;
@@ -678,17 +690,17 @@ __global__ __launch_bounds__(kGradThreads,
     auto load = [&](int s) {
       const int c = s + g * 8;
       const bool on = tok < valid && c < a.dv;
-      const int64_t from = (row0 + tok) * a.dv + c;
-      dh = load8(a.dh, from, on);
-      dR = load8(a.dR, from, on);
-      X = load8(a.sv.X, from, on);
+      const unsigned from = tok * a.dv + c;
+      dh = load8(a.dh + row0 * a.dv, from, on);
+      dR = load8(a.dR + row0 * a.dv, from, on);
+      X = load8(a.sv.X + row0 * a.dv, from, on);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int kc = col0 + row_of(p, m);
         const bool k_on = kc < a.dk_dim && c < a.dv;
-        const int64_t k_from = (at * a.dk_dim + kc) * a.dv + c;
-        S[p] = load8(a.sv.S, k_from, k_on);
-        Z[p] = load8(a.sv.Z, k_from, k_on);
+        const unsigned k_from = kc * a.dv + c;
+        S[p] = load8(a.sv.S + at * a.dk_dim * a.dv, k_from, k_on);
+        Z[p] = load8(a.sv.Z + at * a.dk_dim * a.dv, k_from, k_on);
       }
     };
     load(0);
@@ -793,7 +805,7 @@ __global__ __launch_bounds__(kGradThreads,
 }
 
 // The gradients of beta and of the gates: a wave per head and chunk.
-template <typename T>
+template <typename T, bool kApart>
 __global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
   const int chunk = blockIdx.x % a.chunks, lane = threadIdx.x;
   const int64_t head = blockIdx.x / a.chunks, at = blockIdx.x;
@@ -804,9 +816,10 @@ __global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
 #pragma unroll 8
   for (int i = 0; i < a.tiles; ++i) {
     t1 += part[i * 3 * kC + lane];
-    if (a.apart && i > 0) continue;
-    t3 += part[i * 3 * kC + kC + lane];
-    t2 += part[i * 3 * kC + 2 * kC + lane];
+    if (!kApart || i == 0) {
+      t3 += part[i * 3 * kC + kC + lane];
+      t2 += part[i * 3 * kC + 2 * kC + lane];
+    }
   }
   const float* decay = a.ws.decay + at * 3 * kC;
   const double s3 = double(decay[2 * kC + lane]) * t3;
@@ -871,17 +884,16 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
   const int groups = int((s.dk + 127) / 128);
   const Grads<T> b = {a.q, a.k, a.v, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
                       static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
-                      a.dv, l.ks, a.tiles, groups, int(s.exp_forget), int(l.side_by_side), a.scale};
+                      a.dv, l.ks, a.tiles, groups, int(s.exp_forget), a.scale};
   const unsigned each = unsigned(a.H * a.chunks);
-  if (l.side_by_side)
-    delta_pairs_kernel<T, true><<<each, kGradThreads, 0, stream>>>(b);
-  else
-    delta_pairs_kernel<T, false><<<each, kGradThreads, 0, stream>>>(b);
+  const auto pairs = l.side_by_side ? delta_pairs_kernel<T, true> : delta_pairs_kernel<T, false>;
+  pairs<<<each, kGradThreads, 0, stream>>>(b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  delta_grads_kernel<T>
-      <<<unsigned(s.B * s.NHK * a.chunks * groups), kGradThreads, 0, stream>>>(b);
+  const auto grads = s.NH > s.NHK ? delta_grads_kernel<T, true> : delta_grads_kernel<T, false>;
+  grads<<<unsigned(s.B * s.NHK * a.chunks * groups), kGradThreads, 0, stream>>>(b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  delta_gates_kernel<T><<<each, 64, 0, stream>>>(b);
+  const auto gates = l.side_by_side ? delta_gates_kernel<T, true> : delta_gates_kernel<T, false>;
+  gates<<<each, 64, 0, stream>>>(b);
   return hipGetLastError();
 }
 
