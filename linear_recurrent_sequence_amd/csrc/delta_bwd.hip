@@ -43,7 +43,7 @@ namespace {
 
 // The stages of a chunk: P^T, K by blocks for both halves of the memory's rows,
 // (I + At)^-T, then Q^T and K^T by row tiles.
-// kApart: it runs beside the memory's pass, without X (and V).
+// kApart: without X (and V), as it has to be beside the memory's pass.
 template <typename T, int KS, bool kApart>
 struct BackStages {
   static constexpr bool kBf16 = sizeof(T) == 2;
@@ -53,9 +53,10 @@ struct BackStages {
   static constexpr int nK = (KS / 2 + kT - 1) / kT, nT = (KS + kI - 1) / kI;
   static constexpr int kInv = 1 + nK, kQueryT = kInv + 1, kKeyT = kQueryT + nT, n = kKeyT + nT;
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
-  // bf16: X and V come through LDS, with the inverse (a wave that stores and then
-  // loads waits for its stores); one buffer each, so less than a chunk ahead
-  static constexpr bool kStaged = kBf16 && !kApart;
+  // X and V come through LDS, with the inverse (a wave that stores and then loads
+  // waits for its stores); one buffer each, so less than a chunk ahead
+  static constexpr bool kStaged = !kApart;
+  static_assert(kApart || kBf16, "float32: LDS is full");
   static constexpr int kMost = kBf16 ? 3 : 2;
   static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
   static constexpr int kSlots = kAhead + 1;
@@ -208,9 +209,7 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
     auto at_tile = [&](int what, int i) {
       return *reinterpret_cast<const f32x4*>(decay + what * kC + acc_row(i, g));
     };
-    // of values: this wave's tokens are rows + (4 i + r) dv + mine0
-    const int64_t rows = (head * a.T_len + tok0) * dv;
-    const unsigned mine0 = (32 * half + 8 * g) * dv + col;
+    const int64_t rows = (head * a.T_len + tok0) * dv;  // of values
     // P^T dh: of this wave's tokens, and for the first half of the others too
     f32x4 dh[4], dU[4] = {};
     {
@@ -229,17 +228,6 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
     }
     // this wave's tokens of X and V - X
     f32x4 X[2] = {}, pred[2] = {};
-    if (!kApart && !St::kStaged && mine)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int tok = acc_row(2 * half + i, g) + r;
-          if (tok < valid) {
-            X[i][r] = elem(a.sv.X + rows + (4 * i + r) * dv, mine0);
-            pred[i][r] = load_elem(&elem(a.v + rows + (4 * i + r) * dv, mine0)) - X[i][r];
-          }
-        }
     // K Z over this half's rows
     f32x4 kz[4] = {};
     static_for<St::nK>([&](auto stage) {
@@ -389,22 +377,24 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
 }
 
 // The two chains: one after the other, or (kBoth) side by side, one in the first
-// half of the workgroups.
+// half of the workgroups.  Float32's gradient never takes X: loads of X
+// and V behind its own stores took a third of its time.
 enum Chains { kMemory, kGradient, kBoth };
 
 template <typename T, int KS, Chains kWhich>
 __global__ __launch_bounds__(kThreads) void delta_chains_kernel(Chain<T> a, const float* C_in,
                                                                 const float* dC_in, T* dv_out,
                                                                 float* dC_out) {
+  constexpr bool kApart = kWhich == kBoth || sizeof(T) == 4;
   constexpr int kAgain = ForwardStages<T, KS, kAgainPass>::kShared,
-                kBack = BackStages<T, KS, kWhich == kBoth>::kShared;
+                kBack = BackStages<T, KS, kApart>::kShared;
   __shared__ __attribute__((aligned(1024))) char
       lds[kWhich == kMemory ? kAgain : kWhich == kGradient || kBack > kAgain ? kBack : kAgain];
   const int64_t first = kWhich == kBoth ? a.H * a.per_head : 0, wg = blockIdx.x;
   if (kWhich == kMemory || wg < first)
     forward_chain<T, KS, kAgainPass>(a, Segments{}, C_in, nullptr, nullptr, wg, lds);
   else
-    back_chain<T, KS, kWhich == kBoth>(a, dC_in, dv_out, dC_out, wg - first, lds);
+    back_chain<T, KS, kApart>(a, dC_in, dv_out, dC_out, wg - first, lds);
 }
 
 // planes of 8 neighbouring values
@@ -860,7 +850,7 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
     return hipGetLastError();
   };
   auto chains = [&](auto blocks) {
-    if (l.side_by_side) return run(blocks, std::integral_constant<Chains, kBoth>{});
+    if (side_by_side(s)) return run(blocks, std::integral_constant<Chains, kBoth>{});
     const hipError_t first = run(blocks, std::integral_constant<Chains, kMemory>{});
     return first != hipSuccess ? first
                                : run(blocks, std::integral_constant<Chains, kGradient>{});
@@ -886,13 +876,14 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
                       static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
                       a.dv, l.ks, a.tiles, groups, int(s.exp_forget), a.scale};
   const unsigned each = unsigned(a.H * a.chunks);
-  const auto pairs = l.side_by_side ? delta_pairs_kernel<T, true> : delta_pairs_kernel<T, false>;
+  constexpr bool kAlways = sizeof(T) == 4;
+  const auto pairs = l.apart ? delta_pairs_kernel<T, true> : delta_pairs_kernel<T, kAlways>;
   pairs<<<each, kGradThreads, 0, stream>>>(b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const auto grads = s.NH > s.NHK ? delta_grads_kernel<T, true> : delta_grads_kernel<T, false>;
   grads<<<unsigned(s.B * s.NHK * a.chunks * groups), kGradThreads, 0, stream>>>(b);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const auto gates = l.side_by_side ? delta_gates_kernel<T, true> : delta_gates_kernel<T, false>;
+  const auto gates = l.apart ? delta_gates_kernel<T, true> : delta_gates_kernel<T, kAlways>;
   gates<<<each, 64, 0, stream>>>(b);
   return hipGetLastError();
 }

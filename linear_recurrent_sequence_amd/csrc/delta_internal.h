@@ -69,7 +69,10 @@ inline Segments segments_of(const DeltaShape& s) {
 // above.  The whole backward pass, one after the other and side by side: 4 x 4
 // heads of 384 x 2048 (96 workgroups) in bf16 1049 and 786 us, 12 x 4 of 384 x
 // 1024 (288) 1319 and 1182, 2 x 16 of 128 x 2048 (64) in float32 982 and 627.
-// With as many rounds either way it is apart: X and V then need not be read again.
+// With as many rounds either way bf16's run one after the other, where the second
+// has the sums with X at hand (8 x 4 of 384 x 2048 1431 us, 1497 with the sums left
+// to the pairs; float32, whose second chain gains by leaving them, 8 x 16 of 128 x
+// 1024 875 and 830).
 inline bool side_by_side(const DeltaShape& s) {
   const int64_t wgs = s.B * s.NH * ((s.dv + 63) / 64);
   const int64_t apart = 2 * ((wgs + kCUs - 1) / kCUs), together = (2 * wgs + kCUs - 1) / kCUs;
@@ -81,7 +84,7 @@ struct Layout {
   Saved sv;
   Segments seg;
   int ks;
-  bool side_by_side;  // the backward's chains
+  bool apart;  // the backward's gradient of the memory takes no X (see back_chain)
   size_t bytes;
 };
 
@@ -126,8 +129,8 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.sv.Z = floats(H * state);
     l.sv.X = floats(rows * size_t(s.NH * s.dv));
     if (s.is_bf16) l.sv.dR = floats(rows * size_t(s.NH * s.dv));
-    l.side_by_side = side_by_side(s);
-    if (l.side_by_side) l.sv.KZ = floats(rows * size_t(s.NH * s.dv));
+    l.apart = side_by_side(s) || !s.is_bf16;
+    if (l.apart) l.sv.KZ = floats(rows * size_t(s.NH * s.dv));
     l.sv.part = floats(H * size_t(s.dv / 16) * 3 * kC);
     const size_t npd = s.is_bf16 ? 2 : 3;
     l.sv.pairs = planes(H * 3 * npd * square);
