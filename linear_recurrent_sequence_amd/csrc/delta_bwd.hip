@@ -89,7 +89,7 @@ struct BackStages {
 // The memory's gradient backward: Z at each chunk's end, dR (and dV), and the
 // parts X . (e^(G_C - G) Z^T k) and dR . (V - X) that each 16 columns give (kApart:
 // e^(G_C - G) Z^T k itself, from which delta_pairs_kernel forms them).
-// Built as the forward is (delta_fwd.hip): the operands are upper triangular
+// Built as the forward is (delta_forward.h): the operands are upper triangular
 // here, so the first half's wave takes what the second's does there.
 template <typename T, int KS, bool kApart>
 __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_out, float* dC_out,

@@ -21,7 +21,7 @@ constexpr int64_t kCUs = 256;
 // A sequence cut into n segments of `chunks` chunks (the last one shorter).
 struct Segments {
   int n, chunks;
-  float* maps;   // [H][n - 1][dv + dk][dk]: the memory after each (see delta_fwd_kernel)
+  float* maps;   // [H][n - 1][dv + dk][dk]: the memory after each (see forward_chain)
   float* start;  // [H][dv][dk]: the memory before the first
 
   __host__ __device__ int n_of(bool map) const { return map ? n - 1 : n; }

@@ -32,7 +32,8 @@ namespace delta {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPitch = kC + 4;  // floats between rows in LDS: 16-byte rows, columns without conflicts
+// floats between rows in LDS: 16-byte rows, columns without conflicts
+constexpr int kPitch = kC + 4;
 
 __device__ inline f32x4 mma_f32(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);

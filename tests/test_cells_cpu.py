@@ -116,12 +116,12 @@ DELTA = dict(q=F[0], k=F[1], v=F[2], beta=F[3], fgate=F[4], C_in=F[5], h=F[6], C
              dC_out=F[16], nws=1 << 30, B=2, NHK=2, NH=4, T=100, ddk=64, ddv=48, dtype=1,
              forget=0, stream=0)
 FWD = "q k v beta fgate C_in h C_out ws nws B NHK NH T ddk ddv dtype forget stream".split()
-BWD = ("q k v beta fgate C_in dh dC_in dq dk dv dbeta dfgate dC_out ws nws B NHK NH T ddk ddv dtype "
-       "forget stream").split()
+BWD = ("q k v beta fgate C_in dh dC_in dq dk dv dbeta dfgate dC_out ws nws B NHK NH T ddk ddv "
+       "dtype forget stream").split()
 STEP = "q k v beta fgate C_in C_out h B NHK NH ddk ddv dtype forget stream".split()
 
-SIZES = [(dict(B=0), -2), (dict(NH=0), -2), (dict(NHK=0), -2), (dict(ddk=0), -2), (dict(ddv=-16), -2),
-         (dict(dtype=2), -3), (dict(ddk=24), -4), (dict(ddk=528), -4), (dict(ddv=40), -4),
+SIZES = [(dict(B=0), -2), (dict(NH=0), -2), (dict(NHK=0), -2), (dict(ddk=0), -2),
+         (dict(ddv=-16), -2), (dict(dtype=2), -3), (dict(ddk=24), -4), (dict(ddk=528), -4), (dict(ddv=40), -4),
          (dict(ddv=1040), -4), (dict(NH=5), -12), (dict(NHK=8), -12), (dict(forget=2), -10),
          (dict(forget=-1), -10), (dict(B=BIG), -2), (dict(B=1 << 20, NH=1 << 16, NHK=1), -2)]
 
