@@ -31,10 +31,10 @@
 // What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
 // chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
 // bf16: chunk terms 85 us, the chains 440 and 465, pairs 120, key gradients 420,
-// gates 9; the 1.2 GB of memories alone are 240 us each way at a copy's rate.  Stored all at once at a chunk's start the memories stood 7 us in
-// the way of each chunk; and a chain's wave that loads from memory waits for its
-// own stores first, so V, X and dh come through LDS (bf16), which took the chains
-// from 630 to 460 us.
+// gates 9; the 1.2 GB of memories alone are 240 us each way at a copy's rate.
+// Stored all at once at a chunk's start the memories stood 7 us in the way of each
+// chunk; and a chain's wave that loads from memory waits for its own stores first,
+// so V, X and dh come through LDS (bf16), which took the chains from 630 to 460 us.
 #include "delta_forward.h"
 
 namespace mlstm {
