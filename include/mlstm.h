@@ -379,8 +379,8 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
  *
  * All sums, the memory and the products that feed it are float32 (bf16
  * operands are exact; float32 operands of a matrix product are split into
- * three bf16 planes), gate sums are float64; for MLSTM_BF16 the operands of h
- * that are not inputs carry 16 bits, and h is rounded to nearest even.
+ * three bf16 planes), gate sums are float64; for MLSTM_BF16 h is rounded once, to
+ * nearest even.
  * Results are bitwise reproducible (no atomics, fixed order).
  */
 

@@ -239,7 +239,7 @@ constexpr int kSquare = kC * kC;
 struct Work {
   __bf16* inv;    // [H][chunks][3] planes of (I + At)^-1
   __bf16* invT;   // its transpose (backward)
-  __bf16* score;  // [H][chunks][NPP] planes of P
+  __bf16* score;  // [H][chunks][3] planes of P
   __bf16* scoreT; // its transpose (backward)
   __bf16* keyT;   // [HK][chunks][NPL] planes of K^T
   __bf16* queryT; // (backward)

@@ -21,7 +21,6 @@ struct ForwardStages {
   static constexpr bool kAgain = kPass == kAgainPass, kMap = kPass == kMapPass;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int NPL = kBf16 ? 1 : 3;             // planes of q and k
-  static constexpr int NPP = kBf16 && !kAgain ? 2 : 3;  // of P, and of S and U where h is formed
   static constexpr int kI = kBf16 ? 4 : 2;              // row tiles of K^T for each half
   static constexpr int nKQ = kBf16 || kMap ? KS / 2 : KS, nKT = (KS + kI - 1) / kI;
   static constexpr int kInv = nKQ, kKeyT = nKQ + (kPass == kForward ? 2 : 1),
@@ -35,8 +34,8 @@ struct ForwardStages {
   static constexpr int kMost = kStaged ? 3 : kBf16 ? 4 : 2;
   static constexpr int kAhead = n - kStaged < kMost ? n - kStaged : kMost;
   // between a value tile's two waves: to the first (K S and Q S of tokens 0-31,
-  // then U's planes) and to the second
-  static constexpr int kToFirst = 4 > 3 + NPP ? 4 : 3 + NPP, kPart = (kToFirst + 6) * kFrag;
+  // then six planes made of U) and to the second
+  static constexpr int kToFirst = 6, kPart = (kToFirst + 6) * kFrag;
   static constexpr int kSlots = kAhead + 1;
   static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
                        kPartAt = kDecayAt + 2 * kFrag, kDhAt = kPartAt + kWaves * kPart,
@@ -50,7 +49,7 @@ struct ForwardStages {
     s %= n;
     if (s < nKQ) return (!kBf16 ? 6 : kMap ? 2 : 4) + (s == 0 ? Values<T>::kCopies + 1 : 0);
     if (s == kInv) return Copier::square_copies(3) + (kStaged ? Values<T>::kCopies : 0);
-    if (s < kKeyT) return Copier::square_copies(NPP);
+    if (s < kKeyT) return Copier::square_copies(3);
     return tiles_of(s) * NPL;
   }
   static constexpr int in_flight(int s) {
@@ -75,7 +74,7 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
   using St = ForwardStages<T, KS, kPass>;
   using V = Values<T>;
   constexpr bool kAgain = St::kAgain, kMap = St::kMap;
-  constexpr int NPL = St::NPL, NPP = St::NPP;
+  constexpr int NPL = St::NPL;
   constexpr int64_t kPlane = int64_t(KS) * 32 * kC;
   int64_t head;
   int block;
@@ -132,7 +131,7 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
           cp.values(a.dh, (head * a.T_len + tok0) * dv, valid, dv, block * 16 * kWaves, St::kDhAt);
         cp.template square<3, true>(a.ws.inv + at * 3 * kSquare, dst);
       } else if constexpr (s < St::kKeyT) {
-        cp.template square<NPP, true>(a.ws.score + at * NPP * kSquare, dst);
+        cp.template square<3, true>(a.ws.score + at * 3 * kSquare, dst);
       } else {
         cp.template transposed<NPL, KS, St::kI>(a.ws.keyT + kat * NPL * kPlane,
                                                 (s - St::kKeyT) * St::kI, St::tiles_of(s), dst);
@@ -250,7 +249,7 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[i] = lds_frag<NPL>(slot, 4 + i, 4, lane);
       }
-      each_product<NPP, NPL, 3>([&](int x, int y) {
+      each_product<3, NPL, 3>([&](int x, int y) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) qs[i] = mma(qf[i].p[x], b.p[y], qs[i]);
       });
@@ -305,8 +304,8 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
     }
     const f32x4 own_u[2] = {x[0] * at_tile(2, 2 * half), x[1] * at_tile(2, 2 * half + 1)};
     // of U for h, of e^(G_C - G) U for the memory
-    Planes<NPP> for_h;
-    if (kPass == kForward) for_h = split<NPP>(pair(own_u[0], own_u[1]));
+    Planes<3> for_h;
+    if (kPass == kForward) for_h = split<3>(pair(own_u[0], own_u[1]));
     const Planes<3> for_s = split<3>(
         pair(own_u[0] * at_tile(1, 2 * half), own_u[1] * at_tile(1, 2 * half + 1)));
     asm volatile("" ::: "memory");  // what lies there has been read, as another type
@@ -315,7 +314,7 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
     for (int n = 0; n < 3; ++n) out[n * 64] = for_s.p[n];
     if (kPass == kForward && half == 0)
 #pragma unroll
-      for (int n = 0; n < NPP; ++n) out[(3 + n) * 64] = for_h.p[n];
+      for (int n = 0; n < 3; ++n) out[(3 + n) * 64] = for_h.p[n];
     if constexpr (kAgain) {
       // X, and e^G dh . (S^T q^) summed over the tile's columns
 #pragma unroll
@@ -340,12 +339,12 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
     if constexpr (kPass == kForward) {
       // h = e^G Q^ S + P U, for this wave's tokens
       if (half == 0) {
-        add_square<NPP, false>(slot, lane, kLowFirst, for_h, for_h, hs[0], hs[1]);
+        add_square<3, false>(slot, lane, kLowFirst, for_h, for_h, hs[0], hs[1]);
       } else {
-        Planes<NPP> other;
+        Planes<3> other;
 #pragma unroll
-        for (int n = 0; n < NPP; ++n) other.p[n] = in[(3 + n) * 64];
-        add_square<NPP, true>(slot, lane, kLowSecond, other, for_h, hs[0], hs[1]);
+        for (int n = 0; n < 3; ++n) other.p[n] = in[(3 + n) * 64];
+        add_square<3, true>(slot, lane, kLowSecond, other, for_h, hs[0], hs[1]);
       }
       // to where the values were; the copying waves store it
       char* const my_half = my_value + half * V::acc_at(2, 0);

@@ -13,9 +13,10 @@
 // the chunks of their head; they add their parts of K S and Q S, and take half
 // of the tokens' rows of X and h each, through LDS.  The four products of a
 // chunk run on the bf16 matrix instruction with float32 operands as sums of bf16
-// planes (delta_common.h).  What is rounded to fewer bits: for bf16 inputs the
-// operands of h alone (S, U and P to 16 bits; h is then rounded to 8), never what
-// the memory takes in.
+// planes (delta_common.h), three to an operand that is no bf16 input.  Two (16 bits)
+// for the operands of h would take 4 to 8 % off a call with bf16 inputs, and make
+// h another neighbour than the rounded float32 value's now and then (1.5e-4 in the
+// 2-norm, 7e-6 as it is): not done.
 //
 // What bounds it: the chain.  A chunk of 128 wide heads takes a workgroup 4.5 us
 // (about 8700 cycles) whatever runs beside it; of these a SIMD's vector unit is

@@ -94,7 +94,7 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
   l.ks = key_blocks(s.dk);
   const size_t chunks = size_t((s.T + kC - 1) / kC), H = size_t(s.B * s.NH) * chunks,
                HK = size_t(s.B * s.NHK) * chunks;
-  const size_t npl = s.is_bf16 ? 1 : 3, npp = s.is_bf16 && !backward ? 2 : 3;
+  const size_t npl = s.is_bf16 ? 1 : 3;
   const size_t rows = size_t(l.ks) * 32 * kC * sizeof(__bf16), square = kSquare * sizeof(__bf16);
   auto take = [&](size_t n) {
     char* p = base ? static_cast<char*>(base) + l.bytes : nullptr;
@@ -103,7 +103,7 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
   };
   auto planes = [&](size_t n) { return reinterpret_cast<__bf16*>(take(n)); };
   l.ws.inv = planes(H * 3 * square);
-  l.ws.score = planes(H * npp * square);
+  l.ws.score = planes(H * 3 * square);
   l.ws.keyT = planes(HK * npl * rows);
   if (npl == 3) {
     l.ws.key = planes(HK * npl * rows);
@@ -112,7 +112,7 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
   if (backward) l.ws.queryT = planes(HK * npl * rows);
   if (backward) {
     l.ws.invT = planes(H * 3 * square);
-    l.ws.scoreT = planes(H * npp * square);
+    l.ws.scoreT = planes(H * 3 * square);
   }
   l.ws.decay = reinterpret_cast<float*>(take(H * 3 * kC * sizeof(float)));
   l.seg = segments_of(s);

@@ -19,7 +19,7 @@
 // digits where neighbouring keys are alike: entries grow as binomials before
 // they cancel.
 //
-// What bounds it: memory, about 78 KiB of reads and writes per chunk of a 128
+// What bounds it: memory, about 84 KiB of reads and writes per chunk of a 128
 // wide bf16 head.  4096 such chunks take 88 us, 64 us at a copy's rate; a chunk
 // alone takes 11 us.  Before the transposes went through the matrix unit and one
 // matrix in LDS served P and At (18 KiB instead of 42, six workgroups to a CU
@@ -53,9 +53,9 @@ __device__ inline void store_tile(float* to, f32x4 c, float sign, int lane) {
   for (int r = 0; r < 4; ++r) to[((lane >> 4) * 4 + r) * kPitch + (lane & 15)] = sign * c[r];
 }
 
-// Writes NP planes of the lower triangular 64 x 64 matrix in LDS (or of its
+// Writes the planes of the lower triangular 64 x 64 matrix in LDS (or of its
 // transpose) in load order: the six (row tile, half) pairs that hold something.
-template <int NP, bool kTranspose>
+template <bool kTranspose>
 __device__ inline void write_square(const float (*m)[kPitch], __bf16* to) {
   for (int i = threadIdx.x; i < 6 * 64; i += kThreads) {
     const int lane = i & 63;
@@ -70,9 +70,9 @@ __device__ inline void write_square(const float (*m)[kPitch], __bf16* to) {
       v = pair(*reinterpret_cast<const f32x4*>(&m[row][col]),
                *reinterpret_cast<const f32x4*>(&m[row][col + 4]));
     }
-    const Planes<NP> s = split<NP>(v);
+    const Planes<3> s = split<3>(v);
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
+    for (int n = 0; n < 3; ++n)
       *reinterpret_cast<bf16x8*>(to + n * kSquare + (frag * 64 + lane) * 8) = s.p[n];
   }
 }
@@ -187,9 +187,8 @@ __global__ __launch_bounds__(kThreads, NPL == 1 ? 6 : 4) void delta_prep_kernel(
       kk[j][r] = c < row ? e * kk[j][r] * bt[c] : 0.0f;
     }
   __syncthreads();
-  constexpr int NPP = NPL == 1 && !kBackward ? 2 : 3;
-  write_square<NPP, false>(A, ws.score + at * NPP * kSquare);
-  if (kBackward) write_square<NPP, true>(A, ws.scoreT + at * NPP * kSquare);
+  write_square<false>(A, ws.score + at * 3 * kSquare);
+  if (kBackward) write_square<true>(A, ws.scoreT + at * 3 * kSquare);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -240,8 +239,8 @@ __global__ __launch_bounds__(kThreads, NPL == 1 ? 6 : 4) void delta_prep_kernel(
     store_tile(&A[32 + i][j], c, -1.0f, lane);  // no wave reads this block any more
   }
   __syncthreads();
-  write_square<3, false>(A, ws.inv + at * 3 * kSquare);
-  if (kBackward) write_square<3, true>(A, ws.invT + at * 3 * kSquare);
+  write_square<false>(A, ws.inv + at * 3 * kSquare);
+  if (kBackward) write_square<true>(A, ws.invT + at * 3 * kSquare);
 }
 
 }  // namespace

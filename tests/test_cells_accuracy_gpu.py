@@ -1,0 +1,34 @@
+"""How exact the gated delta rule and the block norm are on the GPU, beyond the
+tolerances of test_cells_gpu.py, whose inputs and oracle these tests share.
+
+A bf16 result is the float32 one rounded once.  With heads of 64 every sum has
+64 terms: float32 errors of either sign make sqrt(64) 2^-24 = 2^-21 of the sum's
+size, and four such products follow one another in a chunk, 2 * 2^-21 = 2^-20 in
+the 2-norm (e).  Rounded, a value differs from the oracle's rounded value only
+where a rounding border lies between the two, which it does with a chance of
+e / u, u <= 2^-7 |y| being the step, and then by u: the sum of the squares is
+sum e u <= 2^-20 2^-7 |y|^2, 2^-13.5 of y in the 2-norm.
+"""
+import numpy as np
+import pytest
+import torch
+
+from linear_recurrent_sequence_amd import mlstm
+from test_cells_gpu import BF, DEV, host, inputs, oracle_of
+
+pytestmark = pytest.mark.gpu
+ONE_ROUNDING = 2 ** -13.5
+
+
+def rounded_once(name, t, ref):
+    want = host(torch.tensor(ref, device=DEV).to(BF))
+    off = np.linalg.norm(host(t) - want) / np.linalg.norm(want)
+    assert t.dtype == BF and off <= ONE_ROUNDING, (name, off)
+
+
+@pytest.mark.parametrize("NHK,NH,T,forget", [(2, 4, 500, "sigmoid"), (1, 1, 2100, "exp")])
+def test_delta_forward_rounds_once(NHK, NH, T, forget):
+    """(1 x 1 x 2100 runs in segments.)"""
+    args, C0, _, _ = inputs(2 if T < 1000 else 1, NHK, NH, T, 64, 64, BF, 40, forget)
+    h, _ = mlstm.delta_fwd(*args, state=C0, forget=forget)
+    rounded_once("h", h, oracle_of(args, C0, forget)[0])
