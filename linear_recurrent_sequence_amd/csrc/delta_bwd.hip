@@ -24,9 +24,8 @@
 // chunks at once, the pairs of tokens, the gradients of q and k, and those of beta
 // and the gates.  The two chains need each other only for sums of X with Z^T k
 // and run in one launch where the card holds both (side_by_side).  Everything that
-// the float32 gradients (beta, gates, memory) come from has float32 accuracy (three
-// bf16 planes); for bf16 inputs the products that only dq and dk take carry two
-// planes per operand (16 bits), dq and dk being rounded to 8.
+// the gradients come from has float32 accuracy (three bf16 planes to an operand that
+// is no bf16 input); for bf16 inputs dq, dk and dv are rounded once, at the end.
 //
 // What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
 // chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
@@ -447,8 +446,8 @@ struct Grads {
   float scale;
 };
 
-// writes N planes of m (or its transpose) in load order
-template <int N, bool kTranspose>
+// writes the planes of m (or its transpose) in load order
+template <bool kTranspose>
 __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* to) {
   for (int i = threadIdx.x; i < kSquare / 8; i += kGradThreads) {
     const int lane = i & 63, frag = i >> 6;
@@ -457,9 +456,9 @@ __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* 
     f32x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = by * (kTranspose ? m[col + e][row] : m[row][col + e]);
-    const Planes<N> s = split<N>(v);
+    const Planes<3> s = split<3>(v);
 #pragma unroll
-    for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(to + n * kSquare + i * 8) = s.p[n];
+    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(to + n * kSquare + i * 8) = s.p[n];
   }
 }
 
@@ -468,8 +467,7 @@ __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* 
 // X . (e^(G_C - G) Z^T k) and dR . (V - X), for the one tile of Saved::part.
 template <typename T, bool kApart>
 __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a) {
-  constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int NPL = kBf16 ? 1 : 3, NPD = kBf16 ? 2 : 3;
+  constexpr int NPL = sizeof(T) == 2 ? 1 : 3;
   __shared__ double G[kC];
   __shared__ float bt[kC], row_g[kC], col_g[kWaves][kC], col_b[kWaves][kC];
   __shared__ float mat[kC][kPitch];
@@ -611,9 +609,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
     if (m == 0) row_g[16 * w + 4 * g + r] = s;
   }
   __syncthreads();
-  __bf16* const out = a.sv.pairs + at * 3 * NPD * kSquare;
-  write_planes<NPD, false>(mat, 1.0f, out);
-  write_planes<NPD, true>(mat, a.scale, out + NPD * kSquare);
+  __bf16* const out = a.sv.pairs + at * 9 * kSquare;
+  write_planes<false>(mat, 1.0f, out);
+  write_planes<true>(mat, a.scale, out + 3 * kSquare);
   if (w == 0) {
     float cg = row_g[lane], cb = 0.0f;
 #pragma unroll
@@ -634,7 +632,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
       if (c == row) mat[row][c] = 0.0f;
     }
   __syncthreads();
-  write_planes<NPD, false>(mat, 1.0f, out + 2 * NPD * kSquare);
+  write_planes<false>(mat, 1.0f, out + 6 * kSquare);
 }
 
 // The gradients of q and k: a workgroup takes a key head's chunk and 128
@@ -643,15 +641,14 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
 // dR and X into planes in LDS (two buffers, one barrier), and each wave the
 // columns of S and Z that it alone needs; the next 32 are loaded meanwhile.
 // Registers are what is short: kShared only where value heads share a key head,
-// since dq then lives through the loop (460 us on the layer above; without, and
-// with 32-bit offsets, nothing spills: 420).
+// since dq then lives through the loop.  There bf16 spills 46 of them at two
+// workgroups to a CU, and at one, without spills, 8 x 8 / 16 heads of 128 x 1024
+// take 593 us instead of 573 backward (2 x 2 / 4 of 64 x 555, 114 instead of 126).
 template <typename T, bool kShared>
 __global__ __launch_bounds__(kGradThreads,
                              sizeof(T) == 2 ? 2 : 1) void delta_grads_kernel(Grads<T> a) {
-  constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int NPL = kBf16 ? 1 : 3;  // planes of q, k, dh
-  constexpr int NPD = kBf16 ? 2 : 3;  // planes of what only dq and dk take
-  constexpr int kSet = NPL + 2 * NPD;
+  constexpr int NPL = sizeof(T) == 2 ? 1 : 3;  // planes of q, k, dh
+  constexpr int kSet = NPL + 6;
   __shared__ __attribute__((aligned(16))) char lds[2][4][kSet][kFrag];
   __shared__ float e0[kC], inner[kWaves];
   const int64_t id = blockIdx.x / a.groups;
@@ -698,38 +695,38 @@ __global__ __launch_bounds__(kGradThreads,
     for (int s = 0, side = 0; s < a.dv; s += 32, side ^= 1) {
       {
         const Planes<NPL> h = to_planes<NPL>(dh);
-        const Planes<NPD> r = split<NPD>(dR * by_r), x = split<NPD>(X * by_x);
+        const Planes<3> r = split<3>(dR * by_r), x = split<3>(X * by_x);
         auto put = [&](int n, bf16x8 v) {
           *reinterpret_cast<bf16x8*>(&lds[side][w][n][lane * 16]) = v;
         };
 #pragma unroll
         for (int n = 0; n < NPL; ++n) put(n, h.p[n]);
 #pragma unroll
-        for (int n = 0; n < NPD; ++n) {
+        for (int n = 0; n < 3; ++n) {
           put(NPL + n, r.p[n]);
-          put(NPL + NPD + n, x.p[n]);
+          put(NPL + 3 + n, x.p[n]);
         }
       }
-      Planes<NPD> Sp[2], Zp[2];
+      Planes<3> Sp[2], Zp[2];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dot += S[p][e] * Z[p][e];
-        Sp[p] = split<NPD>(S[p]);
-        Zp[p] = split<NPD>(Z[p]);
+        Sp[p] = split<3>(S[p]);
+        Zp[p] = split<3>(Z[p]);
       }
       __syncthreads();
       load(s + 32);  // nothing behind the last column
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Planes<NPL> h = lds_frag<NPL>(lds[side][i][0], 0, 1, lane);
-        const Planes<NPD> r = lds_frag<NPD>(lds[side][i][NPL], 0, 1, lane);
-        const Planes<NPD> x = lds_frag<NPD>(lds[side][i][NPL + NPD], 0, 1, lane);
-        each_product<NPD, NPL, NPD>([&](int y, int z) {
+        const Planes<3> r = lds_frag<3>(lds[side][i][NPL], 0, 1, lane);
+        const Planes<3> x = lds_frag<3>(lds[side][i][NPL + 3], 0, 1, lane);
+        each_product<3, NPL, 3>([&](int y, int z) {
 #pragma unroll
           for (int p = 0; p < 2; ++p) own[i][p] = mma(h.p[y], Sp[p].p[z], own[i][p]);
         });
-        each_product<NPD, NPD, NPD>([&](int y, int z) {
+        each_product<3, 3, 3>([&](int y, int z) {
 #pragma unroll
           for (int p = 0; p < 2; ++p) dk[i][p] = mma(r.p[y], Sp[p].p[z], dk[i][p]);
 #pragma unroll
@@ -738,7 +735,7 @@ __global__ __launch_bounds__(kGradThreads,
       }
     }
     // e^G dh S^T + B K, B^T Q^ - (N + N^T) K
-    const __bf16* pairs = a.sv.pairs + at * 3 * NPD * kSquare;
+    const __bf16* pairs = a.sv.pairs + at * 9 * kSquare;
     const __bf16* keyT = a.ws.keyT + (khead * a.chunks + chunk) * NPL * plane;
     const __bf16* queryT = a.ws.queryT + (khead * a.chunks + chunk) * NPL * plane;
 #pragma unroll
@@ -762,9 +759,8 @@ __global__ __launch_bounds__(kGradThreads,
         for (int i = 0; i < 4; ++i) {
           const int f = i * 2 + s;
           auto add = [&](int which, const Planes<NPL>(&b)[2], f32x4(&c)[2]) {
-            const Planes<NPD> x =
-                load_frag<NPD>(pairs + which * NPD * kSquare, kSquare, f, lane);
-            each_product<NPD, NPD, NPL>([&](int y, int z) {
+            const Planes<3> x = load_frag<3>(pairs + which * 3 * kSquare, kSquare, f, lane);
+            each_product<3, 3, NPL>([&](int y, int z) {
 #pragma unroll
               for (int p = 0; p < 2; ++p) c[p] = mma(x.p[y], b[p].p[z], c[p]);
             });

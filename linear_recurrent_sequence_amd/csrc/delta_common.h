@@ -256,7 +256,7 @@ struct Saved {
   float* dR;    // [H][T][dv] (bf16 inputs: dV is rounded)
   float* KZ;    // [H][T][dv] e^(G_C - G) Z^T k (Layout::apart)
   float* part;  // [H][chunks][dv / 16][3][64] parts of the gates' gradients
-  __bf16* pairs;  // [H][chunks][3][NPD] planes of B, B^T / sqrt(dk), -(N + N^T)
+  __bf16* pairs;  // [H][chunks][3][3] planes of B, B^T / sqrt(dk), -(N + N^T)
   float* gates;   // [H][chunks][2][64] what the pairs of tokens give to dG, dbeta
   float* inner;   // [H][chunks][blocks of 128 dk] parts of <S, Z>
 };

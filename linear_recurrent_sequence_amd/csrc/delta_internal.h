@@ -132,8 +132,7 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.apart = side_by_side(s) || !s.is_bf16;
     if (l.apart) l.sv.KZ = floats(rows * size_t(s.NH * s.dv));
     l.sv.part = floats(H * size_t(s.dv / 16) * 3 * kC);
-    const size_t npd = s.is_bf16 ? 2 : 3;
-    l.sv.pairs = planes(H * 3 * npd * square);
+    l.sv.pairs = planes(H * 9 * square);
     l.sv.gates = floats(H * 2 * kC);
     l.sv.inner = floats(H * size_t((s.dk + 127) / 128));
   }

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from linear_recurrent_sequence_amd import mlstm
-from test_cells_gpu import BF, DEV, host, inputs, oracle_of
+from test_cells_gpu import BF, DEV, NAMES, delta_ref, host, inputs, oracle_of
 
 pytestmark = pytest.mark.gpu
 ONE_ROUNDING = 2 ** -13.5
@@ -32,3 +32,14 @@ def test_delta_forward_rounds_once(NHK, NH, T, forget):
     args, C0, _, _ = inputs(2 if T < 1000 else 1, NHK, NH, T, 64, 64, BF, 40, forget)
     h, _ = mlstm.delta_fwd(*args, state=C0, forget=forget)
     rounded_once("h", h, oracle_of(args, C0, forget)[0])
+
+
+# the first two run the backward's two chains side by side, the third one after the other
+@pytest.mark.parametrize("B,NHK,NH,T,forget", [(2, 2, 4, 500, "sigmoid"), (1, 2, 2, 300, "exp"),
+                                               (2, 66, 66, 130, "sigmoid")])
+def test_delta_backward_rounds_once(B, NHK, NH, T, forget):
+    args, C0, dh, dC = inputs(B, NHK, NH, T, 64, 64, BF, 42, forget)
+    got = mlstm.delta_bwd(*args, dh, state=C0, dstate=dC, forget=forget)
+    ref = delta_ref(args, dh, C0, dC, forget)
+    for name, a, (b, _) in list(zip(NAMES, got, ref))[:3]:
+        rounded_once(name, a, b)
