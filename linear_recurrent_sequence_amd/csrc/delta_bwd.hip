@@ -177,13 +177,7 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
   const bool mine = col < dv;
   const int first_row = half * KS * 16;
   f32x4 Z[KS];
-#pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    const int row = first_row + acc_row(i, g);
-    Z[i] = f32x4{};
-    if (dC_in && mine && row < dk)
-      Z[i] = *reinterpret_cast<const f32x4*>(dC_in + (head * dv + col) * dk + row);
-  }
+  load_memory<KS>(dC_in ? dC_in + head * dv * dk : nullptr, first_row, col, mine, dk, g, Z);
   // K Z of all tokens to the first half's wave, of tokens 32-63 to the
   // second's; then each one's dR to the other
   f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;

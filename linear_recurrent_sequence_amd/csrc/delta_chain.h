@@ -89,6 +89,28 @@ struct Values {
 // memory row from the half's first on.
 __device__ inline int acc_row(int i, int g) { return (i >> 1) * 32 + 8 * g + 4 * (i & 1); }
 
+// A wave's slice of a memory x [dv][dk] (NULL: zeros): rows first_row .. of value
+// column col, zeros beyond dk and where not `mine`.  Every lane loads, from the
+// first row where it has none: around a branch the compiler may spill a register of
+// all lanes while some are off (seen with 168 registers in use: the lane's number,
+// stored before the branch's lanes are on again).
+template <int KS>
+__device__ inline void load_memory(const float* x, int first_row, int col, bool mine, int dk,
+                                   int g, f32x4 (&S)[KS]) {
+#pragma unroll
+  for (int i = 0; i < KS; ++i) S[i] = f32x4{};
+  if (!x) return;
+  x += int64_t(mine ? col : 0) * dk;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const int row = first_row + acc_row(i, g);
+    const bool on = mine && row < dk;
+    const f32x4 s = *reinterpret_cast<const f32x4*>(x + (row < dk ? row : 0));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[i][r] = on ? s[r] : 0.0f;
+  }
+}
+
 // Two tiles (32 rows from `row` on) of a wave's slice of the memory, one value
 // column per lane, to x [dk][dv], and 4 tokens of a value column per lane to x
 // [T][dv]: transposed over quads of lanes, so that a lane stores 16 bytes and 16

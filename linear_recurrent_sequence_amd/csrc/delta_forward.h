@@ -164,21 +164,17 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
   const int col = (block * kWaves + tile) * 16 + m;  // value column
   const bool mine = col < columns;  // whole waves; the others keep the barriers company
   const int first_row = half * KS * 16;
-  const float* const from =
-      kMap || kAgain || segment == 0 ? C_in : seg.before(head, segment, dk, dv);
+  const float* from = kMap || kAgain || segment == 0 ? C_in : seg.before(head, segment, dk, dv);
+  if (kMap && segment != 0) from = nullptr;
+  if (from && segment == 0) from += head * dv * dk;
   f32x4 S[KS];
+  load_memory<KS>(from, first_row, col, col < dv, dk, g, S);
+  if (kMap)
 #pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    const int row = first_row + acc_row(i, g);
-    S[i] = f32x4{};
-    if (kMap && col >= dv) {
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = row + r == col - dv ? 1.0f : 0.0f;
-    } else if (from && mine && row < dk && (!kMap || segment == 0)) {
-      S[i] = *reinterpret_cast<const f32x4*>(
-          from + (int64_t(segment == 0 ? head : 0) * dv + col) * dk + row);
-    }
-  }
+      for (int r = 0; r < 4; ++r)
+        S[i][r] = first_row + acc_row(i, g) + r == col - dv ? 1.0f : S[i][r];
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
   // the second's: V - e^G K S of all, Q S of tokens 32-63 (six).  What a wave has read
   // it overwrites with planes of its U, for the other one.
