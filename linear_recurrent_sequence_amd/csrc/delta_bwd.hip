@@ -11,19 +11,21 @@
 //   dq^ = e^G dh S^T + B K
 //   dk  = e^(G_C - G) U Z^T + B^T Q^ - e^G dR S^T - (N + N^T) K
 //   dbeta_j = X_j . dU_j - sum_i D_ij (dR_i . X_j) (k_i . k_j)
-//   dG_j = e^(G_j) dh_j . (S^T q^_j) + sum_(i<j) P_ji (dh_j . U_i) - sum_(i>j) P_ij (dh_i . U_j)
-//          - dR_j . (V_j - X_j) + sum_(i>j) N_ij (k_i . k_j) - e^(G_C - G_j) U_j . (Z^T k_j)
-//   dG_C += sum_j e^(G_C - G_j) U_j . (Z^T k_j) + e^(G_C) <S, Z>
+//   dlog f_t = sum_(i>=t) (e^(G_i) dh_i . (S^T q^_i) - dR_i . Y_i)
+//              + sum_(j<t) e^(G_C - G_j) U_j . (Z^T k_j) + e^(G_C) <S, Z>
+//              + sum_(i>=t>j) (P_ij (dh_i . U_j) - N_ij (k_i . k_j)),   Y_i = e^(G_i) S^T k_i:
 //
-// (V_j - X_j is what the memory predicted for token j), and dlog f is the sum
-// of dG from its token to the chunk's end, so no sum is longer than a chunk.
+// what passes from before token t to behind it, and so has f_t as a factor in
+// every term.  (As the sum of dL/dG from t to the chunk's end it would be a
+// difference of terms without f_t, and noise where f_t is small.)  No sum is longer
+// than a chunk.
 //
 // Six passes: the terms that all columns share (delta_prep.hip), the memory
-// forward once more (delta_forward.h; its start and X of every chunk are kept,
+// forward once more (delta_forward.h; its start, X and Y of every chunk are kept,
 // float32), the gradient of the memory backward (Z and dR kept), and, over all
 // chunks at once, the pairs of tokens, the gradients of q and k, and those of beta
 // and the gates.  The two chains need each other only for sums of X with Z^T k
-// and run in one launch where the card holds both (side_by_side).  Everything that
+// and of dR with Y, and run in one launch where the card holds both (side_by_side).  Everything that
 // the gradients come from has float32 accuracy (three bf16 planes to an operand that
 // is no bf16 input); for bf16 inputs dq, dk and dv are rounded once, at the end.
 //
@@ -42,7 +44,7 @@ namespace {
 
 // The stages of a chunk: P^T, K by blocks for both halves of the memory's rows,
 // (I + At)^-T, then Q^T and K^T by row tiles.
-// kApart: without X (and V), as it has to be beside the memory's pass.
+// kApart: without X and Y, as it has to be beside the memory's pass.
 template <typename T, int KS, bool kApart>
 struct BackStages {
   static constexpr bool kBf16 = sizeof(T) == 2;
@@ -52,7 +54,7 @@ struct BackStages {
   static constexpr int nK = (KS / 2 + kT - 1) / kT, nT = (KS + kI - 1) / kI;
   static constexpr int kInv = 1 + nK, kQueryT = kInv + 1, kKeyT = kQueryT + nT, n = kKeyT + nT;
   static constexpr int kSlot = (kBf16 ? 20 : 24) * kFrag;
-  // X and V come through LDS, with the inverse (a wave that stores and then loads
+  // X and Y come through LDS, with the inverse (a wave that stores and then loads
   // waits for its stores); one buffer each, so less than a chunk ahead
   static constexpr bool kStaged = !kApart;
   static_assert(kApart || kBf16, "float32: LDS is full");
@@ -62,8 +64,8 @@ struct BackStages {
   static constexpr int kPart = 6 * kFrag;  // a value tile's sums between its two waves
   static constexpr int kValueAt = kSlots * kSlot, kDecayAt = kValueAt + 2 * Values<T>::kBytes,
                        kPartAt = kDecayAt + 2 * kFrag, kXAt = kPartAt + kWaves * kPart,
-                       kVAt = kXAt + (kStaged ? Values<float>::kBytes : 0),
-                       kShared = kVAt + (kStaged ? Values<T>::kBytes : 0);
+                       kYAt = kXAt + (kStaged ? Values<float>::kBytes : 0),
+                       kShared = kYAt + (kStaged ? Values<float>::kBytes : 0);
 
   static constexpr int blocks_of(int s) {  // of K, for each half
     return KS / 2 - (s - 1) * kT < kT ? KS / 2 - (s - 1) * kT : kT;
@@ -75,7 +77,7 @@ struct BackStages {
     if (s < kInv) return 2 * NPL * blocks_of(s);
     if (s == kInv)
       return Copier::square_copies(3) +
-             (kStaged ? Values<float>::kCopies + Values<T>::kCopies : 0);
+             (kStaged ? 2 * Values<float>::kCopies : 0);
     return tiles_of((s - kQueryT) % nT) * NPL;
   }
   static constexpr int in_flight(int s) {
@@ -86,7 +88,7 @@ struct BackStages {
 };
 
 // The memory's gradient backward: Z at each chunk's end, dR (and dV), and the
-// parts X . (e^(G_C - G) Z^T k) and dR . (V - X) that each 16 columns give (kApart:
+// parts X . (e^(G_C - G) Z^T k) and dR . Y that each 16 columns give (kApart:
 // e^(G_C - G) Z^T k itself, from which delta_pairs_kernel forms them).
 // Built as the forward is (delta_forward.h): the operands are upper triangular
 // here, so the first half's wave takes what the second's does there.
@@ -141,7 +143,8 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
           const int64_t from = (head * a.T_len + tok0) * dv;
           cp.values(static_cast<const float*>(a.sv.X), from, valid, dv, block * 16 * kWaves,
                     St::kXAt);
-          cp.values(a.v, from, valid, dv, block * 16 * kWaves, St::kVAt);
+          cp.values(static_cast<const float*>(a.sv.Y), from, valid, dv, block * 16 * kWaves,
+                    St::kYAt);
         }
         cp.template square<3, false>(a.ws.invT + at * 3 * kSquare, dst);
       } else {
@@ -219,8 +222,8 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
       add_square<3, false>(slot, lane, kHighSecond, h1, h1, dU[2], dU[3]);
       if (half == 0) add_square<3, true>(slot, lane, kHighFirst, h0, h1, dU[0], dU[1]);
     }
-    // this wave's tokens of X and V - X
-    f32x4 X[2] = {}, pred[2] = {};
+    // this wave's tokens of X and Y
+    f32x4 X[2] = {}, Y[2] = {};
     // K Z over this half's rows
     f32x4 kz[4] = {};
     static_for<St::nK>([&](auto stage) {
@@ -260,12 +263,10 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
 #pragma unroll
           for (int r = 0; r < 4; ++r) {  // zeros behind the end
             using F = Values<float>;
-            X[i][r] = *reinterpret_cast<const float*>(lds + St::kXAt + F::lane_at(g) +
-                                                      (tile * 16 + m) * 4 +
-                                                      half * F::acc_at(2, 0) + F::acc_at(i, r));
-            pred[i][r] = load_elem(reinterpret_cast<const T*>(
-                             lds + St::kVAt + V::lane_at(g) + (tile * 16 + m) * sizeof(T) +
-                             half * V::acc_at(2, 0) + V::acc_at(i, r))) - X[i][r];
+            const char* const x = lds + St::kXAt + F::lane_at(g) + (tile * 16 + m) * 4 +
+                                  half * F::acc_at(2, 0) + F::acc_at(i, r);
+            X[i][r] = *reinterpret_cast<const float*>(x);
+            Y[i][r] = *reinterpret_cast<const float*>(x + (St::kYAt - St::kXAt));
           }
       // e^(G_C - G) K Z, nothing behind the end
       auto whole = [&](int i, f32x4 other) {
@@ -312,7 +313,7 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (!kApart) write_part(2, i, own[i], pred[i]);
+        if (!kApart) write_part(2, i, own[i], Y[i]);
         const int tok = acc_row(2 * half + i, g);
 #pragma unroll
         for (int r = 0; r < 4; ++r)  // the other wave has read dh (before this stage's barrier)
@@ -370,8 +371,8 @@ __device__ inline void back_chain(const Chain<T>& a, const float* dC_in, T* dv_o
 }
 
 // The two chains: one after the other, or (kBoth) side by side, one in the first
-// half of the workgroups.  Float32's gradient never takes X: loads of X
-// and V behind its own stores took a third of its time.
+// half of the workgroups.  Float32's gradient never takes X: loads of values
+// behind its own stores took a third of its time.
 enum Chains { kMemory, kGradient, kBoth };
 
 template <typename T, int KS, Chains kWhich>
@@ -428,7 +429,7 @@ constexpr int kPitch = kC + 1;
 
 template <typename T>
 struct Grads {
-  const T *q, *k, *v, *dh;
+  const T *q, *k, *dh;
   const float* fgate;
   const float* dR;
   Work ws;
@@ -457,13 +458,13 @@ __device__ inline void write_planes(const float (*m)[kPitch], float by, __bf16* 
 }
 
 // The 64 x 64 matrices of a head's chunk: B, B^T / sqrt(dk) and -(N + N^T) in
-// planes for delta_grads_kernel, and what they give to dG and dbeta.  kApart: also
-// X . (e^(G_C - G) Z^T k) and dR . (V - X), for the one tile of Saved::part.
+// planes for delta_grads_kernel, and what they give to the gates and dbeta.
+// kApart: also X . (e^(G_C - G) Z^T k) and dR . Y, for the one tile of Saved::part.
 template <typename T, bool kApart>
 __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a) {
   constexpr int NPL = sizeof(T) == 2 ? 1 : 3;
   __shared__ double G[kC];
-  __shared__ float bt[kC], row_g[kC], col_g[kWaves][kC], col_b[kWaves][kC];
+  __shared__ float bt[kC], col_g[kWaves][kC], col_b[kWaves][kC];
   __shared__ float mat[kC][kPitch];
   const int chunk = blockIdx.x % a.chunks;
   const int64_t head = blockIdx.x / a.chunks, at = blockIdx.x;
@@ -482,16 +483,16 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
   const bool r_on = 16 * w + m < valid;
   // the next 32 columns are on their way while these are worked on
   {
-    typename Eight<T>::type h, v;
-    f32x8 r, x[4], z;
-    float xz = 0.0f, rv = 0.0f;
+    typename Eight<T>::type h;
+    f32x8 r, x[4], y, z;
+    float xz = 0.0f, ry = 0.0f;
     auto load = [&](int s) {
       const int c = s + g * 8;
       const bool c_on = c < a.dv;
       h = load8(a.dh, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
       r = load8(a.dR, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
       if (kApart) {
-        v = load8(a.v, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
+        y = load8(a.sv.Y, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
         z = load8(a.sv.KZ, (row0 + 16 * w + m) * a.dv + c, c_on && r_on);
       }
 #pragma unroll
@@ -511,7 +512,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           xz += own[e] * z[e];
-          rv += r[e] * (float(v[e]) - own[e]);
+          ry += r[e] * y[e];
         }
       }
       load(s + 32);  // nothing behind the last column
@@ -527,12 +528,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
 #pragma unroll
       for (int o = 16; o < 64; o <<= 1) {
         xz += __shfl_xor(xz, o, 64);
-        rv += __shfl_xor(rv, o, 64);
+        ry += __shfl_xor(ry, o, 64);
       }
       float* const part = a.sv.part + at * a.tiles * 3 * kC + 16 * w + m;
       if (g == 0) {
         part[kC] = xz;
-        part[2 * kC] = rv;
+        part[2 * kC] = ry;
       }
     }
   }
@@ -568,7 +569,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
     }
   }
   __syncthreads();
-  f32x4 rows = {};
+  // To the gate of token t: the pairs (i, j) with j < t <= i.  A row's sums from its
+  // first column on (16 lanes by DPP, `before` from the tiles before), added up
+  // over the rows behind the column, are column t - 1's.
+  f32x4 before = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float cg = 0.0f, cb = 0.0f;
@@ -578,15 +582,17 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
       const float d = c <= row ? exp2_once(G[row] - G[c]) : 0.0f, b = bt[c];
       const float p = d * qk[j][r] * a.scale;
       mat[row][c] = c <= row ? d * b * hx[j][r] : 0.0f;
-      float n = 0.0f;
+      float n = 0.0f, e = 0.0f;
       if (c <= row) cb += p * hx[j][r];
       if (c < row) {
         n = d * b * rx[j][r];
         cb -= d * rx[j][r] * kk[j][r];
-        rows[r] += p * b * hx[j][r];
-        cg += n * kk[j][r] - p * b * hx[j][r];
+        e = p * b * hx[j][r] - n * kk[j][r];
       }
       rx[j][r] = n;
+      const float up_to = before[r] + row_prefix(e);
+      if (c < row) cg += up_to;
+      before[r] += row_sum(e);
     }
     cg += __shfl_xor(cg, 16, 64);
     cg += __shfl_xor(cg, 32, 64);
@@ -597,17 +603,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_pairs_kernel(Grads<T> a
       col_b[w][16 * j + m] = cb;
     }
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float s = row_sum(rows[r]);
-    if (m == 0) row_g[16 * w + 4 * g + r] = s;
-  }
   __syncthreads();
   __bf16* const out = a.sv.pairs + at * 9 * kSquare;
   write_planes<false>(mat, 1.0f, out);
   write_planes<true>(mat, a.scale, out + 3 * kSquare);
   if (w == 0) {
-    float cg = row_g[lane], cb = 0.0f;
+    float cg = 0.0f, cb = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
       cg += col_g[i][lane];
@@ -802,20 +803,18 @@ __global__ __launch_bounds__(64) void delta_gates_kernel(Grads<T> a) {
     }
   }
   const float* decay = a.ws.decay + at * 3 * kC;
-  const double s3 = double(decay[2 * kC + lane]) * t3;
-  double dg = double(t1) + a.sv.gates[at * 2 * kC + lane] - t2 - s3;
-  // to the chunk's end: the tokens' writes and what the memory keeps
-  double all = s3, kept = 0.0;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o, 64);
-  for (int i = 0; i < a.groups; ++i) kept += a.sv.inner[at * a.groups + i];
-  if (lane == 63) dg += all + double(decay[kC - 1]) * kept;
-  // sums from each token to the end
+  // reads of the memory from each token to the end, writes to it up to each token
+  double reads = double(t1) - t2, writes = double(decay[2 * kC + lane]) * t3, kept = 0.0;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const double right = __shfl_down(dg, o, 64);
-    if (lane + o < 64) dg += right;
+    const double right = __shfl_down(reads, o, 64), left = __shfl_up(writes, o, 64);
+    if (lane + o < 64) reads += right;
+    if (lane >= o) writes += left;
   }
+  for (int i = 0; i < a.groups; ++i) kept += a.sv.inner[at * a.groups + i];
+  const double pairs = a.sv.gates[at * 2 * kC + (lane > 0 ? lane - 1 : 0)];
+  writes = __shfl_up(writes, 1, 64);  // of the tokens before
+  const double dg = reads + (lane > 0 ? writes + pairs : 0.0) + double(decay[kC - 1]) * kept;
   if (lane < valid) {
     const float x = a.fgate[row0 + lane];
     // d log sigma(x) = sigma(-x), from e^-|x|
@@ -862,7 +861,7 @@ hipError_t backward(const DeltaShape& s, const DeltaGrads& d, const Layout& l, c
   if (e != hipSuccess) return e;
   const float* dR = sizeof(T) == 2 ? l.sv.dR : static_cast<const float*>(d.dv);
   const int groups = int((s.dk + 127) / 128);
-  const Grads<T> b = {a.q, a.k, a.v, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
+  const Grads<T> b = {a.q, a.k, a.dh, fgate, dR, l.ws, l.sv, static_cast<T*>(d.dq),
                       static_cast<T*>(d.dk), d.dbeta, d.dfgate, s.T, a.chunks, a.NH, a.NHK, a.dk,
                       a.dv, l.ks, a.tiles, groups, int(s.exp_forget), a.scale};
   const unsigned each = unsigned(a.H * a.chunks);

@@ -204,6 +204,19 @@ __device__ inline float row_sum(float x) {
   return x;
 }
 
+// sum over the lanes of a row up to this one
+__device__ inline float row_prefix(float x) {
+  auto dpp = [](float v, auto ctrl) {  // from the lane 1, 2, 4 or 8 before, 0 if there is none
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x += dpp(x, std::integral_constant<int, 0x111>{});
+  x += dpp(x, std::integral_constant<int, 0x112>{});
+  x += dpp(x, std::integral_constant<int, 0x114>{});
+  x += dpp(x, std::integral_constant<int, 0x118>{});
+  return x;
+}
+
 // The products of planes i + j < kMost, small ones first, as one list: f(i, j)
 // for each, so that a caller can run one product over independent accumulators
 // before the next one (a dependent matrix instruction waits for the last).
@@ -253,11 +266,12 @@ struct Saved {
   float* S;     // [H][chunks][dk][dv] memory at each chunk's start
   float* Z;     // [H][chunks][dk][dv] its gradient at each chunk's end
   float* X;     // [H][T][dv]
+  float* Y;     // [H][T][dv] e^G S^T k, what the memory at the chunk's start predicts
   float* dR;    // [H][T][dv] (bf16 inputs: dV is rounded)
   float* KZ;    // [H][T][dv] e^(G_C - G) Z^T k (Layout::apart)
   float* part;  // [H][chunks][dv / 16][3][64] parts of the gates' gradients
   __bf16* pairs;  // [H][chunks][3][3] planes of B, B^T / sqrt(dk), -(N + N^T)
-  float* gates;   // [H][chunks][2][64] what the pairs of tokens give to dG, dbeta
+  float* gates;   // [H][chunks][2][64] what the pairs of tokens give to the gates, dbeta
   float* inner;   // [H][chunks][blocks of 128 dk] parts of <S, Z>
 };
 

@@ -176,8 +176,8 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
       for (int r = 0; r < 4; ++r)
         S[i][r] = first_row + acc_row(i, g) + r == col - dv ? 1.0f : S[i][r];
   // to the first half's wave: K S and Q S of tokens 0-31 (four fragments); to
-  // the second's: V - e^G K S of all, Q S of tokens 32-63 (six).  What a wave has read
-  // it overwrites with planes of its U, for the other one.
+  // the second's: V - e^G K S (kAgain: K S) of all, Q S of tokens 32-63 (six).  What a
+  // wave has read it overwrites with planes of its U, for the other one.
   f32x4* const to_first = reinterpret_cast<f32x4*>(lds + St::kPartAt + tile * St::kPart) + lane;
   f32x4* const to_second = to_first + St::kToFirst * 64;
 
@@ -256,6 +256,10 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
     if (half == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if constexpr (kAgain) {  // the memory's prediction by itself, see Y
+          to_second[i * 64] = ks[i];
+          continue;
+        }
         const f32x4 e = at_tile(0, i);
 #pragma unroll
         for (int r = 0; r < 4; ++r) R[i][r] = load_elem(value_of(i, r)) - e[r] * ks[i][r];
@@ -269,8 +273,17 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
       to_first[2 * 64] = qs[0];
       to_first[3 * 64] = qs[1];
     }
+    f32x4 Y[2];  // kAgain: e^G K S of this wave's tokens
     auto whole = [&](int i, f32x4 part, f32x4 ks) {
-      f32x4 x = part - at_tile(0, i) * ks;
+      f32x4 x;
+      if constexpr (kAgain) {
+        const f32x4 y = at_tile(0, i) * (part + ks);
+        if ((i >> 1) == half) Y[i & 1] = y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = load_elem(value_of(i, r)) - y[r];
+      } else {
+        x = part - at_tile(0, i) * ks;
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r)  // behind the end: nothing, whatever the memory holds
         x[r] = acc_row(i, g) + r < valid ? x[r] : 0.0f;
@@ -282,7 +295,8 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
     {
       const char* slot = enter();
       if (half == 0) {
-        const f32x4 r0 = whole(0, R[0], to_first[0]), r1 = whole(1, R[1], to_first[64]);
+        const f32x4 r0 = whole(0, kAgain ? ks[0] : R[0], to_first[0]),
+                    r1 = whole(1, kAgain ? ks[1] : R[1], to_first[64]);
         hs[0] = qs[0] + to_first[2 * 64];
         hs[1] = qs[1] + to_first[3 * 64];
         const Planes<3> b = split<3>(pair(r0, r1));
@@ -312,11 +326,14 @@ __device__ inline void forward_chain(const Chain<T>& a, const Segments& seg, con
 #pragma unroll
       for (int n = 0; n < 3; ++n) out[(3 + n) * 64] = for_h.p[n];
     if constexpr (kAgain) {
-      // X, and e^G dh . (S^T q^) summed over the tile's columns
+      // X, Y, and e^G dh . (S^T q^) summed over the tile's columns
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = acc_row(2 * half + i, g);
-        if (mine) store_tokens(a.sv.X + rows, x[i], tok, valid, dv, col, lane);
+        if (mine) {
+          store_tokens(a.sv.X + rows, x[i], tok, valid, dv, col, lane);
+          store_tokens(a.sv.Y + rows, Y[i], tok, valid, dv, col, lane);
+        }
         f32x4 s;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {

@@ -128,6 +128,7 @@ inline Layout layout(const DeltaShape& s, bool backward, void* base) {
     l.sv.S = floats(H * state);
     l.sv.Z = floats(H * state);
     l.sv.X = floats(rows * size_t(s.NH * s.dv));
+    l.sv.Y = floats(rows * size_t(s.NH * s.dv));
     if (s.is_bf16) l.sv.dR = floats(rows * size_t(s.NH * s.dv));
     l.apart = side_by_side(s) || !s.is_bf16;
     if (l.apart) l.sv.KZ = floats(rows * size_t(s.NH * s.dv));

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from linear_recurrent_sequence_amd import mlstm
-from test_cells_gpu import BF, DEV, NAMES, delta_ref, host, inputs, oracle_of
+from test_cells_gpu import BF, DEV, FP, NAMES, delta_ref, host, inputs, oracle_of
 
 pytestmark = pytest.mark.gpu
 ONE_ROUNDING = 2 ** -13.5
@@ -43,3 +43,21 @@ def test_delta_backward_rounds_once(B, NHK, NH, T, forget):
     ref = delta_ref(args, dh, C0, dC, forget)
     for name, a, (b, _) in list(zip(NAMES, got, ref))[:3]:
         rounded_once(name, a, b)
+
+
+@pytest.mark.parametrize("B,H,T,d,dtype", [(1, 2, 150, 64, BF), (1, 2, 150, 64, FP),
+                                           (2, 66, 70, 32, BF), (2, 66, 70, 32, FP)])
+@pytest.mark.parametrize("forget,fmean", [("sigmoid", 0.0), ("sigmoid", -6.0), ("exp", -3.0),
+                                          ("exp", -16.0)])
+def test_delta_gate_gradients_where_little_is_kept(B, H, T, d, dtype, forget, fmean):
+    """dL/df~_t has f_t as a factor in every term, however small: each one is held
+    to the size of its own terms.  (A float32 sum of 64 x 64 terms is within 64 2^-24
+    = 2^-18 of that, two such products follow one another, and the largest of
+    some thousands of errors is within eight times their size: 2^-14.)  Where f =
+    0 it is 0.  (2 x 66 heads run the backward's chains one after the other.)"""
+    args, C0, dh, dC = inputs(B, 1, H, T, d, 64, dtype, 43, forget, fmean=fmean)
+    args[4][:, :, 40] = args[4][:, :, 64] = -np.inf
+    got = mlstm.delta_bwd(*args, dh, state=C0, dstate=dC, forget=forget)[4]
+    ref, size = delta_ref(args, dh, C0, dC, forget)[4]
+    assert (np.abs(host(got) - ref) <= 2 ** -14 * size).all()
+    assert not got[:, :, 40].any() and not got[:, :, 64].any()
