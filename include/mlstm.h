@@ -374,8 +374,9 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
  * beta |k|^2 <= 2 (unit keys and strengths in (0, 1), as a rule).  A position
  * with beta = 0 and f = 1 (f~ = +infinity, or 0 with MLSTM_FORGET_EXP) leaves
  * the memory as it is, which is how a batch is padded.  f~ = -infinity forgets
- * everything.  Inputs are otherwise finite: NaN and infinities propagate, and
- * may reach other positions of the same 64.
+ * everything.  f > 1 (MLSTM_FORGET_EXP) is taken as long as the products of up to
+ * 64 neighbouring f are float32 numbers.  Inputs are otherwise finite: NaN and
+ * infinities propagate, and may reach other positions of the same 64.
  *
  * All sums, the memory and the products that feed it are float32 (bf16
  * operands are exact; float32 operands of a matrix product are split into
