@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from linear_recurrent_sequence_amd import mlstm
-from test_cells_gpu import (BF, DEV, FP, NAMES, close, delta_ref, host, inputs,
+from test_cells_gpu import (BF, DEV, FP, NAMES, close, delta_ref, host, host_kw, inputs,
                             norm_inputs, oracle_of)
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +125,65 @@ def test_results_do_not_depend_on_what_the_workspaces_hold(dtype):
     finally:
         torch.use_deterministic_algorithms(before)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ----------------------------------------------------------------- block norm
+
+# every workgroup takes three rows and more, with the rows over several waves (or
+# several rows to a workgroup, or both), and not all of them in the last turn
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("NH,d,rows,norm,activation", [
+    (4, 384, 5003, "layer", "sigmoid"), (2, 264, 8003, "layer", "silu"),
+    (15, 520, 801, "layer", "sigmoid"), (1, 8192, 801, "layer", "sigmoid"),
+    (31, 264, 801, "rms", "silu"), (7, 1032, 801, "layer", "silu"), (9, 768, 803, "rms", "sigmoid"),
+    (3, 2056, 801, "layer", "sigmoid"), (1, 4096, 803, "rms", "sigmoid"),
+    (20, 384, 803, "layer", "silu"), (3, 128, 7001, "layer", "sigmoid")])
+def test_block_norm_of_many_rows(NH, d, rows, norm, activation, dtype):
+    p, w, kw, dr, dy = norm_inputs(1, NH, rows, d, dtype, norm, activation, 1, 1, 1, 1, 60)
+    r, y = mlstm.block_norm_fwd(p, w, **kw)
+    rr, yr = oracle.block_norm(host(p), host(w), **host_kw(kw))
+    close("r", r, rr)
+    close("y", y, yr)
+    got = mlstm.block_norm_bwd(p, w, dr, dy, **kw)
+    ref = oracle.block_norm(host(p), host(w), **host_kw(kw), dr=host(dr), dy=host(dy), grads=True)
+    assert set(got) == set(ref)
+    for name in ref:
+        close(name, got[name], ref[name])
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_block_norm_gradients_of_extreme_rows(norm, dtype):
+    """Rows without spread: n1 = 0 exactly and 1 / sqrt(eps) before the gradient.
+    Rows far from zero (m = 1000 and 500, spread 1): their mean adds up 64 (128)
+    values with at most 12 roundings on the way, so with the layer norm n is off by
+    c = 12 * 2^-24 m inv, the same in all of a row (a - mean is exact), and the gradient
+    inv (g - n mean(g n) - mean(g)) by inv c (|mean(g n)| + |n mean(g)|) <= 5 c times
+    its size, |n| <= 4 here.  The weights' gradients sum eight rows of it."""
+    p, w, kw, dr, dy = norm_inputs(1, 2, 8, 64, dtype, norm, "silu", 1, 1, 1, 1, 61)
+    p[0, :, 0] = 0.0
+    p[0, :, 1] = 3.0
+    p[0, :, 2] += 1000.0
+    kw["residual"][0, 6] += 500.0
+    got = mlstm.block_norm_bwd(p, w, dr, dy, **kw)
+    ref = oracle.block_norm(host(p), host(w), **host_kw(kw), dr=host(dr), dy=host(dy), grads=True)
+
+    def far(name, a, b, m):
+        a, rms = host(a), np.sqrt((b ** 2).mean())
+        rounding = 2 ** -8 * np.abs(b) if got[name].dtype == BF else 0.0
+        assert (np.abs(a - b) <= rounding + 5 * 12 * 2 ** -24 * m * rms).all(), name
+
+    for t in range(8):
+        for name in ("dp", "dgate", "dresidual"):
+            a, b = ((x[:, t] if name == "dresidual" else x[:, :, t]) for x in (got[name], ref[name]))
+            if t < 2 and name == "dgate" and not np.abs(b).any():
+                assert not a.any()  # n1 = 0
+            elif norm == "layer" and t in (2, 6):
+                far(name, a, b, 1000.0 if t == 2 else 500.0)
+            else:
+                close(name, a, b)
+    for name in ("dweight", "dscale", "dnext_weight"):
+        if norm == "layer":
+            far(name, got[name], ref[name], 1000.0)
+        else:
+            close(name, got[name], ref[name])
