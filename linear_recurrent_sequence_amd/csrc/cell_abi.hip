@@ -11,12 +11,10 @@ namespace {
 using mlstm::BlockNorm;
 using mlstm::BlockNormGrads;
 using mlstm::DeltaShape;
-using mlstm::abi::aligned16;
 using mlstm::abi::check_alias;
 using mlstm::abi::check_aligned;
 using mlstm::abi::check_given;
 using mlstm::abi::hip_status;
-using mlstm::abi::overlaps;
 
 constexpr int64_t kMaxT = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 46;
