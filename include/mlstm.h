@@ -370,19 +370,20 @@ int mlstm_recurrent_step(const void* q, const void* k, const void* v,
  *   dv       a multiple of 16 in [16, 1024];  T >= 1;  fewer than 2^18 heads
  *            B NH, and 2^22 chunks B NH ceil(T / 64) (one token: fewer than 2^24
  *            value columns in sixteens, B NH dv / 16)
- * k is not normalized here.  The recurrence is stable for
- * beta |k|^2 <= 2 (unit keys and strengths in (0, 1), as a rule).  A position
- * with beta = 0 and f = 1 (f~ = +infinity, or 0 with MLSTM_FORGET_EXP) leaves
- * the memory as it is, which is how a batch is padded.  f~ = -infinity forgets
- * everything.  f > 1 (MLSTM_FORGET_EXP) is taken as long as the products of up to
- * 64 neighbouring f are float32 numbers.  Inputs are otherwise finite: NaN and
- * infinities propagate, and may reach other positions of the same 64.
+ * k is not normalized here.  The recurrence is stable for beta |k|^2 <= 2 (unit
+ * keys and strengths in (0, 1), as a rule); near 2 and with keys that are all
+ * alike the terms of a chunk cancel, and results keep 14 to 15 bits of float32's
+ * 24.  A position with beta = 0 and f = 1 (f~ = +infinity, or 0 with
+ * MLSTM_FORGET_EXP) leaves the memory as it is, which is how a batch is padded.
+ * f~ = -infinity forgets everything.  f > 1 (MLSTM_FORGET_EXP) is taken as long as
+ * the products of up to 64 neighbouring f are float32 numbers.  Inputs are
+ * otherwise finite: NaN and infinities propagate, and may reach other positions of
+ * the same 64.
  *
  * All sums, the memory and the products that feed it are float32 (bf16
  * operands are exact; float32 operands of a matrix product are split into
- * three bf16 planes), gate sums are float64; for MLSTM_BF16 h is rounded once, to
- * nearest even.
- * Results are bitwise reproducible (no atomics, fixed order).
+ * three bf16 planes), gate sums are float64; for MLSTM_BF16 h, dq, dk and dv are
+ * rounded once, to nearest even.  Results are bitwise reproducible (no atomics, fixed order).
  */
 
 /*

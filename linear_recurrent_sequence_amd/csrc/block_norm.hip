@@ -35,7 +35,12 @@
 // 4 x 384 67 us, 51 us being a copy's time for the same bytes; 4 x 2048 rows of
 // 8 x 512 95 us (67); backward there 176 us and 6 us for the weights' sums (108).
 // What is left is the vector work of a row beside its loads: about 280
-// instructions per 8 channels forward and 600 backward.  The next row is loaded
+// instructions per 8 channels forward and 600 backward (bf16 spills 16 registers
+// there, 60 bytes a lane).  Rows of more vectors of 8 channels than eight waves have
+// lanes take two or four of them a lane, and with four the backward spills 137 to 231
+// registers: 4 x 2048 rows of 20 x 384 in bf16 take 244 us forward and 1177 us
+// backward (a copy of the same bytes 126 and 202), of 1 x 4096, two vectors, 78 and
+// 169 (67 and 108).  The next row is loaded
 // while one is worked on (two rows ahead gain nothing); with divisions by T per
 // row, sums through LDS shuffles and the precise exponential the same took 96 us
 // and 324 us.
@@ -448,7 +453,7 @@ __global__ __launch_bounds__(
 #pragma unroll
     for (int e = 0; e < kVec; ++e) da[c][e] = dw2[c][e] = 0.0f;
   // w1, s and w2 (`what` 0 - 2) of a lane's channels: with one vector per lane
-  // from LDS, written and read by the same lane (12 KiB a wave); with more they
+  // from LDS, written and read by the same lane (6 KiB a wave); with more they
   // would not fit, and come from the cache
   constexpr bool kHeld = NC == 1;
   extern __shared__ __attribute__((aligned(16))) float weights[];

@@ -25,17 +25,21 @@
 // float32), the gradient of the memory backward (Z and dR kept), and, over all
 // chunks at once, the pairs of tokens, the gradients of q and k, and those of beta
 // and the gates.  The two chains need each other only for sums of X with Z^T k
-// and of dR with Y, and run in one launch where the card holds both (side_by_side).  Everything that
-// the gradients come from has float32 accuracy (three bf16 planes to an operand that
-// is no bf16 input); for bf16 inputs dq, dk and dv are rounded once, at the end.
+// and of dR with Y, and run in one launch where the card holds both (side_by_side).
+// Everything that the gradients come from has float32 accuracy (three bf16 planes to
+// an operand that is no bf16 input); for bf16 inputs dq, dk and dv are rounded once,
+// at the end.
 //
 // What bounds it: the memories, 8 dk dv bytes per head and chunk, written by the
 // chains and read once by the key gradients.  On 8 x 4 heads of 384 x 2048 in
-// bf16: chunk terms 85 us, the chains 440 and 465, pairs 120, key gradients 420,
-// gates 9; the 1.2 GB of memories alone are 240 us each way at a copy's rate.
+// bf16: chunk terms 83 us, the chains 459 and 429, pairs 116, key gradients 436,
+// gates 8; the 1.2 GB of memories alone are 240 us each way at a copy's rate.
 // Stored all at once at a chunk's start the memories stood 7 us in the way of each
 // chunk; and a chain's wave that loads from memory waits for its own stores first,
-// so V, X and dh come through LDS (bf16), which took the chains from 630 to 460 us.
+// so V, X, Y and dh come through LDS (bf16), which took the chains from 630 to 460
+// us.  A chain's waves hold the memory in registers, and spill up to 20 of them for dk
+// of 257 to 384 and up to 62 above; in float32 (more planes on the way) up to 24
+// from dk = 65 on, 64 above 256 and 170 above 384.
 #include "delta_forward.h"
 
 namespace mlstm {

@@ -18,16 +18,17 @@
 // h another neighbour than the rounded float32 value's now and then (1.5e-4 in the
 // 2-norm, 7e-6 as it is): not done.
 //
-// What bounds it: the chain.  A chunk of 128 wide heads takes a workgroup 4.5 us
-// (about 8700 cycles) whatever runs beside it; of these a SIMD's vector unit is
-// busy 47 %, its matrix unit 33 %, the CU's LDS 32 %, and the five barriers and
+// What bounds it: the chain.  A chunk of 128 wide heads takes a workgroup 5.0 us
+// (about 9400 cycles) whatever runs beside it; of these a SIMD's vector unit is
+// busy 47 %, its matrix unit 37 %, the CU's LDS 31 %, and the five barriers and
 // the chain's own latencies are the rest.  8 x 16 heads of 128 x 2048 in bf16:
-// 145 us for this kernel and 88 us for delta_prep.hip, 58 us being what a copy of
-// the inputs and outputs takes.  Measured on the way there: one wave to a value
-// tile that loads its operands from memory 750 us; through an LDS ring 195 us;
-// with copying waves of its own 138 us, and no less with two waves to a tile, which
-// take 317 -> 248 us on 8 x 4 heads of 384 x 2048, where one wave's registers
-// spilled.  Slots enough for a whole chunk ahead change nothing there (197 us with
+// 161 us for this kernel and 88 us for delta_prep.hip, 58 us being what a copy of
+// the inputs and outputs takes.  Measured on the way there (with 16 bits to the
+// operands of h, 145 us at the end): one wave to a value tile that loads its
+// operands from memory 750 us; through an LDS ring 195 us; with copying waves of its
+// own 138 us.  Two waves to a tile are 5 % slower than that there, and take 317 -> 248
+// us on 8 x 4 heads of 384 x 2048, where one wave's registers spilled (above dk = 384
+// two waves' do, 8 to 32 of them).  Slots enough for a whole chunk ahead change nothing there (197 us with
 // 7, 195 with 3, before the copying waves).
 #include "delta_forward.h"
 

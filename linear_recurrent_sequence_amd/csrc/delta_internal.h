@@ -36,12 +36,16 @@ struct Segments {
 // How many segments.  The chains of a sequence's chunks run one workgroup to a
 // CU, so where heads times value columns leave CUs idle, a longer sequence is cut
 // and each segment's effect on a memory taken first: (dv + dk) / dv times the
-// work, but segments side by side.  In units of a chunk's time (4.5 us at dk =
-// 128), from the rounds of workgroups that each pass takes, 0.8 for a chunk of the
+// work, but segments side by side.  In units of a chunk's time (5.9 us at dk =
+// 256), from the rounds of workgroups that each pass takes, 0.8 for a chunk of the
 // map pass, three for joining a segment at dk = 256 and four for the launches; taken
-// if a fifth is won.  8 heads of 256 x 16384 in bf16: the chains 1334 us in one
-// piece; in eight segments 297 us for the map pass, 47 to join and 205 for the
-// forward.
+// if a fifth is won.  Whole calls in one piece and cut, bf16: 8 heads of 256 x 16384
+// 1392 and 560 us (chunk terms 84; in eight segments 244 for the map pass, 41 to join,
+// 188 for the forward), 8 of 128 x 8192 504 and 167, 2 x 4 of 384 x 8192 886 and 615,
+// 4 of 64 x 1024 68 and 48; float32, 4 of 128 x 8192 705 and 167.  The charges are
+// above what that first call shows (0.65 for a chunk of the map pass, 1.2 for a
+// join), so some long sequences of few wide heads stay in one piece that might gain
+// by a cut: 4 heads of 512 x 8192, 1042 us, and of 384 x 4096, 443.
 inline Segments segments_of(const DeltaShape& s) {
   const int64_t chunks = (s.T + kC - 1) / kC, H = s.B * s.NH;
   auto rounds = [&](int64_t wgs) { return (wgs + kCUs - 1) / kCUs; };
@@ -67,12 +71,12 @@ inline Segments segments_of(const DeltaShape& s) {
 // in one launch (delta_pairs_kernel then forms what needs both): where that
 // saves a tenth of the rounds of workgroups: up to 128 of them, and some numbers
 // above.  The whole backward pass, one after the other and side by side: 4 x 4
-// heads of 384 x 2048 (96 workgroups) in bf16 1049 and 786 us, 12 x 4 of 384 x
-// 1024 (288) 1319 and 1182, 2 x 16 of 128 x 2048 (64) in float32 982 and 627.
+// heads of 384 x 2048 (96 workgroups) in bf16 1051 and 821 us, 12 x 4 of 384 x
+// 1024 (288) 1314 and 1209, 2 x 16 of 128 x 2048 (64) in float32 802 and 605.
 // With as many rounds either way bf16's run one after the other, where the second
-// has the sums with X at hand (8 x 4 of 384 x 2048 1431 us, 1497 with the sums left
-// to the pairs; float32, whose second chain gains by leaving them, 8 x 16 of 128 x
-// 1024 875 and 830).
+// has the sums with X and Y at hand (8 x 4 of 384 x 2048 1528 us, 1575 side by side,
+// 1596 with the sums left to the pairs; in float32 the second chain always leaves
+// them, as LDS has no room for X and Y: 8 x 16 of 128 x 1024 879 and 873).
 inline bool side_by_side(const DeltaShape& s) {
   const int64_t wgs = s.B * s.NH * ((s.dv + 63) / 64);
   const int64_t apart = 2 * ((wgs + kCUs - 1) / kCUs), together = (2 * wgs + kCUs - 1) / kCUs;

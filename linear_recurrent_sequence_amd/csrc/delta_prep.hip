@@ -20,7 +20,7 @@
 // they cancel.
 //
 // What bounds it: memory, about 84 KiB of reads and writes per chunk of a 128
-// wide bf16 head.  4096 such chunks take 88 us, 64 us at a copy's rate; a chunk
+// wide bf16 head.  4096 such chunks take 88 us, 69 us at a copy's rate; a chunk
 // alone takes 11 us.  Before the transposes went through the matrix unit and one
 // matrix in LDS served P and At (18 KiB instead of 42, six workgroups to a CU
 // instead of three) they took 122 us.

@@ -1,5 +1,6 @@
 """How exact the gated delta rule and the block norm are on the GPU, beyond the
-tolerances of test_cells_gpu.py, whose inputs and oracle these tests share.
+tolerances of test_cells_gpu.py, whose inputs and oracle these tests share.  (Those
+allow for 16 bits in the operands of bf16 h, dq and dk, which carry 24 now.)
 
 A bf16 result is the float32 one rounded once.  With heads of 64 every sum has
 64 terms: float32 errors of either sign make sqrt(64) 2^-24 = 2^-21 of the sum's
