@@ -45,6 +45,22 @@ def test_delta_segments_of_every_width(NHK, NH, T, dk, dv, dtype, forget):
     close("C", C3, Cr)
 
 
+# each number of 32-column blocks again, ragged ones (memories whose rows end inside a
+# wave's), with the backward's chains side by side (3 heads) and one after the other (130)
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("B,NHK,NH", [(1, 1, 3), (2, 65, 65)])
+@pytest.mark.parametrize("dk", [16, 48, 80, 144, 208, 272, 336, 400, 464])
+def test_delta_of_every_width(B, NHK, NH, dk, dtype):
+    args, C0, dh, dC = inputs(B, NHK, NH, 70, dk, 16, dtype, 58)
+    h, C = mlstm.delta_fwd(*args, state=C0)
+    hr, Cr = oracle_of(args, C0)
+    close("h", h, hr)
+    close("C", C, Cr)
+    got = mlstm.delta_bwd(*args, dh, state=C0, dstate=dC)
+    for name, a, b in zip(NAMES, got, delta_ref(args, dh, C0, dC)):
+        close(name, a, *b)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("with_state,with_dstate", [(True, False), (False, True)])
 def test_delta_backward_with_one_memory(dtype, with_state, with_dstate):
