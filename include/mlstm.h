@@ -1,6 +1,7 @@
 /*
  * mlstm.h -- C ABI of the MI355X (gfx950) stabilized parallel mLSTM forward pass,
- * and, further down, of the gated delta rule and the block norm.
+ * and, further down, of the gated delta rule, the block norm, the short causal
+ * convolution, the selective scan and the gated feed-forward.
  *
  * The operation is the stabilized parallel forward pass of the mLSTM cell of
  * "xLSTM: Extended Long Short-Term Memory", Appendix A.3: the parallel form
@@ -120,10 +121,12 @@ enum {
   MLSTM_ERR_WORKSPACE = -7,   /* caller workspace smaller than mlstm_workspace_bytes */
   MLSTM_ERR_KERNEL = -8,      /* unknown kernel selector, or an MFMA selector for fp32 */
   MLSTM_ERR_ALIAS = -9,       /* an output overlaps an input or another output */
-  MLSTM_ERR_ACTIVATION = -10, /* unknown forget-gate activation */
+  MLSTM_ERR_ACTIVATION = -10, /* unknown activation (forget gate, convolution, feed-forward) */
   MLSTM_ERR_SCRATCH = -11,    /* beyond the allocation-free entry point's fixed workspace */
   MLSTM_ERR_HEADS = -12,      /* NH not a multiple of NHK */
-  MLSTM_ERR_NORM = -13        /* unknown norm or gate activation, or eps not a number >= 0 */
+  MLSTM_ERR_NORM = -13,       /* unknown norm or gate activation, or eps not a number >= 0 */
+  MLSTM_ERR_WIDTH = -14,      /* convolution width outside [2, 8], or scan states outside [1, 64] */
+  MLSTM_ERR_ROW = -15         /* a row pitch shorter than its row, or not a multiple of 8 */
 };
 
 /*
@@ -495,6 +498,142 @@ int mlstm_block_norm_bwd(const void* p, const void* gate, const void* residual,
                          void* workspace, size_t workspace_bytes,
                          int64_t B, int64_t NH, int64_t T, int64_t d, int dtype,
                          int norm, int gate_activation, float eps, void* stream);
+
+/*
+ * Short causal convolution with an activation: what a recurrent cell's inputs
+ * pass through, each channel by itself.  With z the state's W - 1 inputs followed
+ * by x_0 .. x_{n-1},
+ *
+ *   a_t = bias + sum_{j < W} weight_j z_{t+j},   y_t = act(a_t)
+ *
+ *   x        [B][T] rows of C = NH d channels, dtype, x_row elements apart (a
+ *            multiple of 8, at least C: x may be part of a wider projection)
+ *   weight   [C][W] float32, the last one on the newest input;  bias [C] float32 or NULL
+ *   state    [B][W - 1][C] dtype, oldest input first; the state before the
+ *            sequence may be NULL (zeros)
+ *   lengths  [B] int32 in device memory, or NULL (T).  Sequence b has the first
+ *            lengths[b] positions (kept in [0, T]); beyond them y and dx are zeros,
+ *            nothing is read and the state stays as it is there
+ *   y        [B][NH][T][d] dtype, as the cells above read it (NH = 1: rows)
+ *   W in [2, 8], d a multiple of 8, C <= 2^20.  act: a sigma(a) (MLSTM_CONV_SILU)
+ * or a.  Sums are float32, and a bf16 result is rounded once.  Tensors 16-byte
+ * aligned (lengths 4).  Bitwise reproducible.  T = 1 is the step of generation.
+ */
+enum { MLSTM_CONV_NONE = 0, MLSTM_CONV_SILU = 1 };
+
+/* state_out: the last W - 1 inputs after the sequence; may be state_in (in place) */
+int mlstm_short_conv_fwd(const void* x, int64_t x_row, const float* weight, const float* bias,
+                         const void* state_in, const int32_t* lengths, void* y, void* state_out,
+                         int64_t B, int64_t NH, int64_t T, int64_t d, int64_t width, int dtype,
+                         int activation, void* stream);
+
+/*
+ * mlstm_short_conv_bwd -- its gradients, from dy [B][NH][T][d] and dstate, that
+ * of the state after the sequence ([B][W - 1][C] dtype, or NULL: zeros).
+ *   dx [B][T][C] dtype;  dweight [C][W], dbias [C] float32 (dbias with bias, else
+ *   NULL);  dstate_out: of the state before, or NULL
+ *   workspace  mlstm_short_conv_workspace_bytes bytes, 256-byte aligned
+ */
+size_t mlstm_short_conv_workspace_bytes(int64_t B, int64_t NH, int64_t T, int64_t d,
+                                        int64_t width, int dtype);
+int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, const float* bias,
+                         const void* state_in, const int32_t* lengths, const void* dy,
+                         const void* dstate, void* dx, float* dweight, float* dbias,
+                         void* dstate_out, void* workspace, size_t workspace_bytes, int64_t B,
+                         int64_t NH, int64_t T, int64_t d, int64_t width, int dtype,
+                         int activation, void* stream);
+
+/*
+ * Selective state space scan: a recurrent cell of N states to a channel, whose
+ * step and in- and output weights depend on the token.  Per channel c of group g,
+ *
+ *   Delta_t = softplus(dt_t + dt_bias_c)
+ *   s_t = exp(Delta_t A_c) s_{t-1} + Delta_t u_t B_t
+ *   y_t = (C_t . s_t + D_c u_t) z_t sigma(z_t)
+ *
+ *   u, dt, gate z  [batch][T] rows of `channels`, dtype, u_row, dt_row and gate_row
+ *                  elements apart (multiples of 8); gate NULL: no last factor
+ *   A              [channels][N] float32 (negative, as a rule; any finite value)
+ *   B, C           [batch][T] rows of [G][N] dtype, B_row and C_row elements apart;
+ *                  channel c reads group c / (channels / G)
+ *   D, dt_bias     [channels] float32, or NULL (0)
+ *   state          [batch][channels][N] float32; before the sequence NULL: zeros
+ *   lengths        [batch] int32 in device memory, or NULL, as above: positions
+ *                  beyond are not read, y and gradients there are zeros and the
+ *                  state stays as it is
+ *   y              [batch][T][channels] dtype
+ *   channels / G a multiple of 8, channels <= 2^20, N in [1, 64],
+ *   batch T G N <= 2^31, batch channels <= 2^26
+ * dt = -infinity gives Delta = 0, which leaves the state as it is; inputs are
+ * otherwise finite.  All sums, Delta and the states are float32; a bf16 result is
+ * rounded once.  Tensors 16-byte aligned (B and C to their elements, lengths 4).
+ * Bitwise reproducible.
+ */
+size_t mlstm_scan_workspace_bytes(int64_t batch, int64_t T, int64_t channels, int64_t G, int64_t N,
+                                  int dtype, int backward);
+
+/*
+ * mlstm_scan_fwd -- a sequence (T = 1: the step of generation, bound by the
+ * state's traffic).  state_out: the state after it; may be state_in (in place).
+ *   workspace  mlstm_scan_workspace_bytes(..., 0) bytes, 256-byte aligned: none for
+ *              T = 1 and where the channels fill the card; else long sequences are
+ *              cut into segments that run side by side, so a position's result may
+ *              differ in its last bits from that of a shorter call
+ */
+int mlstm_scan_fwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row, const float* A,
+                   const void* B, int64_t B_row, const void* C, int64_t C_row, const float* D,
+                   const void* gate, int64_t gate_row, const float* dt_bias,
+                   const float* state_in, const int32_t* lengths, void* y, float* state_out,
+                   void* workspace, size_t workspace_bytes, int64_t batch, int64_t T,
+                   int64_t channels, int64_t G, int64_t N, int dtype, void* stream);
+
+/*
+ * mlstm_scan_bwd -- its gradients, from dy [batch][T][channels] and dstate, that of
+ * the state after the sequence (or NULL: zeros).
+ *   du, ddt, dgate  [batch][T][channels] dtype;  dB, dC [batch][T][G][N] dtype
+ *   dA [channels][N], dD, ddt_bias [channels] float32
+ *   dD, dgate and ddt_bias with D, gate and dt_bias, else NULL
+ *   dstate_out      of the state before, or NULL
+ *   workspace       mlstm_scan_workspace_bytes(..., 1) bytes, 256-byte aligned:
+ *                   chiefly the states at every 16th token (8th for N > 32), and 8 N
+ *                   bytes for each token and 64 channels
+ * The forward pass is formed again; nothing of it is kept.
+ */
+int mlstm_scan_bwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row, const float* A,
+                   const void* B, int64_t B_row, const void* C, int64_t C_row, const float* D,
+                   const void* gate, int64_t gate_row, const float* dt_bias,
+                   const float* state_in, const int32_t* lengths, const void* dy,
+                   const float* dstate, void* du, void* ddt, float* dA, void* dB, void* dC,
+                   float* dD, void* dgate, float* ddt_bias, float* dstate_out, void* workspace,
+                   size_t workspace_bytes, int64_t batch, int64_t T, int64_t channels, int64_t G,
+                   int64_t N, int dtype, void* stream);
+
+/*
+ * Gated feed-forward: both input projections of a block's feed-forward, the
+ * activation and the product,
+ *
+ *   h = act(x w_gate^T) * (x w_up^T)       act(g) = g sigma(g) or g Phi(g)
+ *
+ *   x [M][D], w_gate, w_up [F][D], h [M][F], all dtype, contiguous
+ *   D and F multiples of 8, at most 2^16; M <= 2^20, M max(D, 2 F) <= 2^33
+ * Products are summed in float32 (float32 operands as three bf16 planes, 24
+ * bits), and a bf16 h is rounded once.  mlstm_gated_ffn_bwd forms both products
+ * again; for bf16 their gradients are rounded to bf16 as operands of the
+ * products behind dx, dw_gate and dw_up.  Inputs finite.  Tensors 16-byte
+ * aligned; workspace mlstm_gated_ffn_workspace_bytes bytes, 256-byte aligned.
+ * Bitwise reproducible.
+ */
+enum { MLSTM_FFN_SILU = 0, MLSTM_FFN_GELU = 1 };
+
+size_t mlstm_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F, int dtype, int backward);
+int mlstm_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h,
+                        void* workspace, size_t workspace_bytes, int64_t M, int64_t D, int64_t F,
+                        int dtype, int activation, void* stream);
+/* dh [M][F] in; dx [M][D], dw_gate, dw_up [F][D] out, all dtype */
+int mlstm_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, const void* dh,
+                        void* dx, void* dw_gate, void* dw_up, void* workspace,
+                        size_t workspace_bytes, int64_t M, int64_t D, int64_t F, int dtype,
+                        int activation, void* stream);
 
 /* Human-readable text of a status code (static storage). */
 const char* mlstm_strerror(int status);

@@ -1,0 +1,350 @@
+// Gated feed-forward: h = act(x Wg^T) * (x Wu^T), rows of x.
+//
+// Forward: both products share the tiles of x, and a wave holds g and u of the
+// same outputs, so the activation and the product are formed in its registers and
+// h is all that is written.  Backward, with g and u formed again the same way:
+//
+//   dg = dh u act'(g),  du = dh act(g)             (G = [dg | du], M x 2F)
+//   dx = G [Wg ; Wu],   [dWg ; dWu] = G^T x
+//
+// All products run on one kind of tile (product_tiles.h), whose operands are rows
+// of the summed index: the weights, x and G are transposed into the workspace for
+// the last two.  For bf16, G is rounded to bf16 as the operand of those products
+// (2^-9 of each term, as much as the rounding of the results); everything before
+// is float32.
+#include "gated_ffn.h"
+
+#include "product_tiles.h"
+#include "row_vec.h"
+
+namespace mlstm {
+namespace ffn {
+namespace {
+
+using product::f32x4;
+using product::Operand;
+
+using Large = product::Shape<256, 256, 2, 4>;
+using Small = product::Shape<128, 128, 2, 2>;
+
+constexpr int kPlanes = 3, kTerms = 6;  // of float32
+
+struct Act {
+  float value, slope;
+};
+__device__ inline Act activation(float g, bool gelu) {
+  if (gelu) {  // g Phi(g); the slope is Phi(g) + g phi(g)
+    const float phi = 0.3989422804014327f * rowvec::exp2_fast(-0.5f * rowvec::kLog2e * g * g);
+    const float cdf = 0.5f * erfcf(-0.7071067811865476f * g);
+    return {g * cdf, __builtin_fmaf(g, phi, cdf)};
+  }
+  const float s = rowvec::sigmoid(g);
+  return {g * s, rowvec::silu_slope(g, s)};
+}
+
+__device__ inline void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+__device__ inline void store4(__hip_bfloat16* p, f32x4 x) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(rowvec::to_bf16(x[0], x[1]), rowvec::to_bf16(x[2], x[3]));
+}
+
+struct Sizes {
+  int64_t M, D, F;
+  int terms;
+  bool gelu;
+};
+
+// h, or with GRAD G = [dg | du], for a tile of rows and of F
+template <typename T, typename S, bool GRAD>
+__global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operand wu, Operand x,
+                                                              Sizes n, const T* dh, T* out) {
+  __shared__ __align__(1024) char lds[S::kLds];
+  constexpr int kF = S::kBP / 2;
+  unsigned ip, iq;
+  product::map_tile(blockIdx.x, unsigned((n.F + kF - 1) / kF),
+                    unsigned((n.M + S::kBQ - 1) / S::kBQ), ip, iq);
+  const int64_t p0 = int64_t(ip) * kF, q0 = int64_t(iq) * S::kBQ;
+  f32x4 acc[S::kP][S::kQ];
+  product::multiply<S, true>(wg, wu, x, n.D, n.terms, p0, q0, lds, acc);
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t f0 = p0 + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
+                m0 = q0 + wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+#pragma unroll
+  for (int j = 0; j < S::kQ; ++j) {
+    const int64_t m = m0 + j * 16;
+    if (m >= n.M) continue;
+#pragma unroll
+    for (int i = 0; i < S::kP / 2; ++i) {
+      const int64_t f = f0 + i * 16;
+      if (f >= n.F) continue;
+      const f32x4 g = acc[i][j], u = acc[i + S::kP / 2][j];
+      f32x4 a, b;
+      if constexpr (GRAD) {
+        float d[4];
+        rowvec::load(dh + m * n.F + f, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const Act act = activation(g[e], n.gelu);
+          a[e] = d[e] * u[e] * act.slope;
+          b[e] = d[e] * act.value;
+        }
+        store4(out + m * 2 * n.F + f, a);
+        store4(out + (m * 2 + 1) * n.F + f, b);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = activation(g[e], n.gelu).value * u[e];
+        store4(out + m * n.F + f, a);
+      }
+    }
+  }
+}
+
+// out[q][p], rows q from `split` on in out2
+template <typename T, typename S>
+__global__ __launch_bounds__(S::kThreads) void product_kernel(Operand left, Operand right,
+                                                              int64_t k, int terms, T* out,
+                                                              T* out2, int64_t split) {
+  __shared__ __align__(1024) char lds[S::kLds];
+  unsigned ip, iq;
+  product::map_tile(blockIdx.x, unsigned((left.rows + S::kBP - 1) / S::kBP),
+                    unsigned((right.rows + S::kBQ - 1) / S::kBQ), ip, iq);
+  const int64_t p0 = int64_t(ip) * S::kBP, q0 = int64_t(iq) * S::kBQ;
+  f32x4 acc[S::kP][S::kQ];
+  product::multiply<S, false>(left, left, right, k, terms, p0, q0, lds, acc);
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t first = p0 + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4,
+                q1 = q0 + wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+#pragma unroll
+  for (int j = 0; j < S::kQ; ++j) {
+    const int64_t q = q1 + j * 16;
+    if (q >= right.rows) continue;
+    T* row = q < split ? out + q * left.rows : out2 + (q - split) * left.rows;
+#pragma unroll
+    for (int i = 0; i < S::kP; ++i)
+      if (first + i * 16 < left.rows) store4(row + first + i * 16, acc[i][j]);
+  }
+}
+
+// ---- operands: planes of float32, and transposes
+
+// three bf16 planes of x
+__device__ inline void planes_of(float x, uint16_t (&p)[kPlanes]) {
+#pragma unroll
+  for (int i = 0; i < kPlanes; ++i) {
+    p[i] = uint16_t(rowvec::to_bf16(x, 0.0f));
+    x -= __uint_as_float(unsigned(p[i]) << 16);
+  }
+}
+
+// planes of n values (a multiple of 4)
+__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t n, uint16_t* out,
+                                                    int64_t plane) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float4 f = *reinterpret_cast<const float4*>(x + i);
+  const float v[4] = {f.x, f.y, f.z, f.w};
+  uint16_t p[4][kPlanes];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) planes_of(v[e], p[e]);
+#pragma unroll
+  for (int k = 0; k < kPlanes; ++k)
+    *reinterpret_cast<ushort4*>(out + k * plane + i) =
+        make_ushort4(p[0][k], p[1][k], p[2][k], p[3][k]);
+}
+
+// out[c][r] = in[r][c] with rows of `width` outputs, `pitch` apart, zeros for r from
+// `rows` on; in 64 x 64 tiles through LDS.  float32 becomes planes.
+template <typename T>
+__global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t rows, int64_t cols,
+                                                        uint16_t* out, int64_t width,
+                                                        int64_t pitch, int64_t plane) {
+  constexpr int N = sizeof(T) == 4 ? kPlanes : 1;
+  __shared__ uint16_t tile[N][64][66];
+  const int64_t tiles = (cols + 63) / 64;
+  const int64_t c0 = blockIdx.x % tiles * 64, r0 = blockIdx.x / tiles * 64;
+  for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+    const int r = i / 16, c = i % 16 * 4;
+    float v[4] = {};
+    if (r0 + r < rows && c0 + c < cols) rowvec::load(in + (r0 + r) * cols + c0 + c, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (N == 1) {
+        tile[0][c + e][r] = uint16_t(__float_as_uint(v[e]) >> 16);
+      } else {
+        uint16_t p[kPlanes];
+        planes_of(v[e], p);
+#pragma unroll
+        for (int k = 0; k < N; ++k) tile[k][c + e][r] = p[k];
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 16; i += 256) {
+    const int c = i / 16, r = i % 16 * 4;
+    if (c0 + c < cols && r0 + r < width)
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        *reinterpret_cast<ushort4*>(out + k * plane + (c0 + c) * pitch + r0 + r) = make_ushort4(
+            tile[k][c][r], tile[k][c][r + 1], tile[k][c][r + 2], tile[k][c][r + 3]);
+  }
+}
+
+// ---- launches
+
+size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// a workspace taken in order; with a null base, its size
+struct Arena {
+  char* base;
+  size_t at = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + at);
+    at += pad256(size_t(n) * sizeof(T));
+    return p;
+  }
+};
+
+template <typename T>
+constexpr int kCopies = sizeof(T) == 4 ? kPlanes : 1;
+template <typename T>
+constexpr int kTermsOf = sizeof(T) == 4 ? kTerms : 1;
+
+// an operand of the products: a bf16 matrix as it is, the planes of a float32 one
+template <typename T>
+Operand as_rows(const void* p, int64_t rows, int64_t k, Arena& ws, hipStream_t stream, bool run) {
+  if constexpr (sizeof(T) == 2) {
+    return {static_cast<const uint16_t*>(p), rows, 0};
+  } else {
+    uint16_t* out = ws.take<uint16_t>(kPlanes * rows * k);
+    if (run)
+      split_kernel<<<unsigned((rows * k + 1023) / 1024), 256, 0, stream>>>(
+          static_cast<const float*>(p), rows * k, out, rows * k);
+    return {out, rows, rows * k};
+  }
+}
+
+// a matrix [rows][cols] as `cols` rows of `width` (rows, rounded up to 8)
+template <typename T>
+void transposed(const void* p, int64_t rows, int64_t cols, uint16_t* out, int64_t width,
+                int64_t pitch, int64_t plane, hipStream_t stream) {
+  const int64_t n = ((cols + 63) / 64) * ((width + 63) / 64);
+  transpose_kernel<T><<<unsigned(n), 256, 0, stream>>>(static_cast<const T*>(p), rows, cols, out,
+                                                       width, pitch, plane);
+}
+
+constexpr int64_t kCUs = 256;
+// Tiles of 256 x 256, one workgroup to a CU, where they fill the card; else 128 x 128
+bool large_tiles(int64_t p, int64_t q) {
+  return ((p + 255) / 256) * ((q + 255) / 256) >= kCUs / 2;
+}
+
+template <typename T, typename S, bool GRAD>
+hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
+                   const void* dh, void* out, hipStream_t stream) {
+  auto kernel = gate_up_kernel<T, S, GRAD>;
+  constexpr int kF = S::kBP / 2;
+  const int64_t wgs = ((n.F + kF - 1) / kF) * ((n.M + S::kBQ - 1) / S::kBQ);
+  kernel<<<unsigned(wgs), S::kThreads, 0, stream>>>(wg, wu, x, n, static_cast<const T*>(dh),
+                                                          static_cast<T*>(out));
+  return hipGetLastError();
+}
+template <typename T, bool GRAD>
+hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
+                   const void* dh, void* out, hipStream_t stream) {
+  return large_tiles(2 * n.F, n.M) ? gate_up<T, Large, GRAD>(wg, wu, x, n, dh, out, stream)
+                                   : gate_up<T, Small, GRAD>(wg, wu, x, n, dh, out, stream);
+}
+
+template <typename T, typename S>
+hipError_t multiply_as(const Operand& l, const Operand& r, int64_t k, void* out, void* out2,
+                       int64_t split, hipStream_t stream) {
+  auto kernel = product_kernel<T, S>;
+  const int64_t wgs = ((l.rows + S::kBP - 1) / S::kBP) * ((r.rows + S::kBQ - 1) / S::kBQ);
+  kernel<<<unsigned(wgs), S::kThreads, 0, stream>>>(l, r, k, kTermsOf<T>,
+                                                          static_cast<T*>(out),
+                                                          static_cast<T*>(out2), split);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t multiply(const Operand& l, const Operand& r, int64_t k, void* out, void* out2,
+                    int64_t split, hipStream_t stream) {
+  return large_tiles(l.rows, r.rows) ? multiply_as<T, Large>(l, r, k, out, out2, split, stream)
+                                     : multiply_as<T, Small>(l, r, k, out, out2, split, stream);
+}
+
+// `run` false: only the workspace's size
+template <typename T>
+hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bool run) {
+  const Operand wg = as_rows<T>(a.w_gate, a.F, a.D, ws, stream, run),
+                wu = as_rows<T>(a.w_up, a.F, a.D, ws, stream, run),
+                x = as_rows<T>(a.x, a.M, a.D, ws, stream, run);
+  if (!run) return hipSuccess;
+  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, stream);
+}
+
+template <typename T>
+hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStream_t stream,
+                    bool run) {
+  const int64_t M = a.M, D = a.D, F = a.F, pitch = (M + 7) / 8 * 8;
+  const Operand wg = as_rows<T>(a.w_gate, F, D, ws, stream, run),
+                wu = as_rows<T>(a.w_up, F, D, ws, stream, run),
+                x = as_rows<T>(a.x, M, D, ws, stream, run);
+  T* G = ws.take<T>(M * 2 * F);
+  const int64_t wt_plane = D * 2 * F, xt_plane = D * pitch, gt_plane = 2 * F * pitch;
+  uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);  // [D][Wg^T | Wu^T]
+  uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);  // [D][M]
+  uint16_t* gt = ws.take<uint16_t>(kCopies<T> * gt_plane);  // [2F][M]
+  if (run) {
+    const hipError_t e =
+        gate_up<T, true>(wg, wu, x, {M, D, F, kTermsOf<T>, a.gelu}, g.dh, G, stream);
+    if (e != hipSuccess) return e;
+  }
+  const Operand G_rows = as_rows<T>(G, M, 2 * F, ws, stream, run);
+  if (!run) return hipSuccess;
+  // the two halves of wt, each [D] rows of 2 F
+  transposed<T>(a.w_gate, F, D, wt, F, 2 * F, wt_plane, stream);
+  transposed<T>(a.w_up, F, D, wt + F, F, 2 * F, wt_plane, stream);
+  transposed<T>(a.x, M, D, xt, pitch, pitch, xt_plane, stream);
+  transposed<T>(G, M, 2 * F, gt, pitch, pitch, gt_plane, stream);
+  const hipError_t e = multiply<T>({wt, D, wt_plane}, G_rows, 2 * F, g.dx, nullptr, M, stream);
+  if (e != hipSuccess) return e;
+  return multiply<T>({xt, D, xt_plane}, {gt, 2 * F, gt_plane}, pitch, g.dw_gate, g.dw_up, F,
+                     stream);
+}
+
+}  // namespace
+}  // namespace ffn
+
+size_t gated_ffn_fwd_workspace_bytes(const GatedFfn& a) {
+  ffn::Arena ws{nullptr};
+  if (a.is_bf16)
+    (void)ffn::forward<__hip_bfloat16>(a, nullptr, ws, nullptr, false);
+  else
+    (void)ffn::forward<float>(a, nullptr, ws, nullptr, false);
+  return ws.at;
+}
+
+hipError_t launch_gated_ffn_fwd(const GatedFfn& a, void* h, void* workspace, hipStream_t stream) {
+  ffn::Arena ws{static_cast<char*>(workspace)};
+  return a.is_bf16 ? ffn::forward<__hip_bfloat16>(a, h, ws, stream, true)
+                   : ffn::forward<float>(a, h, ws, stream, true);
+}
+
+size_t gated_ffn_bwd_workspace_bytes(const GatedFfn& a) {
+  ffn::Arena ws{nullptr};
+  if (a.is_bf16)
+    (void)ffn::backward<__hip_bfloat16>(a, {}, ws, nullptr, false);
+  else
+    (void)ffn::backward<float>(a, {}, ws, nullptr, false);
+  return ws.at;
+}
+
+hipError_t launch_gated_ffn_bwd(const GatedFfn& a, const GatedFfnGrads& g, void* workspace,
+                                hipStream_t stream) {
+  ffn::Arena ws{static_cast<char*>(workspace)};
+  return a.is_bf16 ? ffn::backward<__hip_bfloat16>(a, g, ws, stream, true)
+                   : ffn::backward<float>(a, g, ws, stream, true);
+}
+
+}  // namespace mlstm

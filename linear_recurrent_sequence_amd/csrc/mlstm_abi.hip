@@ -467,6 +467,8 @@ const char* mlstm_strerror(int status) {
     case MLSTM_ERR_SCRATCH: return "the problem needs more workspace than the allocation-free entry point's fixed buffer holds (MLSTM_NOALLOC_SCRATCH_BYTES)";
     case MLSTM_ERR_HEADS: return "the number of value heads must be a multiple of the number of key heads";
     case MLSTM_ERR_NORM: return "unknown norm or gate activation, or eps is not a number >= 0";
+    case MLSTM_ERR_WIDTH: return "a convolution's width must be 2 to 8, a scan's states per channel 1 to 64";
+    case MLSTM_ERR_ROW: return "a row pitch is shorter than its row, or not a multiple of 8 elements";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,260 @@
+// The selective scan over a sequence.
+#include "selective_common.h"
+
+namespace mlstm {
+namespace selective {
+namespace {
+
+constexpr int kTile = 32;  // tokens
+
+// The ends of segments, and then the states before them.
+struct Joints {
+  float* states;  // [segment][batch][N][channels]
+  float* deltas;  // [segment][batch][channels]: the sum of Delta
+  __device__ float* state(const SelectiveScan& a, int64_t seg, int64_t b) const {
+    return states + (seg * a.batch + b) * a.N * a.channels;
+  }
+  __device__ float* delta(const SelectiveScan& a, int64_t seg, int64_t b) const {
+    return deltas + (seg * a.batch + b) * a.channels;
+  }
+};
+
+// ENDS: a segment's effect from a state of zeros, and the sum of its Delta.
+// Otherwise: y, and the state after the last segment.
+template <typename T, int NW, int NS, bool GATE, bool ENDS>
+__global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, float* state_out,
+                                                       Segments seg, Joints joints) {
+  constexpr int TL = kTile, kThreads = 64 * NW;
+  constexpr int V = NW < 8 ? 8 : 4, kVecs = kChannels / V;
+  constexpr int kItems = TL * kVecs / kThreads;
+  static_assert(TL * kVecs % kThreads == 0, "every thread has as many");
+  __shared__ float2 steps[TL][kChannels];  // Delta, Delta u
+  __shared__ __align__(16) float shared[TL * 2 * NW * NS];
+  __shared__ __align__(16) float parts[ENDS ? 1 : NW][ENDS ? 1 : TL][kChannels];
+
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t tiles = a.G * tiles_of_group(a.channels, a.G);
+  const Channels ch = channels_of(a, blockIdx.x % tiles);
+  const int64_t segments = ENDS ? seg.n - 1 : seg.n;
+  const int64_t s_at = blockIdx.x / tiles % segments, b = blockIdx.x / tiles / segments;
+  const int64_t first = s_at * seg.tiles * TL;
+  const int64_t last = first + seg.tiles * TL < a.T ? first + seg.tiles * TL : a.T;
+  const int64_t n = rowvec::length_of(a.lengths, b, a.T);
+
+  float A[NS], s[NS];
+  load_rates(a, ch, wave, lane, A);
+  if constexpr (ENDS) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) s[j] = 0.0f;
+  } else if (seg.n > 1) {
+    load_kept(a, joints.state(a, s_at, b), ch, wave, lane, s);
+  } else {
+    load_state(a, a.state, b, ch, wave, lane, s);
+  }
+  float sum = 0.0f;
+
+  Raw<T, V> u[kItems], dt[kItems], z[kItems];
+  Shared<T, NW, NS, TL> bc;
+  auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
+  auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
+  auto load = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int64_t t = t0 + row_of(i);
+      u[i] = dt[i] = z[i] = {};
+      if (t < n && t < last && vec_of(i) < ch.count) {
+        const int64_t row = b * a.T + t, c = ch.first + vec_of(i);
+        u[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.u) + row * a.u_row + c);
+        dt[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.dt) + row * a.dt_row + c);
+        if constexpr (GATE && !ENDS)
+          z[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.gate) + row * a.gate_row + c);
+      }
+    }
+    bc.load(a, b, ch.group, t0, n < last ? n : last);
+  };
+
+  load(first);
+  for (int64_t t0 = first; t0 < last; t0 += TL) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int64_t c = ch.first + vec_of(i);
+      const bool on = t0 + row_of(i) < n && t0 + row_of(i) < last && vec_of(i) < ch.count;
+      float x[V], bias[V] = {}, v[V];
+      rowvec::floats(dt[i], x);
+      rowvec::floats(u[i], v);
+      if (a.dt_bias && on) rowvec::load(a.dt_bias + c, bias);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = on ? softplus(x[e] + bias[e]).value : 0.0f;
+        steps[row_of(i)][vec_of(i) + e] = make_float2(d, d * v[e]);
+      }
+    }
+    bc.put(shared);
+    __syncthreads();
+    Raw<T, V> u0[kItems], z0[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) u0[i] = u[i], z0[i] = z[i];
+    if (t0 + TL < last) load(t0 + TL);
+
+#pragma unroll 8
+    for (int t = 0; t < TL; ++t) {
+      const float2 d = steps[t][lane];
+      float B[NS], C[NS];
+      const float* row = shared + (t * NW + wave) * 2 * NS;
+      read(row, B);
+      if constexpr (ENDS) {
+        sum += d.x;
+      } else {
+        read(row + NS, C);
+      }
+      float p = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        s[j] = __builtin_fmaf(rowvec::exp2_fast(d.x * A[j]), s[j], d.y * B[j]);
+        if constexpr (!ENDS) p = __builtin_fmaf(C[j], s[j], p);
+      }
+      if constexpr (!ENDS) parts[wave][t][lane] = p;
+    }
+    __syncthreads();
+    if constexpr (!ENDS) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int64_t t = t0 + row_of(i), c = ch.first + vec_of(i);
+        if (t >= last || vec_of(i) >= ch.count) continue;
+        float o[V], x[V], skip[V] = {};
+        if (a.D) rowvec::load(a.D + c, skip);
+        rowvec::floats(u0[i], x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = skip[e] * x[e];
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] += parts[w][row_of(i)][vec_of(i) + e];
+        if constexpr (GATE) {
+          rowvec::floats(z0[i], x);
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] *= x[e] * rowvec::sigmoid(x[e]);
+        }
+        rowvec::store(y + (b * a.T + t) * a.channels + c, o);
+      }
+    }
+  }
+  if constexpr (ENDS) {
+    store_kept(a, joints.state(a, s_at, b), ch, wave, lane, s);
+    if (wave == 0 && lane < ch.count) joints.delta(a, s_at, b)[ch.first + lane] = sum;
+  } else if (s_at == seg.n - 1) {
+    store_state(a, state_out, b, ch, wave, lane, s);
+  }
+}
+
+// the state before each segment, in the place of the segment's end
+__global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joints, int segments) {
+  const int64_t all = a.N * a.channels, blocks = (all + 255) / 256;
+  const int64_t b = blockIdx.x / blocks, i = (blockIdx.x % blocks) * 256 + threadIdx.x;
+  if (i >= all) return;
+  const int64_t c = i % a.channels, n = i / a.channels;
+  const float A = a.A[c * a.N + n] * rowvec::kLog2e;
+  float s = a.state ? a.state[(b * a.channels + c) * a.N + n] : 0.0f;
+  for (int k = 0; k < segments; ++k) {
+    float* at = joints.state(a, k, b) + i;
+    if (k == segments - 1) {
+      *at = s;
+    } else {
+      const float end = *at;
+      *at = s;
+      s = __builtin_fmaf(rowvec::exp2_fast(A * joints.delta(a, k, b)[c]), s, end);
+    }
+  }
+}
+
+constexpr int64_t kSimds = 1024;
+
+int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+
+// How many segments: those of a sequence run side by side, for the effect of each
+// on a state (7 operations to the scan's 8), taken first.  A SIMD takes the waves
+// that it has in turn, so the time is that of the SIMD with the most.
+Segments segments_of(const SelectiveScan& a) {
+  const int64_t tiles = (a.T + kTile - 1) / kTile;
+  const int64_t waves = a.batch * a.G * tiles_of_group(a.channels, a.G) * waves_of(a.N);
+  Segments best = {1, tiles};
+  double least = double(tiles) * double((waves + kSimds - 1) / kSimds);
+  for (int n = 2; n <= 64 && n * 4 <= tiles; ++n) {
+    const int64_t len = (tiles + n - 1) / n;
+    if ((tiles + len - 1) / len != n) continue;
+    const double t = double(len) * (double((waves * n + kSimds - 1) / kSimds) +
+                                    0.9 * double((waves * (n - 1) + kSimds - 1) / kSimds)) + 8.0;
+    if (t < 0.9 * least) {
+      least = t;
+      best = {n, len};
+    }
+  }
+  return best;
+}
+
+size_t state_bytes(const SelectiveScan& a, int n) {
+  return pad256(size_t(n) * size_t(a.batch * a.N * a.channels) * 4);
+}
+
+template <typename T, int NW, int NS, bool GATE>
+void launch(const SelectiveScan& a, void* y, float* state_out, const Segments& seg,
+            const Joints& joints, hipStream_t stream) {
+  const int64_t per = a.batch * a.G * tiles_of_group(a.channels, a.G);
+  if (seg.n > 1) {
+    scan_kernel<T, NW, NS, false, true><<<unsigned(per * (seg.n - 1)), 64 * NW, 0, stream>>>(
+        a, nullptr, nullptr, seg, joints);
+    join_kernel<<<unsigned(a.batch * ((a.N * a.channels + 255) / 256)), 256, 0, stream>>>(
+        a, joints, seg.n);
+  }
+  scan_kernel<T, NW, NS, GATE, false><<<unsigned(per * seg.n), 64 * NW, 0, stream>>>(
+      a, static_cast<T*>(y), state_out, seg, joints);
+}
+
+template <typename T, bool GATE>
+void dispatch(const SelectiveScan& a, void* y, float* state_out, const Segments& seg,
+              const Joints& joints, hipStream_t stream) {
+  if (a.N <= 4)
+    launch<T, 1, 4, GATE>(a, y, state_out, seg, joints, stream);
+  else if (a.N <= 8)
+    launch<T, 2, 4, GATE>(a, y, state_out, seg, joints, stream);
+  else if (a.N <= 16)
+    launch<T, 4, 4, GATE>(a, y, state_out, seg, joints, stream);
+  else if (a.N <= 32)
+    launch<T, 8, 4, GATE>(a, y, state_out, seg, joints, stream);
+  else
+    launch<T, 8, 8, GATE>(a, y, state_out, seg, joints, stream);
+}
+
+}  // namespace
+}  // namespace selective
+
+size_t selective_fwd_workspace_bytes(const SelectiveScan& a) {
+  const selective::Segments seg = selective::segments_of(a);
+  if (seg.n == 1) return 0;
+  return selective::state_bytes(a, seg.n) +
+         selective::pad256(size_t(seg.n) * size_t(a.batch * a.channels) * 4);
+}
+
+hipError_t launch_selective_fwd(const SelectiveScan& a, void* y, float* state_out, void* workspace,
+                                hipStream_t stream) {
+  using namespace selective;
+  const Segments seg = segments_of(a);
+  char* ws = static_cast<char*>(workspace);
+  Joints joints = {nullptr, nullptr};
+  if (seg.n > 1)
+    joints = {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + state_bytes(a, seg.n))};
+  if (a.is_bf16) {
+    if (a.gate)
+      dispatch<__hip_bfloat16, true>(a, y, state_out, seg, joints, stream);
+    else
+      dispatch<__hip_bfloat16, false>(a, y, state_out, seg, joints, stream);
+  } else {
+    if (a.gate)
+      dispatch<float, true>(a, y, state_out, seg, joints, stream);
+    else
+      dispatch<float, false>(a, y, state_out, seg, joints, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mlstm

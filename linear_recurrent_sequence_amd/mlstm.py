@@ -14,8 +14,10 @@ Returns h~ (same dtype as q), m and n (float32), as defined by Eqs. 80, 84 and
 stabilized forward pass).
 
 Beside the cell: the gated delta rule (``delta_fwd``, ``delta_bwd``,
-``delta_step``) and the block norm (``block_norm_fwd``, ``block_norm_bwd``), with
-the same conventions.
+``delta_step``), the block norm (``block_norm_fwd``, ``block_norm_bwd``), the short
+causal convolution (``short_conv_fwd``, ``short_conv_bwd``, ``short_conv_step``), the
+selective scan (``scan_fwd``, ``scan_bwd``, ``scan_step``) and the gated feed-forward
+(``gated_ffn_fwd``, ``gated_ffn_bwd``), with the same conventions.
 """
 
 import contextlib
@@ -33,6 +35,8 @@ KERNELS = {"auto": 0, "mfma": 1, "vector": 2, "mfma_all_tiles": 3, "mfma_single"
 FORGET_ACTIVATIONS = {"sigmoid": 0, "exp": 1}
 NORMS = {"layer": 0, "rms": 1}
 GATE_ACTIVATIONS = {"sigmoid": 0, "silu": 1}
+CONV_ACTIVATIONS = {"none": 0, "silu": 1}
+FFN_ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 _lib = None
 
@@ -88,6 +92,25 @@ def load_library():
     lib.mlstm_block_norm_workspace_bytes.restype = f
     lib.mlstm_block_norm_bwd.argtypes = [vp] * 15 + [f] + [i64] * 4 + [i32] * 3 + [fl, vp]
     lib.mlstm_block_norm_bwd.restype = i32
+    lib.mlstm_short_conv_fwd.argtypes = [vp, i64] + [vp] * 6 + [i64] * 5 + [i32, i32, vp]
+    lib.mlstm_short_conv_fwd.restype = i32
+    lib.mlstm_short_conv_workspace_bytes.argtypes = [i64] * 5 + [i32]
+    lib.mlstm_short_conv_workspace_bytes.restype = f
+    lib.mlstm_short_conv_bwd.argtypes = [vp, i64] + [vp] * 11 + [f] + [i64] * 5 + [i32, i32, vp]
+    lib.mlstm_short_conv_bwd.restype = i32
+    lib.mlstm_scan_workspace_bytes.argtypes = [i64] * 5 + [i32, i32]
+    lib.mlstm_scan_workspace_bytes.restype = f
+    scan = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp]
+    lib.mlstm_scan_fwd.argtypes = scan + [vp] * 3 + [f] + [i64] * 5 + [i32, vp]
+    lib.mlstm_scan_fwd.restype = i32
+    lib.mlstm_scan_bwd.argtypes = scan + [vp] * 12 + [f] + [i64] * 5 + [i32, vp]
+    lib.mlstm_scan_bwd.restype = i32
+    lib.mlstm_gated_ffn_workspace_bytes.argtypes = [i64] * 3 + [i32, i32]
+    lib.mlstm_gated_ffn_workspace_bytes.restype = f
+    lib.mlstm_gated_ffn_fwd.argtypes = [vp] * 5 + [f] + [i64] * 3 + [i32, i32, vp]
+    lib.mlstm_gated_ffn_fwd.restype = i32
+    lib.mlstm_gated_ffn_bwd.argtypes = [vp] * 8 + [f] + [i64] * 3 + [i32, i32, vp]
+    lib.mlstm_gated_ffn_bwd.restype = i32
     lib.mlstm_strerror.argtypes = [i32]
     lib.mlstm_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -638,3 +661,350 @@ def block_norm_bwd(p, weight, dr, dy, gate=None, residual=None, scale=None, next
     if st != 0:
         raise MlstmError(st, "mlstm_block_norm_bwd")
     return g
+
+
+def _require_rows(named, device):
+    """Raise unless each (name, tensor, shape, dtype) is rows of contiguous
+    elements with one pitch, on ``device`` -> the pitches, in elements.  ``shape``:
+    its first two (B, T) or first (B) sizes count rows, ``row`` elements each."""
+    pitches = []
+    for name, t, shape, dtype, row in named:
+        if t is None:
+            pitches.append(row)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.is_contiguous():
+            pitches.append(row)
+            continue
+        size, stride = list(t.shape), list(t.stride())
+        inner, step = 1, 1  # the elements of a row
+        while inner < row:
+            n, st = size.pop(), stride.pop()
+            if n > 1 and st != step:
+                raise ValueError(f"{name}'s rows must be contiguous")
+            inner, step = inner * n, step * n
+        pitch = None  # of the rows: the last dimension with more than one of them
+        while size:
+            n, st = size.pop(), stride.pop()
+            if n > 1 and pitch is None:
+                pitch, span = st, st * n
+            elif n > 1:
+                if st != span:
+                    raise ValueError(f"{name}'s rows must be evenly spaced")
+                span *= n
+        pitches.append(row if pitch is None else pitch)
+    for name, t, *_ in named:
+        if t is not None:
+            _require_device(name, t, device)
+    return pitches
+
+
+def _named_code(what, table, name):
+    if name not in table:
+        raise ValueError(f"{what} must be one of {tuple(table)}, got {name!r}")
+    return table[name]
+
+
+def _check_floats(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _workspace(n, device):
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _check_conv(x, weight, bias, heads, lengths, dims, states, dy=None):
+    _check_floats("x", x)
+    if x.dim() != dims:
+        raise ValueError(f"x must be [B, {'T, ' if dims == 3 else ''}C], got shape "
+                         f"{tuple(x.shape)}")
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError(f"weight must be a torch.Tensor, got {type(weight).__name__}")
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [C, W], got shape {tuple(weight.shape)}")
+    B, C, W = x.shape[0], x.shape[-1], weight.shape[1]
+    T = x.shape[1] if dims == 3 else 1
+    NH = 1 if heads is None else heads
+    if not isinstance(NH, int) or NH < 1 or C % NH:
+        raise ValueError(f"heads must be a divisor of the {C} channels, got {heads!r}")
+    x_row, = _require_rows([("x", x, x.shape, x.dtype, C)], x.device)
+    named = [("weight", weight, (C, W), torch.float32)]
+    if bias is not None:
+        named.append(("bias", bias, (C,), torch.float32))
+    if lengths is not None:
+        named.append(("lengths", lengths, (B,), torch.int32))
+    if dy is not None:
+        named.append(("dy", dy, _conv_shape(B, heads, T, C, dims), x.dtype))
+    for name, t in states.items():
+        if t is not None:
+            named.append((name, t, (B, W - 1, C), x.dtype))
+    _require_all(named, x.device)
+    return x_row, B, NH, T, C // NH, W
+
+
+def _conv_shape(B, heads, T, C, dims):
+    """The shape of y: rows without heads, else head-major."""
+    if dims == 2:
+        return (B, C) if heads is None else (B, heads, C // heads)
+    return (B, T, C) if heads is None else (B, heads, T, C // heads)
+
+
+def conv_state(B, C, width, dtype, device):
+    """A fresh state of the short convolution: zeros [B, width - 1, C]."""
+    return torch.zeros((B, width - 1, C), dtype=dtype, device=device)
+
+
+def _short_conv(x, weight, bias, state, out_state, heads, lengths, activation, dims):
+    lib = load_library()
+    x_row, B, NH, T, d, W = _check_conv(x, weight, bias, heads, lengths, dims,
+                                        {"state": state, "out_state": out_state})
+    code = _named_code("activation", CONV_ACTIVATIONS, activation)
+    with _on(x.device):
+        if out_state is None:
+            out_state = torch.empty((B, W - 1, NH * d), dtype=x.dtype, device=x.device)
+        y = torch.empty(_conv_shape(B, heads, T, NH * d, dims), dtype=x.dtype, device=x.device)
+        st = lib.mlstm_short_conv_fwd(
+            x.data_ptr(), x_row, weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
+            y.data_ptr(), out_state.data_ptr(), B, NH, T, d, W, _dtype_code(x), code,
+            _stream_ptr(x.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_short_conv_fwd")
+    return y, out_state
+
+
+def short_conv_fwd(x, weight, bias=None, state=None, out_state=None, heads=None, lengths=None,
+                   activation="silu"):
+    """The causal convolution before a recurrent cell -> (y, new state).
+
+        y_t = act(bias + sum_j weight[:, j] x_{t - W + 1 + j})   channel by channel
+
+    x: [B, T, C] float32 or bfloat16, rows of contiguous channels (they may be part
+    of wider rows); weight: [C, W] and bias: [C], float32, W from 2 to 8.
+    ``state``: the W - 1 inputs before the sequence, [B, W - 1, C] (zeros by
+    default); ``out_state`` receives the last W - 1 after it and may be ``state``.
+    heads: y is [B, heads, T, C // heads], as the cells read it; None: [B, T, C].
+    lengths: [B] int32, each sequence's positions (beyond them y is zeros);
+    activation: "silu" or "none".
+    """
+    return _short_conv(x, weight, bias, state, out_state, heads, lengths, activation, 3)
+
+
+def short_conv_step(x, weight, state, bias=None, heads=None, out_state=None, activation="silu"):
+    """One token of ``short_conv_fwd``: x [B, C] -> (y [B, heads, C // heads] or
+    [B, C], new state); ``state`` is updated in place unless ``out_state`` is given."""
+    if not isinstance(state, torch.Tensor):
+        raise TypeError(f"state must be a torch.Tensor, got {type(state).__name__}")
+    return _short_conv(x, weight, bias, state, state if out_state is None else out_state, heads,
+                       None, activation, 2)
+
+
+def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, heads=None, lengths=None,
+                   activation="silu"):
+    """Gradients of ``short_conv_fwd`` given dy and ``dstate`` = dL/d(new state)
+    (zeros by default) -> a dict with "dx", "dweight", with bias "dbias", and
+    "dstate", that of the state before the sequence."""
+    lib = load_library()
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError(f"dy must be a torch.Tensor, got {type(dy).__name__}")
+    x_row, B, NH, T, d, W = _check_conv(x, weight, bias, heads, lengths, 3,
+                                        {"state": state, "dstate": dstate}, dy)
+    code, dtype = _named_code("activation", CONV_ACTIVATIONS, activation), _dtype_code(x)
+    with _on(x.device):
+        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+             "dweight": torch.empty_like(weight)}
+        if bias is not None:
+            g["dbias"] = torch.empty_like(bias)
+        g["dstate"] = torch.empty((B, W - 1, NH * d), dtype=x.dtype, device=x.device)
+        ws = _workspace(lib.mlstm_short_conv_workspace_bytes(B, NH, T, d, W, dtype), x.device)
+        st = lib.mlstm_short_conv_bwd(
+            x.data_ptr(), x_row, weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
+            dy.data_ptr(), _ptr(dstate), g["dx"].data_ptr(), g["dweight"].data_ptr(),
+            _ptr(g.get("dbias")), g["dstate"].data_ptr(), _ptr(ws),
+            0 if ws is None else ws.numel(), B, NH, T, d, W, dtype, code, _stream_ptr(x.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_short_conv_bwd")
+    return g
+
+
+def _check_scan(u, dt, A, B, C, D, gate, dt_bias, lengths, dims, states, dy=None):
+    """Checks the scan's tensors -> (the arguments that a call begins with, sizes);
+    ``dims`` 3 with a length, 2 for one token."""
+    _check_floats("u", u)
+    form = "T, " if dims == 3 else ""
+    if u.dim() != dims:
+        raise ValueError(f"u must be [B, {form}channels], got shape {tuple(u.shape)}")
+    if not isinstance(A, torch.Tensor):
+        raise TypeError(f"A must be a torch.Tensor, got {type(A).__name__}")
+    if A.dim() != 2:
+        raise ValueError(f"A must be [channels, N], got shape {tuple(A.shape)}")
+    if not isinstance(B, torch.Tensor):
+        raise TypeError(f"B must be a torch.Tensor, got {type(B).__name__}")
+    if B.dim() != dims + 1:
+        raise ValueError(f"B must be [B, {form}G, N], got shape {tuple(B.shape)}")
+    batch, channels, N, G = u.shape[0], u.shape[-1], A.shape[1], B.shape[-2]
+    T = u.shape[1] if dims == 3 else 1
+    shared = (*u.shape[:-1], G, N)
+    rows = _require_rows([("u", u, u.shape, u.dtype, channels),
+                          ("dt", dt, u.shape, u.dtype, channels),
+                          ("B", B, shared, u.dtype, G * N), ("C", C, shared, u.dtype, G * N),
+                          ("gate", gate, u.shape, u.dtype, channels)], u.device)
+    named = [("A", A, (channels, N), torch.float32)]
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        if t is not None:
+            named.append((name, t, (channels,), torch.float32))
+    if lengths is not None:
+        named.append(("lengths", lengths, (batch,), torch.int32))
+    if dy is not None:
+        named.append(("dy", dy, u.shape, u.dtype))
+    for name, t in states.items():
+        if t is not None:
+            named.append((name, t, (batch, channels, N), torch.float32))
+    _require_all(named, u.device)
+    args = (u.data_ptr(), rows[0], dt.data_ptr(), rows[1], A.data_ptr(), B.data_ptr(), rows[2],
+            C.data_ptr(), rows[3], _ptr(D), _ptr(gate), rows[4], _ptr(dt_bias),
+            _ptr(states["state"]), _ptr(lengths))
+    return args, (batch, T, channels, G, N)
+
+
+def scan_state(B, channels, N, device):
+    """A fresh state of the selective scan: zeros [B, channels, N], float32."""
+    return torch.zeros((B, channels, N), dtype=torch.float32, device=device)
+
+
+def _scan(u, dt, A, B, C, D, gate, dt_bias, state, out_state, lengths, dims):
+    lib = load_library()
+    args, sizes = _check_scan(u, dt, A, B, C, D, gate, dt_bias, lengths, dims,
+                              {"state": state, "out_state": out_state})
+    code = _dtype_code(u)
+    with _on(u.device):
+        if out_state is None:
+            out_state = torch.empty((sizes[0], *A.shape), dtype=torch.float32, device=u.device)
+        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        ws = _workspace(lib.mlstm_scan_workspace_bytes(*sizes, code, 0), u.device)
+        st = lib.mlstm_scan_fwd(*args, y.data_ptr(), out_state.data_ptr(), _ptr(ws),
+                                0 if ws is None else ws.numel(), *sizes, code,
+                                _stream_ptr(u.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_scan_fwd")
+    return y, out_state
+
+
+def scan_fwd(u, dt, A, B, C, D=None, gate=None, dt_bias=None, state=None, out_state=None,
+             lengths=None):
+    """The selective state space scan over a sequence -> (y, new state).
+
+        s_t = exp(Delta_t A) s_{t-1} + Delta_t u_t B_t,   Delta_t = softplus(dt_t + dt_bias)
+        y_t = (C_t . s_t + D u_t) silu(gate_t)
+
+    u, dt, gate: [B, T, channels], B, C: [B, T, G, N] (channel c reads group
+    c // (channels // G)), all float32 or all bfloat16, rows of contiguous elements
+    that may be part of wider rows; A: [channels, N], D, dt_bias: [channels],
+    float32.  D, gate and dt_bias are left out where None.  ``state``: before the
+    sequence, [B, channels, N] float32 (zeros by default); ``out_state`` receives
+    the state after it and may be ``state``.  lengths: [B] int32, each sequence's
+    positions (beyond them y is zeros and the state stays).
+    """
+    return _scan(u, dt, A, B, C, D, gate, dt_bias, state, out_state, lengths, 3)
+
+
+def scan_step(u, dt, A, B, C, state, D=None, gate=None, dt_bias=None, out_state=None):
+    """One token of ``scan_fwd``: u, dt, gate [B, channels], B, C [B, G, N] -> (y,
+    new state); ``state`` is updated in place unless ``out_state`` is given."""
+    if not isinstance(state, torch.Tensor):
+        raise TypeError(f"state must be a torch.Tensor, got {type(state).__name__}")
+    return _scan(u, dt, A, B, C, D, gate, dt_bias, state,
+                 state if out_state is None else out_state, None, 2)
+
+
+def scan_bwd(u, dt, A, B, C, dy, D=None, gate=None, dt_bias=None, state=None, dstate=None,
+             lengths=None):
+    """Gradients of ``scan_fwd`` given dy and ``dstate`` = dL/d(new state) (zeros by
+    default) -> a dict with "du", "ddt", "dA", "dB", "dC", "dstate" (of the state
+    before the sequence) and, for the inputs that are given, "dD", "dgate",
+    "ddt_bias"."""
+    lib = load_library()
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError(f"dy must be a torch.Tensor, got {type(dy).__name__}")
+    args, sizes = _check_scan(u, dt, A, B, C, D, gate, dt_bias, lengths, 3,
+                              {"state": state, "dstate": dstate}, dy)
+    code = _dtype_code(u)
+
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+    with _on(u.device):
+        g = {n: like(t) for n, t in (("du", u), ("ddt", dt), ("dA", A), ("dB", B), ("dC", C),
+                                     ("dD", D), ("dgate", gate), ("ddt_bias", dt_bias))}
+        g["dstate"] = torch.empty((sizes[0], *A.shape), dtype=torch.float32, device=u.device)
+        ws = _workspace(lib.mlstm_scan_workspace_bytes(*sizes, code, 1), u.device)
+        st = lib.mlstm_scan_bwd(
+            *args, dy.data_ptr(), _ptr(dstate), *(_ptr(t) for t in g.values()), _ptr(ws),
+            0 if ws is None else ws.numel(), *sizes, code, _stream_ptr(u.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_scan_bwd")
+    return {n: t for n, t in g.items() if t is not None}
+
+
+def _check_ffn(x, w_gate, w_up, activation, dh=None):
+    _check_floats("x", x)
+    if x.dim() < 2:
+        raise ValueError(f"x must be [..., D], got shape {tuple(x.shape)}")
+    if not isinstance(w_gate, torch.Tensor):
+        raise TypeError(f"w_gate must be a torch.Tensor, got {type(w_gate).__name__}")
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate must be [F, D], got shape {tuple(w_gate.shape)}")
+    F, D = w_gate.shape[0], x.shape[-1]
+    named = [("x", x, x.shape, x.dtype), ("w_gate", w_gate, (F, D), x.dtype),
+             ("w_up", w_up, (F, D), x.dtype)]
+    if dh is not None:
+        named.append(("dh", dh, (*x.shape[:-1], F), x.dtype))
+    _require_all(named, x.device)
+    return (x.numel() // D if D else 0, D, F), _named_code("activation", FFN_ACTIVATIONS,
+                                                           activation)
+
+
+def gated_ffn_fwd(x, w_gate, w_up, activation="silu"):
+    """The gated feed-forward's input half -> h = act(x w_gate^T) * (x w_up^T).
+
+    x: [..., D], w_gate, w_up: [F, D] (as a linear layer's weights), all float32 or
+    all bfloat16, contiguous; h: [..., F].  activation: "silu" or "gelu" (g Phi(g)).
+    """
+    lib = load_library()
+    sizes, act = _check_ffn(x, w_gate, w_up, activation)
+    code = _dtype_code(x)
+    with _on(x.device):
+        h = torch.empty((*x.shape[:-1], sizes[2]), dtype=x.dtype, device=x.device)
+        ws = _workspace(lib.mlstm_gated_ffn_workspace_bytes(*sizes, code, 0), x.device)
+        st = lib.mlstm_gated_ffn_fwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                     h.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     *sizes, code, act, _stream_ptr(x.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_gated_ffn_fwd")
+    return h
+
+
+def gated_ffn_bwd(x, w_gate, w_up, dh, activation="silu"):
+    """Gradients of ``gated_ffn_fwd`` given dh -> (dx, dw_gate, dw_up)."""
+    lib = load_library()
+    if not isinstance(dh, torch.Tensor):
+        raise TypeError(f"dh must be a torch.Tensor, got {type(dh).__name__}")
+    sizes, act = _check_ffn(x, w_gate, w_up, activation, dh)
+    code = _dtype_code(x)
+    with _on(x.device):
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w_gate), torch.empty_like(w_up)
+        ws = _workspace(lib.mlstm_gated_ffn_workspace_bytes(*sizes, code, 1), x.device)
+        st = lib.mlstm_gated_ffn_bwd(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                     dh.data_ptr(), dx.data_ptr(), dwg.data_ptr(),
+                                     dwu.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     *sizes, code, act, _stream_ptr(x.device))
+    if st != 0:
+        raise MlstmError(st, "mlstm_gated_ffn_bwd")
+    return dx, dwg, dwu
