@@ -25,6 +25,7 @@ using product::f32x4;
 using product::Operand;
 
 using Large = product::Shape<256, 256, 2, 4>;
+using Medium = product::Shape<128, 256, 2, 4>;
 using Small = product::Shape<128, 128, 2, 2>;
 
 constexpr int kPlanes = 3, kTerms = 6;  // of float32
@@ -42,87 +43,76 @@ __device__ inline Act activation(float g, bool gelu) {
   return {g * s, rowvec::silu_slope(g, s)};
 }
 
-__device__ inline void store4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
-__device__ inline void store4(__hip_bfloat16* p, f32x4 x) {
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(rowvec::to_bf16(x[0], x[1]), rowvec::to_bf16(x[2], x[3]));
-}
-
 struct Sizes {
   int64_t M, D, F;
   int terms;
   bool gelu;
 };
 
-// h, or with GRAD G = [dg | du], for a tile of rows and of F
+// h, or with GRAD G = [dg | du], in tiles of rows and of F
 template <typename T, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operand wu, Operand x,
                                                               Sizes n, const T* dh, T* out) {
   __shared__ __align__(1024) char lds[S::kLds];
-  constexpr int kF = S::kBP / 2;
-  unsigned ip, iq;
-  product::map_tile(blockIdx.x, unsigned((n.F + kF - 1) / kF),
-                    unsigned((n.M + S::kBQ - 1) / S::kBQ), ip, iq);
-  const int64_t p0 = int64_t(ip) * kF, q0 = int64_t(iq) * S::kBQ;
-  f32x4 acc[S::kP][S::kQ];
-  product::multiply<S, true>(wg, wu, x, n.D, n.terms, p0, q0, lds, acc);
+  constexpr int kF = S::kBP / 2, kStores = (GRAD ? S::kP : S::kP / 2) * S::kQ;
+  const unsigned np = unsigned((n.F + kF - 1) / kF), nq = unsigned((n.M + S::kBQ - 1) / S::kBQ);
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t f0 = p0 + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
-                m0 = q0 + wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+  product::tiles<S, true, kStores>(
+      wg, wu, x, n.D, n.terms, np, nq, 1, lds,
+      [&](unsigned ip, unsigned iq, const f32x4(&acc)[S::kP][S::kQ]) {
+        const int64_t f0 = int64_t(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
+                      q0 = int64_t(iq) * S::kBQ;
+        const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+        const product::Rows<T> rows(out, q0, n.M, GRAD ? 2 * n.F : n.F);
 #pragma unroll
-  for (int j = 0; j < S::kQ; ++j) {
-    const int64_t m = m0 + j * 16;
-    if (m >= n.M) continue;
+        for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
-    for (int i = 0; i < S::kP / 2; ++i) {
-      const int64_t f = f0 + i * 16;
-      if (f >= n.F) continue;
-      const f32x4 g = acc[i][j], u = acc[i + S::kP / 2][j];
-      f32x4 a, b;
-      if constexpr (GRAD) {
-        float d[4];
-        rowvec::load(dh + m * n.F + f, d);
+          for (int i = 0; i < S::kP / 2; ++i) {
+            const int64_t f = f0 + i * 16, m = q0 + m0 + j * 16;
+            const f32x4 g = acc[i][j], u = acc[i + S::kP / 2][j];
+            f32x4 a, b;
+            if constexpr (GRAD) {
+              float d[4] = {};
+              if (m < n.M && f < n.F) rowvec::load(dh + m * n.F + f, d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const Act act = activation(g[e], n.gelu);
-          a[e] = d[e] * u[e] * act.slope;
-          b[e] = d[e] * act.value;
-        }
-        store4(out + m * 2 * n.F + f, a);
-        store4(out + (m * 2 + 1) * n.F + f, b);
-      } else {
+              for (int e = 0; e < 4; ++e) {
+                const Act act = activation(g[e], n.gelu);
+                a[e] = d[e] * u[e] * act.slope;
+                b[e] = d[e] * act.value;
+              }
+              rows.put(m0 + j * 16, f, n.F, a);
+              rows.put(m0 + j * 16, n.F + f, 2 * n.F, b);
+            } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = activation(g[e], n.gelu).value * u[e];
-        store4(out + m * n.F + f, a);
-      }
-    }
-  }
+              for (int e = 0; e < 4; ++e) a[e] = activation(g[e], n.gelu).value * u[e];
+              rows.put(m0 + j * 16, f, n.F, a);
+            }
+          }
+      });
 }
 
-// out[q][p], rows q from `split` on in out2
+// out[q][p], with two groups of q the second one in out2
 template <typename T, typename S>
 __global__ __launch_bounds__(S::kThreads) void product_kernel(Operand left, Operand right,
-                                                              int64_t k, int terms, T* out,
-                                                              T* out2, int64_t split) {
+                                                              int64_t k, int terms, int groups,
+                                                              T* out, T* out2) {
   __shared__ __align__(1024) char lds[S::kLds];
-  unsigned ip, iq;
-  product::map_tile(blockIdx.x, unsigned((left.rows + S::kBP - 1) / S::kBP),
-                    unsigned((right.rows + S::kBQ - 1) / S::kBQ), ip, iq);
-  const int64_t p0 = int64_t(ip) * S::kBP, q0 = int64_t(iq) * S::kBQ;
-  f32x4 acc[S::kP][S::kQ];
-  product::multiply<S, false>(left, left, right, k, terms, p0, q0, lds, acc);
+  const unsigned np = unsigned((left.rows + S::kBP - 1) / S::kBP),
+                 of_group = unsigned((right.rows + S::kBQ - 1) / S::kBQ);
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t first = p0 + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4,
-                q1 = q0 + wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+  product::tiles<S, false, S::kP * S::kQ>(
+      left, left, right, k, terms, np, of_group * groups, groups, lds,
+      [&](unsigned ip, unsigned iq, const f32x4(&acc)[S::kP][S::kQ]) {
+        const int64_t p0 = int64_t(ip) * S::kBP + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4;
+        const int q0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+        const product::Rows<T> rows(iq < of_group ? out : out2, int64_t(iq % of_group) * S::kBQ,
+                                    right.rows, left.rows);
 #pragma unroll
-  for (int j = 0; j < S::kQ; ++j) {
-    const int64_t q = q1 + j * 16;
-    if (q >= right.rows) continue;
-    T* row = q < split ? out + q * left.rows : out2 + (q - split) * left.rows;
+        for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
-    for (int i = 0; i < S::kP; ++i)
-      if (first + i * 16 < left.rows) store4(row + first + i * 16, acc[i][j]);
-  }
+          for (int i = 0; i < S::kP; ++i)
+            rows.put(q0 + j * 16, p0 + i * 16, left.rows, acc[i][j]);
+      });
 }
 
 // ---- operands: planes of float32, and transposes
@@ -214,13 +204,13 @@ constexpr int kTermsOf = sizeof(T) == 4 ? kTerms : 1;
 template <typename T>
 Operand as_rows(const void* p, int64_t rows, int64_t k, Arena& ws, hipStream_t stream, bool run) {
   if constexpr (sizeof(T) == 2) {
-    return {static_cast<const uint16_t*>(p), rows, 0};
+    return {static_cast<const uint16_t*>(p), rows, 0, 0};
   } else {
     uint16_t* out = ws.take<uint16_t>(kPlanes * rows * k);
     if (run)
       split_kernel<<<unsigned((rows * k + 1023) / 1024), 256, 0, stream>>>(
           static_cast<const float*>(p), rows * k, out, rows * k);
-    return {out, rows, rows * k};
+    return {out, rows, rows * k, 0};
   }
 }
 
@@ -234,43 +224,53 @@ void transposed(const void* p, int64_t rows, int64_t cols, uint16_t* out, int64_
 }
 
 constexpr int64_t kCUs = 256;
-// Tiles of 256 x 256, one workgroup to a CU, where they fill the card; else 128 x 128
-bool large_tiles(int64_t p, int64_t q) {
-  return ((p + 255) / 256) * ((q + 255) / 256) >= kCUs / 2;
+
+template <typename S>
+int64_t tiles_of(int64_t p, int64_t q) {
+  return ((p + S::kBP - 1) / S::kBP) * ((q + S::kBQ - 1) / S::kBQ);
+}
+// Workgroups that a CU holds at a time
+template <typename S>
+constexpr int kPerCu = S::kLds <= 64 * 1024 ? 2 : 1;
+
+// f(shape) with the tile of the least time for p x q outputs (in each of `groups`):
+// the rounds of tiles that a CU takes, at what each takes.
+template <typename F>
+hipError_t with_shape(int64_t p, int64_t q, int64_t groups, F&& f) {
+  auto rounds = [&](int64_t tiles, int64_t at_once) {
+    return double((tiles * groups + kCUs * at_once - 1) / (kCUs * at_once));
+  };
+  const double large = rounds(tiles_of<Large>(p, q), 1),
+               medium = 0.6 * rounds(tiles_of<Medium>(p, q), 1);
+  const int64_t n = tiles_of<Small>(p, q) * groups;
+  const double small = n <= kCUs ? 0.4 : 0.65 * rounds(tiles_of<Small>(p, q), 2);
+  if (small < large && small < medium) return f(Small{});
+  if (medium < large) return f(Medium{});
+  return f(Large{});
 }
 
-template <typename T, typename S, bool GRAD>
-hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
-                   const void* dh, void* out, hipStream_t stream) {
-  auto kernel = gate_up_kernel<T, S, GRAD>;
-  constexpr int kF = S::kBP / 2;
-  const int64_t wgs = ((n.F + kF - 1) / kF) * ((n.M + S::kBQ - 1) / S::kBQ);
-  kernel<<<unsigned(wgs), S::kThreads, 0, stream>>>(wg, wu, x, n, static_cast<const T*>(dh),
-                                                          static_cast<T*>(out));
-  return hipGetLastError();
-}
 template <typename T, bool GRAD>
 hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
                    const void* dh, void* out, hipStream_t stream) {
-  return large_tiles(2 * n.F, n.M) ? gate_up<T, Large, GRAD>(wg, wu, x, n, dh, out, stream)
-                                   : gate_up<T, Small, GRAD>(wg, wu, x, n, dh, out, stream);
+  return with_shape(2 * n.F, n.M, 1, [&](auto shape) {
+    using S = decltype(shape);
+    const int64_t tiles = tiles_of<S>(2 * n.F, n.M), most = kCUs * kPerCu<S>;
+    gate_up_kernel<T, S, GRAD><<<unsigned(tiles < most ? tiles : most), S::kThreads, 0, stream>>>(
+        wg, wu, x, n, static_cast<const T*>(dh), static_cast<T*>(out));
+    return hipGetLastError();
+  });
 }
 
-template <typename T, typename S>
-hipError_t multiply_as(const Operand& l, const Operand& r, int64_t k, void* out, void* out2,
-                       int64_t split, hipStream_t stream) {
-  auto kernel = product_kernel<T, S>;
-  const int64_t wgs = ((l.rows + S::kBP - 1) / S::kBP) * ((r.rows + S::kBQ - 1) / S::kBQ);
-  kernel<<<unsigned(wgs), S::kThreads, 0, stream>>>(l, r, k, kTermsOf<T>,
-                                                          static_cast<T*>(out),
-                                                          static_cast<T*>(out2), split);
-  return hipGetLastError();
-}
 template <typename T>
-hipError_t multiply(const Operand& l, const Operand& r, int64_t k, void* out, void* out2,
-                    int64_t split, hipStream_t stream) {
-  return large_tiles(l.rows, r.rows) ? multiply_as<T, Large>(l, r, k, out, out2, split, stream)
-                                     : multiply_as<T, Small>(l, r, k, out, out2, split, stream);
+hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int groups, void* out,
+                    void* out2, hipStream_t stream) {
+  return with_shape(l.rows, r.rows, groups, [&](auto shape) {
+    using S = decltype(shape);
+    const int64_t tiles = tiles_of<S>(l.rows, r.rows) * groups, most = kCUs * kPerCu<S>;
+    product_kernel<T, S><<<unsigned(tiles < most ? tiles : most), S::kThreads, 0, stream>>>(
+        l, r, k, kTermsOf<T>, groups, static_cast<T*>(out), static_cast<T*>(out2));
+    return hipGetLastError();
+  });
 }
 
 // `run` false: only the workspace's size
@@ -307,10 +307,11 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
   transposed<T>(a.w_up, F, D, wt + F, F, 2 * F, wt_plane, stream);
   transposed<T>(a.x, M, D, xt, pitch, pitch, xt_plane, stream);
   transposed<T>(G, M, 2 * F, gt, pitch, pitch, gt_plane, stream);
-  const hipError_t e = multiply<T>({wt, D, wt_plane}, G_rows, 2 * F, g.dx, nullptr, M, stream);
+  const hipError_t e =
+      multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, stream);
   if (e != hipSuccess) return e;
-  return multiply<T>({xt, D, xt_plane}, {gt, 2 * F, gt_plane}, pitch, g.dw_gate, g.dw_up, F,
-                     stream);
+  return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, 2, g.dw_gate,
+                     g.dw_up, stream);
 }
 
 }  // namespace

@@ -1,15 +1,19 @@
 // Tiles of a matrix product on the bf16 matrix instruction, for the gated
 // feed-forward: out[q][p] = sum_k L[p][k] R[q][k], both operands rows of k.
 //
-// A workgroup has BP x BQ outputs; its WP x WQ waves have a block each, in
-// 16 x 16 accumulators.  The left operand's rows are the outputs' fast index, so
+// A workgroup has BP x BQ outputs at a time; its WP x WQ waves have a block each,
+// in 16 x 16 accumulators.  The left operand's rows are the outputs' fast index, so
 // a lane holds four neighbouring outputs of a row (lane l: q = l % 16, p = 4 (l /
-// 16) ..) and stores them together.  Both operands' tiles of 64 columns are copied
-// global -> LDS without registers into two buffers, the next tile's while one is
-// multiplied; eight lanes copy a row of 128 bytes, and the 16-byte pieces of a row
-// lie in the order piece ^ (row & 7), so that the 16 rows that an instruction's
-// lanes read in one column do not share banks.  Rows beyond an operand's, and
-// columns beyond k, are read out of the buffer's range: zeros.
+// 16) ..) and stores them together.  Both operands' pieces of 64 columns are copied
+// global -> LDS without registers into two slots.  A wave reads the fragments of 32
+// columns into registers while it multiplies those of the 32 before, so a slot is
+// free when half of its products are done, and is filled again, two pieces ahead,
+// beside the other half's.  Workgroups stay for several tiles: the copies run on
+// into the next tile, whose first pieces come in while this one is stored.  Eight
+// lanes copy a row's 128 bytes, a cache line, and its 16-byte parts lie in the order
+// part ^ (row & 7), so that the 16 rows that an instruction's lanes read in one
+// column do not share banks.  Rows beyond an operand's, and columns beyond k, are
+// read out of the buffer's range: zeros.
 //
 // float32 operands come as three bf16 planes (24 bits: exact), and the product is
 // the sum of the six plane products above 2^-24, taken one after the other as if k
@@ -17,6 +21,7 @@
 // small sums.
 #pragma once
 
+#include "row_vec.h"
 #include "tile_common.h"
 
 namespace mlstm {
@@ -26,12 +31,14 @@ using tilecommon::bf16x8;
 using tilecommon::i32x4;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kStep = 64;  // columns of a tile
+constexpr int kStep = 64;  // columns of a piece
 
-// rows of k elements; planes of a float32 operand are `plane` elements apart
+// rows of k elements; planes of a float32 operand are `plane` elements apart.  A
+// right operand may be several groups of rows, `group` elements apart, each with
+// tiles of its own.
 struct Operand {
   const uint16_t* p;
-  int64_t rows, plane;
+  int64_t rows, plane, group;
 };
 
 template <int BP, int BQ, int WP, int WQ>
@@ -39,10 +46,23 @@ struct Shape {
   static constexpr int kBP = BP, kBQ = BQ, kWP = WP, kWQ = WQ;
   static constexpr int kThreads = 64 * WP * WQ;
   static constexpr int kPassRows = kThreads / 8;  // rows that one copy of every thread covers
+  static constexpr int kPassesP = BP / kPassRows, kPassesQ = BQ / kPassRows;
   static constexpr int kP = BP / WP / 16, kQ = BQ / WQ / 16;  // a wave's accumulators
-  static constexpr int kBuffer = (BP + BQ) * kStep * 2;       // bytes
-  static constexpr int kLds = 2 * kBuffer;
+  static constexpr int kSlot = (BP + BQ) * kStep * 2;         // bytes
+  static constexpr int kLds = 2 * kSlot;
 };
+
+// 16 bytes per lane from rsrc + voffset to LDS at dst + 16 * lane (dst is
+// wave-uniform).  The wait is the caller's.  The wait states cover scalar registers
+// that a vector instruction has just written (5).
+__device__ inline void copy_piece(i32x4 rsrc, unsigned voffset, unsigned dst) {
+  rsrc = tilecommon::sreg(rsrc);
+  dst = tilecommon::sreg(dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(dst), "v"(voffset), "s"(rsrc)
+               : "memory", "m0");
+}
 
 // The planes of term s of six (a bf16 operand has plane 0 only)
 __device__ inline int left_plane(int s) { return (0x001102 >> (4 * s)) & 15; }   // 2 0 1 1 0 0
@@ -61,90 +81,183 @@ __device__ inline void map_tile(unsigned wg, unsigned np, unsigned nq, unsigned&
   ip = in / high;
 }
 
-// acc[i][j]: accumulators of the wave's p block i and q block j.  DUAL: the left
+// What a wave multiplies at a time: 32 columns of its rows
+template <typename S>
+struct Fragments {
+  bf16x8 l[S::kP], r[S::kQ];
+};
+
+// The workgroup's tiles of np x nq, one after the other (of R's groups nq / groups
+// each); store(ip, iq, acc) with
+// acc[i][j] the accumulators of the wave's p block i and q block j.  DUAL: the left
 // rows are those of two operands in turn, a wave's first half of its blocks from L
-// and the second half from L2, for the same output columns (BP / 2 of them from
-// p0 on).
-template <typename S, bool DUAL>
-__device__ inline void multiply(const Operand& L, const Operand& L2, const Operand& R, int64_t k,
-                                int terms, int64_t p0, int64_t q0, char* lds,
-                                f32x4 (&acc)[S::kP][S::kQ]) {
+// and the second half from L2, for the same output columns (BP / 2 to a tile).
+// `store` issues STORES stores, whatever the tile: their completion is not waited
+// for with the next tile's first copies, which are older.
+template <typename S, bool DUAL, int STORES, typename F>
+__device__ inline void tiles(const Operand& L, const Operand& L2, const Operand& R, int64_t k,
+                             int terms, unsigned np, unsigned nq, unsigned groups, char* lds,
+                             F&& store) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wp = wave / S::kWQ, wq = wave % S::kWQ;
-  // the copy of this lane: row threadIdx.x / 8 of a pass, LDS piece threadIdx.x % 8
-  const int row = threadIdx.x / 8, piece = (threadIdx.x % 8) ^ (row & 7);
-  const unsigned pitch = unsigned(k) * 2, at = row * pitch + piece * 16;
-  const unsigned out = tilecommon::lds_addr(lds) + wave * 1024;
+  const unsigned n = np * nq, of_group = nq / groups;
   const int steps = int((k + kStep - 1) / kStep);
-  auto words = [&](const Operand& o, int64_t first, int plane) {
+
+  // ---- copies: a cursor over the pieces of all tiles
+  constexpr int kHalf = S::kBP / S::kWP / 2;  // DUAL: rows of one operand
+  static_assert(kHalf % 8 == 0, "a wave's copy is of one operand");
+  const int row = threadIdx.x / 8, part = (threadIdx.x % 8) ^ (row & 7);
+  const unsigned pitch = unsigned(k) * 2, lane_at = (lane / 8) * pitch + part * 16;
+  const unsigned out = tilecommon::lds_addr(lds) + wave * 1024;
+  auto words = [&](const Operand& o, int64_t first, int plane, unsigned group) {
     const int64_t left = o.rows - first;
-    return tilecommon::rsrc_words(o.p + plane * o.plane + first * k,
+    return tilecommon::rsrc_words(o.p + plane * o.plane + group * o.group + first * k,
                                   left > 0 ? (left < 256 ? left : 256) * k * 2 : 0);
   };
-  constexpr int kPassesP = S::kBP / S::kPassRows, kPassesQ = S::kBQ / S::kPassRows;
-  constexpr int kHalf = DUAL ? S::kBP / S::kWP / 2 : 0;
-  static_assert(!DUAL || kHalf == S::kPassRows, "a pass is of one operand");
   i32x4 left = {}, left2 = {}, right = {};
-  auto copy = [&](int s, int step, int buffer) {
-    if (step == 0) {
-      const int lp = terms > 1 ? left_plane(s) : 0, rp = terms > 1 ? right_plane(s) : 0;
-      left = words(L, p0, lp);
-      if constexpr (DUAL) left2 = words(L2, p0, lp);
-      right = words(R, q0, rp);
+  unsigned tile = blockIdx.x;
+  int step = 0, term = 0, slot = 0;
+  // The next piece's copies, for which begin() makes ready; beyond the last tile
+  // they read zeros, so that as many are in flight at any time.
+  unsigned col = 0;
+  bool in = false;
+  auto begin = [&]() {
+    if (step == 0 && tile < n) {
+      unsigned ip, iq;
+      map_tile(tile, np, nq, ip, iq);
+      const int64_t p0 = int64_t(ip) * (DUAL ? S::kBP / 2 : S::kBP), q0 = int64_t(iq % of_group) * S::kBQ;
+      const int lp = terms > 1 ? left_plane(term) : 0, rp = terms > 1 ? right_plane(term) : 0;
+      left = words(L, p0, lp, 0);
+      if constexpr (DUAL) left2 = words(L2, p0, lp, 0);
+      right = words(R, q0, rp, iq / of_group);
     }
-    // columns beyond k (a multiple of 8) in the last tile
-    const unsigned off =
-        step * kStep + piece * 8 < k ? at + step * (kStep * 2) : tilecommon::kOutOfRange;
-    const unsigned to = out + buffer * S::kBuffer;
-#pragma unroll
-    for (int i = 0; i < kPassesP; ++i) {
-      const int first = DUAL ? i / 2 * S::kPassRows : i * S::kPassRows;
-      tilecommon::copy16(DUAL && (i & 1) ? left2 : left, off + first * pitch,
-                         to + i * S::kPassRows * 128);
+    // columns beyond k (a multiple of 8) in a plane's last piece are zeros
+    in = tile < n && step * kStep + part * 8 < k;
+    col = step * (kStep * 2);
+    if (++step == steps) {
+      step = 0;
+      if (++term == terms) term = 0, tile += gridDim.x;
     }
-#pragma unroll
-    for (int i = 0; i < kPassesQ; ++i)
-      tilecommon::copy16(right, off + i * S::kPassRows * pitch,
-                         to + (S::kBP + i * S::kPassRows) * 128);
   };
-#pragma unroll
-  for (int i = 0; i < S::kP; ++i)
-#pragma unroll
-    for (int j = 0; j < S::kQ; ++j) acc[i][j] = f32x4{};
+  auto copy = [&](int i) {  // pass i of kPassesP + kPassesQ
+    const int first = i * S::kPassRows + wave * 8;
+    const unsigned to = out + slot * S::kSlot + i * S::kPassRows * (kStep * 2);
+    if (i < S::kPassesP) {
+      const bool second = DUAL && (first / kHalf & 1);
+      const int from = DUAL ? first / (2 * kHalf) * kHalf + first % kHalf : first;
+      copy_piece(second ? left2 : left,
+                 in ? lane_at + col + from * pitch : tilecommon::kOutOfRange, to);
+    } else {
+      const int from = first - S::kBP;
+      copy_piece(right, in ? lane_at + col + from * pitch : tilecommon::kOutOfRange, to);
+    }
+  };
+  constexpr int kCopies = S::kPassesP + S::kPassesQ;
 
-  copy(0, 0, 0);
-  int s = 0, step = 0, buffer = 0;
-  for (;;) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    int s1 = s, step1 = step + 1;
-    if (step1 == steps) step1 = 0, ++s1;
-    const bool more = s1 < terms;
-    if (more) copy(s1, step1, buffer ^ 1);
-    const char* base = lds + buffer * S::kBuffer;
-    const char* lp = base + (wp * (S::kBP / S::kWP) + lane % 16) * 128;
-    const char* rp = base + (S::kBP + wq * (S::kBQ / S::kWQ) + lane % 16) * 128;
+  // ---- reads and products
+  const int half[2] = {((lane / 16) ^ (lane & 7)) * 16, ((4 + lane / 16) ^ (lane & 7)) * 16};
+  const char* lp = lds + (wp * (S::kBP / S::kWP) + lane % 16) * (kStep * 2);
+  const char* rp = lds + (S::kBP + wq * (S::kBQ / S::kWQ) + lane % 16) * (kStep * 2);
+  auto read_l = [&](int from, int h, int i, Fragments<S>& f) {
+    f.l[i] = *reinterpret_cast<const bf16x8*>(lp + from * S::kSlot + i * 16 * (kStep * 2) + half[h]);
+  };
+  auto read_r = [&](int from, int h, int j, Fragments<S>& f) {
+    f.r[j] = *reinterpret_cast<const bf16x8*>(rp + from * S::kSlot + j * 16 * (kStep * 2) + half[h]);
+  };
+  f32x4 acc[S::kP][S::kQ];
+  // The products of `now`, and in turn with them the reads of half h of slot `from`
+  // into `next`, and if `with` says so the next piece's copies.
+  auto multiply = [&](const Fragments<S>& now, Fragments<S>& next, int from, int h, auto with) {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int slot = ((kk * 4 + lane / 16) ^ (lane & 7)) * 16;
-      bf16x8 l[S::kP], r[S::kQ];
+    for (int i = 0; i < S::kP; ++i) {
+      if constexpr (with()) {
+#pragma unroll
+        for (int c = i; c < kCopies; c += S::kP) copy(c);
+      }
+#pragma unroll
+      for (int j = i; j < S::kQ; j += S::kP) read_r(from, h, j, next);
+      read_l(from, h, i, next);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < S::kQ; ++j)
-        r[j] = *reinterpret_cast<const bf16x8*>(rp + j * 16 * 128 + slot);
-#pragma unroll
-      for (int i = 0; i < S::kP; ++i)
-        l[i] = *reinterpret_cast<const bf16x8*>(lp + i * 16 * 128 + slot);
-#pragma unroll
-      for (int i = 0; i < S::kP; ++i)
-#pragma unroll
-        for (int j = 0; j < S::kQ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(l[i], r[j], acc[i][j], 0, 0, 0);
+        acc[i][j] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.l[i], now.r[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (!more) break;
-    s = s1, step = step1, buffer ^= 1;
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // waits for this wave's copies but for the newest `left` operations, and its
+  // reads, then for the workgroup's
+  auto arrive = [&](auto newer) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(newer()) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    begin();
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(i);
+    slot ^= 1;
   }
+  arrive(std::integral_constant<int, kCopies>{});
+  Fragments<S> a, b;
+#pragma unroll
+  for (int j = 0; j < S::kQ; ++j) read_r(0, 0, j, a);
+#pragma unroll
+  for (int i = 0; i < S::kP; ++i) read_l(0, 0, i, a);
+  bool stored = false;
+  for (unsigned t = blockIdx.x; t < n; t += gridDim.x) {
+#pragma unroll
+    for (int i = 0; i < S::kP; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kQ; ++j) acc[i][j] = f32x4{};
+    for (int s = steps * terms; s > 0; --s) {
+      multiply(a, b, slot, 1, std::false_type{});
+      // this slot has been read, and the other one is whole
+      if (stored)
+        arrive(std::integral_constant<int, STORES>{});
+      else
+        arrive(std::integral_constant<int, 0>{});
+      stored = false;
+      begin();
+      multiply(b, a, slot ^ 1, 0, std::true_type{});
+      slot ^= 1;
+    }
+    unsigned ip, iq;
+    map_tile(t, np, nq, ip, iq);
+    store(ip, iq, acc);
+    stored = true;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
+
+// Rows of outputs, 256 at most, from `first` on.  Stores beyond the last row or a
+// row's end are dropped, but issued all the same (see `tiles`).
+template <typename T>
+struct Rows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int64_t width;
+  __device__ Rows(T* base, int64_t first, int64_t rows, int64_t width_)
+      : rsrc(tilecommon::make_rsrc(
+            base + first * width_,
+            (rows - first < 256 ? rows - first : 256) * width_ * int64_t(sizeof(T)))),
+        width(width_) {}
+  // columns c .. c + 3 of row `first` + i, where c is below `columns`
+  __device__ void put(int i, int64_t c, int64_t columns, f32x4 x) const {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    const unsigned at = c < columns ? unsigned((i * width + c) * int64_t(sizeof(T)))
+                                    : tilecommon::kOutOfRange;
+    if constexpr (sizeof(T) == 4)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rsrc, at, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(
+          u32x2{rowvec::to_bf16(x[0], x[1]), rowvec::to_bf16(x[2], x[3])}, rsrc, at, 0, 0);
+  }
+};
 
 }  // namespace product
 }  // namespace mlstm
