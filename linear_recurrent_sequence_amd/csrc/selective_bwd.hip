@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
       if (a.dt_bias && on) rowvec::load(a.dt_bias + w.ch.first + vec_of(i), bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float dl = on ? softplus(x[e] + bias[e]).value : 0.0f;
+        const float dl = on ? softplus(x[e] + bias[e]) : 0.0f;
         steps[row_of(i)][vec_of(i) + e] = make_float2(dl, dl * v[e]);
       }
       if constexpr (CUT) {
@@ -231,7 +231,7 @@ __device__ inline void channel_sums(float (&x)[128], int lane) {
 }
 
 template <typename T, int NW, int NS, int TL, bool GATE, bool CUT>
-__global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, SelectiveGrads gr,
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(SelectiveScan a, SelectiveGrads gr,
                                                         Segments seg, Kept kept) {
   static_assert(NS * TL == 64, "a wave's products of a tile are 128 to a lane");
   constexpr int kThreads = 64 * NW, V = Vec<NW, NS, TL>::V, kVecs = kChannels / V;
@@ -286,7 +286,6 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
   int64_t t0 = w.first + (w.last - 1 - w.first) / TL * TL;
   load(t0);
   for (; t0 >= w.first; t0 -= TL) {
-    float delta[kItems][V], slope[kItems][V], g[kItems][V];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       if (row_of(i) >= TL) continue;
@@ -297,29 +296,28 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
       if (a.dt_bias && on) rowvec::load(a.dt_bias + w.ch.first + vec_of(i), bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const Softplus sp = softplus(x[e] + bias[e]);
-        delta[i][e] = on ? sp.value : 0.0f;
-        slope[i][e] = on ? sp.slope : 0.0f;
-        steps[row_of(i)][vec_of(i) + e] = make_float2(delta[i][e], delta[i][e] * v[e]);
+        const float delta = on ? softplus(x[e] + bias[e]) : 0.0f;
+        steps[row_of(i)][vec_of(i) + e] = make_float2(delta, delta * v[e]);
       }
-      rowvec::floats(d[i], g[i]);
+      rowvec::floats(d[i], x);
       if constexpr (GATE) {
         rowvec::floats(z[i], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[i][e] *= v[e] * rowvec::sigmoid(v[e]);
+        for (int e = 0; e < V; ++e) x[e] *= v[e] * rowvec::sigmoid(v[e]);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) gs[row_of(i)][vec_of(i) + e] = g[i][e];
+      for (int e = 0; e < V; ++e) gs[row_of(i)][vec_of(i) + e] = x[e];
     }
     bc.put(shared);
     __syncthreads();
 
     float x[128];  // [token][state]: s and a, then the products behind dB and dC
-    float start[NS];
+    float start[NS], own[NS], through = 0.0f;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       start[j] = CUT ? __builtin_fmaf(rowvec::exp2_fast(A[j] * sum), s0[j], s[j]) : s[j];
       s[j] = start[j];
+      own[j] = 0.0f;
     }
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
@@ -337,7 +335,18 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
         x[2 * (t * NS + j) + 1] = s[j];
       }
       if constexpr (GATE) parts[2][wave][t][lane] = p;
+      through += st.x;
+      if (t % 2) __builtin_amdgcn_sched_barrier(0);
     }
+    // the way back reads LDS again: kept from here, what it reads would take all the
+    // registers that are left
+    asm volatile("" ::: "memory");
+    // what the tile's own g make of the gradient before it, beside the gradient
+    // itself: that of the tokens behind then takes one rounded factor a tile, not one a
+    // token, and what is left of it after thousands of tokens stays exact
+    float last[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) last[j] = S[j];
 #pragma unroll
     for (int t = TL - 1; t >= 0; --t) {
       const float2 st = steps[t][lane];
@@ -351,6 +360,7 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
         const int at = 2 * (t * NS + j);
         const float now = x[at + 1], old = t > 0 ? x[t > 0 ? at + 1 - 2 * NS : 0] : start[j];
         S[j] = __builtin_fmaf(gt, C[j], S[j]);
+        own[j] = __builtin_fmaf(gt, C[j], own[j]) * x[at];
         h = __builtin_fmaf(S[j], B[j], h);
         const float e = S[j] * x[at], f = e * old;
         q = __builtin_fmaf(f, A[j], q);
@@ -361,7 +371,14 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
       }
       parts[0][wave][t][lane] = h;
       parts[1][wave][t][lane] = q * rowvec::kLn2;  // A' is A log2 e
+      // here, not where they are needed: their operands would have to be kept
+#pragma unroll
+      for (int j = 0; j < NS; ++j) asm volatile("" : "+v"(dA[j]), "+v"(own[j]));
+      if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      S[j] = __builtin_fmaf(rowvec::exp2_fast(A[j] * through), last[j], own[j]);
     channel_sums(x, lane);
     {
       const int64_t t = t0 + lane / NS, n = wave * NS + lane % NS;
@@ -369,9 +386,9 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
         kept.shared[((blockIdx.x % (a.G * tiles_of_group(a.channels, a.G)) * a.batch + w.b) * a.T +
                      t) * a.N + n] = make_float2(x[0], x[1]);
     }
-    Raw<T, V> u0[kItems], z0[kItems], d0[kItems];
+    Raw<T, V> u0[kItems], z0[kItems], d0[kItems], dt0[kItems];
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) u0[i] = u[i], z0[i] = z[i], d0[i] = d[i];
+    for (int i = 0; i < kItems; ++i) u0[i] = u[i], z0[i] = z[i], d0[i] = d[i], dt0[i] = dt[i];
     if (t0 > w.first) load(t0 - TL);
     __syncthreads();
 #pragma unroll
@@ -392,13 +409,18 @@ __global__ __launch_bounds__(64 * NW) void grads_kernel(SelectiveScan a, Selecti
       const int64_t at = (w.b * a.T + t) * a.channels + c;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        o[e] = __builtin_fmaf(delta[i][e], h[e], skip[e] * g[i][e]);
-        dD[i][e] = __builtin_fmaf(g[i][e], uu[e], dD[i][e]);
+        const float g = gs[r][v0 + e];  // this thread's own
+        o[e] = __builtin_fmaf(steps[r][v0 + e].x, h[e], skip[e] * g);
+        dD[i][e] = __builtin_fmaf(g, uu[e], dD[i][e]);
       }
       rowvec::store(static_cast<T*>(gr.du) + at, o);
+      float pre[V], bias[V] = {};
+      rowvec::floats(dt0[i], pre);
+      if (a.dt_bias) rowvec::load(a.dt_bias + c, bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        o[e] = __builtin_fmaf(uu[e], h[e], q[e]) * slope[i][e];
+        o[e] = t < end ? __builtin_fmaf(uu[e], h[e], q[e]) * rowvec::sigmoid(pre[e] + bias[e])
+                       : 0.0f;
         dbias[i][e] += o[e];
       }
       rowvec::store(static_cast<T*>(gr.ddt) + at, o);
@@ -480,19 +502,22 @@ constexpr int64_t kSimds = 1024;
 int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 int tile_of(int64_t N) { return N <= 32 ? 16 : 8; }
 
-// How many segments; see the forward's rule.  Operations to a state and token:
-// 27 in one piece, 30 cut.
+// How many segments: operations to a state and token are 27 in one piece, 30 cut;
+// see the forward's time_of.
 Segments segments_of(const SelectiveScan& a) {
   const int64_t tiles = (a.T + tile_of(a.N) - 1) / tile_of(a.N);
   const int64_t waves = a.batch * a.G * tiles_of_group(a.channels, a.G) * waves_of(a.N);
-  auto rounds = [&](int64_t n) { return double((waves * n + kSimds - 1) / kSimds); };
+  auto time_of = [&](int64_t len, int64_t n) {
+    return double(len) * (waves * n <= kSimds
+                              ? 0.65 : double((waves * n + 2 * kSimds - 1) / (2 * kSimds)));
+  };
   Segments best = {1, tiles};
-  double least = 27.0 * double(tiles) * rounds(1);
-  for (int n = 2; n <= 64 && n * 4 <= tiles; ++n) {
+  double least = 27.0 * time_of(tiles, 1);
+  for (int n = 2; n <= 64 && n * 2 <= tiles; ++n) {
     const int64_t len = (tiles + n - 1) / n;
     if ((tiles + len - 1) / len != n) continue;
-    const double t = 30.0 * double(len) * rounds(n) + 200.0;
-    if (t < 0.9 * least) {
+    const double t = 30.0 * time_of(len, n) + 60.0;
+    if (t < 0.95 * least) {
       least = t;
       best = {n, len};
     }

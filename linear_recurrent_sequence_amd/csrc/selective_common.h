@@ -25,14 +25,9 @@ using rowvec::Raw;
 
 constexpr int kChannels = 64;  // of a workgroup
 
-// log(1 + e^x) and its slope sigma(x)
-struct Softplus {
-  float value, slope;
-};
-__device__ inline Softplus softplus(float x) {
-  const float e = rowvec::exp2_fast(-rowvec::kLog2e * fabsf(x));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return {fmaxf(x, 0.0f) + scan::log1p_unit(e), x >= 0.0f ? r : e * r};
+// log(1 + e^x); its slope is sigma(x)
+__device__ inline float softplus(float x) {
+  return fmaxf(x, 0.0f) + scan::log1p_unit(rowvec::exp2_fast(-rowvec::kLog2e * fabsf(x)));
 }
 
 // The channels of a workgroup: `tile` of all groups' tiles of 64
@@ -86,9 +81,13 @@ struct Shared {
 template <int NS>
 __device__ inline void read(const float* p, float (&x)[NS]) {
 #pragma unroll
-  for (int i = 0; i < NS; i += 4) {
+  for (int i = 0; i + 4 <= NS; i += 4) {
     const float4 f = *reinterpret_cast<const float4*>(p + i);
     x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+  }
+  if constexpr (NS == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    x[0] = f.x, x[1] = f.y;
   }
 }
 

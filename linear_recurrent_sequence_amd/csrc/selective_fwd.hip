@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
       if (a.dt_bias && on) rowvec::load(a.dt_bias + c, bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = on ? softplus(x[e] + bias[e]).value : 0.0f;
+        const float d = on ? softplus(x[e] + bias[e]) : 0.0f;
         steps[row_of(i)][vec_of(i) + e] = make_float2(d, d * v[e]);
       }
     }
@@ -167,23 +167,30 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joint
   }
 }
 
-constexpr int64_t kSimds = 1024;
+constexpr int64_t kCUs = 256, kSimds = 4 * kCUs;
 
+// Waves of four states each (eight beyond 32)
 int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+int64_t workgroups_of(const SelectiveScan& a) {
+  return a.batch * a.G * tiles_of_group(a.channels, a.G);
+}
+
+// The time of `n` tiles of tokens of `waves` waves: a SIMD with two waves keeps its
+// vector unit three quarters busy, with one little more than half.
+double time_of(int64_t n, int64_t waves) {
+  return double(n) * (waves <= kSimds ? 0.65 : double((waves + 2 * kSimds - 1) / (2 * kSimds)));
+}
 
 // How many segments: those of a sequence run side by side, for the effect of each
-// on a state (7 operations to the scan's 8), taken first.  A SIMD takes the waves
-// that it has in turn, so the time is that of the SIMD with the most.
+// on a state (0.8 of the scan's time) taken first.
 Segments segments_of(const SelectiveScan& a) {
-  const int64_t tiles = (a.T + kTile - 1) / kTile;
-  const int64_t waves = a.batch * a.G * tiles_of_group(a.channels, a.G) * waves_of(a.N);
+  const int64_t tiles = (a.T + kTile - 1) / kTile, waves = workgroups_of(a) * waves_of(a.N);
   Segments best = {1, tiles};
-  double least = double(tiles) * double((waves + kSimds - 1) / kSimds);
-  for (int n = 2; n <= 64 && n * 4 <= tiles; ++n) {
+  double least = time_of(tiles, waves);
+  for (int n = 2; n <= 64 && n * 2 <= tiles; ++n) {
     const int64_t len = (tiles + n - 1) / n;
     if ((tiles + len - 1) / len != n) continue;
-    const double t = double(len) * (double((waves * n + kSimds - 1) / kSimds) +
-                                    0.9 * double((waves * (n - 1) + kSimds - 1) / kSimds)) + 8.0;
+    const double t = time_of(len, waves * n) + 0.8 * time_of(len, waves * (n - 1)) + 6.0;
     if (t < 0.9 * least) {
       least = t;
       best = {n, len};
@@ -199,7 +206,7 @@ size_t state_bytes(const SelectiveScan& a, int n) {
 template <typename T, int NW, int NS, bool GATE>
 void launch(const SelectiveScan& a, void* y, float* state_out, const Segments& seg,
             const Joints& joints, hipStream_t stream) {
-  const int64_t per = a.batch * a.G * tiles_of_group(a.channels, a.G);
+  const int64_t per = workgroups_of(a);
   if (seg.n > 1) {
     scan_kernel<T, NW, NS, false, true><<<unsigned(per * (seg.n - 1)), 64 * NW, 0, stream>>>(
         a, nullptr, nullptr, seg, joints);
@@ -213,7 +220,15 @@ void launch(const SelectiveScan& a, void* y, float* state_out, const Segments& s
 template <typename T, bool GATE>
 void dispatch(const SelectiveScan& a, void* y, float* state_out, const Segments& seg,
               const Joints& joints, hipStream_t stream) {
-  if (a.N <= 4)
+  // two states to a wave where that gives a CU's one workgroup more waves
+  const bool few = workgroups_of(a) * seg.n <= kCUs;
+  if (few && a.N <= 4)
+    launch<T, 2, 2, GATE>(a, y, state_out, seg, joints, stream);
+  else if (few && a.N <= 8)
+    launch<T, 4, 2, GATE>(a, y, state_out, seg, joints, stream);
+  else if (few && a.N <= 16)
+    launch<T, 8, 2, GATE>(a, y, state_out, seg, joints, stream);
+  else if (a.N <= 4)
     launch<T, 1, 4, GATE>(a, y, state_out, seg, joints, stream);
   else if (a.N <= 8)
     launch<T, 2, 4, GATE>(a, y, state_out, seg, joints, stream);

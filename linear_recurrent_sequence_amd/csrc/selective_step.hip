@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256) void step_kernel(SelectiveScan a, T* y, float*
   if (live) {
     u = rowvec::to_float(static_cast<const T*>(a.u)[b * a.u_row + c]);
     const float x = rowvec::to_float(static_cast<const T*>(a.dt)[b * a.dt_row + c]);
-    delta = softplus(a.dt_bias ? x + a.dt_bias[c] : x).value;
+    delta = softplus(a.dt_bias ? x + a.dt_bias[c] : x);
   }
   const float v = delta * u;
   float p = 0.0f, s[V] = {};
