@@ -241,6 +241,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
   __shared__ float gs[TL][kChannels];
   __shared__ __align__(16) float shared[TL * 2 * NW * NS];
   __shared__ __align__(16) float parts[kParts][NW][TL][kChannels];
+  // what a thread read of the tile, for its end: registers are for the next one's
+  __shared__ __align__(16) Raw<T, V> held[GATE ? 4 : 3][kItems][kThreads];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Where w = where<TL>(a, seg);
   const int64_t tiles = (a.T + TL - 1) / TL, end = w.n < w.last ? w.n : w.last;
@@ -307,18 +309,23 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) gs[row_of(i)][vec_of(i) + e] = x[e];
+      held[0][i][threadIdx.x] = u[i];
+      held[1][i][threadIdx.x] = dt[i];
+      held[2][i][threadIdx.x] = d[i];
+      if constexpr (GATE) held[3][i][threadIdx.x] = z[i];
     }
     bc.put(shared);
-    __syncthreads();
-
-    float x[128];  // [token][state]: s and a, then the products behind dB and dC
     float start[NS], own[NS], through = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
+    for (int j = 0; j < NS; ++j)
       start[j] = CUT ? __builtin_fmaf(rowvec::exp2_fast(A[j] * sum), s0[j], s[j]) : s[j];
-      s[j] = start[j];
-      own[j] = 0.0f;
-    }
+    __syncthreads();
+    if (t0 > w.first) load(t0 - TL);
+
+    float x[128];  // [token][state]: s and a, then the products behind dB and dC
+    float now[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) now[j] = start[j], own[j] = 0.0f;
 #pragma unroll
     for (int t = 0; t < TL; ++t) {
       const float2 st = steps[t][lane];
@@ -329,14 +336,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
         const float e = rowvec::exp2_fast(st.x * A[j]);
-        s[j] = __builtin_fmaf(e, s[j], st.y * B[j]);
-        if constexpr (GATE) p = __builtin_fmaf(C[j], s[j], p);
+        now[j] = __builtin_fmaf(e, now[j], st.y * B[j]);
+        if constexpr (GATE) p = __builtin_fmaf(C[j], now[j], p);
         x[2 * (t * NS + j)] = e;
-        x[2 * (t * NS + j) + 1] = s[j];
+        x[2 * (t * NS + j) + 1] = now[j];
       }
       if constexpr (GATE) parts[2][wave][t][lane] = p;
       through += st.x;
-      if (t % 2) __builtin_amdgcn_sched_barrier(0);
+      if (t % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
     // the way back reads LDS again: kept from here, what it reads would take all the
     // registers that are left
@@ -358,7 +365,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
         const int at = 2 * (t * NS + j);
-        const float now = x[at + 1], old = t > 0 ? x[t > 0 ? at + 1 - 2 * NS : 0] : start[j];
+        const float here = x[at + 1], old = t > 0 ? x[t > 0 ? at + 1 - 2 * NS : 0] : start[j];
         S[j] = __builtin_fmaf(gt, C[j], S[j]);
         own[j] = __builtin_fmaf(gt, C[j], own[j]) * x[at];
         h = __builtin_fmaf(S[j], B[j], h);
@@ -366,7 +373,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
         q = __builtin_fmaf(f, A[j], q);
         dA[j] = __builtin_fmaf(f, st.x, dA[j]);
         x[at] = S[j] * st.y;
-        x[at + 1] = gt * now;
+        x[at + 1] = gt * here;
         S[j] = e;
       }
       parts[0][wave][t][lane] = h;
@@ -374,7 +381,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       // here, not where they are needed: their operands would have to be kept
 #pragma unroll
       for (int j = 0; j < NS; ++j) asm volatile("" : "+v"(dA[j]), "+v"(own[j]));
-      if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+      if (t % 4 == 0) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < NS; ++j)
@@ -386,10 +393,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
         kept.shared[((blockIdx.x % (a.G * tiles_of_group(a.channels, a.G)) * a.batch + w.b) * a.T +
                      t) * a.N + n] = make_float2(x[0], x[1]);
     }
-    Raw<T, V> u0[kItems], z0[kItems], d0[kItems], dt0[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) u0[i] = u[i], z0[i] = z[i], d0[i] = d[i], dt0[i] = dt[i];
-    if (t0 > w.first) load(t0 - TL);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
@@ -398,7 +401,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       if (r >= TL || t >= w.last || v0 >= w.ch.count) continue;
       float skip[V] = {}, uu[V], h[V] = {}, q[V] = {}, o[V];
       if (a.D) rowvec::load(a.D + c, skip);
-      rowvec::floats(u0[i], uu);
+      rowvec::floats(held[0][i][threadIdx.x], uu);
 #pragma unroll
       for (int k = 0; k < NW; ++k)
 #pragma unroll
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       }
       rowvec::store(static_cast<T*>(gr.du) + at, o);
       float pre[V], bias[V] = {};
-      rowvec::floats(dt0[i], pre);
+      rowvec::floats(held[1][i][threadIdx.x], pre);
       if (a.dt_bias) rowvec::load(a.dt_bias + c, bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -426,8 +429,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       rowvec::store(static_cast<T*>(gr.ddt) + at, o);
       if constexpr (GATE) {
         float zz[V], dd[V];
-        rowvec::floats(z0[i], zz);
-        rowvec::floats(d0[i], dd);
+        rowvec::floats(held[3][i][threadIdx.x], zz);
+        rowvec::floats(held[2][i][threadIdx.x], dd);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float raw = skip[e] * uu[e];
@@ -480,14 +483,21 @@ __global__ __launch_bounds__(256) void shared_sums_kernel(SelectiveScan a, const
   rowvec::put(dC + i, c);
 }
 
-// dA, dD and dbias: sums over sequences and segments
+// dA, dD and dbias: sums over sequences and segments; a workgroup takes 32 columns,
+// its eight rows of lanes every eighth partial, joined in order
 __global__ __launch_bounds__(256) void weight_sums_kernel(SelectiveScan a, const float* parts,
                                                           int64_t n, float* dA, float* dD,
                                                           float* dbias) {
-  const int64_t all = (a.N + 2) * a.channels, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= all) return;
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x % 32, first = threadIdx.x / 32;
+  const int64_t all = (a.N + 2) * a.channels, i = int64_t(blockIdx.x) * 32 + lane;
   float s = 0.0f;
-  for (int64_t k = 0; k < n; ++k) s += parts[k * all + i];
+  if (i < all)
+    for (int64_t k = first; k < n; k += 8) s += parts[k * all + i];
+  sums[first][lane] = s;
+  __syncthreads();
+  if (first != 0 || i >= all) return;
+  for (int r = 1; r < 8; ++r) s += sums[r][lane];
   const int64_t row = i / a.channels, c = i % a.channels;
   if (row < a.N)
     dA[c * a.N + row] = s;
@@ -590,7 +600,7 @@ void dispatch(const SelectiveScan& a, const SelectiveGrads& g, const Segments& s
   const int64_t all = a.batch * a.T * a.G * a.N;
   shared_sums_kernel<T><<<unsigned((all + 255) / 256), 256, 0, stream>>>(
       a, kept.shared, static_cast<T*>(g.dB), static_cast<T*>(g.dC));
-  weight_sums_kernel<<<unsigned(((a.N + 2) * a.channels + 255) / 256), 256, 0, stream>>>(
+  weight_sums_kernel<<<unsigned(((a.N + 2) * a.channels + 31) / 32), 256, 0, stream>>>(
       a, kept.weights, int64_t(seg.n) * a.batch, g.dA, g.dD, g.ddt_bias);
 }
 
