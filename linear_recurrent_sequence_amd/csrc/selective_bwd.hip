@@ -64,6 +64,36 @@ __device__ inline Where where(const SelectiveScan& a, const Segments& seg) {
   return w;
 }
 
+// The offsets of a thread's vectors in a tile's rows
+template <int ITEMS>
+struct Offsets {
+  unsigned u[ITEMS], dt[ITEMS], z[ITEMS], row[ITEMS];
+  __device__ Offsets(const SelectiveScan& a, const Channels& ch, int tokens, int vec, int vecs,
+                     int threads, int size) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int at = i * threads + threadIdx.x, r = at / vecs, c = at % vecs * vec;
+      const bool on = r < tokens && c < ch.count;
+      u[i] = offset_of(on, r, a.u_row, c, size);
+      dt[i] = offset_of(on, r, a.dt_row, c, size);
+      z[i] = offset_of(on, r, a.gate_row, c, size);
+      row[i] = offset_of(on, r, a.channels, c, size);
+    }
+  }
+};
+
+struct Inputs {
+  Rows u, dt, z, dy, b, c;
+  __device__ Inputs(const SelectiveScan& a, const void* dy_, const Channels& ch, int64_t row,
+                    int size)
+      : u(a.u, row, a.u_row, ch.first, size), dt(a.dt, row, a.dt_row, ch.first, size),
+        z(a.gate, row, a.gate_row, ch.first, size), dy(dy_, row, a.channels, ch.first, size),
+        b(a.B, row, a.B_row, ch.group * a.N, size), c(a.C, row, a.C_row, ch.group * a.N, size) {}
+  __device__ void move(int rows) {
+    u.move(rows), dt.move(rows), z.move(rows), dy.move(rows), b.move(rows), c.move(rows);
+  }
+};
+
 // ---- the first pass
 
 template <typename T, int NW, int NS, int TL, bool GATE, bool CUT>
@@ -89,45 +119,50 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
   const int64_t end = w.n < w.last ? w.n : w.last;
-  auto load = [&](int64_t t0) {
+  constexpr int kSize = sizeof(T);
+  const Offsets<kItems> at(a, w.ch, TL, V, kVecs, kThreads, kSize);
+  Inputs in(a, dy, w.ch, w.b * a.T + w.first, kSize);
+  auto load = [&](int64_t t0) {  // and on to the next tile
+    const int rows = rows_left(t0, end);
+    const auto ru = in.u.rsrc(rows), rt = in.dt.rsrc(rows), rd = in.dy.rsrc(rows),
+               rz = in.z.rsrc(rows);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int64_t t = t0 + row_of(i);
-      u[i] = dt[i] = z[i] = d[i] = {};
-      if (row_of(i) < TL && t < end && vec_of(i) < w.ch.count) {
-        const int64_t row = w.b * a.T + t, c = w.ch.first + vec_of(i);
-        u[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.u) + row * a.u_row + c);
-        dt[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.dt) + row * a.dt_row + c);
-        if constexpr (CUT) {
-          d[i] = rowvec::load_raw<T, V>(static_cast<const T*>(dy) + row * a.channels + c);
-          if constexpr (GATE)
-            z[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.gate) + row * a.gate_row + c);
-        }
-      }
+      u[i] = load_rows<T, V>(ru, at.u[i]);
+      dt[i] = load_rows<T, V>(rt, at.dt[i]);
+      if constexpr (CUT) d[i] = load_rows<T, V>(rd, at.row[i]);
+      if constexpr (CUT && GATE) z[i] = load_rows<T, V>(rz, at.z[i]);
     }
-    bc.load(a, w.b, w.ch.group, t0, end);
+    bc.load(a, in.b, in.c, rows);
+    in.move(TL);
   };
+  __shared__ Constants constants;
+  constants.load(a, w.ch);
   load(w.first);
+  __syncthreads();
   for (int64_t t0 = w.first; t0 < w.last; t0 += TL) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       if (row_of(i) >= TL) continue;
-      const bool on = t0 + row_of(i) < end && vec_of(i) < w.ch.count;
-      float x[V], bias[V] = {}, v[V];
+      const bool on = t0 + row_of(i) < end;
+      float x[V], v[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
-      if (a.dt_bias && on) rowvec::load(a.dt_bias + w.ch.first + vec_of(i), bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float dl = on ? softplus(x[e] + bias[e]) : 0.0f;
+        // softplus(-infinity) = 0
+        const float dl = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
         steps[row_of(i)][vec_of(i) + e] = make_float2(dl, dl * v[e]);
       }
       if constexpr (CUT) {
         rowvec::floats(d[i], x);
-        rowvec::floats(z[i], v);
+        if constexpr (GATE) {
+          rowvec::floats(z[i], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          gs[row_of(i)][vec_of(i) + e] = GATE ? x[e] * (v[e] * rowvec::sigmoid(v[e])) : x[e];
+          for (int e = 0; e < V; ++e) x[e] *= v[e] * rowvec::sigmoid(v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) gs[row_of(i)][vec_of(i) + e] = x[e];
       }
     }
     bc.put(shared);
@@ -265,40 +300,47 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
   float s[NS], sum = 0.0f;
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
-  auto load = [&](int64_t t0) {
+  constexpr int kSize = sizeof(T);
+  const Offsets<kItems> at(a, w.ch, TL, V, kVecs, kThreads, kSize);
+  int64_t t0 = w.first + (w.last - 1 - w.first) / TL * TL;  // the last tile
+  Inputs in(a, gr.dy, w.ch, w.b * a.T + t0, kSize);
+  auto load = [&](int64_t t0) {  // and on to the tile before
+    const int rows = rows_left(t0, end);
+    const auto ru = in.u.rsrc(rows), rt = in.dt.rsrc(rows), rd = in.dy.rsrc(rows),
+               rz = in.z.rsrc(rows);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int64_t t = t0 + row_of(i);
-      u[i] = dt[i] = z[i] = d[i] = {};
-      if (row_of(i) < TL && t < end && vec_of(i) < w.ch.count) {
-        const int64_t row = w.b * a.T + t, c = w.ch.first + vec_of(i);
-        u[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.u) + row * a.u_row + c);
-        dt[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.dt) + row * a.dt_row + c);
-        d[i] = rowvec::load_raw<T, V>(static_cast<const T*>(gr.dy) + row * a.channels + c);
-        if constexpr (GATE)
-          z[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.gate) + row * a.gate_row + c);
-      }
+      u[i] = load_rows<T, V>(ru, at.u[i]);
+      dt[i] = load_rows<T, V>(rt, at.dt[i]);
+      d[i] = load_rows<T, V>(rd, at.row[i]);
+      if constexpr (GATE) z[i] = load_rows<T, V>(rz, at.z[i]);
     }
-    bc.load(a, w.b, w.ch.group, t0, end);
+    bc.load(a, in.b, in.c, rows);
+    in.move(-TL);
     const int64_t tile = w.b * tiles + t0 / TL;
     load_kept(a, kept.states + tile * a.N * a.channels, w.ch, wave, lane, s);
     if (CUT) sum = lane < w.ch.count ? kept.sums[tile * a.channels + w.ch.first + lane] : 0.0f;
   };
 
-  int64_t t0 = w.first + (w.last - 1 - w.first) / TL * TL;
+  const int64_t row0 = w.b * a.T + t0;
+  Rows du_rows(gr.du, row0, a.channels, w.ch.first, kSize),
+      ddt_rows(gr.ddt, row0, a.channels, w.ch.first, kSize),
+      dz_rows(gr.dgate, row0, a.channels, w.ch.first, kSize);
+  __shared__ Constants constants;
+  constants.load(a, w.ch);
   load(t0);
+  __syncthreads();
   for (; t0 >= w.first; t0 -= TL) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       if (row_of(i) >= TL) continue;
-      const bool on = t0 + row_of(i) < end && vec_of(i) < w.ch.count;
-      float x[V], bias[V] = {}, v[V];
+      const bool on = t0 + row_of(i) < end;
+      float x[V], v[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
-      if (a.dt_bias && on) rowvec::load(a.dt_bias + w.ch.first + vec_of(i), bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float delta = on ? softplus(x[e] + bias[e]) : 0.0f;
+        const float delta = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
         steps[row_of(i)][vec_of(i) + e] = make_float2(delta, delta * v[e]);
       }
       rowvec::floats(d[i], x);
@@ -394,13 +436,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
                      t) * a.N + n] = make_float2(x[0], x[1]);
     }
     __syncthreads();
+    const int rows = rows_left(t0, w.last);
+    const auto ru = du_rows.rsrc(rows), rt = ddt_rows.rsrc(rows), rz = dz_rows.rsrc(rows);
+    du_rows.move(-TL), ddt_rows.move(-TL), dz_rows.move(-TL);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int r = row_of(i), v0 = vec_of(i);
-      const int64_t t = t0 + r, c = w.ch.first + v0;
-      if (r >= TL || t >= w.last || v0 >= w.ch.count) continue;
-      float skip[V] = {}, uu[V], h[V] = {}, q[V] = {}, o[V];
-      if (a.D) rowvec::load(a.D + c, skip);
+      if (r >= TL) continue;
+      float uu[V], h[V] = {}, q[V] = {}, o[V];
       rowvec::floats(held[0][i][threadIdx.x], uu);
 #pragma unroll
       for (int k = 0; k < NW; ++k)
@@ -409,36 +452,35 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
           h[e] += parts[0][k][r][v0 + e];
           q[e] += parts[1][k][r][v0 + e];
         }
-      const int64_t at = (w.b * a.T + t) * a.channels + c;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float g = gs[r][v0 + e];  // this thread's own
-        o[e] = __builtin_fmaf(steps[r][v0 + e].x, h[e], skip[e] * g);
+        o[e] = __builtin_fmaf(steps[r][v0 + e].x, h[e], constants.skip[v0 + e] * g);
         dD[i][e] = __builtin_fmaf(g, uu[e], dD[i][e]);
       }
-      rowvec::store(static_cast<T*>(gr.du) + at, o);
-      float pre[V], bias[V] = {};
+      store_rows<T, V>(ru, at.row[i], o);
+      float pre[V];
       rowvec::floats(held[1][i][threadIdx.x], pre);
-      if (a.dt_bias) rowvec::load(a.dt_bias + c, bias);
+      const bool on = t0 + r < end;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        o[e] = t < end ? __builtin_fmaf(uu[e], h[e], q[e]) * rowvec::sigmoid(pre[e] + bias[e])
-                       : 0.0f;
+        const float slope = on ? rowvec::sigmoid(pre[e] + constants.bias[v0 + e]) : 0.0f;
+        o[e] = __builtin_fmaf(uu[e], h[e], q[e]) * slope;
         dbias[i][e] += o[e];
       }
-      rowvec::store(static_cast<T*>(gr.ddt) + at, o);
+      store_rows<T, V>(rt, at.row[i], o);
       if constexpr (GATE) {
         float zz[V], dd[V];
         rowvec::floats(held[3][i][threadIdx.x], zz);
         rowvec::floats(held[2][i][threadIdx.x], dd);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          float raw = skip[e] * uu[e];
+          float raw = constants.skip[v0 + e] * uu[e];
 #pragma unroll
           for (int k = 0; k < NW; ++k) raw += parts[2][k][r][v0 + e];
           o[e] = dd[e] * raw * rowvec::silu_slope(zz[e], rowvec::sigmoid(zz[e]));
         }
-        rowvec::store(static_cast<T*>(gr.dgate) + at, o);
+        store_rows<T, V>(rz, at.row[i], o);
       }
     }
   }

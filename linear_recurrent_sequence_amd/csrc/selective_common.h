@@ -17,6 +17,7 @@
 #include "mlstm_internal.h"
 #include "scan_common.h"
 #include "selective_scan.h"
+#include "tile_common.h"
 
 namespace mlstm {
 namespace selective {
@@ -50,30 +51,126 @@ struct Segments {
   int64_t tiles;
 };
 
+// ---- rows of a tile, by buffer loads and stores: what lies beyond the tile's last
+// row reads as zeros and is not stored, and a lane's offset is the same for all tiles
+
+// A tensor's rows of the current tile
+struct Rows {
+  const char* base;
+  unsigned pitch;  // bytes
+  // from element `first` of `row` on; `pitch` elements apart
+  __device__ Rows(const void* p, int64_t row, int64_t pitch_, int64_t first, int element)
+      : base(static_cast<const char*>(p) + (row * pitch_ + first) * element),
+        pitch(unsigned(pitch_ * element)) {}
+  __device__ void move(int rows) { base += int64_t(rows) * pitch; }
+  // `rows` of them, 32 at most
+  __device__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, rows * pitch,
+                                             tilecommon::kRsrcFlags);
+  }
+};
+__device__ inline int rows_left(int64_t from, int64_t end) {
+  return end <= from ? 0 : end - from < 32 ? int(end - from) : 32;
+}
+// of element c of row r, where `on`
+__device__ inline unsigned offset_of(bool on, int64_t r, int64_t pitch, int64_t c, int element) {
+  return on ? unsigned((r * pitch + c) * element) : tilecommon::kOutOfRange;
+}
+template <typename T, int V>
+__device__ inline Raw<T, V> load_rows(__amdgpu_buffer_rsrc_t rsrc, unsigned at) {
+  constexpr int kWords = sizeof(T) * V / 4;
+  typedef unsigned words __attribute__((ext_vector_type(kWords < 4 ? kWords : 4)));
+  Raw<T, V> r;
+#pragma unroll
+  for (int i = 0; i < kWords; i += 4) {
+    if constexpr (kWords == 1) {
+      r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+    } else {
+      words x;
+      if constexpr (kWords == 2)
+        x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0);
+      else
+        x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + i * 4, 0, 0);
+#pragma unroll
+      for (int e = 0; e < kWords && e < 4; ++e) r.w[i + e] = x[e];
+    }
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ inline void store_rows(__amdgpu_buffer_rsrc_t rsrc, unsigned at, const float (&x)[V]) {
+  constexpr int kWords = sizeof(T) * V / 4;
+  typedef unsigned words __attribute__((ext_vector_type(kWords < 4 ? kWords : 4)));
+  unsigned w[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if constexpr (sizeof(T) == 4)
+      w[i] = __float_as_uint(x[i]);
+    else
+      w[i] = rowvec::to_bf16(x[2 * i], x[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; i += 4) {
+    if constexpr (kWords == 1) {
+      __builtin_amdgcn_raw_buffer_store_b32(w[0], rsrc, at, 0, 0);
+    } else {
+      words v;
+#pragma unroll
+      for (int e = 0; e < kWords && e < 4; ++e) v[e] = w[i + e];
+      if constexpr (kWords == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(v, rsrc, at, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at + i * 4, 0, 0);
+    }
+  }
+}
+
 // B and C of a tile, as float32 in LDS [token][wave][B: NS, C: NS], zeros for
 // states beyond N and tokens from `end` on.  In two steps, so that the loads can
 // be in flight while the tile before is worked on.
 template <typename T, int NW, int NS, int TL>
 struct Shared {
-  static constexpr int kThreads = 64 * NW, kRow = 2 * NW * NS;
-  static constexpr int kItems = TL * kRow / kThreads;
-  static_assert(TL * kRow % kThreads == 0, "every thread has as many");
-  T raw[kItems];
+  static constexpr int kThreads = 64 * NW, kN = NW * NS, kItems = TL * kN / kThreads;
+  static_assert(TL * kN % kThreads == 0, "every thread has as many");
+  unsigned B[kItems], C[kItems];  // as loaded
 
-  __device__ void load(const SelectiveScan& a, int64_t b, int64_t group, int64_t t0, int64_t end) {
+  __device__ static unsigned one(__amdgpu_buffer_rsrc_t rsrc, unsigned at) {
+    if constexpr (sizeof(T) == 4)
+      return __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+    else
+      return __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
+  }
+  __device__ static float value(unsigned x) {
+    return __uint_as_float(sizeof(T) == 4 ? x : x << 16);
+  }
+  __device__ void load(const SelectiveScan& a, const Rows& b_rows, const Rows& c_rows, int rows) {
+    const auto rb = b_rows.rsrc(rows), rc = c_rows.rsrc(rows);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int at = i * kThreads + threadIdx.x;
-      const int t = at / kRow, k = at % kRow, n = k / (2 * NS) * NS + k % NS;
-      const bool is_c = (k / NS) & 1;
-      const T* p = static_cast<const T*>(is_c ? a.C : a.B) +
-                   (b * a.T + t0 + t) * (is_c ? a.C_row : a.B_row) + group * a.N + n;
-      raw[i] = t0 + t < end && n < a.N ? *p : T(0.0f);
+      const int at = i * kThreads + threadIdx.x, t = at / kN, n = at % kN;
+      B[i] = one(rb, offset_of(n < a.N, t, a.B_row, n, sizeof(T)));
+      C[i] = one(rc, offset_of(n < a.N, t, a.C_row, n, sizeof(T)));
     }
   }
   __device__ void put(float* lds) const {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) lds[i * kThreads + threadIdx.x] = rowvec::to_float(raw[i]);
+    for (int i = 0; i < kItems; ++i) {
+      const int at = i * kThreads + threadIdx.x, t = at / kN, n = at % kN;
+      float* p = lds + (t * NW + n / NS) * 2 * NS + n % NS;
+      p[0] = value(B[i]);
+      p[NS] = value(C[i]);
+    }
+  }
+};
+
+// dt_bias and D of the workgroup's channels (0 where they are not given)
+struct Constants {
+  float bias[kChannels], skip[kChannels];
+  __device__ void load(const SelectiveScan& a, const Channels& ch) {
+    const int c = threadIdx.x;
+    if (c >= kChannels) return;
+    bias[c] = a.dt_bias && c < ch.count ? a.dt_bias[ch.first + c] : 0.0f;
+    skip[c] = a.D && c < ch.count ? a.D[ch.first + c] : 0.0f;
   }
 };
 

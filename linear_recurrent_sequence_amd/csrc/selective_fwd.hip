@@ -31,6 +31,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
   __shared__ float2 steps[TL][kChannels];  // Delta, Delta u
   __shared__ __align__(16) float shared[TL * 2 * NW * NS];
   __shared__ __align__(16) float parts[ENDS ? 1 : NW][ENDS ? 1 : TL][kChannels];
+  __shared__ Constants constants;
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int64_t tiles = a.G * tiles_of_group(a.channels, a.G);
@@ -57,35 +58,50 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
   Shared<T, NW, NS, TL> bc;
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
-  auto load = [&](int64_t t0) {
+  const int64_t end = n < last ? n : last;  // of what is read
+  constexpr int kSize = sizeof(T);
+  unsigned u_at[kItems], dt_at[kItems], z_at[kItems], y_at[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const bool on = vec_of(i) < ch.count;
+    u_at[i] = offset_of(on, row_of(i), a.u_row, vec_of(i), kSize);
+    dt_at[i] = offset_of(on, row_of(i), a.dt_row, vec_of(i), kSize);
+    z_at[i] = offset_of(on, row_of(i), a.gate_row, vec_of(i), kSize);
+    y_at[i] = offset_of(on, row_of(i), a.channels, vec_of(i), kSize);
+  }
+  const int64_t row0 = b * a.T + first;
+  Rows u_rows(a.u, row0, a.u_row, ch.first, kSize), dt_rows(a.dt, row0, a.dt_row, ch.first, kSize),
+      z_rows(a.gate, row0, a.gate_row, ch.first, kSize),
+      y_rows(y, row0, a.channels, ch.first, kSize),
+      b_rows(a.B, row0, a.B_row, ch.group * a.N, kSize),
+      c_rows(a.C, row0, a.C_row, ch.group * a.N, kSize);
+  auto load = [&](int64_t t0) {  // and on to the next tile
+    const int rows = rows_left(t0, end);
+    const auto ru = u_rows.rsrc(rows), rd = dt_rows.rsrc(rows), rz = z_rows.rsrc(rows);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int64_t t = t0 + row_of(i);
-      u[i] = dt[i] = z[i] = {};
-      if (t < n && t < last && vec_of(i) < ch.count) {
-        const int64_t row = b * a.T + t, c = ch.first + vec_of(i);
-        u[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.u) + row * a.u_row + c);
-        dt[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.dt) + row * a.dt_row + c);
-        if constexpr (GATE && !ENDS)
-          z[i] = rowvec::load_raw<T, V>(static_cast<const T*>(a.gate) + row * a.gate_row + c);
-      }
+      u[i] = load_rows<T, V>(ru, u_at[i]);
+      dt[i] = load_rows<T, V>(rd, dt_at[i]);
+      if constexpr (GATE && !ENDS) z[i] = load_rows<T, V>(rz, z_at[i]);
     }
-    bc.load(a, b, ch.group, t0, n < last ? n : last);
+    bc.load(a, b_rows, c_rows, rows);
+    u_rows.move(TL), dt_rows.move(TL), z_rows.move(TL), b_rows.move(TL), c_rows.move(TL);
   };
 
+  constants.load(a, ch);
   load(first);
+  __syncthreads();
   for (int64_t t0 = first; t0 < last; t0 += TL) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int64_t c = ch.first + vec_of(i);
-      const bool on = t0 + row_of(i) < n && t0 + row_of(i) < last && vec_of(i) < ch.count;
-      float x[V], bias[V] = {}, v[V];
+      const bool on = t0 + row_of(i) < end;
+      float x[V], v[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
-      if (a.dt_bias && on) rowvec::load(a.dt_bias + c, bias);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = on ? softplus(x[e] + bias[e]) : 0.0f;
+        // softplus(-infinity) = 0
+        const float d = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
         steps[row_of(i)][vec_of(i) + e] = make_float2(d, d * v[e]);
       }
     }
@@ -117,15 +133,14 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
     }
     __syncthreads();
     if constexpr (!ENDS) {
+      const auto ry = y_rows.rsrc(rows_left(t0, last));
+      y_rows.move(TL);
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const int64_t t = t0 + row_of(i), c = ch.first + vec_of(i);
-        if (t >= last || vec_of(i) >= ch.count) continue;
-        float o[V], x[V], skip[V] = {};
-        if (a.D) rowvec::load(a.D + c, skip);
+        float o[V], x[V];
         rowvec::floats(u0[i], x);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = skip[e] * x[e];
+        for (int e = 0; e < V; ++e) o[e] = constants.skip[vec_of(i) + e] * x[e];
 #pragma unroll
         for (int w = 0; w < NW; ++w)
 #pragma unroll
@@ -135,7 +150,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
 #pragma unroll
           for (int e = 0; e < V; ++e) o[e] *= x[e] * rowvec::sigmoid(x[e]);
         }
-        rowvec::store(y + (b * a.T + t) * a.channels + c, o);
+        store_rows<T, V>(ry, y_at[i], o);
       }
     }
   }
