@@ -115,7 +115,7 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
   for (int j = 0; j < NS; ++j) P[j] = 1.0f, S[j] = 0.0f;
 
   Raw<T, V> u[kItems], dt[kItems], z[kItems], d[kItems];
-  Shared<T, NW, NS, TL> bc;
+  Shared<T, NW, NS, TL> bc(a);
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
   const int64_t end = w.n < w.last ? w.n : w.last;
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
       if constexpr (CUT) d[i] = load_rows<T, V>(rd, at.row[i]);
       if constexpr (CUT && GATE) z[i] = load_rows<T, V>(rz, at.z[i]);
     }
-    bc.load(a, in.b, in.c, rows);
+    bc.load(in.b, in.c, rows);
     in.move(TL);
   };
   __shared__ Constants constants;
@@ -145,15 +145,13 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
     for (int i = 0; i < kItems; ++i) {
       if (row_of(i) >= TL) continue;
       const bool on = t0 + row_of(i) < end;
-      float x[V], v[V];
+      float x[V], v[V], dl[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
+      deltas(x, constants.bias + vec_of(i), on, dl);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // softplus(-infinity) = 0
-        const float dl = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
-        steps[row_of(i)][vec_of(i) + e] = make_float2(dl, dl * v[e]);
-      }
+      for (int e = 0; e < V; ++e)
+        steps[row_of(i)][vec_of(i) + e] = make_float2(dl[e], dl[e] * v[e]);
       if constexpr (CUT) {
         rowvec::floats(d[i], x);
         if constexpr (GATE) {
@@ -172,26 +170,42 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
     if (CUT && wave == 0 && lane < w.ch.count)
       kept.sums[tile * a.channels + w.ch.first + lane] = sum;
     if (t0 + TL < w.last) load(t0 + TL);
-#pragma unroll 8
-    for (int t = 0; t < TL; ++t) {
-      const float2 st = steps[t][lane];
-      float B[NS], C[NS], g;
-      const float* row = shared + (t * NW + wave) * 2 * NS;
-      read(row, B);
-      if constexpr (CUT) {
-        read(row + NS, C);
-        g = gs[t][lane];
-        sum += st.x;
-      }
+    // kBlock tokens at a time, the next ones' data read beside them
+    constexpr int kBlock = NS <= 4 ? 4 : 2;
+    Token<NS, CUT> now[kBlock], next[kBlock];
+    float g[kBlock], g_next[kBlock];
+    auto fetch = [&](Token<NS, CUT>(&to)[kBlock], float(&to_g)[kBlock], int t) {
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        const float e = rowvec::exp2_fast(st.x * A[j]);
-        s[j] = __builtin_fmaf(e, s[j], st.y * B[j]);
-        if constexpr (CUT) {
-          P[j] *= e;
-          S[j] = __builtin_fmaf(P[j], C[j] * g, S[j]);
+      for (int k = 0; k < kBlock; ++k) {
+        to[k].load(steps, shared, NW, wave, t + k, lane);
+        to_g[k] = CUT ? gs[CUT ? t + k : 0][lane] : 0.0f;
+      }
+    };
+    fetch(now, g, 0);
+#pragma unroll
+    for (int t = 0; t < TL; t += kBlock) {
+      if (t + kBlock < TL) fetch(next, g_next, t + kBlock);
+      __builtin_amdgcn_sched_barrier(0);
+      float decay[kBlock][NS];
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) decay[k][j] = rowvec::exp2_fast(now[k].d.x * A[j]);
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k) {
+        if constexpr (CUT) sum += now[k].d.x;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          s[j] = __builtin_fmaf(decay[k][j], s[j], now[k].d.y * now[k].B[j]);
+          if constexpr (CUT) {
+            P[j] *= decay[k][j];
+            S[j] = __builtin_fmaf(P[j], now[k].C[j] * g[k], S[j]);
+          }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k) now[k] = next[k], g[k] = g_next[k];
     }
     __syncthreads();
   }
@@ -296,7 +310,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
   float dD[kItems][V] = {}, dbias[kItems][V] = {};
 
   Raw<T, V> u[kItems], dt[kItems], z[kItems], d[kItems];
-  Shared<T, NW, NS, TL> bc;
+  Shared<T, NW, NS, TL> bc(a);
   float s[NS], sum = 0.0f;
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
@@ -315,7 +329,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       d[i] = load_rows<T, V>(rd, at.row[i]);
       if constexpr (GATE) z[i] = load_rows<T, V>(rz, at.z[i]);
     }
-    bc.load(a, in.b, in.c, rows);
+    bc.load(in.b, in.c, rows);
     in.move(-TL);
     const int64_t tile = w.b * tiles + t0 / TL;
     load_kept(a, kept.states + tile * a.N * a.channels, w.ch, wave, lane, s);
@@ -335,14 +349,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
     for (int i = 0; i < kItems; ++i) {
       if (row_of(i) >= TL) continue;
       const bool on = t0 + row_of(i) < end;
-      float x[V], v[V];
+      float x[V], v[V], dl[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
+      deltas(x, constants.bias + vec_of(i), on, dl);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float delta = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
-        steps[row_of(i)][vec_of(i) + e] = make_float2(delta, delta * v[e]);
-      }
+      for (int e = 0; e < V; ++e)
+        steps[row_of(i)][vec_of(i) + e] = make_float2(dl[e], dl[e] * v[e]);
       rowvec::floats(d[i], x);
       if constexpr (GATE) {
         rowvec::floats(z[i], v);
@@ -446,12 +459,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
       float uu[V], h[V] = {}, q[V] = {}, o[V];
       rowvec::floats(held[0][i][threadIdx.x], uu);
 #pragma unroll
-      for (int k = 0; k < NW; ++k)
+      for (int k = 0; k < NW; ++k) {
+        float ph[V], pq[V];
+        read(&parts[0][k][r][v0], ph);
+        read(&parts[1][k][r][v0], pq);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[e] += parts[0][k][r][v0 + e];
-          q[e] += parts[1][k][r][v0 + e];
-        }
+        for (int e = 0; e < V; ++e) h[e] += ph[e], q[e] += pq[e];
+      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float g = gs[r][v0 + e];  // this thread's own
@@ -473,13 +487,20 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
         float zz[V], dd[V];
         rowvec::floats(held[3][i][threadIdx.x], zz);
         rowvec::floats(held[2][i][threadIdx.x], dd);
+        float raw[V];
+        read(constants.skip + v0, raw);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float raw = constants.skip[v0 + e] * uu[e];
+        for (int e = 0; e < V; ++e) raw[e] *= uu[e];
 #pragma unroll
-          for (int k = 0; k < NW; ++k) raw += parts[2][k][r][v0 + e];
-          o[e] = dd[e] * raw * rowvec::silu_slope(zz[e], rowvec::sigmoid(zz[e]));
+        for (int k = 0; k < NW; ++k) {
+          float part[V];
+          read(&parts[2][k][r][v0], part);
+#pragma unroll
+          for (int e = 0; e < V; ++e) raw[e] += part[e];
         }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          o[e] = dd[e] * raw[e] * rowvec::silu_slope(zz[e], rowvec::sigmoid(zz[e]));
         store_rows<T, V>(rz, at.row[i], o);
       }
     }

@@ -74,7 +74,8 @@ __device__ inline int rows_left(int64_t from, int64_t end) {
 }
 // of element c of row r, where `on`
 __device__ inline unsigned offset_of(bool on, int64_t r, int64_t pitch, int64_t c, int element) {
-  return on ? unsigned((r * pitch + c) * element) : tilecommon::kOutOfRange;
+  const unsigned at = unsigned((r * pitch + c) * element);
+  return on ? at : tilecommon::kOutOfRange;
 }
 template <typename T, int V>
 __device__ inline Raw<T, V> load_rows(__amdgpu_buffer_rsrc_t rsrc, unsigned at) {
@@ -133,6 +134,16 @@ struct Shared {
   static constexpr int kThreads = 64 * NW, kN = NW * NS, kItems = TL * kN / kThreads;
   static_assert(TL * kN % kThreads == 0, "every thread has as many");
   unsigned B[kItems], C[kItems];  // as loaded
+  unsigned B_at[kItems], C_at[kItems];
+
+  __device__ explicit Shared(const SelectiveScan& a) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int at = i * kThreads + threadIdx.x, t = at / kN, n = at % kN;
+      B_at[i] = offset_of(n < a.N, t, a.B_row, n, sizeof(T));
+      C_at[i] = offset_of(n < a.N, t, a.C_row, n, sizeof(T));
+    }
+  }
 
   __device__ static unsigned one(__amdgpu_buffer_rsrc_t rsrc, unsigned at) {
     if constexpr (sizeof(T) == 4)
@@ -143,13 +154,12 @@ struct Shared {
   __device__ static float value(unsigned x) {
     return __uint_as_float(sizeof(T) == 4 ? x : x << 16);
   }
-  __device__ void load(const SelectiveScan& a, const Rows& b_rows, const Rows& c_rows, int rows) {
+  __device__ void load(const Rows& b_rows, const Rows& c_rows, int rows) {
     const auto rb = b_rows.rsrc(rows), rc = c_rows.rsrc(rows);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int at = i * kThreads + threadIdx.x, t = at / kN, n = at % kN;
-      B[i] = one(rb, offset_of(n < a.N, t, a.B_row, n, sizeof(T)));
-      C[i] = one(rc, offset_of(n < a.N, t, a.C_row, n, sizeof(T)));
+      B[i] = one(rb, B_at[i]);
+      C[i] = one(rc, C_at[i]);
     }
   }
   __device__ void put(float* lds) const {
@@ -164,7 +174,7 @@ struct Shared {
 };
 
 // dt_bias and D of the workgroup's channels (0 where they are not given)
-struct Constants {
+struct alignas(16) Constants {
   float bias[kChannels], skip[kChannels];
   __device__ void load(const SelectiveScan& a, const Channels& ch) {
     const int c = threadIdx.x;
@@ -187,6 +197,31 @@ __device__ inline void read(const float* p, float (&x)[NS]) {
     x[0] = f.x, x[1] = f.y;
   }
 }
+
+// Delta of V channels of a row, from dt as read; 0 where the row is not `on`
+// (softplus(-infinity) = 0)
+template <int V>
+__device__ inline void deltas(const float (&dt)[V], const float* bias, bool on, float (&d)[V]) {
+  const float mask = on ? 0.0f : -INFINITY;
+  float b[V];
+  read(bias, b);
+#pragma unroll
+  for (int e = 0; e < V; ++e) d[e] = softplus(dt[e] + b[e] + mask);
+}
+
+// What a wave reads of a token: Delta, Delta u, B, and C if it is asked for
+template <int NS, bool WITH_C>
+struct Token {
+  float2 d;
+  float B[NS], C[WITH_C ? NS : 1];
+  __device__ void load(const float2 (*steps)[kChannels], const float* shared, int waves, int wave,
+                       int t, int lane) {
+    d = steps[t][lane];
+    const float* row = shared + (t * waves + wave) * 2 * NS;
+    read(row, B);
+    if constexpr (WITH_C) read(row + NS, C);
+  }
+};
 
 // A wave's share of A', zeros beyond N and the workgroup's channels
 template <int NS>

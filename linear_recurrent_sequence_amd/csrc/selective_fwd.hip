@@ -55,7 +55,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
   float sum = 0.0f;
 
   Raw<T, V> u[kItems], dt[kItems], z[kItems];
-  Shared<T, NW, NS, TL> bc;
+  Shared<T, NW, NS, TL> bc(a);
   auto vec_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) % kVecs * V; };
   auto row_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) / kVecs; };
   const int64_t end = n < last ? n : last;  // of what is read
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
       dt[i] = load_rows<T, V>(rd, dt_at[i]);
       if constexpr (GATE && !ENDS) z[i] = load_rows<T, V>(rz, z_at[i]);
     }
-    bc.load(a, b_rows, c_rows, rows);
+    bc.load(b_rows, c_rows, rows);
     u_rows.move(TL), dt_rows.move(TL), z_rows.move(TL), b_rows.move(TL), c_rows.move(TL);
   };
 
@@ -95,15 +95,13 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const bool on = t0 + row_of(i) < end;
-      float x[V], v[V];
+      float x[V], v[V], d[V];
       rowvec::floats(dt[i], x);
       rowvec::floats(u[i], v);
+      deltas(x, constants.bias + vec_of(i), on, d);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // softplus(-infinity) = 0
-        const float d = softplus(on ? x[e] + constants.bias[vec_of(i) + e] : -INFINITY);
-        steps[row_of(i)][vec_of(i) + e] = make_float2(d, d * v[e]);
-      }
+      for (int e = 0; e < V; ++e)
+        steps[row_of(i)][vec_of(i) + e] = make_float2(d[e], d[e] * v[e]);
     }
     bc.put(shared);
     __syncthreads();
@@ -112,24 +110,37 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
     for (int i = 0; i < kItems; ++i) u0[i] = u[i], z0[i] = z[i];
     if (t0 + TL < last) load(t0 + TL);
 
-#pragma unroll 8
-    for (int t = 0; t < TL; ++t) {
-      const float2 d = steps[t][lane];
-      float B[NS], C[NS];
-      const float* row = shared + (t * NW + wave) * 2 * NS;
-      read(row, B);
-      if constexpr (ENDS) {
-        sum += d.x;
-      } else {
-        read(row + NS, C);
-      }
-      float p = 0.0f;
+    // kBlock tokens at a time, the next ones' data read beside them
+    constexpr int kBlock = NS <= 4 ? 4 : 2;
+    Token<NS, !ENDS> now[kBlock], next[kBlock];
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        s[j] = __builtin_fmaf(rowvec::exp2_fast(d.x * A[j]), s[j], d.y * B[j]);
-        if constexpr (!ENDS) p = __builtin_fmaf(C[j], s[j], p);
+    for (int k = 0; k < kBlock; ++k) now[k].load(steps, shared, NW, wave, k, lane);
+#pragma unroll
+    for (int t = 0; t < TL; t += kBlock) {
+      if (t + kBlock < TL)
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k)
+          next[k].load(steps, shared, NW, wave, t + kBlock + k, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      float decay[kBlock][NS];
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) decay[k][j] = rowvec::exp2_fast(now[k].d.x * A[j]);
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k) {
+        float p = 0.0f;
+        if constexpr (ENDS) sum += now[k].d.x;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          s[j] = __builtin_fmaf(decay[k][j], s[j], now[k].d.y * now[k].B[j]);
+          if constexpr (!ENDS) p = __builtin_fmaf(now[k].C[j], s[j], p);
+        }
+        if constexpr (!ENDS) parts[wave][t + k][lane] = p;
       }
-      if constexpr (!ENDS) parts[wave][t][lane] = p;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k) now[k] = next[k];
     }
     __syncthreads();
     if constexpr (!ENDS) {
@@ -139,12 +150,16 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
       for (int i = 0; i < kItems; ++i) {
         float o[V], x[V];
         rowvec::floats(u0[i], x);
+        read(constants.skip + vec_of(i), o);
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = constants.skip[vec_of(i) + e] * x[e];
+        for (int e = 0; e < V; ++e) o[e] *= x[e];
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
+        for (int w = 0; w < NW; ++w) {
+          float part[V];
+          read(&parts[w][row_of(i)][vec_of(i)], part);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += parts[w][row_of(i)][vec_of(i) + e];
+          for (int e = 0; e < V; ++e) o[e] += part[e];
+        }
         if constexpr (GATE) {
           rowvec::floats(z0[i], x);
 #pragma unroll
