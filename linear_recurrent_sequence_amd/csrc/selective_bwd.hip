@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * NW) void states_kernel(SelectiveScan a, const 
       kept.sums[tile * a.channels + w.ch.first + lane] = sum;
     if (t0 + TL < w.last) load(t0 + TL);
     // kBlock tokens at a time, the next ones' data read beside them
-    constexpr int kBlock = NS <= 4 ? 4 : 2;
+    constexpr int kBlock = NS <= 4 && !CUT ? 4 : 2;
     Token<NS, CUT> now[kBlock], next[kBlock];
     float g[kBlock], g_next[kBlock];
     auto fetch = [&](Token<NS, CUT>(&to)[kBlock], float(&to_g)[kBlock], int t) {
