@@ -58,8 +58,8 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
   const unsigned np = unsigned((n.F + kF - 1) / kF), nq = unsigned((n.M + S::kBQ - 1) / S::kBQ);
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   product::tiles<S, true, kStores>(
-      wg, wu, x, n.D, n.terms, np, nq, 1, lds,
-      [&](unsigned ip, unsigned iq, const f32x4(&acc)[S::kP][S::kQ]) {
+      wg, wu, x, n.D, n.terms, np, nq, 1, 1, lds,
+      [&](unsigned ip, unsigned iq, unsigned, const f32x4(&acc)[S::kP][S::kQ]) {
         const int64_t f0 = int64_t(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
                       q0 = int64_t(iq) * S::kBQ;
         const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
@@ -91,28 +91,153 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
       });
 }
 
-// out[q][p], with two groups of q the second one in out2
+// out[q][p], with two groups of q the second one in out2; with splits, each one's
+// share in rows of its own, all groups of q behind one another
 template <typename T, typename S>
 __global__ __launch_bounds__(S::kThreads) void product_kernel(Operand left, Operand right,
                                                               int64_t k, int terms, int groups,
-                                                              T* out, T* out2) {
+                                                              int splits, T* out, T* out2) {
   __shared__ __align__(1024) char lds[S::kLds];
   const unsigned np = unsigned((left.rows + S::kBP - 1) / S::kBP),
                  of_group = unsigned((right.rows + S::kBQ - 1) / S::kBQ);
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   product::tiles<S, false, S::kP * S::kQ>(
-      left, left, right, k, terms, np, of_group * groups, groups, lds,
-      [&](unsigned ip, unsigned iq, const f32x4(&acc)[S::kP][S::kQ]) {
+      left, left, right, k, terms, np, of_group * groups, groups, splits, lds,
+      [&](unsigned ip, unsigned iq, unsigned split, const f32x4(&acc)[S::kP][S::kQ]) {
         const int64_t p0 = int64_t(ip) * S::kBP + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4;
         const int q0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
-        const product::Rows<T> rows(iq < of_group ? out : out2, int64_t(iq % of_group) * S::kBQ,
-                                    right.rows, left.rows);
+        T* to = iq < of_group ? out : out2;
+        if (splits > 1)
+          to = out + (int64_t(split) * groups + iq / of_group) * right.rows * left.rows;
+        const product::Rows<T> rows(to, int64_t(iq % of_group) * S::kBQ, right.rows, left.rows);
 #pragma unroll
         for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
           for (int i = 0; i < S::kP; ++i)
             rows.put(q0 + j * 16, p0 + i * 16, left.rows, acc[i][j]);
       });
+}
+
+// out, out2 = sums of `splits` shares, in order; n values to each (a multiple of 4)
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(const float* shares, int64_t n, int groups,
+                                                   int splits, T* out, T* out2) {
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n * groups) return;
+  float s[4] = {};
+  for (int k = 0; k < splits; ++k) {
+    float x[4];
+    rowvec::load(shares + k * n * groups + i, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += x[e];
+  }
+  rowvec::store(i < n ? out + i : out2 + (i - n), s);
+}
+
+// ---- few rows
+
+// h for up to 16 MT rows: bound by the weights' bytes, which a wave reads straight
+// into the registers of its products.  A workgroup has 16 columns of h; its eight
+// waves have a share of D each, and their sums are joined through LDS in order.
+constexpr int kFewRows = 64, kFewWaves = 8;
+
+template <typename T>
+struct FewProduct;
+// 32 columns of D: lane l has row l % 16 and 8 columns from 8 (l / 16) on
+template <>
+struct FewProduct<__hip_bfloat16> {
+  static constexpr int kStep = 32, kLane = 8;
+  typedef __bf16 Piece __attribute__((ext_vector_type(8)));
+  __device__ static f32x4 add(Piece a, Piece b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+// 16 columns, 4 to a lane, on the float32 instruction, of which each takes one
+template <>
+struct FewProduct<float> {
+  static constexpr int kStep = 16, kLane = 4;
+  typedef f32x4 Piece;
+  __device__ static f32x4 add(Piece a, Piece b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+};
+
+template <typename T, int MT>
+__global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const T* wg, const T* wu,
+                                                                  const T* x, Sizes n, T* h) {
+  using P = FewProduct<T>;
+  using Piece = typename P::Piece;
+  __shared__ f32x4 sums[kFewWaves][2 * MT][64];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t f0 = int64_t(blockIdx.x) * 16, f = f0 + lane % 16;
+  const int64_t row = (f < n.F ? f : n.F - 1) * n.D;
+  const int64_t steps = (n.D + P::kStep - 1) / P::kStep,
+                share = (steps + kFewWaves - 1) / kFewWaves;
+  const int64_t from = wave * share, to = from + share < steps ? from + share : steps;
+  f32x4 g[MT], u[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) g[m] = u[m] = f32x4{};
+  constexpr int kAhead = MT <= 2 ? 4 : 2;  // steps whose loads are in flight together
+  for (int64_t s = from; s < to; s += kAhead) {
+    Piece a[kAhead], b[kAhead], v[kAhead][MT];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t k = (s + i) * P::kStep + lane / 16 * P::kLane;
+      const bool on = s + i < to && k < n.D;  // D is a multiple of a lane's columns
+      const int64_t at = on ? k : 0;
+      a[i] = *reinterpret_cast<const Piece*>(wg + row + at);
+      b[i] = *reinterpret_cast<const Piece*>(wu + row + at);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int64_t r = m * 16 + lane % 16;
+        const Piece p = *reinterpret_cast<const Piece*>(x + (r < n.M ? r : 0) * n.D + at);
+        v[i][m] = on && r < n.M ? p : Piece{};
+      }
+      if (!on) a[i] = b[i] = Piece{};
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        g[m] = P::add(a[i], v[i][m], g[m]);
+        u[m] = P::add(b[i], v[i][m], u[m]);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) sums[wave][2 * m][lane] = g[m], sums[wave][2 * m + 1][lane] = u[m];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 a = {}, b = {};
+#pragma unroll
+  for (int w = 0; w < kFewWaves; ++w) {
+    a += sums[w][2 * wave][lane];
+    b += sums[w][2 * wave + 1][lane];
+  }
+  // lane l: columns 4 (l / 16) .. of row l % 16
+  const int64_t r = wave * 16 + lane % 16, c = f0 + lane / 16 * 4;
+  if (r >= n.M || c >= n.F) return;
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = activation(a[e], n.gelu).value * b[e];
+  rowvec::store(h + r * n.F + c, o);
+}
+
+template <typename T>
+hipError_t few_rows(const GatedFfn& a, void* h, hipStream_t stream) {
+  const T *wg = static_cast<const T*>(a.w_gate), *wu = static_cast<const T*>(a.w_up),
+          *x = static_cast<const T*>(a.x);
+  const Sizes n = {a.M, a.D, a.F, 1, a.gelu};
+  const unsigned wgs = unsigned((a.F + 15) / 16);
+  T* out = static_cast<T*>(h);
+  if (a.M <= 16)
+    few_rows_kernel<T, 1><<<wgs, 64 * kFewWaves, 0, stream>>>(wg, wu, x, n, out);
+  else if (a.M <= 32)
+    few_rows_kernel<T, 2><<<wgs, 64 * kFewWaves, 0, stream>>>(wg, wu, x, n, out);
+  else
+    few_rows_kernel<T, 4><<<wgs, 64 * kFewWaves, 0, stream>>>(wg, wu, x, n, out);
+  return hipGetLastError();
 }
 
 // ---- operands: planes of float32, and transposes
@@ -261,14 +386,40 @@ hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const
   });
 }
 
+// How often a product's summed index is split, so that tiles that leave CUs idle are
+// taken by several: each share at least eight pieces long.
+template <typename T>
+int splits_of(int64_t p, int64_t q, int64_t k, int groups) {
+  const int64_t tiles = tiles_of<Small>(p, q) * groups,
+                pieces = (k + product::kStep - 1) / product::kStep * kTermsOf<T>;
+  int64_t n = kCUs / tiles;
+  if (n > pieces / 8) n = pieces / 8;
+  if (n < 2) return 1;
+  const int64_t share = (pieces + n - 1) / n;
+  return int((pieces + share - 1) / share);  // every share has a piece
+}
+
 template <typename T>
 hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int groups, void* out,
-                    void* out2, hipStream_t stream) {
+                    void* out2, Arena& ws, hipStream_t stream, bool run) {
+  const int splits = splits_of<T>(l.rows, r.rows, k, groups);
+  if (splits > 1) {
+    const int64_t n = l.rows * r.rows;
+    float* shares = ws.take<float>(splits * groups * n);
+    if (!run) return hipSuccess;
+    product_kernel<float, Small><<<unsigned(tiles_of<Small>(l.rows, r.rows) * groups * splits),
+                                   Small::kThreads, 0, stream>>>(l, r, k, kTermsOf<T>, groups,
+                                                                 splits, shares, shares);
+    join_kernel<T><<<unsigned((n * groups + 1023) / 1024), 256, 0, stream>>>(
+        shares, n, groups, splits, static_cast<T*>(out), static_cast<T*>(out2));
+    return hipGetLastError();
+  }
+  if (!run) return hipSuccess;
   return with_shape(l.rows, r.rows, groups, [&](auto shape) {
     using S = decltype(shape);
     const int64_t tiles = tiles_of<S>(l.rows, r.rows) * groups, most = kCUs * kPerCu<S>;
     product_kernel<T, S><<<unsigned(tiles < most ? tiles : most), S::kThreads, 0, stream>>>(
-        l, r, k, kTermsOf<T>, groups, static_cast<T*>(out), static_cast<T*>(out2));
+        l, r, k, kTermsOf<T>, groups, 1, static_cast<T*>(out), static_cast<T*>(out2));
     return hipGetLastError();
   });
 }
@@ -276,6 +427,7 @@ hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int groups, v
 // `run` false: only the workspace's size
 template <typename T>
 hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bool run) {
+  if (a.M <= kFewRows) return run ? few_rows<T>(a, h, stream) : hipSuccess;
   const Operand wg = as_rows<T>(a.w_gate, a.F, a.D, ws, stream, run),
                 wu = as_rows<T>(a.w_up, a.F, a.D, ws, stream, run),
                 x = as_rows<T>(a.x, a.M, a.D, ws, stream, run);
@@ -301,17 +453,17 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
     if (e != hipSuccess) return e;
   }
   const Operand G_rows = as_rows<T>(G, M, 2 * F, ws, stream, run);
-  if (!run) return hipSuccess;
-  // the two halves of wt, each [D] rows of 2 F
-  transposed<T>(a.w_gate, F, D, wt, F, 2 * F, wt_plane, stream);
-  transposed<T>(a.w_up, F, D, wt + F, F, 2 * F, wt_plane, stream);
-  transposed<T>(a.x, M, D, xt, pitch, pitch, xt_plane, stream);
-  transposed<T>(G, M, 2 * F, gt, pitch, pitch, gt_plane, stream);
+  if (run) {  // the two halves of wt, each [D] rows of 2 F
+    transposed<T>(a.w_gate, F, D, wt, F, 2 * F, wt_plane, stream);
+    transposed<T>(a.w_up, F, D, wt + F, F, 2 * F, wt_plane, stream);
+    transposed<T>(a.x, M, D, xt, pitch, pitch, xt_plane, stream);
+    transposed<T>(G, M, 2 * F, gt, pitch, pitch, gt_plane, stream);
+  }
   const hipError_t e =
-      multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, stream);
+      multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, ws, stream, run);
   if (e != hipSuccess) return e;
   return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, 2, g.dw_gate,
-                     g.dw_up, stream);
+                     g.dw_up, ws, stream, run);
 }
 
 }  // namespace

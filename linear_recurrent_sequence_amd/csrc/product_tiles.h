@@ -88,7 +88,7 @@ struct Fragments {
 };
 
 // The workgroup's tiles of np x nq, one after the other (of R's groups nq / groups
-// each); store(ip, iq, acc) with
+// each), each of them `splits` times with a share of the pieces; store(ip, iq, split, acc) with
 // acc[i][j] the accumulators of the wave's p block i and q block j.  DUAL: the left
 // rows are those of two operands in turn, a wave's first half of its blocks from L
 // and the second half from L2, for the same output columns (BP / 2 to a tile).
@@ -96,12 +96,18 @@ struct Fragments {
 // for with the next tile's first copies, which are older.
 template <typename S, bool DUAL, int STORES, typename F>
 __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand& R, int64_t k,
-                             int terms, unsigned np, unsigned nq, unsigned groups, char* lds,
-                             F&& store) {
+                             int terms, unsigned np, unsigned nq, unsigned groups, int splits,
+                             char* lds, F&& store) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wp = wave / S::kWQ, wq = wave % S::kWQ;
-  const unsigned n = np * nq, of_group = nq / groups;
-  const int steps = int((k + kStep - 1) / kStep);
+  const unsigned one = np * nq, n = one * splits, of_group = nq / groups;
+  const int steps = int((k + kStep - 1) / kStep), pieces = steps * terms;
+  const int share = (pieces + splits - 1) / splits;  // none is without a piece
+  auto first_of = [&](unsigned t) { return int(t / one) * share; };
+  auto last_of = [&](unsigned t) {
+    const int end = (int(t / one) + 1) * share;
+    return end < pieces ? end : pieces;
+  };
 
   // ---- copies: a cursor over the pieces of all tiles
   constexpr int kHalf = S::kBP / S::kWP / 2;  // DUAL: rows of one operand
@@ -116,15 +122,16 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
   };
   i32x4 left = {}, left2 = {}, right = {};
   unsigned tile = blockIdx.x;
-  int step = 0, term = 0, slot = 0;
+  int piece = tile < n ? first_of(tile) : 0, step = piece % steps, term = piece / steps, slot = 0;
+  bool fresh = true;  // a tile, or a plane, begins
   // The next piece's copies, for which begin() makes ready; beyond the last tile
   // they read zeros, so that as many are in flight at any time.
   unsigned col = 0;
   bool in = false;
   auto begin = [&]() {
-    if (step == 0 && tile < n) {
+    if (fresh && tile < n) {
       unsigned ip, iq;
-      map_tile(tile, np, nq, ip, iq);
+      map_tile(tile % one, np, nq, ip, iq);
       const int64_t p0 = int64_t(ip) * (DUAL ? S::kBP / 2 : S::kBP), q0 = int64_t(iq % of_group) * S::kBQ;
       const int lp = terms > 1 ? left_plane(term) : 0, rp = terms > 1 ? right_plane(term) : 0;
       left = words(L, p0, lp, 0);
@@ -134,9 +141,12 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
     // columns beyond k (a multiple of 8) in a plane's last piece are zeros
     in = tile < n && step * kStep + part * 8 < k;
     col = step * (kStep * 2);
-    if (++step == steps) {
-      step = 0;
-      if (++term == terms) term = 0, tile += gridDim.x;
+    fresh = false;
+    if (++step == steps) step = 0, ++term, fresh = true;
+    if (tile < n && ++piece == last_of(tile)) {
+      tile += gridDim.x;
+      fresh = true;
+      if (tile < n) piece = first_of(tile), step = piece % steps, term = piece / steps;
     }
   };
   auto copy = [&](int i) {  // pass i of kPassesP + kPassesQ
@@ -214,7 +224,7 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
     for (int i = 0; i < S::kP; ++i)
 #pragma unroll
       for (int j = 0; j < S::kQ; ++j) acc[i][j] = f32x4{};
-    for (int s = steps * terms; s > 0; --s) {
+    for (int s = last_of(t) - first_of(t); s > 0; --s) {
       multiply(a, b, slot, 1, std::false_type{});
       // this slot has been read, and the other one is whole
       if (stored)
@@ -227,8 +237,8 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
       slot ^= 1;
     }
     unsigned ip, iq;
-    map_tile(t, np, nq, ip, iq);
-    store(ip, iq, acc);
+    map_tile(t % one, np, nq, ip, iq);
+    store(ip, iq, t / one, acc);
     stored = true;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");

@@ -16,36 +16,35 @@ __global__ __launch_bounds__(256) void step_kernel(SelectiveScan a, T* y, float*
   const bool on = at < a.batch * a.channels;
   const int64_t row = on ? at : 0;  // lanes beyond take part in the sums
   const int64_t b = row / a.channels, c = row % a.channels, group = c / (a.channels / a.G);
-  const bool live = rowvec::length_of(a.lengths, b, 1) == 1, mine = n < a.N;
-  float u = 0.0f, delta = 0.0f;
-  if (live) {
-    u = rowvec::to_float(static_cast<const T*>(a.u)[b * a.u_row + c]);
-    const float x = rowvec::to_float(static_cast<const T*>(a.dt)[b * a.dt_row + c]);
-    delta = softplus(a.dt_bias ? x + a.dt_bias[c] : x);
-  }
-  const float v = delta * u;
-  float p = 0.0f, s[V] = {};
-  if (mine) {
-    float A[V];
-    rowvec::load(a.A + c * a.N + n, A);
-    if (a.state) rowvec::load(a.state + row * a.N + n, s);
-    const T* B = static_cast<const T*>(a.B) + b * a.B_row + group * a.N + n;
-    const T* C = static_cast<const T*>(a.C) + b * a.C_row + group * a.N + n;
+  // every load is issued before the first is waited for
+  const bool mine = n < a.N;
+  const int64_t at_n = mine ? n : 0;
+  const float u_in = rowvec::to_float(static_cast<const T*>(a.u)[b * a.u_row + c]);
+  const float dt = rowvec::to_float(static_cast<const T*>(a.dt)[b * a.dt_row + c]);
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.D ? a.D[c] : 0.0f;
+  const float z = a.gate ? rowvec::to_float(static_cast<const T*>(a.gate)[b * a.gate_row + c])
+                         : 0.0f;
+  const T* Bp = static_cast<const T*>(a.B) + b * a.B_row + group * a.N + at_n;
+  const T* Cp = static_cast<const T*>(a.C) + b * a.C_row + group * a.N + at_n;
+  float A[V], s[V] = {}, B[V], C[V];
+  rowvec::load(a.A + c * a.N + at_n, A);
+  if (a.state) rowvec::load(a.state + row * a.N + at_n, s);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float in = live ? v * rowvec::to_float(B[e]) : 0.0f;
-      s[e] = __builtin_fmaf(rowvec::exp2_fast(delta * (A[e] * rowvec::kLog2e)), s[e], in);
-      if (live) p = __builtin_fmaf(rowvec::to_float(C[e]), s[e], p);
-    }
-    if (on) rowvec::store(state_out + row * a.N + n, s);
+  for (int e = 0; e < V; ++e) B[e] = rowvec::to_float(Bp[e]), C[e] = rowvec::to_float(Cp[e]);
+  const bool live = rowvec::length_of(a.lengths, b, 1) == 1;
+  const float u = live ? u_in : 0.0f, delta = live ? softplus(dt + bias) : 0.0f, v = delta * u;
+  float p = 0.0f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float in = live ? v * B[e] : 0.0f;
+    s[e] = __builtin_fmaf(rowvec::exp2_fast(delta * (A[e] * rowvec::kLog2e)), s[e], in);
+    if (live && mine) p = __builtin_fmaf(C[e], s[e], p);
   }
+  if (on && mine) rowvec::store(state_out + row * a.N + n, s);
   for (int m = 1; m < (1 << lane_shift); m *= 2) p += __shfl_xor(p, m);
   if (on && n == 0) {
-    if (a.D) p = __builtin_fmaf(a.D[c], u, p);
-    if (a.gate && live) {
-      const float z = rowvec::to_float(static_cast<const T*>(a.gate)[b * a.gate_row + c]);
-      p *= z * rowvec::sigmoid(z);
-    }
+    p = __builtin_fmaf(skip, u, p);
+    if (a.gate) p = live ? p * (z * rowvec::sigmoid(z)) : 0.0f;
     rowvec::put(y + row, p);
   }
 }

@@ -441,9 +441,10 @@ def _require_all(named, device):
     on failure the messages of _require, devices last, so that a malformed
     tensor is named first."""
     if device.type == "cuda":
+        index = device.index
         for _, t, shape, dtype in named:
-            if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
-                    and t.device == device and t.is_contiguous()):
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                    and t.get_device() == index and t.is_contiguous()):
                 break
         else:
             return
@@ -667,6 +668,15 @@ def _require_rows(named, device):
     """Raise unless each (name, tensor, shape, dtype) is rows of contiguous
     elements with one pitch, on ``device`` -> the pitches, in elements.  ``shape``:
     its first two (B, T) or first (B) sizes count rows, ``row`` elements each."""
+    if device.type == "cuda":  # the common case, as in _require_all
+        index = device.index
+        for _, t, shape, dtype, _ in named:
+            if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype
+                                      and t.shape == shape and t.get_device() == index
+                                      and t.is_contiguous()):
+                break
+        else:
+            return [row for _, _, _, _, row in named]
     pitches = []
     for name, t, shape, dtype, row in named:
         if t is None:
@@ -818,7 +828,7 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, heads=None
                                         {"state": state, "dstate": dstate}, dy)
     code, dtype = _named_code("activation", CONV_ACTIVATIONS, activation), _dtype_code(x)
     with _on(x.device):
-        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+        g = {"dx": torch.empty_like(x, memory_format=torch.contiguous_format),
              "dweight": torch.empty_like(weight)}
         if bias is not None:
             g["dbias"] = torch.empty_like(bias)
@@ -887,8 +897,10 @@ def _scan(u, dt, A, B, C, D, gate, dt_bias, state, out_state, lengths, dims):
     with _on(u.device):
         if out_state is None:
             out_state = torch.empty((sizes[0], *A.shape), dtype=torch.float32, device=u.device)
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        ws = _workspace(lib.mlstm_scan_workspace_bytes(*sizes, code, 0), u.device)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
+        ws = None
+        if sizes[1] > 1:
+            ws = _workspace(lib.mlstm_scan_workspace_bytes(*sizes, code, 0), u.device)
         st = lib.mlstm_scan_fwd(*args, y.data_ptr(), out_state.data_ptr(), _ptr(ws),
                                 0 if ws is None else ws.numel(), *sizes, code,
                                 _stream_ptr(u.device))
@@ -938,7 +950,7 @@ def scan_bwd(u, dt, A, B, C, dy, D=None, gate=None, dt_bias=None, state=None, ds
     code = _dtype_code(u)
 
     def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
     with _on(u.device):
         g = {n: like(t) for n, t in (("du", u), ("ddt", dt), ("dA", A), ("dB", B), ("dC", C),
