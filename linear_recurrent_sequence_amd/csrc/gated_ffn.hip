@@ -23,6 +23,7 @@ namespace {
 
 using product::f32x4;
 using product::Operand;
+using product::Plan;
 
 using Large = product::Shape<256, 256, 2, 4>;
 using Medium = product::Shape<128, 256, 2, 4>;
@@ -49,89 +50,138 @@ struct Sizes {
   bool gelu;
 };
 
+// Four outputs from g and u: h (a), or with GRAD dg and du, from dh
+struct Pair {
+  f32x4 a, b;
+};
+template <bool GRAD>
+__device__ inline Pair gate_up_of(f32x4 g, f32x4 u, const float (&d)[4], bool gelu) {
+  Pair o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const Act act = activation(g[e], gelu);
+    if constexpr (GRAD) {
+      o.a[e] = d[e] * u[e] * act.slope;
+      o.b[e] = d[e] * act.value;
+    } else {
+      o.a[e] = act.value * u[e];
+    }
+  }
+  return o;
+}
+
 // h, or with GRAD G = [dg | du], in tiles of rows and of F
 template <typename T, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operand wu, Operand x,
-                                                              Sizes n, const T* dh, T* out) {
+                                                              Sizes n, Plan plan, const T* dh,
+                                                              T* out, float* shares) {
   __shared__ __align__(1024) char lds[S::kLds];
   constexpr int kF = S::kBP / 2, kStores = (GRAD ? S::kP : S::kP / 2) * S::kQ;
-  const unsigned np = unsigned((n.F + kF - 1) / kF), nq = unsigned((n.M + S::kBQ - 1) / S::kBQ);
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   product::tiles<S, true, kStores>(
-      wg, wu, x, n.D, n.terms, np, nq, 1, 1, lds,
-      [&](unsigned ip, unsigned iq, unsigned, const f32x4(&acc)[S::kP][S::kQ]) {
-        const int64_t f0 = int64_t(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
-                      q0 = int64_t(iq) * S::kBQ;
+      wg, wu, x, n.D, n.terms, plan, lds,
+      [&](unsigned ip, unsigned iq, const product::Item& item,
+          const f32x4(&acc)[S::kP][S::kQ]) {
+        if (item.split >= 0)
+          return product::put_share<S>(
+              product::Rows<float>(product::share_at<S>(plan, shares, item), 0, S::kBQ, S::kBP),
+              acc);
+        const int f0 = int(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
+                  q0 = int(iq) * S::kBQ, F = int(n.F), M = int(n.M);
         const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
-        const product::Rows<T> rows(out, q0, n.M, GRAD ? 2 * n.F : n.F);
+        const product::Rows<T> rows(out, q0, M, GRAD ? 2 * F : F);
 #pragma unroll
         for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
           for (int i = 0; i < S::kP / 2; ++i) {
-            const int64_t f = f0 + i * 16, m = q0 + m0 + j * 16;
-            const f32x4 g = acc[i][j], u = acc[i + S::kP / 2][j];
-            f32x4 a, b;
-            if constexpr (GRAD) {
-              float d[4] = {};
-              if (m < n.M && f < n.F) rowvec::load(dh + m * n.F + f, d);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const Act act = activation(g[e], n.gelu);
-                a[e] = d[e] * u[e] * act.slope;
-                b[e] = d[e] * act.value;
-              }
-              rows.put(m0 + j * 16, f, n.F, a);
-              rows.put(m0 + j * 16, n.F + f, 2 * n.F, b);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) a[e] = activation(g[e], n.gelu).value * u[e];
-              rows.put(m0 + j * 16, f, n.F, a);
-            }
+            const int f = f0 + i * 16, m = q0 + m0 + j * 16;
+            float d[4] = {};
+            if (GRAD && m < M && f < F) rowvec::load(dh + int64_t(m) * F + f, d);
+            const Pair o = gate_up_of<GRAD>(acc[i][j], acc[i + S::kP / 2][j], d, n.gelu);
+            rows.put(m0 + j * 16, f, F, o.a);
+            if constexpr (GRAD) rows.put(m0 + j * 16, f < F ? F + f : 2 * F, 2 * F, o.b);
           }
       });
 }
 
-// out[q][p], with two groups of q the second one in out2; with splits, each one's
-// share in rows of its own, all groups of q behind one another
+// out[q][p], with two groups of q the second one in out2
 template <typename T, typename S>
 __global__ __launch_bounds__(S::kThreads) void product_kernel(Operand left, Operand right,
-                                                              int64_t k, int terms, int groups,
-                                                              int splits, T* out, T* out2) {
+                                                              int64_t k, int terms, Plan plan,
+                                                              T* out, T* out2, float* shares) {
   __shared__ __align__(1024) char lds[S::kLds];
-  const unsigned np = unsigned((left.rows + S::kBP - 1) / S::kBP),
-                 of_group = unsigned((right.rows + S::kBQ - 1) / S::kBQ);
+  const unsigned of_group = plan.nq / plan.groups;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   product::tiles<S, false, S::kP * S::kQ>(
-      left, left, right, k, terms, np, of_group * groups, groups, splits, lds,
-      [&](unsigned ip, unsigned iq, unsigned split, const f32x4(&acc)[S::kP][S::kQ]) {
-        const int64_t p0 = int64_t(ip) * S::kBP + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4;
-        const int q0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
-        T* to = iq < of_group ? out : out2;
-        if (splits > 1)
-          to = out + (int64_t(split) * groups + iq / of_group) * right.rows * left.rows;
-        const product::Rows<T> rows(to, int64_t(iq % of_group) * S::kBQ, right.rows, left.rows);
+      left, left, right, k, terms, plan, lds,
+      [&](unsigned ip, unsigned iq, const product::Item& item,
+          const f32x4(&acc)[S::kP][S::kQ]) {
+        if (item.split >= 0)
+          return product::put_share<S>(
+              product::Rows<float>(product::share_at<S>(plan, shares, item), 0, S::kBQ, S::kBP),
+              acc);
+        const int p0 = int(ip) * S::kBP + wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4,
+                  q0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16, width = int(left.rows);
+        const product::Rows<T> rows(iq < of_group ? out : out2, int64_t(iq % of_group) * S::kBQ,
+                                    right.rows, width);
 #pragma unroll
         for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
           for (int i = 0; i < S::kP; ++i)
-            rows.put(q0 + j * 16, p0 + i * 16, left.rows, acc[i][j]);
+            rows.put(q0 + j * 16, p0 + i * 16, width, acc[i][j]);
       });
 }
 
-// out, out2 = sums of `splits` shares, in order; n values to each (a multiple of 4)
-template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(const float* shares, int64_t n, int groups,
-                                                   int splits, T* out, T* out2) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= n * groups) return;
-  float s[4] = {};
-  for (int k = 0; k < splits; ++k) {
-    float x[4];
-    rowvec::load(shares + k * n * groups + i, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] += x[e];
+// Four neighbouring columns of a tile of the plan's rest: its shares added in order
+template <typename S>
+__device__ inline f32x4 joined(const Plan& plan, const float* shares, unsigned rest, int q, int p) {
+  f32x4 s = {};
+  for (int k = 0; k < plan.splits; ++k)
+    s += *reinterpret_cast<const f32x4*>(
+        shares + ((int64_t(k) * plan.rest() + rest) * S::kBQ + q) * S::kBP + p);
+  return s;
+}
+
+// The rest of product_kernel's tiles; four rows of a tile to a workgroup of 256
+template <typename T, typename S>
+__global__ __launch_bounds__(S::kBP) void join_kernel(Plan plan, const float* shares, int64_t p_rows,
+                                                      int64_t q_rows, T* out, T* out2) {
+  const unsigned rest = blockIdx.x / (S::kBQ / 4), of_group = plan.nq / plan.groups;
+  unsigned ip, iq;
+  product::map_tile(plan.whole + rest, plan.np, plan.nq, ip, iq);
+  const int q = int(blockIdx.x % (S::kBQ / 4)) * 4 + threadIdx.x / (S::kBP / 4),
+            p = threadIdx.x % (S::kBP / 4) * 4;
+  const int64_t row = int64_t(iq % of_group) * S::kBQ + q, col = int64_t(ip) * S::kBP + p;
+  if (row >= q_rows || col >= p_rows) return;
+  const f32x4 s = joined<S>(plan, shares, rest, q, p);
+  const float x[4] = {s[0], s[1], s[2], s[3]};
+  rowvec::store((iq < of_group ? out : out2) + row * p_rows + col, x);
+}
+
+// The rest of gate_up_kernel's tiles, eight rows of a tile to a workgroup
+template <typename T, typename S, bool GRAD>
+__global__ __launch_bounds__(S::kBP) void join_gate_up_kernel(Plan plan, const float* shares,
+                                                              Sizes n, const T* dh, T* out) {
+  constexpr int kF = S::kBP / 2, kHalf = kF / S::kWP;  // columns; of a wave's rows of one operand
+  const unsigned rest = blockIdx.x / (S::kBQ / 8);
+  unsigned ip, iq;
+  product::map_tile(plan.whole + rest, plan.np, plan.nq, ip, iq);
+  const int q = int(blockIdx.x % (S::kBQ / 8)) * 8 + threadIdx.x / (kF / 4),
+            c = threadIdx.x % (kF / 4) * 4, p = c / kHalf * 2 * kHalf + c % kHalf;
+  const int64_t m = int64_t(iq) * S::kBQ + q, f = int64_t(ip) * kF + c;
+  if (m >= n.M || f >= n.F) return;
+  float d[4] = {};
+  if (GRAD) rowvec::load(dh + m * n.F + f, d);
+  const Pair o = gate_up_of<GRAD>(joined<S>(plan, shares, rest, q, p),
+                                  joined<S>(plan, shares, rest, q, p + kHalf), d, n.gelu);
+  const float a[4] = {o.a[0], o.a[1], o.a[2], o.a[3]};
+  if constexpr (GRAD) {
+    const float b[4] = {o.b[0], o.b[1], o.b[2], o.b[3]};
+    rowvec::store(out + m * 2 * n.F + f, a);
+    rowvec::store(out + (m * 2 + 1) * n.F + f, b);
+  } else {
+    rowvec::store(out + m * n.F + f, a);
   }
-  rowvec::store(i < n ? out + i : out2 + (i - n), s);
 }
 
 // ---- few rows
@@ -251,56 +301,67 @@ __device__ inline void planes_of(float x, uint16_t (&p)[kPlanes]) {
   }
 }
 
-// planes of n values (a multiple of 4)
-__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t n, uint16_t* out,
-                                                    int64_t plane) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  const float4 f = *reinterpret_cast<const float4*>(x + i);
-  const float v[4] = {f.x, f.y, f.z, f.w};
-  uint16_t p[4][kPlanes];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) planes_of(v[e], p[e]);
-#pragma unroll
-  for (int k = 0; k < kPlanes; ++k)
-    *reinterpret_cast<ushort4*>(out + k * plane + i) =
-        make_ushort4(p[0][k], p[1][k], p[2][k], p[3][k]);
-}
-
-// out[c][r] = in[r][c] with rows of `width` outputs, `pitch` apart, zeros for r from
-// `rows` on; in 64 x 64 tiles through LDS.  float32 becomes planes.
+// A matrix [rows][cols] made an operand: as it lies (`straight`), and turned into
+// `cols` rows of `width` (rows, rounded up to 8; zeros there), `pitch` apart
+// (`turned`); either may be NULL.  float32 becomes planes, `plane` and `turned_plane`
+// elements apart.  64 x 64 tiles through LDS; up to three matrices in a launch.
+struct Job {
+  const void* in;
+  int64_t rows, cols;
+  uint16_t* straight;
+  int64_t plane;
+  uint16_t* turned;
+  int64_t width, pitch, turned_plane;
+  __host__ __device__ int64_t tiles() const {
+    const int64_t high = width > rows ? width : rows;
+    return ((cols + 63) / 64) * ((high + 63) / 64);
+  }
+};
+struct Jobs {
+  Job job[3];
+  int n;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t rows, int64_t cols,
-                                                        uint16_t* out, int64_t width,
-                                                        int64_t pitch, int64_t plane) {
+__global__ __launch_bounds__(256) void operands_kernel(Jobs jobs) {
   constexpr int N = sizeof(T) == 4 ? kPlanes : 1;
   __shared__ uint16_t tile[N][64][66];
-  const int64_t tiles = (cols + 63) / 64;
-  const int64_t c0 = blockIdx.x % tiles * 64, r0 = blockIdx.x / tiles * 64;
+  int64_t at = blockIdx.x;
+  int which = 0;
+  while (which + 1 < jobs.n && at >= jobs.job[which].tiles()) at -= jobs.job[which++].tiles();
+  const Job& j = jobs.job[which];
+  const T* in = static_cast<const T*>(j.in);
+  const int64_t across = (j.cols + 63) / 64;
+  const int64_t c0 = at % across * 64, r0 = at / across * 64;
   for (int i = threadIdx.x; i < 64 * 16; i += 256) {
     const int r = i / 16, c = i % 16 * 4;
+    const bool on = r0 + r < j.rows && c0 + c < j.cols;
     float v[4] = {};
-    if (r0 + r < rows && c0 + c < cols) rowvec::load(in + (r0 + r) * cols + c0 + c, v);
+    if (on) rowvec::load(in + (r0 + r) * j.cols + c0 + c, v);
+    uint16_t p[4][N];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if constexpr (N == 1) {
-        tile[0][c + e][r] = uint16_t(__float_as_uint(v[e]) >> 16);
-      } else {
-        uint16_t p[kPlanes];
-        planes_of(v[e], p);
+      if constexpr (N == 1)
+        p[e][0] = uint16_t(__float_as_uint(v[e]) >> 16);
+      else
+        planes_of(v[e], p[e]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) tile[k][c + e][r] = p[k];
-      }
+      for (int k = 0; k < N; ++k) tile[k][c + e][r] = p[e][k];
     }
+    if (on && j.straight)
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        *reinterpret_cast<ushort4*>(j.straight + k * j.plane + (r0 + r) * j.cols + c0 + c) =
+            make_ushort4(p[0][k], p[1][k], p[2][k], p[3][k]);
   }
+  if (!j.turned) return;
   __syncthreads();
   for (int i = threadIdx.x; i < 64 * 16; i += 256) {
     const int c = i / 16, r = i % 16 * 4;
-    if (c0 + c < cols && r0 + r < width)
+    if (c0 + c < j.cols && r0 + r < j.width)
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        *reinterpret_cast<ushort4*>(out + k * plane + (c0 + c) * pitch + r0 + r) = make_ushort4(
-            tile[k][c][r], tile[k][c][r + 1], tile[k][c][r + 2], tile[k][c][r + 3]);
+        *reinterpret_cast<ushort4*>(j.turned + k * j.turned_plane + (c0 + c) * j.pitch + r0 + r) =
+            make_ushort4(tile[k][c][r], tile[k][c][r + 1], tile[k][c][r + 2], tile[k][c][r + 3]);
   }
 }
 
@@ -325,101 +386,123 @@ constexpr int kCopies = sizeof(T) == 4 ? kPlanes : 1;
 template <typename T>
 constexpr int kTermsOf = sizeof(T) == 4 ? kTerms : 1;
 
-// an operand of the products: a bf16 matrix as it is, the planes of a float32 one
+// a matrix as an operand: a bf16 one as it is, a float32 one as planes, which `job`
+// is told to make
 template <typename T>
-Operand as_rows(const void* p, int64_t rows, int64_t k, Arena& ws, hipStream_t stream, bool run) {
-  if constexpr (sizeof(T) == 2) {
-    return {static_cast<const uint16_t*>(p), rows, 0, 0};
-  } else {
-    uint16_t* out = ws.take<uint16_t>(kPlanes * rows * k);
-    if (run)
-      split_kernel<<<unsigned((rows * k + 1023) / 1024), 256, 0, stream>>>(
-          static_cast<const float*>(p), rows * k, out, rows * k);
-    return {out, rows, rows * k, 0};
-  }
+Operand as_rows(const void* p, int64_t rows, int64_t k, Arena& ws, Job& job) {
+  job = {p, rows, k, nullptr, 0, nullptr, 0, 0, 0};
+  if constexpr (sizeof(T) == 2) return {static_cast<const uint16_t*>(p), rows, 0, 0};
+  job.straight = ws.take<uint16_t>(kPlanes * rows * k);
+  job.plane = rows * k;
+  return {job.straight, rows, rows * k, 0};
 }
-
-// a matrix [rows][cols] as `cols` rows of `width` (rows, rounded up to 8)
+// and turned
+void turn(Job& job, uint16_t* out, int64_t width, int64_t pitch, int64_t plane) {
+  job.turned = out;
+  job.width = width;
+  job.pitch = pitch;
+  job.turned_plane = plane;
+}
 template <typename T>
-void transposed(const void* p, int64_t rows, int64_t cols, uint16_t* out, int64_t width,
-                int64_t pitch, int64_t plane, hipStream_t stream) {
-  const int64_t n = ((cols + 63) / 64) * ((width + 63) / 64);
-  transpose_kernel<T><<<unsigned(n), 256, 0, stream>>>(static_cast<const T*>(p), rows, cols, out,
-                                                       width, pitch, plane);
+void prepare(const Jobs& jobs, hipStream_t stream) {
+  int64_t n = 0;
+  for (int i = 0; i < jobs.n; ++i) n += jobs.job[i].tiles();
+  operands_kernel<T><<<unsigned(n), 256, 0, stream>>>(jobs);
 }
 
 constexpr int64_t kCUs = 256;
 
-template <typename S>
-int64_t tiles_of(int64_t p, int64_t q) {
-  return ((p + S::kBP - 1) / S::kBP) * ((q + S::kBQ - 1) / S::kBQ);
-}
 // Workgroups that a CU holds at a time
 template <typename S>
 constexpr int kPerCu = S::kLds <= 64 * 1024 ? 2 : 1;
 
-// f(shape) with the tile of the least time for p x q outputs (in each of `groups`):
-// the rounds of tiles that a CU takes, at what each takes.
+// The plan for p x q outputs (in each of `groups`) of `pieces` pieces, and the
+// microseconds that it is expected to take: a round of tiles takes 4 and `piece` for
+// each piece, and the tiles that do not fill a round are split where that takes less,
+// with 6 for joining the shares and their way to memory and back at 4.5 TB/s.
+struct Choice {
+  Plan plan;
+  double time;
+};
+template <typename S>
+Choice choose(int64_t p, int64_t q, unsigned groups, int64_t pieces, double piece) {
+  const unsigned np = unsigned((p + S::kBP - 1) / S::kBP),
+                 nq = unsigned((q + S::kBQ - 1) / S::kBQ) * groups;
+  const unsigned at_once = unsigned(kCUs) * kPerCu<S>, n = np * nq;
+  auto rounds = [&](unsigned items) { return double((items + at_once - 1) / at_once); };
+  auto round = [&](int64_t m) { return 4.0 + piece * double(m); };
+  Choice best = {{np, nq, groups, n, 1}, rounds(n) * round(pieces)};
+  const unsigned rest = n % at_once;
+  if (rest == 0) return best;
+  for (int s = 2; s <= 16 && int64_t(s) * 4 <= pieces; ++s) {
+    const int64_t share = (pieces + s - 1) / s;
+    if ((pieces + share - 1) / share != s) continue;  // every share has a piece
+    const double t = rounds(n - rest) * round(pieces) + rounds(rest * s) * round(share) + 6.0 +
+                     double(rest) * s * (S::kBP * S::kBQ * 8) / 4.5e6;
+    if (t < 0.97 * best.time) best = {{np, nq, groups, n - rest, s}, t};
+  }
+  return best;
+}
+
+// f(shape, plan) with the tiles of the least time.  A piece takes 1.75 us in tiles of
+// 256 x 256 on all CUs, 1.05 in 128 x 256, and 1.15 in 128 x 128, two to a CU (8192
+// rows through 2048 x 5504 and their gradients).
 template <typename F>
-hipError_t with_shape(int64_t p, int64_t q, int64_t groups, F&& f) {
-  auto rounds = [&](int64_t tiles, int64_t at_once) {
-    return double((tiles * groups + kCUs * at_once - 1) / (kCUs * at_once));
-  };
-  const double large = rounds(tiles_of<Large>(p, q), 1),
-               medium = 0.6 * rounds(tiles_of<Medium>(p, q), 1);
-  const int64_t n = tiles_of<Small>(p, q) * groups;
-  const double small = n <= kCUs ? 0.4 : 0.65 * rounds(tiles_of<Small>(p, q), 2);
-  if (small < large && small < medium) return f(Small{});
-  if (medium < large) return f(Medium{});
-  return f(Large{});
+hipError_t with_shape(int64_t p, int64_t q, unsigned groups, int64_t pieces, F&& f) {
+  const Choice large = choose<Large>(p, q, groups, pieces, 1.75),
+               medium = choose<Medium>(p, q, groups, pieces, 1.05),
+               small = choose<Small>(p, q, groups, pieces, 1.15);
+  if (small.time < large.time && small.time < medium.time) return f(Small{}, small.plan);
+  if (medium.time < large.time) return f(Medium{}, medium.plan);
+  return f(Large{}, large.plan);
+}
+
+template <typename S>
+unsigned workgroups_of(const Plan& plan) {
+  const unsigned most = unsigned(kCUs) * kPerCu<S>;
+  return plan.items() < most ? plan.items() : most;
+}
+template <typename S>
+float* take_shares(const Plan& plan, Arena& ws) {
+  return plan.splits > 1
+             ? ws.take<float>(int64_t(plan.rest()) * plan.splits * (S::kBP * S::kBQ)) : nullptr;
+}
+template <typename T>
+int64_t pieces_of(int64_t k) {
+  return (k + product::kStep - 1) / product::kStep * kTermsOf<T>;
 }
 
 template <typename T, bool GRAD>
 hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
-                   const void* dh, void* out, hipStream_t stream) {
-  return with_shape(2 * n.F, n.M, 1, [&](auto shape) {
+                   const void* dh, void* out, Arena& ws, hipStream_t stream, bool run) {
+  return with_shape(2 * n.F, n.M, 1, pieces_of<T>(n.D), [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
-    const int64_t tiles = tiles_of<S>(2 * n.F, n.M), most = kCUs * kPerCu<S>;
-    gate_up_kernel<T, S, GRAD><<<unsigned(tiles < most ? tiles : most), S::kThreads, 0, stream>>>(
-        wg, wu, x, n, static_cast<const T*>(dh), static_cast<T*>(out));
+    float* shares = take_shares<S>(plan, ws);
+    if (!run) return hipSuccess;
+    const T* d = static_cast<const T*>(dh);
+    T* o = static_cast<T*>(out);
+    gate_up_kernel<T, S, GRAD><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
+        wg, wu, x, n, plan, d, o, shares);
+    if (shares)
+      join_gate_up_kernel<T, S, GRAD><<<plan.rest() * (S::kBQ / 8), S::kBP, 0, stream>>>(
+          plan, shares, n, d, o);
     return hipGetLastError();
   });
 }
 
-// How often a product's summed index is split, so that tiles that leave CUs idle are
-// taken by several: each share at least eight pieces long.
 template <typename T>
-int splits_of(int64_t p, int64_t q, int64_t k, int groups) {
-  const int64_t tiles = tiles_of<Small>(p, q) * groups,
-                pieces = (k + product::kStep - 1) / product::kStep * kTermsOf<T>;
-  int64_t n = kCUs / tiles;
-  if (n > pieces / 8) n = pieces / 8;
-  if (n < 2) return 1;
-  const int64_t share = (pieces + n - 1) / n;
-  return int((pieces + share - 1) / share);  // every share has a piece
-}
-
-template <typename T>
-hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int groups, void* out,
+hipError_t multiply(const Operand& l, const Operand& r, int64_t k, unsigned groups, void* out,
                     void* out2, Arena& ws, hipStream_t stream, bool run) {
-  const int splits = splits_of<T>(l.rows, r.rows, k, groups);
-  if (splits > 1) {
-    const int64_t n = l.rows * r.rows;
-    float* shares = ws.take<float>(splits * groups * n);
-    if (!run) return hipSuccess;
-    product_kernel<float, Small><<<unsigned(tiles_of<Small>(l.rows, r.rows) * groups * splits),
-                                   Small::kThreads, 0, stream>>>(l, r, k, kTermsOf<T>, groups,
-                                                                 splits, shares, shares);
-    join_kernel<T><<<unsigned((n * groups + 1023) / 1024), 256, 0, stream>>>(
-        shares, n, groups, splits, static_cast<T*>(out), static_cast<T*>(out2));
-    return hipGetLastError();
-  }
-  if (!run) return hipSuccess;
-  return with_shape(l.rows, r.rows, groups, [&](auto shape) {
+  return with_shape(l.rows, r.rows, groups, pieces_of<T>(k), [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
-    const int64_t tiles = tiles_of<S>(l.rows, r.rows) * groups, most = kCUs * kPerCu<S>;
-    product_kernel<T, S><<<unsigned(tiles < most ? tiles : most), S::kThreads, 0, stream>>>(
-        l, r, k, kTermsOf<T>, groups, 1, static_cast<T*>(out), static_cast<T*>(out2));
+    float* shares = take_shares<S>(plan, ws);
+    if (!run) return hipSuccess;
+    T *o = static_cast<T*>(out), *o2 = static_cast<T*>(out2);
+    product_kernel<T, S><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
+        l, r, k, kTermsOf<T>, plan, o, o2, shares);
+    if (shares)
+      join_kernel<T, S><<<plan.rest() * (S::kBQ / 4), S::kBP, 0, stream>>>(plan, shares, l.rows,
+                                                                           r.rows, o, o2);
     return hipGetLastError();
   });
 }
@@ -428,39 +511,43 @@ hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int groups, v
 template <typename T>
 hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bool run) {
   if (a.M <= kFewRows) return run ? few_rows<T>(a, h, stream) : hipSuccess;
-  const Operand wg = as_rows<T>(a.w_gate, a.F, a.D, ws, stream, run),
-                wu = as_rows<T>(a.w_up, a.F, a.D, ws, stream, run),
-                x = as_rows<T>(a.x, a.M, a.D, ws, stream, run);
-  if (!run) return hipSuccess;
-  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, stream);
+  Jobs jobs;
+  jobs.n = 3;
+  const Operand wg = as_rows<T>(a.w_gate, a.F, a.D, ws, jobs.job[0]),
+                wu = as_rows<T>(a.w_up, a.F, a.D, ws, jobs.job[1]),
+                x = as_rows<T>(a.x, a.M, a.D, ws, jobs.job[2]);
+  if (run && sizeof(T) == 4) prepare<T>(jobs, stream);
+  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
+                           run);
 }
 
 template <typename T>
 hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStream_t stream,
                     bool run) {
   const int64_t M = a.M, D = a.D, F = a.F, pitch = (M + 7) / 8 * 8;
-  const Operand wg = as_rows<T>(a.w_gate, F, D, ws, stream, run),
-                wu = as_rows<T>(a.w_up, F, D, ws, stream, run),
-                x = as_rows<T>(a.x, M, D, ws, stream, run);
+  Jobs jobs;
+  jobs.n = 3;
+  const Operand wg = as_rows<T>(a.w_gate, F, D, ws, jobs.job[0]),
+                wu = as_rows<T>(a.w_up, F, D, ws, jobs.job[1]),
+                x = as_rows<T>(a.x, M, D, ws, jobs.job[2]);
   T* G = ws.take<T>(M * 2 * F);
   const int64_t wt_plane = D * 2 * F, xt_plane = D * pitch, gt_plane = 2 * F * pitch;
   uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);  // [D][Wg^T | Wu^T]
   uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);  // [D][M]
   uint16_t* gt = ws.take<uint16_t>(kCopies<T> * gt_plane);  // [2F][M]
-  if (run) {
-    const hipError_t e =
-        gate_up<T, true>(wg, wu, x, {M, D, F, kTermsOf<T>, a.gelu}, g.dh, G, stream);
-    if (e != hipSuccess) return e;
-  }
-  const Operand G_rows = as_rows<T>(G, M, 2 * F, ws, stream, run);
-  if (run) {  // the two halves of wt, each [D] rows of 2 F
-    transposed<T>(a.w_gate, F, D, wt, F, 2 * F, wt_plane, stream);
-    transposed<T>(a.w_up, F, D, wt + F, F, 2 * F, wt_plane, stream);
-    transposed<T>(a.x, M, D, xt, pitch, pitch, xt_plane, stream);
-    transposed<T>(G, M, 2 * F, gt, pitch, pitch, gt_plane, stream);
-  }
-  const hipError_t e =
-      multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, ws, stream, run);
+  turn(jobs.job[0], wt, F, 2 * F, wt_plane);
+  turn(jobs.job[1], wt + F, F, 2 * F, wt_plane);
+  turn(jobs.job[2], xt, pitch, pitch, xt_plane);
+  if (run) prepare<T>(jobs, stream);
+  hipError_t e = gate_up<T, true>(wg, wu, x, {M, D, F, kTermsOf<T>, a.gelu}, g.dh, G, ws, stream,
+                                  run);
+  if (e != hipSuccess) return e;
+  Jobs more;
+  more.n = 1;
+  const Operand G_rows = as_rows<T>(G, M, 2 * F, ws, more.job[0]);
+  turn(more.job[0], gt, pitch, pitch, gt_plane);
+  if (run) prepare<T>(more, stream);
+  e = multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, ws, stream, run);
   if (e != hipSuccess) return e;
   return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, 2, g.dw_gate,
                      g.dw_up, ws, stream, run);

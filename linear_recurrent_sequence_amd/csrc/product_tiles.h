@@ -87,8 +87,29 @@ struct Fragments {
   bf16x8 l[S::kP], r[S::kQ];
 };
 
-// The workgroup's tiles of np x nq, one after the other (of R's groups nq / groups
-// each), each of them `splits` times with a share of the pieces; store(ip, iq, split, acc) with
+// The tiles of a product.  The first `whole` of np x nq are taken as they are; the
+// others by `splits` workgroups each, with a share of the pieces, so that the CUs that
+// the last round of tiles would leave idle have work.
+struct Plan {
+  unsigned np, nq, groups;  // nq / groups tiles of each of R's groups
+  unsigned whole;
+  int splits;
+  __host__ __device__ unsigned tiles() const { return np * nq; }
+  __host__ __device__ unsigned rest() const { return tiles() - whole; }
+  __host__ __device__ unsigned items() const { return whole + rest() * unsigned(splits); }
+};
+// An item of the plan: a tile, and its share (-1: whole)
+struct Item {
+  unsigned tile;
+  int split;
+};
+__device__ inline Item item_of(const Plan& p, unsigned i) {
+  if (i < p.whole) return {i, -1};
+  const unsigned r = i - p.whole;
+  return {p.whole + r % p.rest(), p.splits > 1 ? int(r / p.rest()) : -1};
+}
+
+// The workgroup's items, one after the other; store(ip, iq, item, acc) with
 // acc[i][j] the accumulators of the wave's p block i and q block j.  DUAL: the left
 // rows are those of two operands in turn, a wave's first half of its blocks from L
 // and the second half from L2, for the same output columns (BP / 2 to a tile).
@@ -96,17 +117,15 @@ struct Fragments {
 // for with the next tile's first copies, which are older.
 template <typename S, bool DUAL, int STORES, typename F>
 __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand& R, int64_t k,
-                             int terms, unsigned np, unsigned nq, unsigned groups, int splits,
-                             char* lds, F&& store) {
+                             int terms, const Plan& plan, char* lds, F&& store) {
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wp = wave / S::kWQ, wq = wave % S::kWQ;
-  const unsigned one = np * nq, n = one * splits, of_group = nq / groups;
+  const unsigned n = plan.items(), np = plan.np, nq = plan.nq, of_group = nq / plan.groups;
   const int steps = int((k + kStep - 1) / kStep), pieces = steps * terms;
-  const int share = (pieces + splits - 1) / splits;  // none is without a piece
-  auto first_of = [&](unsigned t) { return int(t / one) * share; };
-  auto last_of = [&](unsigned t) {
-    const int end = (int(t / one) + 1) * share;
-    return end < pieces ? end : pieces;
+  const int share = (pieces + plan.splits - 1) / plan.splits;  // none is without a piece
+  auto first_of = [&](const Item& t) { return t.split < 0 ? 0 : t.split * share; };
+  auto last_of = [&](const Item& t) {
+    return t.split < 0 || (t.split + 1) * share > pieces ? pieces : (t.split + 1) * share;
   };
 
   // ---- copies: a cursor over the pieces of all tiles
@@ -114,24 +133,25 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
   static_assert(kHalf % 8 == 0, "a wave's copy is of one operand");
   const int row = threadIdx.x / 8, part = (threadIdx.x % 8) ^ (row & 7);
   const unsigned pitch = unsigned(k) * 2, lane_at = (lane / 8) * pitch + part * 16;
-  const unsigned out = tilecommon::lds_addr(lds) + wave * 1024;
+  const unsigned out = tilecommon::lds_addr(lds) + wave * 1024;  // LDS
   auto words = [&](const Operand& o, int64_t first, int plane, unsigned group) {
     const int64_t left = o.rows - first;
     return tilecommon::rsrc_words(o.p + plane * o.plane + group * o.group + first * k,
                                   left > 0 ? (left < 256 ? left : 256) * k * 2 : 0);
   };
   i32x4 left = {}, left2 = {}, right = {};
-  unsigned tile = blockIdx.x;
-  int piece = tile < n ? first_of(tile) : 0, step = piece % steps, term = piece / steps, slot = 0;
+  unsigned at = blockIdx.x;  // the item; there are no more workgroups than items
+  Item item = item_of(plan, at);
+  int piece = first_of(item), step = piece % steps, term = piece / steps, slot = 0;
   bool fresh = true;  // a tile, or a plane, begins
   // The next piece's copies, for which begin() makes ready; beyond the last tile
   // they read zeros, so that as many are in flight at any time.
   unsigned col = 0;
   bool in = false;
   auto begin = [&]() {
-    if (fresh && tile < n) {
+    if (fresh && at < n) {
       unsigned ip, iq;
-      map_tile(tile % one, np, nq, ip, iq);
+      map_tile(item.tile, np, nq, ip, iq);
       const int64_t p0 = int64_t(ip) * (DUAL ? S::kBP / 2 : S::kBP), q0 = int64_t(iq % of_group) * S::kBQ;
       const int lp = terms > 1 ? left_plane(term) : 0, rp = terms > 1 ? right_plane(term) : 0;
       left = words(L, p0, lp, 0);
@@ -139,14 +159,17 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
       right = words(R, q0, rp, iq / of_group);
     }
     // columns beyond k (a multiple of 8) in a plane's last piece are zeros
-    in = tile < n && step * kStep + part * 8 < k;
+    in = at < n && step * kStep + part * 8 < k;
     col = step * (kStep * 2);
     fresh = false;
     if (++step == steps) step = 0, ++term, fresh = true;
-    if (tile < n && ++piece == last_of(tile)) {
-      tile += gridDim.x;
+    if (at < n && ++piece == last_of(item)) {
+      at += gridDim.x;
       fresh = true;
-      if (tile < n) piece = first_of(tile), step = piece % steps, term = piece / steps;
+      if (at < n) {
+        item = item_of(plan, at);
+        piece = first_of(item), step = piece % steps, term = piece / steps;
+      }
     }
   };
   auto copy = [&](int i) {  // pass i of kPassesP + kPassesQ
@@ -224,7 +247,8 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
     for (int i = 0; i < S::kP; ++i)
 #pragma unroll
       for (int j = 0; j < S::kQ; ++j) acc[i][j] = f32x4{};
-    for (int s = last_of(t) - first_of(t); s > 0; --s) {
+    const Item mine = item_of(plan, t);
+    for (int s = last_of(mine) - first_of(mine); s > 0; --s) {
       multiply(a, b, slot, 1, std::false_type{});
       // this slot has been read, and the other one is whole
       if (stored)
@@ -237,11 +261,28 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
       slot ^= 1;
     }
     unsigned ip, iq;
-    map_tile(t % one, np, nq, ip, iq);
-    store(ip, iq, t / one, acc);
+    map_tile(mine.tile, np, nq, ip, iq);
+    store(ip, iq, mine, acc);
     stored = true;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
+// Where an item's share of a tile is kept: [split][tile of the rest][BQ][BP] float32
+template <typename S>
+__device__ inline float* share_at(const Plan& p, float* shares, const Item& item) {
+  return shares + (int64_t(item.split) * p.rest() + (item.tile - p.whole)) * (S::kBP * S::kBQ);
+}
+// A wave's accumulators of a share
+template <typename S, typename R>
+__device__ inline void put_share(const R& rows, const f32x4 (&acc)[S::kP][S::kQ]) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int p = wave / S::kWQ * (S::kBP / S::kWP) + lane / 16 * 4,
+            q = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
+#pragma unroll
+  for (int j = 0; j < S::kQ; ++j)
+#pragma unroll
+    for (int i = 0; i < S::kP; ++i) rows.put(q + j * 16, p + i * 16, S::kBP, acc[i][j]);
 }
 
 // Rows of outputs, 256 at most, from `first` on.  Stores beyond the last row or a
@@ -249,17 +290,17 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
 template <typename T>
 struct Rows {
   __amdgpu_buffer_rsrc_t rsrc;
-  int64_t width;
-  __device__ Rows(T* base, int64_t first, int64_t rows, int64_t width_)
+  int width;
+  __device__ Rows(T* base, int64_t first, int64_t rows, int width_)
       : rsrc(tilecommon::make_rsrc(
             base + first * width_,
             (rows - first < 256 ? rows - first : 256) * width_ * int64_t(sizeof(T)))),
         width(width_) {}
   // columns c .. c + 3 of row `first` + i, where c is below `columns`
-  __device__ void put(int i, int64_t c, int64_t columns, f32x4 x) const {
+  __device__ void put(int i, int c, int columns, f32x4 x) const {
     typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
     typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-    const unsigned at = c < columns ? unsigned((i * width + c) * int64_t(sizeof(T)))
+    const unsigned at = c < columns ? unsigned(i * width + c) * unsigned(sizeof(T))
                                     : tilecommon::kOutOfRange;
     if constexpr (sizeof(T) == 4)
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), rsrc, at, 0, 0);
