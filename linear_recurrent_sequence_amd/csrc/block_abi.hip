@@ -175,7 +175,7 @@ int mlstm_short_conv_fwd(const void* x, int64_t x_row, const float* weight, cons
 size_t mlstm_short_conv_workspace_bytes(int64_t B, int64_t NH, int64_t T, int64_t d,
                                         int64_t width, int dtype) {
   if (check_conv(B, NH, T, d, width, dtype) != MLSTM_OK) return 0;
-  return mlstm::short_conv_bwd_workspace_bytes(B, NH * d, T, int(width), dtype == MLSTM_BF16);
+  return mlstm::short_conv_bwd_workspace_bytes(B, NH * d, T, int(width));
 }
 
 int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, const float* bias,
@@ -195,7 +195,7 @@ int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, cons
   if (!aligned_to(lengths, 4) || !aligned_to(workspace, 256)) return MLSTM_ERR_ALIGN;
   const ShortConv a = {x, weight, bias, state_in, lengths, x_row, B, NH, T, d, int(width),
                        activation == MLSTM_CONV_SILU, dtype == MLSTM_BF16};
-  const size_t need = mlstm::short_conv_bwd_workspace_bytes(B, NH * d, T, a.W, a.is_bf16);
+  const size_t need = mlstm::short_conv_bwd_workspace_bytes(B, NH * d, T, a.W);
   if (workspace_bytes < need) return MLSTM_ERR_WORKSPACE;
   const ConvBytes n = conv_bytes(a, dtype);
   st = check_alias({{x, n.x}, {weight, n.weight}, {bias, n.bias}, {state_in, n.state},

@@ -30,7 +30,7 @@ struct ShortConvGrads {
 };
 
 hipError_t launch_short_conv_fwd(const ShortConv& a, void* y, void* state_out, hipStream_t stream);
-size_t short_conv_bwd_workspace_bytes(int64_t B, int64_t C, int64_t T, int W, bool is_bf16);
+size_t short_conv_bwd_workspace_bytes(int64_t B, int64_t C, int64_t T, int W);
 hipError_t launch_short_conv_bwd(const ShortConv& a, const ShortConvGrads& g, void* workspace,
                                  hipStream_t stream);
 

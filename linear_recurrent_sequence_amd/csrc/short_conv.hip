@@ -12,7 +12,7 @@
 // x, dx and the states are rows of all channels, as a projection writes them; y
 // and dy are head-major, as the cells read them.
 //
-// A lane holds V neighbouring channels (16 bytes) and walks a run of tokens with
+// A lane holds V neighbouring channels and walks a run of tokens with
 // the last W inputs in registers, so an input is read once but for the W - 1 at
 // the start of a run.  The backward forms a_t again and keeps the last W of g as
 // well; its weights' sums stay in registers over the run, are joined over the
@@ -295,8 +295,11 @@ __global__ __launch_bounds__(256) void conv_weight_sums_kernel(const float* part
   }
 }
 
-// Vectors of 16 bytes; with five and more weights to a channel bf16 takes 8 bytes,
-// as the weights, their sums and the last inputs would not fit the registers.
+// Forward vectors of 16 bytes; with five and more weights to a channel bf16 takes 8,
+// as the weights and the last inputs would not fit the registers.  Backward 8 bytes
+// of bf16: with 16 a lane needs 203 registers and two waves fill a SIMD (8 x 2048 rows
+// of 1536: 44 us, with 8 bytes 37).
+constexpr int kBwdVec = 4;
 int vec_of(int W, bool is_bf16) { return is_bf16 && W <= 4 ? 8 : 4; }
 
 // Tokens of a run: 32, fewer where that leaves less than two waves to a SIMD, but
@@ -311,8 +314,8 @@ struct Grid {
   int64_t cols, spans;
   int run;
 };
-Grid grid_of(int64_t B, int64_t C, int64_t T, int W, bool is_bf16) {
-  const int64_t vectors = C / vec_of(W, is_bf16);
+Grid grid_of(int64_t B, int64_t C, int64_t T, int vec) {
+  const int64_t vectors = C / vec;
   const int run = run_of(B, vectors, T);
   return {(vectors + kLanes - 1) / kLanes, B * ((T + run * kRuns - 1) / (run * kRuns)), run};
 }
@@ -328,7 +331,7 @@ void fwd(const ShortConv& a, void* y, void* state_out, const Grid& g, hipStream_
 template <typename T, int W>
 void bwd(const ShortConv& a, const ShortConvGrads& gr, float* partials, const Grid& g,
          hipStream_t stream) {
-  conv_bwd_kernel<T, kVecOf<T, W>, W><<<unsigned(g.cols * g.spans), kLanes * kRuns, 0, stream>>>(
+  conv_bwd_kernel<T, kBwdVec, W><<<unsigned(g.cols * g.spans), kLanes * kRuns, 0, stream>>>(
       a, gr, partials, g.run);
 }
 
@@ -350,7 +353,7 @@ void with_width(int W, F&& f) {
 
 hipError_t launch_short_conv_fwd(const ShortConv& a, void* y, void* state_out,
                                  hipStream_t stream) {
-  const Grid g = grid_of(a.B, a.NH * a.d, a.T, a.W, a.is_bf16);
+  const Grid g = grid_of(a.B, a.NH * a.d, a.T, vec_of(a.W, a.is_bf16));
   with_width(a.W, [&](auto w) {
     if (a.is_bf16)
       fwd<__hip_bfloat16, w()>(a, y, state_out, g, stream);
@@ -360,14 +363,14 @@ hipError_t launch_short_conv_fwd(const ShortConv& a, void* y, void* state_out,
   return hipGetLastError();
 }
 
-size_t short_conv_bwd_workspace_bytes(int64_t B, int64_t C, int64_t T, int W, bool is_bf16) {
-  return size_t(grid_of(B, C, T, W, is_bf16).spans) * size_t(W + 1) * size_t(C) * 4;
+size_t short_conv_bwd_workspace_bytes(int64_t B, int64_t C, int64_t T, int W) {
+  return size_t(grid_of(B, C, T, kBwdVec).spans) * size_t(W + 1) * size_t(C) * 4;
 }
 
 hipError_t launch_short_conv_bwd(const ShortConv& a, const ShortConvGrads& gr, void* workspace,
                                  hipStream_t stream) {
   const int64_t C = a.NH * a.d;
-  const Grid g = grid_of(a.B, C, a.T, a.W, a.is_bf16);
+  const Grid g = grid_of(a.B, C, a.T, kBwdVec);
   float* partials = static_cast<float*>(workspace);
   with_width(a.W, [&](auto w) {
     if (a.is_bf16)
