@@ -457,7 +457,8 @@ const char* mlstm_strerror(int status) {
     case MLSTM_ERR_NULL: return "a required pointer is NULL";
     case MLSTM_ERR_SHAPE: return "invalid shape: B, NH, T, d must be >= 1 and sizes must not overflow";
     case MLSTM_ERR_DTYPE: return "invalid dtype: expected MLSTM_FP32 or MLSTM_BF16";
-    case MLSTM_ERR_HEAD_DIM: return "unsupported head dimension: d must be a multiple of 16 in [16, 1024] (and <= 512 for the one-wave MFMA kernel and for the delta rule's keys; for the block norm a multiple of 8 with NH * d <= 8192)";
+    case MLSTM_ERR_HEAD_DIM: return "unsupported head dimension: d must be a multiple of 16 in [16, 1024] (and <= 512 for the one-wave MFMA kernel and for the delta rule's keys; for the block norm a multiple of 8 with NH * d <= 8192; "
+                                   "for the short convolution, the channels of a scan's group and the feed-forward a multiple of 8)";
     case MLSTM_ERR_ALIGN: return "misaligned pointer: tensors need 16-byte, workspaces 256-byte alignment";
     case MLSTM_ERR_HIP: return "HIP allocation or kernel launch failed";
     case MLSTM_ERR_WORKSPACE: return "workspace smaller than mlstm_workspace_bytes()";

@@ -41,7 +41,9 @@ Parity status of each function (what pins it, in ``tests/test_oracle_pins.py``):
 
 ``delta`` evaluates the gated delta rule and the block norm the same way, from
 their definitions; its gradients are pinned by central differences and its
-forward by closed forms (``tests/test_cells_cpu.py``).
+forward by closed forms (``tests/test_cells_cpu.py``).  ``blocks`` does so for the
+short convolution, the selective scan and the gated feed-forward
+(``tests/test_blocks_cpu.py``).
 """
 
 from .mlstm import (  # noqa: F401
@@ -61,3 +63,11 @@ from .mlstm import (  # noqa: F401
     backward_stabilized,
 )
 from .delta import block_norm, delta_backward, delta_forward  # noqa: F401
+from .blocks import (  # noqa: F401
+    gated_ffn,
+    gated_ffn_grads,
+    selective_scan,
+    selective_scan_grads,
+    short_conv,
+    short_conv_grads,
+)
