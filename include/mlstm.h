@@ -563,9 +563,10 @@ int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, cons
  *                  state stays as it is
  *   y              [batch][T][channels] dtype
  *   channels / G a multiple of 8, channels <= 2^20, N in [1, 64],
- *   batch T G N <= 2^31, batch channels <= 2^26
+ *   batch T G N <= 2^31, batch channels <= 2^25
  * dt = -infinity gives Delta = 0, which leaves the state as it is; inputs are
- * otherwise finite.  All sums, Delta and the states are float32; a bf16 result is
+ * otherwise finite, and a positive A is taken as long as exp(A sum Delta) over the
+ * sequence is a float32 number.  All sums, Delta and the states are float32; a bf16 result is
  * rounded once.  Tensors 16-byte aligned (B and C to their elements, lengths 4).
  * Bitwise reproducible.
  */
@@ -619,8 +620,8 @@ int mlstm_scan_bwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row,
  * Products are summed in float32 (float32 operands as three bf16 planes, 24
  * bits), and a bf16 h is rounded once.  mlstm_gated_ffn_bwd forms both products
  * again; for bf16 their gradients are rounded to bf16 as operands of the
- * products behind dx, dw_gate and dw_up.  Inputs finite.  Tensors 16-byte
- * aligned; workspace mlstm_gated_ffn_workspace_bytes bytes, 256-byte aligned.
+ * products behind dx, dw_gate and dw_up.  Inputs finite (float32 ones below 2^127 in
+ * magnitude).  Tensors 16-byte aligned; workspace mlstm_gated_ffn_workspace_bytes bytes, 256-byte aligned.
  * Bitwise reproducible.
  */
 enum { MLSTM_FFN_SILU = 0, MLSTM_FFN_GELU = 1 };

@@ -79,7 +79,7 @@ int check_scan(int64_t batch, int64_t T, int64_t channels, int64_t G, int64_t N,
   if (channels / G % 8 != 0 || channels > kMaxChannels) return MLSTM_ERR_HEAD_DIM;
   if (N > mlstm::kScanMaxStates) return MLSTM_ERR_WIDTH;
   const int64_t most = int64_t(1) << 31;
-  if (batch > (int64_t(1) << 26) / channels || T > most / batch / (G * N) ||
+  if (batch > (int64_t(1) << 25) / channels || T > most / batch / (G * N) ||
       batch > (int64_t(1) << 22) / (G * ((channels / G + 63) / 64)))
     return MLSTM_ERR_SHAPE;
   return MLSTM_OK;

@@ -226,21 +226,27 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, const float*
   const int64_t c = i % a.channels, n = i / a.channels, at = (b * a.channels + c) * a.N + n;
   const float A = a.A[c * a.N + n] * rowvec::kLog2e;
   auto kept_at = [&](int k) { return (k * a.batch + b) * all + i; };
-  auto decay = [&](int k) {
-    return rowvec::exp2_fast(A * kept.deltas[(k * a.batch + b) * a.channels + c]);
+  constexpr int kAhead = 8;  // segments whose loads are in flight together
+  // x, with each segment's share added to what is left of it, in the order of `at`
+  auto join = [&](float* shares, float x, auto at) {
+    for (int k0 = 0; k0 < segments; k0 += kAhead) {
+      float own[kAhead], decay[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = at(k0 + j < segments ? k0 + j : k0);
+        own[j] = shares[kept_at(k)];
+        decay[j] = kept.deltas[(k * a.batch + b) * a.channels + c];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (k0 + j >= segments) break;
+        shares[kept_at(at(k0 + j))] = x;
+        x = __builtin_fmaf(rowvec::exp2_fast(A * decay[j]), x, own[j]);
+      }
+    }
   };
-  float s = a.state ? a.state[at] : 0.0f;
-  for (int k = 0; k < segments; ++k) {
-    const float end = kept.before[kept_at(k)];
-    kept.before[kept_at(k)] = s;
-    s = __builtin_fmaf(decay(k), s, end);
-  }
-  float S = dstate ? dstate[at] : 0.0f;
-  for (int k = segments - 1; k >= 0; --k) {
-    const float own = kept.after[kept_at(k)];
-    kept.after[kept_at(k)] = S;
-    S = __builtin_fmaf(decay(k), S, own);
-  }
+  join(kept.before, a.state ? a.state[at] : 0.0f, [](int k) { return k; });
+  join(kept.after, dstate ? dstate[at] : 0.0f, [&](int k) { return segments - 1 - k; });
 }
 
 // ---- the second pass

@@ -177,7 +177,8 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(SelectiveScan a, T* y, fl
   }
 }
 
-// the state before each segment, in the place of the segment's end
+// the state before each segment, in the place of the segment's end (of which the
+// first pass leaves that of the last one out)
 __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joints, int segments) {
   const int64_t all = a.N * a.channels, blocks = (all + 255) / 256;
   const int64_t b = blockIdx.x / blocks, i = (blockIdx.x % blocks) * 256 + threadIdx.x;
@@ -185,14 +186,20 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joint
   const int64_t c = i % a.channels, n = i / a.channels;
   const float A = a.A[c * a.N + n] * rowvec::kLog2e;
   float s = a.state ? a.state[(b * a.channels + c) * a.N + n] : 0.0f;
-  for (int k = 0; k < segments; ++k) {
-    float* at = joints.state(a, k, b) + i;
-    if (k == segments - 1) {
-      *at = s;
-    } else {
-      const float end = *at;
-      *at = s;
-      s = __builtin_fmaf(rowvec::exp2_fast(A * joints.delta(a, k, b)[c]), s, end);
+  constexpr int kAhead = 8;  // segments whose loads are in flight together
+  for (int k0 = 0; k0 < segments; k0 += kAhead) {
+    float end[kAhead], decay[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j < segments - 1 ? k0 + j : 0;  // the last one's end is not needed
+      end[j] = joints.state(a, k, b)[i];
+      decay[j] = joints.delta(a, k, b)[c];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k0 + j >= segments) break;
+      joints.state(a, k0 + j, b)[i] = s;
+      s = __builtin_fmaf(rowvec::exp2_fast(A * decay[j]), s, end[j]);
     }
   }
 }

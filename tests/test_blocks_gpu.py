@@ -10,7 +10,7 @@ sign make sqrt(n) 2^-24 of the sum's size sqrt(n) a.
                 2^-18.5 of its size.
   scan          a state takes three roundings a token (factor, product, sum), over at
                 most 1000 tokens: sqrt(3000) 2^-24 = 2^-18.2 of its size; then sums of
-                up to 64 states or 300 channels, 2^-20.
+                up to 64 states or 5000 channels, 2^-20 and 2^-18 of their sizes.
   feed-forward  sums of at most 2000 terms: 2^-18.5 of the sum's size, and three such
                 factors follow one another backward.
 So 2^-17.5 of the sizes in the 2-norm for all, and at one element 2^-14 of the root mean
@@ -226,6 +226,20 @@ def test_scan_in_segments(n, T, c, N, G, lengths, dtype):
     close("state", st, sr)
     check_scan_grads(mlstm.scan_bwd(*args, dy, dstate=dst, lengths=i32(lengths), **kw), x, dy, dst,
                      lengths)
+
+
+# more workgroups than CUs: four states to a wave, and one piece
+@pytest.mark.parametrize("N", [2, 7, 16, 21, 40])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_scan_of_many_channels(N, dtype):
+    x, dy, dst = scan_inputs(5, 37, 4168, N, 1, dtype, 19)
+    kw = {k: v for k, v in x.items() if k not in ("u", "dt", "A", "B", "C")}
+    args = [x[k] for k in ("u", "dt", "A", "B", "C")]
+    y, st = mlstm.scan_fwd(*args, **kw)
+    yr, sr = scan_ref(x)
+    close("y", y, yr, np.full_like(yr, np.sqrt((yr ** 2).mean())))
+    close("state", st, sr)
+    check_scan_grads(mlstm.scan_bwd(*args, dy, dstate=dst, **kw), x, dy, dst)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
