@@ -9,9 +9,10 @@
 //
 // All products run on one kind of tile (product_tiles.h), whose operands are rows
 // of the summed index: the weights, x and G are transposed into the workspace for
-// the last two.  For bf16, G is rounded to bf16 as the operand of those products
-// (2^-9 of each term, as much as the rounding of the results); everything before
-// is float32.
+// the last two.  For bf16 and 512 rows or more, G is rounded to bf16 as the operand of
+// those products (2^-9 of each term, as much as the rounding of the results, at half
+// the time of carrying 16 bits); for fewer rows, whose sums have few terms to average
+// over and take little time, it has two planes, 16 bits.  Everything before is float32.
 #include "gated_ffn.h"
 
 #include "product_tiles.h"
@@ -30,6 +31,7 @@ using Medium = product::Shape<128, 256, 2, 4>;
 using Small = product::Shape<128, 128, 2, 2>;
 
 constexpr int kPlanes = 3, kTerms = 6;  // of float32
+constexpr int64_t kFineRows = 512;      // from which on bf16 gradients of g and u are bf16
 
 struct Act {
   float value, slope;
@@ -71,10 +73,10 @@ __device__ inline Pair gate_up_of(f32x4 g, f32x4 u, const float (&d)[4], bool ge
 }
 
 // h, or with GRAD G = [dg | du], in tiles of rows and of F
-template <typename T, typename S, bool GRAD>
+template <typename T, typename O, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operand wu, Operand x,
                                                               Sizes n, Plan plan, const T* dh,
-                                                              T* out, float* shares) {
+                                                              O* out, float* shares) {
   __shared__ __align__(1024) char lds[S::kLds];
   constexpr int kF = S::kBP / 2, kStores = (GRAD ? S::kP : S::kP / 2) * S::kQ;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
         const int f0 = int(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
                   q0 = int(iq) * S::kBQ, F = int(n.F), M = int(n.M);
         const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
-        const product::Rows<T> rows(out, q0, M, GRAD ? 2 * F : F);
+        const product::Rows<O> rows(out, q0, M, GRAD ? 2 * F : F);
 #pragma unroll
         for (int j = 0; j < S::kQ; ++j)
 #pragma unroll
@@ -159,9 +161,9 @@ __global__ __launch_bounds__(S::kBP) void join_kernel(Plan plan, const float* sh
 }
 
 // The rest of gate_up_kernel's tiles, eight rows of a tile to a workgroup
-template <typename T, typename S, bool GRAD>
+template <typename T, typename O, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kBP) void join_gate_up_kernel(Plan plan, const float* shares,
-                                                              Sizes n, const T* dh, T* out) {
+                                                              Sizes n, const T* dh, O* out) {
   constexpr int kF = S::kBP / 2, kHalf = kF / S::kWP;  // columns; of a wave's rows of one operand
   const unsigned rest = blockIdx.x / (S::kBQ / 8);
   unsigned ip, iq;
@@ -467,39 +469,38 @@ float* take_shares(const Plan& plan, Arena& ws) {
   return plan.splits > 1
              ? ws.take<float>(int64_t(plan.rest()) * plan.splits * (S::kBP * S::kBQ)) : nullptr;
 }
-template <typename T>
-int64_t pieces_of(int64_t k) {
-  return (k + product::kStep - 1) / product::kStep * kTermsOf<T>;
+int64_t pieces_of(int64_t k, int terms) {
+  return (k + product::kStep - 1) / product::kStep * terms;
 }
 
-template <typename T, bool GRAD>
+template <typename T, typename O, bool GRAD>
 hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
                    const void* dh, void* out, Arena& ws, hipStream_t stream, bool run) {
-  return with_shape(2 * n.F, n.M, 1, pieces_of<T>(n.D), [&](auto shape, const Plan& plan) {
+  return with_shape(2 * n.F, n.M, 1, pieces_of(n.D, n.terms), [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
     float* shares = take_shares<S>(plan, ws);
     if (!run) return hipSuccess;
     const T* d = static_cast<const T*>(dh);
-    T* o = static_cast<T*>(out);
-    gate_up_kernel<T, S, GRAD><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
+    O* o = static_cast<O*>(out);
+    gate_up_kernel<T, O, S, GRAD><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
         wg, wu, x, n, plan, d, o, shares);
     if (shares)
-      join_gate_up_kernel<T, S, GRAD><<<plan.rest() * (S::kBQ / 8), S::kBP, 0, stream>>>(
+      join_gate_up_kernel<T, O, S, GRAD><<<plan.rest() * (S::kBQ / 8), S::kBP, 0, stream>>>(
           plan, shares, n, d, o);
     return hipGetLastError();
   });
 }
 
 template <typename T>
-hipError_t multiply(const Operand& l, const Operand& r, int64_t k, unsigned groups, void* out,
-                    void* out2, Arena& ws, hipStream_t stream, bool run) {
-  return with_shape(l.rows, r.rows, groups, pieces_of<T>(k), [&](auto shape, const Plan& plan) {
+hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int terms, unsigned groups,
+                    void* out, void* out2, Arena& ws, hipStream_t stream, bool run) {
+  return with_shape(l.rows, r.rows, groups, pieces_of(k, terms), [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
     float* shares = take_shares<S>(plan, ws);
     if (!run) return hipSuccess;
     T *o = static_cast<T*>(out), *o2 = static_cast<T*>(out2);
     product_kernel<T, S><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
-        l, r, k, kTermsOf<T>, plan, o, o2, shares);
+        l, r, k, terms, plan, o, o2, shares);
     if (shares)
       join_kernel<T, S><<<plan.rest() * (S::kBQ / 4), S::kBP, 0, stream>>>(plan, shares, l.rows,
                                                                            r.rows, o, o2);
@@ -517,7 +518,7 @@ hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bo
                 wu = as_rows<T>(a.w_up, a.F, a.D, ws, jobs.job[1]),
                 x = as_rows<T>(a.x, a.M, a.D, ws, jobs.job[2]);
   if (run && sizeof(T) == 4) prepare<T>(jobs, stream);
-  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
+  return gate_up<T, T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
                            run);
 }
 
@@ -530,27 +531,32 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
   const Operand wg = as_rows<T>(a.w_gate, F, D, ws, jobs.job[0]),
                 wu = as_rows<T>(a.w_up, F, D, ws, jobs.job[1]),
                 x = as_rows<T>(a.x, M, D, ws, jobs.job[2]);
-  T* G = ws.take<T>(M * 2 * F);
+  constexpr bool kFloat = sizeof(T) == 4;
+  const bool fine = kFloat || M < kFineRows;  // G in float32, and its planes
+  void* G = fine ? static_cast<void*>(ws.take<float>(M * 2 * F)) : ws.take<T>(M * 2 * F);
   const int64_t wt_plane = D * 2 * F, xt_plane = D * pitch, gt_plane = 2 * F * pitch;
-  uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);  // [D][Wg^T | Wu^T]
-  uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);  // [D][M]
-  uint16_t* gt = ws.take<uint16_t>(kCopies<T> * gt_plane);  // [2F][M]
+  uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);            // [D][Wg^T | Wu^T]
+  uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);            // [D][M]
+  uint16_t* gt = ws.take<uint16_t>((fine ? kPlanes : 1) * gt_plane);  // [2F][M]
   turn(jobs.job[0], wt, F, 2 * F, wt_plane);
   turn(jobs.job[1], wt + F, F, 2 * F, wt_plane);
   turn(jobs.job[2], xt, pitch, pitch, xt_plane);
   if (run) prepare<T>(jobs, stream);
-  hipError_t e = gate_up<T, true>(wg, wu, x, {M, D, F, kTermsOf<T>, a.gelu}, g.dh, G, ws, stream,
-                                  run);
+  const Sizes n = {M, D, F, kTermsOf<T>, a.gelu};
+  hipError_t e = fine ? gate_up<T, float, true>(wg, wu, x, n, g.dh, G, ws, stream, run)
+                      : gate_up<T, T, true>(wg, wu, x, n, g.dh, G, ws, stream, run);
   if (e != hipSuccess) return e;
   Jobs more;
   more.n = 1;
-  const Operand G_rows = as_rows<T>(G, M, 2 * F, ws, more.job[0]);
+  const Operand G_rows = fine ? as_rows<float>(G, M, 2 * F, ws, more.job[0])
+                              : as_rows<T>(G, M, 2 * F, ws, more.job[0]);
   turn(more.job[0], gt, pitch, pitch, gt_plane);
-  if (run) prepare<T>(more, stream);
-  e = multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, 1, g.dx, nullptr, ws, stream, run);
+  if (run) fine ? prepare<float>(more, stream) : prepare<T>(more, stream);
+  const int terms = kFloat ? kTerms : fine ? 2 : 1;
+  e = multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, terms, 1, g.dx, nullptr, ws, stream, run);
   if (e != hipSuccess) return e;
-  return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, 2, g.dw_gate,
-                     g.dw_up, ws, stream, run);
+  return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, terms, 2,
+                     g.dw_gate, g.dw_up, ws, stream, run);
 }
 
 }  // namespace

@@ -64,9 +64,14 @@ __device__ inline void copy_piece(i32x4 rsrc, unsigned voffset, unsigned dst) {
                : "memory", "m0");
 }
 
-// The planes of term s of six (a bf16 operand has plane 0 only)
-__device__ inline int left_plane(int s) { return (0x001102 >> (4 * s)) & 15; }   // 2 0 1 1 0 0
-__device__ inline int right_plane(int s) { return (0x010120 >> (4 * s)) & 15; }  // 0 2 1 0 1 0
+// The planes of term s of `terms`: six of two float32 operands, two of a bf16 one (left)
+// with the two larger planes of a float32 one, and one of two bf16 operands
+__device__ inline int left_plane(int s, int terms) {
+  return terms == 6 ? (0x001102 >> (4 * s)) & 15 : 0;  // 2 0 1 1 0 0
+}
+__device__ inline int right_plane(int s, int terms) {
+  return terms == 6 ? (0x010120 >> (4 * s)) & 15 : terms - 1 - s;  // 0 2 1 0 1 0
+}
 
 // workgroup -> tile.  Workgroups are dealt to the 8 XCDs round-robin: each XCD
 // takes a run of neighbouring tiles, in blocks of 8 tiles of q whose operands its
@@ -153,7 +158,7 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
       unsigned ip, iq;
       map_tile(item.tile, np, nq, ip, iq);
       const int64_t p0 = int64_t(ip) * (DUAL ? S::kBP / 2 : S::kBP), q0 = int64_t(iq % of_group) * S::kBQ;
-      const int lp = terms > 1 ? left_plane(term) : 0, rp = terms > 1 ? right_plane(term) : 0;
+      const int lp = left_plane(term, terms), rp = right_plane(term, terms);
       left = words(L, p0, lp, 0);
       if constexpr (DUAL) left2 = words(L2, p0, lp, 0);
       right = words(R, q0, rp, iq / of_group);
