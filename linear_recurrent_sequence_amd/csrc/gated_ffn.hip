@@ -92,17 +92,33 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
                   q0 = int(iq) * S::kBQ, F = int(n.F), M = int(n.M);
         const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
         const product::Rows<O> rows(out, q0, M, GRAD ? 2 * F : F);
+        // dh of kAhead blocks of rows at a time, ahead of their stores
+        constexpr int kAhead = GRAD && sizeof(T) == 2 ? S::kQ : 1;
 #pragma unroll
-        for (int j = 0; j < S::kQ; ++j)
+        for (int j0 = 0; j0 < S::kQ; j0 += kAhead) {
+          rowvec::Raw<T, 4> raw[kAhead][S::kP / 2] = {};
+          if constexpr (GRAD) {
 #pragma unroll
-          for (int i = 0; i < S::kP / 2; ++i) {
-            const int f = f0 + i * 16, m = q0 + m0 + j * 16;
-            float d[4] = {};
-            if (GRAD && m < M && f < F) rowvec::load(dh + int64_t(m) * F + f, d);
-            const Pair o = gate_up_of<GRAD>(acc[i][j], acc[i + S::kP / 2][j], d, n.gelu);
-            rows.put(m0 + j * 16, f, F, o.a);
-            if constexpr (GRAD) rows.put(m0 + j * 16, f < F ? F + f : 2 * F, 2 * F, o.b);
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+              for (int i = 0; i < S::kP / 2; ++i) {
+                const int f = f0 + i * 16, m = q0 + m0 + (j0 + j) * 16;
+                if (m < M && f < F)
+                  raw[j][i] = rowvec::load_raw<T, 4>(dh + int64_t(m) * F + f);
+              }
           }
+#pragma unroll
+          for (int jj = 0; jj < kAhead; ++jj)
+#pragma unroll
+            for (int i = 0; i < S::kP / 2; ++i) {
+              const int j = j0 + jj, f = f0 + i * 16;
+              float d[4];
+              rowvec::floats(raw[jj][i], d);
+              const Pair o = gate_up_of<GRAD>(acc[i][j], acc[i + S::kP / 2][j], d, n.gelu);
+              rows.put(m0 + j * 16, f, F, o.a);
+              if constexpr (GRAD) rows.put(m0 + j * 16, f < F ? F + f : 2 * F, 2 * F, o.b);
+            }
+        }
       });
 }
 
