@@ -13,6 +13,13 @@
 // those products (2^-9 of each term, as much as the rounding of the results, at half
 // the time of carrying 16 bits); for fewer rows, whose sums have few terms to average
 // over and take little time, it has two planes, 16 bits.  Everything before is float32.
+//
+// Measured: 16384 rows of 1536 to 4096 forward 345 us (in a trace; product_tiles.h has
+// what bounds it); 8192 rows of 2048 to 5504 forward 345, backward 389 for G, 320 for
+// dx and 340 for the weights' gradients, 99 for turned operands at a copy's rate and 11
+// for joined shares.  8 rows of 1536 to 4096 7.8 us (25 MB, 5.1 at a copy's rate), 17 as
+// tiles.  float32, 999 rows of 392 to 1048, training: 158 us, 350 before split tiles and
+// operands made in one launch.
 #include "gated_ffn.h"
 
 #include "product_tiles.h"

@@ -15,6 +15,13 @@
 // column do not share banks.  Rows beyond an operand's, and columns beyond k, are
 // read out of the buffer's range: zeros.
 //
+// Measured: 8192 x 16384 x 1536 with the gate's epilogue 345 us, 1190 TFLOP/s (the
+// library's product alone 358 to 373); 2048 x 8192 x 11008 320 us, 1150 TFLOP/s (250 to
+// 272).  Without copies the same loop takes 0.78 of the time, without
+// products 0.77, without reads 0.95: the copies and the matrix unit are each other's
+// limit.  Copies and reads spread over the products, at a raised wave priority, gave
+// 4.5 % over copies in one burst.
+//
 // float32 operands come as three bf16 planes (24 bits: exact), and the product is
 // the sum of the six plane products above 2^-24, taken one after the other as if k
 // were six times as long, the smallest first: their roundings are then those of

@@ -24,6 +24,13 @@
 // for the gradient of the state before it (with the running product of a_t), a
 // small kernel joins both, and the second pass adds what the state before the
 // segment has become, exp(A sum Delta), to the states it kept.
+//
+// Bound by the vector unit.  Measured, bf16, N = 16, gate, 8 x 2048 x 1536 in 8 segments:
+// first pass 137 us (unit 97 % busy), second 409 (83 %; 26 instructions a state and
+// token: 5 forward, 10 back, 4.4 of the butterfly, the rest per token), sums 29.  With a
+// tile's LDS reads kept over both ways and the sums sunk behind them, the second pass
+// needed 440 registers and took 549 us on one wave to a SIMD; with its rows' addresses
+// formed for every tile 514.
 #include "selective_common.h"
 
 namespace mlstm {
@@ -582,7 +589,9 @@ int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 int tile_of(int64_t N) { return N <= 32 ? 16 : 8; }
 
 // How many segments: operations to a state and token are 27 in one piece, 30 cut;
-// see the forward's time_of.
+// see the forward's time_of.  Both sides, first and second pass, of one build: 8 x 2048 x
+// 1536 in 8 segments 665 us, in 4 (one and a half rounds of workgroups) 722; float32 2 x
+// 555 x 208 in 12 43, in 7 61.
 Segments segments_of(const SelectiveScan& a) {
   const int64_t tiles = (a.T + tile_of(a.N) - 1) / tile_of(a.N);
   const int64_t waves = a.batch * a.G * tiles_of_group(a.channels, a.G) * waves_of(a.N);
