@@ -33,9 +33,9 @@ using product::f32x4;
 using product::Operand;
 using product::Plan;
 
-using Large = product::Shape<256, 256, 2, 4>;
-using Medium = product::Shape<128, 256, 2, 4>;
-using Small = product::Shape<128, 128, 2, 2>;
+using Large = product::Shape<256, 256, 2, 4, 2>;
+using Medium = product::Shape<128, 256, 2, 4, 3>;
+using Small = product::Shape<128, 128, 2, 2, 2>;
 
 constexpr int kPlanes = 3, kTerms = 6;  // of float32
 constexpr int64_t kFineRows = 512;      // from which on bf16 gradients of g and u are bf16

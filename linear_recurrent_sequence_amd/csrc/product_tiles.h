@@ -5,10 +5,10 @@
 // in 16 x 16 accumulators.  The left operand's rows are the outputs' fast index, so
 // a lane holds four neighbouring outputs of a row (lane l: q = l % 16, p = 4 (l /
 // 16) ..) and stores them together.  Both operands' pieces of 64 columns are copied
-// global -> LDS without registers into two slots.  A wave reads the fragments of 32
-// columns into registers while it multiplies those of the 32 before, so a slot is
-// free when half of its products are done, and is filled again, two pieces ahead,
-// beside the other half's.  Workgroups stay for several tiles: the copies run on
+// global -> LDS without registers into two or three slots.  A wave reads the fragments
+// of 32 columns into registers while it multiplies those of the 32 before, so a slot is
+// free when half of its products are done, and is filled again, as many pieces ahead
+// as there are slots, beside the other half's.  Workgroups stay for several tiles: the copies run on
 // into the next tile, whose first pieces come in while this one is stored.  Eight
 // lanes copy a row's 128 bytes, a cache line, and its 16-byte parts lie in the order
 // part ^ (row & 7), so that the 16 rows that an instruction's lanes read in one
@@ -48,7 +48,7 @@ struct Operand {
   int64_t rows, plane, group;
 };
 
-template <int BP, int BQ, int WP, int WQ>
+template <int BP, int BQ, int WP, int WQ, int SLOTS>
 struct Shape {
   static constexpr int kBP = BP, kBQ = BQ, kWP = WP, kWQ = WQ;
   static constexpr int kThreads = 64 * WP * WQ;
@@ -56,7 +56,7 @@ struct Shape {
   static constexpr int kPassesP = BP / kPassRows, kPassesQ = BQ / kPassRows;
   static constexpr int kP = BP / WP / 16, kQ = BQ / WQ / 16;  // a wave's accumulators
   static constexpr int kSlot = (BP + BQ) * kStep * 2;         // bytes
-  static constexpr int kLds = 2 * kSlot;
+  static constexpr int kSlots = SLOTS, kLds = SLOTS * kSlot;
 };
 
 // 16 bytes per lane from rsrc + voffset to LDS at dst + 16 * lane (dst is
@@ -235,19 +235,20 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
   // waits for this wave's copies but for the newest `left` operations, and its
   // reads, then for the workgroup's
   auto arrive = [&](auto newer) {
+    static_assert(newer() < 64, "vmcnt has 6 bits");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(newer()) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < S::kSlots; ++s) {
     begin();
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy(i);
-    slot ^= 1;
+    if (++slot == S::kSlots) slot = 0;
   }
-  arrive(std::integral_constant<int, kCopies>{});
+  arrive(std::integral_constant<int, (S::kSlots - 1) * kCopies>{});
   Fragments<S> a, b;
 #pragma unroll
   for (int j = 0; j < S::kQ; ++j) read_r(0, 0, j, a);
@@ -262,15 +263,18 @@ __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand&
     const Item mine = item_of(plan, t);
     for (int s = last_of(mine) - first_of(mine); s > 0; --s) {
       multiply(a, b, slot, 1, std::false_type{});
-      // this slot has been read, and the other one is whole
+      // this slot has been read, and the next one is whole; the copies behind that
+      // one's, and after a tile the stores, may still be on their way
+      constexpr int kNewer = (S::kSlots - 2) * kCopies;
       if (stored)
-        arrive(std::integral_constant<int, STORES>{});
+        arrive(std::integral_constant<int, kNewer + STORES>{});
       else
-        arrive(std::integral_constant<int, 0>{});
+        arrive(std::integral_constant<int, kNewer>{});
       stored = false;
       begin();
-      multiply(b, a, slot ^ 1, 0, std::true_type{});
-      slot ^= 1;
+      const int next = slot + 1 == S::kSlots ? 0 : slot + 1;
+      multiply(b, a, next, 0, std::true_type{});
+      slot = next;
     }
     unsigned ip, iq;
     map_tile(mine.tile, np, nq, ip, iq);

@@ -2,7 +2,7 @@
 //
 // Bound by the vector unit: a state and token take a product, an exponential (a quarter
 // of the rate) and three more, 8 issue slots, for 1/8 of a byte.  Measured, bf16, N = 16,
-// gate: 8 x 2048 x 1536 187 us in a trace (192 workgroups, the unit four fifths busy; at
+// gate: 8 x 2048 x 1536 187 us in a trace (192 workgroups on as many CUs, the unit there 73 % busy; at
 // full rate on all CUs the states alone would take 82), 1 x 16384 x 2048 131 us for the
 // effects of 15 of 16 segments, 5 to join them and 170 for the scan.  Blocks of four
 // tokens whose LDS reads are issued a block ahead and whose exponentials come first gave
@@ -221,7 +221,7 @@ int64_t workgroups_of(const SelectiveScan& a) {
 }
 
 // The time of `n` tiles of tokens of `waves` waves: a SIMD with two waves keeps its
-// vector unit four fifths busy, with one little more than half.
+// vector unit three quarters busy, with one little more than half.
 double time_of(int64_t n, int64_t waves) {
   return double(n) * (waves <= kSimds ? 0.65 : double((waves + 2 * kSimds - 1) / (2 * kSimds)));
 }
