@@ -668,15 +668,6 @@ def _require_rows(named, device):
     """Raise unless each (name, tensor, shape, dtype) is rows of contiguous
     elements with one pitch, on ``device`` -> the pitches, in elements.  ``shape``:
     its first two (B, T) or first (B) sizes count rows, ``row`` elements each."""
-    if device.type == "cuda":  # the common case, as in _require_all
-        index = device.index
-        for _, t, shape, dtype, _ in named:
-            if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype
-                                      and t.shape == shape and t.get_device() == index
-                                      and t.is_contiguous()):
-                break
-        else:
-            return [row for _, _, _, _, row in named]
     pitches = []
     for name, t, shape, dtype, row in named:
         if t is None:
@@ -714,6 +705,21 @@ def _require_rows(named, device):
     return pitches
 
 
+def _all_plain(device, checks):
+    """Whether every (tensor or None, shape, dtype) is a contiguous tensor of that
+    shape and type on ``device``, a GPU: the common case of a call's checks in one
+    pass, since a small kernel takes less time than its checks."""
+    if device.type != "cuda":
+        return False
+    index = device.index
+    for t, shape, dtype in checks:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype
+                                  and t.shape == shape and t.get_device() == index
+                                  and t.is_contiguous()):
+            return False
+    return True
+
+
 def _named_code(what, table, name):
     if name not in table:
         raise ValueError(f"{what} must be one of {tuple(table)}, got {name!r}")
@@ -745,6 +751,13 @@ def _check_conv(x, weight, bias, heads, lengths, dims, states, dy=None):
     NH = 1 if heads is None else heads
     if not isinstance(NH, int) or NH < 1 or C % NH:
         raise ValueError(f"heads must be a divisor of the {C} channels, got {heads!r}")
+    sizes = (B, NH, T, C // NH, W)
+    kind, f32, state = x.dtype, torch.float32, (B, W - 1, C)
+    y_shape = _conv_shape(B, heads, T, C, dims)
+    if _all_plain(x.device, ((x, x.shape, kind), (weight, (C, W), f32), (bias, (C,), f32),
+                             (lengths, (B,), torch.int32), (dy, y_shape, kind),
+                             *((t, state, kind) for t in states.values()))):
+        return C, y_shape, sizes
     x_row, = _require_rows([("x", x, x.shape, x.dtype, C)], x.device)
     named = [("weight", weight, (C, W), torch.float32)]
     if bias is not None:
@@ -752,12 +765,12 @@ def _check_conv(x, weight, bias, heads, lengths, dims, states, dy=None):
     if lengths is not None:
         named.append(("lengths", lengths, (B,), torch.int32))
     if dy is not None:
-        named.append(("dy", dy, _conv_shape(B, heads, T, C, dims), x.dtype))
+        named.append(("dy", dy, y_shape, kind))
     for name, t in states.items():
         if t is not None:
-            named.append((name, t, (B, W - 1, C), x.dtype))
+            named.append((name, t, state, kind))
     _require_all(named, x.device)
-    return x_row, B, NH, T, C // NH, W
+    return x_row, y_shape, sizes
 
 
 def _conv_shape(B, heads, T, C, dims):
@@ -774,16 +787,17 @@ def conv_state(B, C, width, dtype, device):
 
 def _short_conv(x, weight, bias, state, out_state, heads, lengths, activation, dims):
     lib = load_library()
-    x_row, B, NH, T, d, W = _check_conv(x, weight, bias, heads, lengths, dims,
+    x_row, y_shape, sizes = _check_conv(x, weight, bias, heads, lengths, dims,
                                         {"state": state, "out_state": out_state})
+    B, NH, _, d, W = sizes
     code = _named_code("activation", CONV_ACTIVATIONS, activation)
     with _on(x.device):
         if out_state is None:
             out_state = torch.empty((B, W - 1, NH * d), dtype=x.dtype, device=x.device)
-        y = torch.empty(_conv_shape(B, heads, T, NH * d, dims), dtype=x.dtype, device=x.device)
+        y = x.new_empty(y_shape)
         st = lib.mlstm_short_conv_fwd(
             x.data_ptr(), x_row, weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
-            y.data_ptr(), out_state.data_ptr(), B, NH, T, d, W, _dtype_code(x), code,
+            y.data_ptr(), out_state.data_ptr(), *sizes, _dtype_code(x), code,
             _stream_ptr(x.device))
     if st != 0:
         raise MlstmError(st, "mlstm_short_conv_fwd")
@@ -824,8 +838,9 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, heads=None
     lib = load_library()
     if not isinstance(dy, torch.Tensor):
         raise TypeError(f"dy must be a torch.Tensor, got {type(dy).__name__}")
-    x_row, B, NH, T, d, W = _check_conv(x, weight, bias, heads, lengths, 3,
-                                        {"state": state, "dstate": dstate}, dy)
+    x_row, _, sizes = _check_conv(x, weight, bias, heads, lengths, 3,
+                                  {"state": state, "dstate": dstate}, dy)
+    B, NH, _, d, W = sizes
     code, dtype = _named_code("activation", CONV_ACTIVATIONS, activation), _dtype_code(x)
     with _on(x.device):
         g = {"dx": torch.empty_like(x, memory_format=torch.contiguous_format),
@@ -833,12 +848,12 @@ def short_conv_bwd(x, weight, dy, bias=None, state=None, dstate=None, heads=None
         if bias is not None:
             g["dbias"] = torch.empty_like(bias)
         g["dstate"] = torch.empty((B, W - 1, NH * d), dtype=x.dtype, device=x.device)
-        ws = _workspace(lib.mlstm_short_conv_workspace_bytes(B, NH, T, d, W, dtype), x.device)
+        ws = _workspace(lib.mlstm_short_conv_workspace_bytes(*sizes, dtype), x.device)
         st = lib.mlstm_short_conv_bwd(
             x.data_ptr(), x_row, weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
             dy.data_ptr(), _ptr(dstate), g["dx"].data_ptr(), g["dweight"].data_ptr(),
             _ptr(g.get("dbias")), g["dstate"].data_ptr(), _ptr(ws),
-            0 if ws is None else ws.numel(), B, NH, T, d, W, dtype, code, _stream_ptr(x.device))
+            0 if ws is None else ws.numel(), *sizes, dtype, code, _stream_ptr(x.device))
     if st != 0:
         raise MlstmError(st, "mlstm_short_conv_bwd")
     return g
@@ -851,21 +866,29 @@ def _check_scan(u, dt, A, B, C, D, gate, dt_bias, lengths, dims, states, dy=None
     form = "T, " if dims == 3 else ""
     if u.dim() != dims:
         raise ValueError(f"u must be [B, {form}channels], got shape {tuple(u.shape)}")
-    if not isinstance(A, torch.Tensor):
-        raise TypeError(f"A must be a torch.Tensor, got {type(A).__name__}")
+    for name, t in (("dt", dt), ("A", A), ("B", B), ("C", C)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if A.dim() != 2:
         raise ValueError(f"A must be [channels, N], got shape {tuple(A.shape)}")
-    if not isinstance(B, torch.Tensor):
-        raise TypeError(f"B must be a torch.Tensor, got {type(B).__name__}")
     if B.dim() != dims + 1:
         raise ValueError(f"B must be [B, {form}G, N], got shape {tuple(B.shape)}")
     batch, channels, N, G = u.shape[0], u.shape[-1], A.shape[1], B.shape[-2]
     T = u.shape[1] if dims == 3 else 1
-    shared = (*u.shape[:-1], G, N)
-    rows = _require_rows([("u", u, u.shape, u.dtype, channels),
-                          ("dt", dt, u.shape, u.dtype, channels),
-                          ("B", B, shared, u.dtype, G * N), ("C", C, shared, u.dtype, G * N),
-                          ("gate", gate, u.shape, u.dtype, channels)], u.device)
+    rows, kind, f32 = u.shape, u.dtype, torch.float32
+    shared = (*rows[:-1], G, N)
+    sizes, state = (batch, T, channels, G, N), (batch, channels, N)
+    if _all_plain(u.device, (
+            (u, rows, kind), (dt, rows, kind), (A, (channels, N), f32), (B, shared, kind),
+            (C, shared, kind), (D, (channels,), f32), (gate, rows, kind),
+            (dt_bias, (channels,), f32), (lengths, (batch,), torch.int32), (dy, rows, kind),
+            *((t, state, f32) for t in states.values()))):
+        pitches = (channels, channels, G * N, G * N, channels)
+        return _scan_args(u, dt, A, B, C, D, gate, dt_bias, states["state"], lengths,
+                          pitches), sizes
+    pitches = _require_rows([("u", u, rows, kind, channels), ("dt", dt, rows, kind, channels),
+                             ("B", B, shared, kind, G * N), ("C", C, shared, kind, G * N),
+                             ("gate", gate, rows, kind, channels)], u.device)
     named = [("A", A, (channels, N), torch.float32)]
     for name, t in (("D", D), ("dt_bias", dt_bias)):
         if t is not None:
@@ -876,12 +899,15 @@ def _check_scan(u, dt, A, B, C, D, gate, dt_bias, lengths, dims, states, dy=None
         named.append(("dy", dy, u.shape, u.dtype))
     for name, t in states.items():
         if t is not None:
-            named.append((name, t, (batch, channels, N), torch.float32))
+            named.append((name, t, state, torch.float32))
     _require_all(named, u.device)
-    args = (u.data_ptr(), rows[0], dt.data_ptr(), rows[1], A.data_ptr(), B.data_ptr(), rows[2],
-            C.data_ptr(), rows[3], _ptr(D), _ptr(gate), rows[4], _ptr(dt_bias),
-            _ptr(states["state"]), _ptr(lengths))
-    return args, (batch, T, channels, G, N)
+    return _scan_args(u, dt, A, B, C, D, gate, dt_bias, states["state"], lengths, pitches), sizes
+
+
+def _scan_args(u, dt, A, B, C, D, gate, dt_bias, state, lengths, pitches):
+    return (u.data_ptr(), pitches[0], dt.data_ptr(), pitches[1], A.data_ptr(), B.data_ptr(),
+            pitches[2], C.data_ptr(), pitches[3], _ptr(D), _ptr(gate), pitches[4], _ptr(dt_bias),
+            _ptr(state), _ptr(lengths))
 
 
 def scan_state(B, channels, N, device):

@@ -309,6 +309,17 @@ def test_binding_refuses_malformed_calls(monkeypatch):
         f(**{**ffn, "w_up": _t(16, 24).T})
 
 
+@needs_lib
+@pytest.mark.parametrize("call,arg", [
+    (c, a) for c, (_, good) in CALLS.items() for a in good
+    if a in "x weight u dt A B C dy w_gate w_up dh".split() or (c.endswith("step") and a == "state")])
+def test_binding_wants_what_is_not_optional(monkeypatch, call, arg):
+    monkeypatch.setattr(mlstm, "_require_device", lambda *a: None)
+    f, good = CALLS[call]
+    with pytest.raises(TypeError, match=f"{arg} must be a torch.Tensor, got NoneType"):
+        f(**{**good, arg: None})
+
+
 def test_pitches_of_rows(monkeypatch):
     """Rows of a wider matrix: one pitch for all of them."""
     monkeypatch.setattr(mlstm, "_require_device", lambda *a: None)
