@@ -10,16 +10,16 @@
 // All products run on one kind of tile (product_tiles.h), whose operands are rows
 // of the summed index: the weights, x and G are transposed into the workspace for
 // the last two.  For bf16 and 512 rows or more, G is rounded to bf16 as the operand of
-// those products (2^-9 of each term, as much as the rounding of the results, at half
+// those products (up to 2^-8 of each term, as much as the rounding of the results, at half
 // the time of carrying 16 bits); for fewer rows, whose sums have few terms to average
 // over and take little time, it has two planes, 16 bits.  Everything before is float32.
 //
-// Measured: 16384 rows of 1536 to 4096 forward 345 us (in a trace; product_tiles.h has
-// what bounds it); 8192 rows of 2048 to 5504 forward 345, backward 389 for G, 320 for
-// dx and 340 for the weights' gradients, 99 for turned operands at a copy's rate and 11
-// for joined shares.  8 rows of 1536 to 4096 7.8 us (25 MB, 5.1 at a copy's rate), 17 as
-// tiles.  float32, 999 rows of 392 to 1048, training: 158 us, 350 before split tiles and
-// operands made in one launch.
+// Measured: 16384 rows of 1536 to 4096 forward 330 us (in a settled trace;
+// product_tiles.h has what bounds it); 8192 rows of 2048 to 5504 forward 321, backward
+// 365 for G, 287 for dx and 309 for the weights' gradients, 95 for turned operands and
+// 11 for joined shares.  8 rows of 1536 to 4096 7.8 us (25 MB, 5.1 at a copy's rate), 17 as
+// tiles.  float32, 999 rows of 392 to 1048, training: 145 us, 350 before split tiles,
+// operands made in one launch and three pieces ahead (158 with two).
 #include "gated_ffn.h"
 
 #include "product_tiles.h"
@@ -469,14 +469,17 @@ Choice choose(int64_t p, int64_t q, unsigned groups, int64_t pieces, double piec
   return best;
 }
 
-// f(shape, plan) with the tiles of the least time.  A piece takes 1.75 us in tiles of
-// 256 x 256 on all CUs, 1.05 in 128 x 256, and 1.15 in 128 x 128, two to a CU (8192
-// rows through 2048 x 5504 and their gradients).
+// f(shape, plan) with the tiles of the least time.  A piece takes 1.7 us in tiles of
+// 256 x 256 on all CUs, 0.92 in 128 x 256, and 1.2 in 128 x 128, two to a CU: measured
+// on 2048 x 8192 x 11008, one round of the first (293 us) and two of the others (323
+// and 422).  With 1.05 for the second, backward passes of ten other sizes took from 7 %
+// more (float32, 8192 rows of 392 to 1048: 490 for 459 us) to 2 % less (float32, 4096
+// rows of 1536 to 4096: 1814 for 1845), 2 % more on average.
 template <typename F>
 hipError_t with_shape(int64_t p, int64_t q, unsigned groups, int64_t pieces, F&& f) {
-  const Choice large = choose<Large>(p, q, groups, pieces, 1.75),
-               medium = choose<Medium>(p, q, groups, pieces, 1.05),
-               small = choose<Small>(p, q, groups, pieces, 1.15);
+  const Choice large = choose<Large>(p, q, groups, pieces, 1.7),
+               medium = choose<Medium>(p, q, groups, pieces, 0.92),
+               small = choose<Small>(p, q, groups, pieces, 1.2);
   if (small.time < large.time && small.time < medium.time) return f(Small{}, small.plan);
   if (medium.time < large.time) return f(Medium{}, medium.plan);
   return f(Large{}, large.plan);

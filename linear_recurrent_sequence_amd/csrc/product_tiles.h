@@ -7,16 +7,16 @@
 // 16) ..) and stores them together.  Both operands' pieces of 64 columns are copied
 // global -> LDS without registers into two or three slots.  A wave reads the fragments
 // of 32 columns into registers while it multiplies those of the 32 before, so a slot is
-// free when half of its products are done, and is filled again, as many pieces ahead
-// as there are slots, beside the other half's.  Workgroups stay for several tiles: the copies run on
-// into the next tile, whose first pieces come in while this one is stored.  Eight
+// free when half of its products are done, and is filled again, as many pieces ahead as
+// there are slots, beside the other half's.  Workgroups stay for several tiles: the
+// copies run on into the next tile, whose first pieces come in while this one is stored.  Eight
 // lanes copy a row's 128 bytes, a cache line, and its 16-byte parts lie in the order
 // part ^ (row & 7), so that the 16 rows that an instruction's lanes read in one
 // column do not share banks.  Rows beyond an operand's, and columns beyond k, are
 // read out of the buffer's range: zeros.
 //
-// Measured: 8192 x 16384 x 1536 with the gate's epilogue 345 us, 1190 TFLOP/s (the
-// library's product alone 358 to 373); 2048 x 8192 x 11008 320 us, 1150 TFLOP/s (250 to
+// Measured: 8192 x 16384 x 1536 with the gate's epilogue 330 us, 1250 TFLOP/s (the
+// library's product alone 358 to 373); 2048 x 8192 x 11008 287 us, 1290 TFLOP/s (250 to
 // 272).  Without copies the same loop takes 0.78 of the time, without
 // products 0.77, without reads 0.95: the copies and the matrix unit are each other's
 // limit.  Copies and reads spread over the products, at a raised wave priority, gave

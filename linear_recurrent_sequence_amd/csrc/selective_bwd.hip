@@ -26,8 +26,8 @@
 // segment has become, exp(A sum Delta), to the states it kept.
 //
 // Bound by the vector unit.  Measured, bf16, N = 16, gate, 8 x 2048 x 1536 in 8 segments:
-// first pass 137 us (unit 97 % busy), second 409 (83 %; 26 instructions a state and
-// token: 5 forward, 10 back, 4.4 of the butterfly, the rest per token), sums 29.  With a
+// first pass 123 us (unit 97 % busy), second 372 (83 %; 26 instructions a state and
+// token: 5 forward, 10 back, 4.4 of the butterfly, the rest per token), sums 20.  With a
 // tile's LDS reads kept over both ways and the sums sunk behind them, the second pass
 // needed 440 registers and took 549 us on one wave to a SIMD; with its rows' addresses
 // formed for every tile 514.

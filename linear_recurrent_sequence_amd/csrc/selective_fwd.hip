@@ -2,9 +2,9 @@
 //
 // Bound by the vector unit: a state and token take a product, an exponential (a quarter
 // of the rate) and three more, 8 issue slots, for 1/8 of a byte.  Measured, bf16, N = 16,
-// gate: 8 x 2048 x 1536 187 us in a trace (192 workgroups on as many CUs, the unit there 73 % busy; at
-// full rate on all CUs the states alone would take 82), 1 x 16384 x 2048 131 us for the
-// effects of 15 of 16 segments, 5 to join them and 170 for the scan.  Blocks of four
+// gate: 8 x 2048 x 1536 177 us in a settled trace (192 workgroups on as many CUs, the unit
+// there 73 % busy; at full rate on all CUs the states alone would take 82), 1 x 16384 x
+// 2048 121 us for the effects of 15 of 16 segments, 5 to join them and 157 for the scan.  Blocks of four
 // tokens whose LDS reads are issued a block ahead and whose exponentials come first gave
 // 192 -> 175 us (calls) on the first and 358 -> 285 on the second.
 #include "selective_common.h"

@@ -20,7 +20,7 @@
 // fixed order: no atomics, results are bitwise reproducible.
 //
 // Bound by memory.  Measured, bf16, W = 4, 8 x 2048 rows of 1536: forward 19.6 us (100 MB,
-// a copy's rate), backward 37 us (150 MB, 83 % of it) and 4 us for the weights' sums.
+// a copy's rate), backward 35 us (150 MB, 86 % of it) and 4 us for the weights' sums.
 #include "short_conv.h"
 
 #include "row_vec.h"
