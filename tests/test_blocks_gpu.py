@@ -687,3 +687,53 @@ def test_in_graphs():
         torch.cuda.synchronize()
         for out in outs:
             assert all(torch.equal(a, r) for a, r in zip(out, ref))
+
+
+@pytest.mark.parametrize("n,T,c", [(1, 4096, 64), (2, 1500, 136)])
+def test_a_long_sequence_updates_its_states_in_place(n, T, c):
+    """The scan in segments and the convolution in many runs, with a state that other
+    workgroups read while the last ones are not done."""
+    x, _, _ = scan_inputs(n, T, c, 16, 1, BF, 40)
+    args = [x[k] for k in ("u", "dt", "A", "B", "C")]
+    kw = {k: x[k] for k in ("D", "gate", "dt_bias")}
+    y, st = mlstm.scan_fwd(*args, state=x["state"], **kw)
+    kept = x["state"].clone()
+    y2, st2 = mlstm.scan_fwd(*args, state=kept, out_state=kept, **kw)
+    assert st2 is kept and torch.equal(y, y2) and torch.equal(st, kept)
+    w, state = gpu(np.random.default_rng(41).normal(size=(c, 4))), x["u"][:, :3].clone()
+    if n == 1:  # the first rows of x themselves
+        with pytest.raises(mlstm.MlstmError, match="overlap"):
+            mlstm.short_conv_fwd(x["u"], w, state=state, out_state=x["u"][:, :3])
+    y, st = mlstm.short_conv_fwd(x["u"], w, state=state)
+    y2, st2 = mlstm.short_conv_fwd(x["u"], w, state=state, out_state=state)
+    assert st2 is state and torch.equal(y, y2) and torch.equal(st, state)
+
+
+def _scan_call():
+    x, dy, dst = scan_inputs(2, 9, 32, 4, 1, FP, 42)
+    return mlstm.scan_bwd, dict(x, dy=dy, dstate=dst, lengths=i32([9, 4]))
+
+
+def _conv_call():
+    r = np.random.default_rng(43)
+    z = lambda *s: gpu(r.normal(size=s))
+    return mlstm.short_conv_bwd, dict(x=z(2, 9, 16), weight=z(16, 4), dy=z(2, 1, 9, 16),
+                                      bias=z(16), state=z(2, 3, 16), dstate=z(2, 3, 16),
+                                      lengths=i32([9, 4]), heads=1)
+
+
+@pytest.mark.parametrize("call", [_scan_call, _conv_call])
+def test_each_tensor_is_checked_among_gpu_tensors(call):
+    f, good = call()
+    f(**good)
+    tensors = [k for k, v in good.items() if isinstance(v, torch.Tensor)]
+    first = tensors[0]  # its device and type are the call's
+    for k in tensors:
+        if k != first:
+            with pytest.raises(ValueError, match=f"{k} "):
+                f(**{**good, k: good[k].cpu()})
+        with pytest.raises((TypeError, ValueError)):
+            f(**{**good, k: good[k].double()})
+        wide = torch.stack([good[k], good[k]], -1)[..., 0]  # every second element
+        with pytest.raises(ValueError, match="contiguous"):
+            f(**{**good, k: wide})
