@@ -619,10 +619,10 @@ int mlstm_scan_bwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row,
  *   D and F multiples of 8, at most 2^16; M <= 2^20, M max(D, 2 F) <= 2^33
  * Products are summed in float32 (float32 operands as three bf16 planes, 24
  * bits), and a bf16 h is rounded once.  mlstm_gated_ffn_bwd forms both products
- * again; for bf16 and M >= 512 their gradients are rounded to bf16 as operands of the
- * products behind dx, dw_gate and dw_up (for fewer rows to 16 bits).  Inputs finite (float32 ones below 2^127 in
- * magnitude).  Tensors 16-byte aligned; workspace mlstm_gated_ffn_workspace_bytes bytes, 256-byte aligned.
- * Bitwise reproducible.
+ * again; for bf16 their gradients have 16 bits as operands of the products behind dx,
+ * dw_gate and dw_up, which are rounded once.  Inputs finite (float32 ones below 2^127 in
+ * magnitude).  Tensors 16-byte aligned; workspace mlstm_gated_ffn_workspace_bytes bytes,
+ * 256-byte aligned.  Bitwise reproducible.
  */
 enum { MLSTM_FFN_SILU = 0, MLSTM_FFN_GELU = 1 };
 

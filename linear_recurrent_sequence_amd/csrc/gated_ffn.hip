@@ -9,15 +9,17 @@
 //
 // All products run on one kind of tile (product_tiles.h), whose operands are rows
 // of the summed index: the weights, x and G are transposed into the workspace for
-// the last two.  For bf16 and 512 rows or more, G is rounded to bf16 as the operand of
-// those products (up to 2^-8 of each term, as much as the rounding of the results, at half
-// the time of carrying 16 bits); for fewer rows, whose sums have few terms to average
-// over and take little time, it has two planes, 16 bits.  Everything before is float32.
+// the last two.  For bf16, G has two bf16 planes, 16 bits, as the operand of those
+// products: up to 2^-17 of each term, little beside the rounding of the results, which are
+// then the float32 gradients rounded once.  (One plane takes half the time of two, but its
+// errors of up to 2^-8 of each term do not average out in a sum of terms of either sign,
+// however long it is: the results would be off by as much again as by their own rounding.)
+// Everything before is float32.
 //
 // Measured: 16384 rows of 1536 to 4096 forward 330 us (in a settled trace;
-// product_tiles.h has what bounds it); 8192 rows of 2048 to 5504 forward 321, backward
-// 365 for G, 287 for dx and 309 for the weights' gradients, 95 for turned operands and
-// 11 for joined shares.  8 rows of 1536 to 4096 7.8 us (25 MB, 5.1 at a copy's rate), 17 as
+// product_tiles.h has what bounds it); 8192 rows of 2048 to 5504 forward 319, backward
+// 466 for G, 550 for dx and 607 for the weights' gradients, 177 for turned operands and
+// 10 for joined shares (with one plane of G 365, 287, 309, 95 and 11).  8 rows of 1536 to 4096 7.8 us (25 MB, 5.1 at a copy's rate), 17 as
 // tiles.  float32, 999 rows of 392 to 1048, training: 145 us, 350 before split tiles,
 // operands made in one launch and three pieces ahead (158 with two).
 #include "gated_ffn.h"
@@ -38,7 +40,7 @@ using Medium = product::Shape<128, 256, 2, 4, 3>;
 using Small = product::Shape<128, 128, 2, 2, 2>;
 
 constexpr int kPlanes = 3, kTerms = 6;  // of float32
-constexpr int64_t kFineRows = 512;      // from which on bf16 gradients of g and u are bf16
+constexpr int kGradPlanes = 2;          // of G, behind bf16 gradients
 
 struct Act {
   float value, slope;
@@ -79,12 +81,15 @@ __device__ inline Pair gate_up_of(f32x4 g, f32x4 u, const float (&d)[4], bool ge
   return o;
 }
 
-// h, or with GRAD G = [dg | du], in tiles of rows and of F
-template <typename T, typename O, typename S, bool GRAD>
+// h, or with GRAD G = [dg | du] (for bf16 its two planes, one behind the other), in tiles
+// of rows and of F
+template <typename T, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operand wu, Operand x,
                                                               Sizes n, Plan plan, const T* dh,
-                                                              O* out, float* shares) {
+                                                              T* out, float* shares) {
   __shared__ __align__(1024) char lds[S::kLds];
+  constexpr bool kTwoPlanes = GRAD && sizeof(T) == 2;
+  // two planes are twice as many stores, but a share of a tile has no more than these
   constexpr int kF = S::kBP / 2, kStores = (GRAD ? S::kP : S::kP / 2) * S::kQ;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   product::tiles<S, true, kStores>(
@@ -98,7 +103,17 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
         const int f0 = int(ip) * kF + wave / S::kWQ * (kF / S::kWP) + lane / 16 * 4,
                   q0 = int(iq) * S::kBQ, F = int(n.F), M = int(n.M);
         const int m0 = wave % S::kWQ * (S::kBQ / S::kWQ) + lane % 16;
-        const product::Rows<O> rows(out, q0, M, GRAD ? 2 * F : F);
+        const product::Rows<T> rows(out, q0, M, GRAD ? 2 * F : F),
+            low_rows(out + (kTwoPlanes ? n.M * 2 * n.F : 0), q0, M, GRAD ? 2 * F : F);
+        auto put = [&](int i, int c, int columns, f32x4 v) {
+          if constexpr (kTwoPlanes) {
+            const product::TwoPlanes p(v);
+            rows.put(i, c, columns, p.high);
+            low_rows.put(i, c, columns, p.low);
+          } else {
+            rows.put(i, c, columns, v);
+          }
+        };
         // dh of kAhead blocks of rows at a time, ahead of their stores
         constexpr int kAhead = GRAD && sizeof(T) == 2 ? S::kQ : 1;
 #pragma unroll
@@ -122,8 +137,8 @@ __global__ __launch_bounds__(S::kThreads) void gate_up_kernel(Operand wg, Operan
               float d[4];
               rowvec::floats(raw[jj][i], d);
               const Pair o = gate_up_of<GRAD>(acc[i][j], acc[i + S::kP / 2][j], d, n.gelu);
-              rows.put(m0 + j * 16, f, F, o.a);
-              if constexpr (GRAD) rows.put(m0 + j * 16, f < F ? F + f : 2 * F, 2 * F, o.b);
+              put(m0 + j * 16, f, F, o.a);
+              if constexpr (GRAD) put(m0 + j * 16, f < F ? F + f : 2 * F, 2 * F, o.b);
             }
         }
       });
@@ -184,9 +199,9 @@ __global__ __launch_bounds__(S::kBP) void join_kernel(Plan plan, const float* sh
 }
 
 // The rest of gate_up_kernel's tiles, eight rows of a tile to a workgroup
-template <typename T, typename O, typename S, bool GRAD>
+template <typename T, typename S, bool GRAD>
 __global__ __launch_bounds__(S::kBP) void join_gate_up_kernel(Plan plan, const float* shares,
-                                                              Sizes n, const T* dh, O* out) {
+                                                              Sizes n, const T* dh, T* out) {
   constexpr int kF = S::kBP / 2, kHalf = kF / S::kWP;  // columns; of a wave's rows of one operand
   const unsigned rest = blockIdx.x / (S::kBQ / 8);
   unsigned ip, iq;
@@ -199,13 +214,22 @@ __global__ __launch_bounds__(S::kBP) void join_gate_up_kernel(Plan plan, const f
   if (GRAD) rowvec::load(dh + m * n.F + f, d);
   const Pair o = gate_up_of<GRAD>(joined<S>(plan, shares, rest, q, p),
                                   joined<S>(plan, shares, rest, q, p + kHalf), d, n.gelu);
-  const float a[4] = {o.a[0], o.a[1], o.a[2], o.a[3]};
-  if constexpr (GRAD) {
-    const float b[4] = {o.b[0], o.b[1], o.b[2], o.b[3]};
-    rowvec::store(out + m * 2 * n.F + f, a);
-    rowvec::store(out + (m * 2 + 1) * n.F + f, b);
+  auto put = [&](int64_t at, f32x4 v) {
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    rowvec::store(out + at, x);
+  };
+  if constexpr (!GRAD) {
+    put(m * n.F + f, o.a);
+  } else if constexpr (sizeof(T) == 2) {
+    const product::TwoPlanes a(o.a), b(o.b);
+    const int64_t low = n.M * 2 * n.F;
+    put(m * 2 * n.F + f, a.high);
+    put(m * 2 * n.F + f + low, a.low);
+    put((m * 2 + 1) * n.F + f, b.high);
+    put((m * 2 + 1) * n.F + f + low, b.low);
   } else {
-    rowvec::store(out + m * n.F + f, a);
+    put(m * 2 * n.F + f, o.a);
+    put((m * 2 + 1) * n.F + f, o.b);
   }
 }
 
@@ -499,7 +523,7 @@ int64_t pieces_of(int64_t k, int terms) {
   return (k + product::kStep - 1) / product::kStep * terms;
 }
 
-template <typename T, typename O, bool GRAD>
+template <typename T, bool GRAD>
 hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
                    const void* dh, void* out, Arena& ws, hipStream_t stream, bool run) {
   return with_shape(2 * n.F, n.M, 1, pieces_of(n.D, n.terms), [&](auto shape, const Plan& plan) {
@@ -507,11 +531,11 @@ hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const
     float* shares = take_shares<S>(plan, ws);
     if (!run) return hipSuccess;
     const T* d = static_cast<const T*>(dh);
-    O* o = static_cast<O*>(out);
-    gate_up_kernel<T, O, S, GRAD><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
+    T* o = static_cast<T*>(out);
+    gate_up_kernel<T, S, GRAD><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
         wg, wu, x, n, plan, d, o, shares);
     if (shares)
-      join_gate_up_kernel<T, O, S, GRAD><<<plan.rest() * (S::kBQ / 8), S::kBP, 0, stream>>>(
+      join_gate_up_kernel<T, S, GRAD><<<plan.rest() * (S::kBQ / 8), S::kBP, 0, stream>>>(
           plan, shares, n, d, o);
     return hipGetLastError();
   });
@@ -544,7 +568,7 @@ hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bo
                 wu = as_rows<T>(a.w_up, a.F, a.D, ws, jobs.job[1]),
                 x = as_rows<T>(a.x, a.M, a.D, ws, jobs.job[2]);
   if (run && sizeof(T) == 4) prepare<T>(jobs, stream);
-  return gate_up<T, T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
+  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
                            run);
 }
 
@@ -558,27 +582,31 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
                 wu = as_rows<T>(a.w_up, F, D, ws, jobs.job[1]),
                 x = as_rows<T>(a.x, M, D, ws, jobs.job[2]);
   constexpr bool kFloat = sizeof(T) == 4;
-  const bool fine = kFloat || M < kFineRows;  // G in float32, and its planes
-  void* G = fine ? static_cast<void*>(ws.take<float>(M * 2 * F)) : ws.take<T>(M * 2 * F);
-  const int64_t wt_plane = D * 2 * F, xt_plane = D * pitch, gt_plane = 2 * F * pitch;
-  uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);            // [D][Wg^T | Wu^T]
-  uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);            // [D][M]
-  uint16_t* gt = ws.take<uint16_t>((fine ? kPlanes : 1) * gt_plane);  // [2F][M]
+  constexpr int kOfG = kFloat ? kPlanes : kGradPlanes;
+  T* G = ws.take<T>((kFloat ? 1 : kGradPlanes) * M * 2 * F);  // float32, or planes
+  const int64_t g_plane = M * 2 * F, wt_plane = D * 2 * F, xt_plane = D * pitch,
+                gt_plane = 2 * F * pitch;
+  uint16_t* wt = ws.take<uint16_t>(kCopies<T> * wt_plane);  // [D][Wg^T | Wu^T]
+  uint16_t* xt = ws.take<uint16_t>(kCopies<T> * xt_plane);  // [D][M]
+  uint16_t* gt = ws.take<uint16_t>(kOfG * gt_plane);        // [2F][M]
   turn(jobs.job[0], wt, F, 2 * F, wt_plane);
   turn(jobs.job[1], wt + F, F, 2 * F, wt_plane);
   turn(jobs.job[2], xt, pitch, pitch, xt_plane);
   if (run) prepare<T>(jobs, stream);
   const Sizes n = {M, D, F, kTermsOf<T>, a.gelu};
-  hipError_t e = fine ? gate_up<T, float, true>(wg, wu, x, n, g.dh, G, ws, stream, run)
-                      : gate_up<T, T, true>(wg, wu, x, n, g.dh, G, ws, stream, run);
+  hipError_t e = gate_up<T, true>(wg, wu, x, n, g.dh, G, ws, stream, run);
   if (e != hipSuccess) return e;
   Jobs more;
-  more.n = 1;
-  const Operand G_rows = fine ? as_rows<float>(G, M, 2 * F, ws, more.job[0])
-                              : as_rows<T>(G, M, 2 * F, ws, more.job[0]);
+  more.n = kFloat ? 1 : kGradPlanes;
+  Operand G_rows = as_rows<T>(G, M, 2 * F, ws, more.job[0]);
   turn(more.job[0], gt, pitch, pitch, gt_plane);
-  if (run) fine ? prepare<float>(more, stream) : prepare<T>(more, stream);
-  const int terms = kFloat ? kTerms : fine ? 2 : 1;
+  if constexpr (!kFloat) {  // the second plane is a matrix of its own
+    G_rows.plane = g_plane;
+    (void)as_rows<T>(G + g_plane, M, 2 * F, ws, more.job[1]);
+    turn(more.job[1], gt + gt_plane, pitch, pitch, gt_plane);
+  }
+  if (run) prepare<T>(more, stream);
+  const int terms = kFloat ? kTerms : kGradPlanes;
   e = multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, terms, 1, g.dx, nullptr, ws, stream, run);
   if (e != hipSuccess) return e;
   return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, terms, 2,

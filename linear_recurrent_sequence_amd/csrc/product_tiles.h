@@ -16,8 +16,8 @@
 // read out of the buffer's range: zeros.
 //
 // Measured: 8192 x 16384 x 1536 with the gate's epilogue 330 us, 1250 TFLOP/s (the
-// library's product alone 358 to 373); 2048 x 8192 x 11008 287 us, 1290 TFLOP/s (250 to
-// 272).  Without copies the same loop takes 0.78 of the time, without
+// library's product alone 358 to 373); 2048 x 8192 x 11008 in two terms 550 us, 1340
+// TFLOP/s.  Without copies the same loop takes 0.78 of the time, without
 // products 0.77, without reads 0.95: the copies and the matrix unit are each other's
 // limit.  Copies and reads spread over the products, at a raised wave priority, gave
 // 4.5 % over copies in one burst.
@@ -72,7 +72,7 @@ __device__ inline void copy_piece(i32x4 rsrc, unsigned voffset, unsigned dst) {
 }
 
 // The planes of term s of `terms`: six of two float32 operands, two of a bf16 one (left)
-// with the two larger planes of a float32 one, and one of two bf16 operands
+// with two planes of a float32 one, and one of two bf16 operands
 __device__ inline int left_plane(int s, int terms) {
   return terms == 6 ? (0x001102 >> (4 * s)) & 15 : 0;  // 2 0 1 1 0 0
 }
@@ -125,8 +125,8 @@ __device__ inline Item item_of(const Plan& p, unsigned i) {
 // acc[i][j] the accumulators of the wave's p block i and q block j.  DUAL: the left
 // rows are those of two operands in turn, a wave's first half of its blocks from L
 // and the second half from L2, for the same output columns (BP / 2 to a tile).
-// `store` issues STORES stores, whatever the tile: their completion is not waited
-// for with the next tile's first copies, which are older.
+// `store` issues STORES stores at least, whatever the tile: the completion of that many
+// is not waited for with the next tile's first copies, which are older.
 template <typename S, bool DUAL, int STORES, typename F>
 __device__ inline void tiles(const Operand& L, const Operand& L2, const Operand& R, int64_t k,
                              int terms, const Plan& plan, char* lds, F&& store) {
@@ -323,6 +323,19 @@ struct Rows {
     else
       __builtin_amdgcn_raw_buffer_store_b64(
           u32x2{rowvec::to_bf16(x[0], x[1]), rowvec::to_bf16(x[2], x[3])}, rsrc, at, 0, 0);
+  }
+};
+
+// Four float32 values as two bf16 planes, 16 bits of them
+struct TwoPlanes {
+  f32x4 high, low;  // rounded to bf16, and what is left
+  __device__ explicit TwoPlanes(f32x4 x) {
+    rowvec::Raw<__hip_bfloat16, 4> r;
+    r.w[0] = rowvec::to_bf16(x[0], x[1]), r.w[1] = rowvec::to_bf16(x[2], x[3]);
+    float h[4];
+    rowvec::floats(r, h);
+    high = f32x4{h[0], h[1], h[2], h[3]};
+    low = x - high;
   }
 };
 
