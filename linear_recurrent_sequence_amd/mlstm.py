@@ -794,7 +794,7 @@ def _short_conv(x, weight, bias, state, out_state, heads, lengths, activation, d
     with _on(x.device):
         if out_state is None:
             out_state = torch.empty((B, W - 1, NH * d), dtype=x.dtype, device=x.device)
-        y = x.new_empty(y_shape)
+        y = torch.empty(y_shape, dtype=x.dtype, device=x.device)
         st = lib.mlstm_short_conv_fwd(
             x.data_ptr(), x_row, weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(lengths),
             y.data_ptr(), out_state.data_ptr(), *sizes, _dtype_code(x), code,
