@@ -636,6 +636,16 @@ int mlstm_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, con
                         size_t workspace_bytes, int64_t M, int64_t D, int64_t F, int dtype,
                         int activation, void* stream);
 
+/*
+ * mlstm_gated_ffn_tiles -- in what tiles a product of a call is taken (on the host; for
+ * tests and timings): tiles[0], [1] columns and rows of a tile's outputs, [2] tiles taken
+ * whole, [3] tiles whose sums are split, [4] into so many shares.  Zeros for the forward
+ * of few rows, which has no tiles.
+ */
+enum { MLSTM_FFN_FORWARD = 0, MLSTM_FFN_AGAIN = 1, MLSTM_FFN_DX = 2, MLSTM_FFN_WEIGHTS = 3 };
+int mlstm_gated_ffn_tiles(int64_t M, int64_t D, int64_t F, int dtype, int product,
+                          int64_t tiles[5]);
+
 /* Human-readable text of a status code (static storage). */
 const char* mlstm_strerror(int status);
 

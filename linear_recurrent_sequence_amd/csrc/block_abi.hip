@@ -292,6 +292,20 @@ size_t mlstm_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F, int dtyp
                   : mlstm::gated_ffn_fwd_workspace_bytes(a);
 }
 
+int mlstm_gated_ffn_tiles(int64_t M, int64_t D, int64_t F, int dtype, int product,
+                          int64_t tiles[5]) {
+  const int st = check_ffn(M, D, F, dtype);
+  if (st != MLSTM_OK) return st;
+  if (product < MLSTM_FFN_FORWARD || product > MLSTM_FFN_WEIGHTS) return MLSTM_ERR_SHAPE;
+  if (!tiles) return MLSTM_ERR_NULL;
+  const mlstm::GatedFfnTiles t =
+      mlstm::gated_ffn_tiles(gated_ffn(nullptr, nullptr, nullptr, M, D, F, dtype, MLSTM_FFN_SILU),
+                             static_cast<mlstm::FfnProduct>(product));
+  const int64_t all[5] = {t.columns, t.rows, t.whole, t.split, t.shares};
+  for (int i = 0; i < 5; ++i) tiles[i] = all[i];
+  return MLSTM_OK;
+}
+
 int mlstm_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h,
                         void* workspace, size_t workspace_bytes, int64_t M, int64_t D, int64_t F,
                         int dtype, int activation, void* stream) {

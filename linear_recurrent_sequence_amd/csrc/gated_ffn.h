@@ -25,6 +25,15 @@ struct GatedFfnGrads {
   void* dw_up;     // [F][D]
 };
 
+// The products of a call: g and u forward, g and u again backward, dx, and the weights'
+// gradients; and the tiles that one is taken in (none where rows are few)
+enum class FfnProduct { kForward, kAgain, kDx, kWeights };
+struct GatedFfnTiles {
+  int64_t columns, rows;        // of a tile's outputs
+  int64_t whole, split, shares;  // tiles in one piece, and those split into so many shares
+};
+GatedFfnTiles gated_ffn_tiles(const GatedFfn& a, FfnProduct which);
+
 size_t gated_ffn_fwd_workspace_bytes(const GatedFfn& a);
 hipError_t launch_gated_ffn_fwd(const GatedFfn& a, void* h, void* workspace, hipStream_t stream);
 size_t gated_ffn_bwd_workspace_bytes(const GatedFfn& a);

@@ -432,8 +432,8 @@ struct Arena {
 
 template <typename T>
 constexpr int kCopies = sizeof(T) == 4 ? kPlanes : 1;
-template <typename T>
-constexpr int kTermsOf = sizeof(T) == 4 ? kTerms : 1;
+// rows of turned operands: whole vectors
+int64_t pitch_of(int64_t M) { return (M + 7) / 8 * 8; }
 
 // a matrix as an operand: a bf16 one as it is, a float32 one as planes, which `job`
 // is told to make
@@ -493,6 +493,22 @@ Choice choose(int64_t p, int64_t q, unsigned groups, int64_t pieces, double piec
   return best;
 }
 
+// A product of a call: p x q outputs (in each of `groups`), sums over k in `terms`
+struct Product {
+  int64_t p, q;
+  unsigned groups;
+  int64_t k;
+  int terms;
+};
+Product product_of(const GatedFfn& a, FfnProduct which) {
+  const int terms = a.is_bf16 ? 1 : kTerms, of_grads = a.is_bf16 ? kGradPlanes : kTerms;
+  switch (which) {
+    case FfnProduct::kDx: return {a.D, a.M, 1, 2 * a.F, of_grads};
+    case FfnProduct::kWeights: return {a.D, a.F, 2, pitch_of(a.M), of_grads};
+    default: return {2 * a.F, a.M, 1, a.D, terms};  // g and u
+  }
+}
+
 // f(shape, plan) with the tiles of the least time.  A piece takes 1.7 us in tiles of
 // 256 x 256 on all CUs, 0.92 in 128 x 256, and 1.2 in 128 x 128, two to a CU: measured
 // on 2048 x 8192 x 11008, one round of the first (293 us) and two of the others (323
@@ -500,10 +516,11 @@ Choice choose(int64_t p, int64_t q, unsigned groups, int64_t pieces, double piec
 // more (float32, 8192 rows of 392 to 1048: 490 for 459 us) to 2 % less (float32, 4096
 // rows of 1536 to 4096: 1814 for 1845), 2 % more on average.
 template <typename F>
-hipError_t with_shape(int64_t p, int64_t q, unsigned groups, int64_t pieces, F&& f) {
-  const Choice large = choose<Large>(p, q, groups, pieces, 1.7),
-               medium = choose<Medium>(p, q, groups, pieces, 0.92),
-               small = choose<Small>(p, q, groups, pieces, 1.2);
+hipError_t with_shape(const Product& m, F&& f) {
+  const int64_t pieces = (m.k + product::kStep - 1) / product::kStep * m.terms;
+  const Choice large = choose<Large>(m.p, m.q, m.groups, pieces, 1.7),
+               medium = choose<Medium>(m.p, m.q, m.groups, pieces, 0.92),
+               small = choose<Small>(m.p, m.q, m.groups, pieces, 1.2);
   if (small.time < large.time && small.time < medium.time) return f(Small{}, small.plan);
   if (medium.time < large.time) return f(Medium{}, medium.plan);
   return f(Large{}, large.plan);
@@ -519,14 +536,13 @@ float* take_shares(const Plan& plan, Arena& ws) {
   return plan.splits > 1
              ? ws.take<float>(int64_t(plan.rest()) * plan.splits * (S::kBP * S::kBQ)) : nullptr;
 }
-int64_t pieces_of(int64_t k, int terms) {
-  return (k + product::kStep - 1) / product::kStep * terms;
-}
 
 template <typename T, bool GRAD>
-hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const Sizes& n,
+hipError_t gate_up(const GatedFfn& a, const Operand& wg, const Operand& wu, const Operand& x,
                    const void* dh, void* out, Arena& ws, hipStream_t stream, bool run) {
-  return with_shape(2 * n.F, n.M, 1, pieces_of(n.D, n.terms), [&](auto shape, const Plan& plan) {
+  const Product m = product_of(a, GRAD ? FfnProduct::kAgain : FfnProduct::kForward);
+  const Sizes n = {a.M, a.D, a.F, m.terms, a.gelu};
+  return with_shape(m, [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
     float* shares = take_shares<S>(plan, ws);
     if (!run) return hipSuccess;
@@ -542,18 +558,18 @@ hipError_t gate_up(const Operand& wg, const Operand& wu, const Operand& x, const
 }
 
 template <typename T>
-hipError_t multiply(const Operand& l, const Operand& r, int64_t k, int terms, unsigned groups,
-                    void* out, void* out2, Arena& ws, hipStream_t stream, bool run) {
-  return with_shape(l.rows, r.rows, groups, pieces_of(k, terms), [&](auto shape, const Plan& plan) {
+hipError_t multiply(const Product& m, const Operand& l, const Operand& r, void* out, void* out2,
+                    Arena& ws, hipStream_t stream, bool run) {
+  return with_shape(m, [&](auto shape, const Plan& plan) {
     using S = decltype(shape);
     float* shares = take_shares<S>(plan, ws);
     if (!run) return hipSuccess;
     T *o = static_cast<T*>(out), *o2 = static_cast<T*>(out2);
     product_kernel<T, S><<<workgroups_of<S>(plan), S::kThreads, 0, stream>>>(
-        l, r, k, terms, plan, o, o2, shares);
+        l, r, m.k, m.terms, plan, o, o2, shares);
     if (shares)
-      join_kernel<T, S><<<plan.rest() * (S::kBQ / 4), S::kBP, 0, stream>>>(plan, shares, l.rows,
-                                                                           r.rows, o, o2);
+      join_kernel<T, S><<<plan.rest() * (S::kBQ / 4), S::kBP, 0, stream>>>(plan, shares, m.p, m.q,
+                                                                           o, o2);
     return hipGetLastError();
   });
 }
@@ -568,14 +584,13 @@ hipError_t forward(const GatedFfn& a, void* h, Arena& ws, hipStream_t stream, bo
                 wu = as_rows<T>(a.w_up, a.F, a.D, ws, jobs.job[1]),
                 x = as_rows<T>(a.x, a.M, a.D, ws, jobs.job[2]);
   if (run && sizeof(T) == 4) prepare<T>(jobs, stream);
-  return gate_up<T, false>(wg, wu, x, {a.M, a.D, a.F, kTermsOf<T>, a.gelu}, nullptr, h, ws, stream,
-                           run);
+  return gate_up<T, false>(a, wg, wu, x, nullptr, h, ws, stream, run);
 }
 
 template <typename T>
 hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStream_t stream,
                     bool run) {
-  const int64_t M = a.M, D = a.D, F = a.F, pitch = (M + 7) / 8 * 8;
+  const int64_t M = a.M, D = a.D, F = a.F, pitch = pitch_of(M);
   Jobs jobs;
   jobs.n = 3;
   const Operand wg = as_rows<T>(a.w_gate, F, D, ws, jobs.job[0]),
@@ -593,8 +608,7 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
   turn(jobs.job[1], wt + F, F, 2 * F, wt_plane);
   turn(jobs.job[2], xt, pitch, pitch, xt_plane);
   if (run) prepare<T>(jobs, stream);
-  const Sizes n = {M, D, F, kTermsOf<T>, a.gelu};
-  hipError_t e = gate_up<T, true>(wg, wu, x, n, g.dh, G, ws, stream, run);
+  hipError_t e = gate_up<T, true>(a, wg, wu, x, g.dh, G, ws, stream, run);
   if (e != hipSuccess) return e;
   Jobs more;
   more.n = kFloat ? 1 : kGradPlanes;
@@ -606,11 +620,11 @@ hipError_t backward(const GatedFfn& a, const GatedFfnGrads& g, Arena& ws, hipStr
     turn(more.job[1], gt + gt_plane, pitch, pitch, gt_plane);
   }
   if (run) prepare<T>(more, stream);
-  const int terms = kFloat ? kTerms : kGradPlanes;
-  e = multiply<T>({wt, D, wt_plane, 0}, G_rows, 2 * F, terms, 1, g.dx, nullptr, ws, stream, run);
+  e = multiply<T>(product_of(a, FfnProduct::kDx), {wt, D, wt_plane, 0}, G_rows, g.dx, nullptr, ws,
+                  stream, run);
   if (e != hipSuccess) return e;
-  return multiply<T>({xt, D, xt_plane, 0}, {gt, F, gt_plane, F * pitch}, pitch, terms, 2,
-                     g.dw_gate, g.dw_up, ws, stream, run);
+  return multiply<T>(product_of(a, FfnProduct::kWeights), {xt, D, xt_plane, 0},
+                     {gt, F, gt_plane, F * pitch}, g.dw_gate, g.dw_up, ws, stream, run);
 }
 
 }  // namespace
@@ -638,6 +652,17 @@ size_t gated_ffn_bwd_workspace_bytes(const GatedFfn& a) {
   else
     (void)ffn::backward<float>(a, {}, ws, nullptr, false);
   return ws.at;
+}
+
+GatedFfnTiles gated_ffn_tiles(const GatedFfn& a, FfnProduct which) {
+  GatedFfnTiles t = {};
+  if (which == FfnProduct::kForward && a.M <= ffn::kFewRows) return t;
+  (void)ffn::with_shape(ffn::product_of(a, which), [&](auto shape, const ffn::Plan& plan) {
+    using S = decltype(shape);
+    t = {S::kBP, S::kBQ, plan.whole, plan.rest(), plan.splits};
+    return hipSuccess;
+  });
+  return t;
 }
 
 hipError_t launch_gated_ffn_bwd(const GatedFfn& a, const GatedFfnGrads& g, void* workspace,

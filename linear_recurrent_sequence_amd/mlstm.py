@@ -107,6 +107,8 @@ def load_library():
     lib.mlstm_scan_bwd.restype = i32
     lib.mlstm_gated_ffn_workspace_bytes.argtypes = [i64] * 3 + [i32, i32]
     lib.mlstm_gated_ffn_workspace_bytes.restype = f
+    lib.mlstm_gated_ffn_tiles.argtypes = [i64] * 3 + [i32, i32, ctypes.POINTER(i64)]
+    lib.mlstm_gated_ffn_tiles.restype = i32
     lib.mlstm_gated_ffn_fwd.argtypes = [vp] * 5 + [f] + [i64] * 3 + [i32, i32, vp]
     lib.mlstm_gated_ffn_fwd.restype = i32
     lib.mlstm_gated_ffn_bwd.argtypes = [vp] * 8 + [f] + [i64] * 3 + [i32, i32, vp]
