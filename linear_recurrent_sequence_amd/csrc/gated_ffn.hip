@@ -24,6 +24,7 @@
 // operands made in one launch and three pieces ahead (158 with two).
 #include "gated_ffn.h"
 
+#include "mlstm_internal.h"
 #include "product_tiles.h"
 #include "row_vec.h"
 
@@ -416,8 +417,6 @@ __global__ __launch_bounds__(256) void operands_kernel(Jobs jobs) {
 
 // ---- launches
 
-size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
-
 // a workspace taken in order; with a null base, its size
 struct Arena {
   char* base;
@@ -425,7 +424,7 @@ struct Arena {
   template <typename T>
   T* take(int64_t n) {
     T* p = reinterpret_cast<T*>(base + at);
-    at += pad256(size_t(n) * sizeof(T));
+    at += align256(size_t(n) * sizeof(T));
     return p;
   }
 };

@@ -583,28 +583,21 @@ __global__ __launch_bounds__(256) void weight_sums_kernel(SelectiveScan a, const
     dbias[c] = s;
 }
 
-constexpr int64_t kSimds = 1024;
-
-int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 int tile_of(int64_t N) { return N <= 32 ? 16 : 8; }
 
 // How many segments: operations to a state and token are 27 in one piece, 30 cut;
-// see the forward's time_of.  Both sides, first and second pass, of one build: 8 x 2048 x
+// see time_of.  Both sides, first and second pass, of one build: 8 x 2048 x
 // 1536 in 8 segments 665 us, in 4 (one and a half rounds of workgroups) 722; float32 2 x
 // 555 x 208 in 12 43, in 7 61.
 Segments segments_of(const SelectiveScan& a) {
   const int64_t tiles = (a.T + tile_of(a.N) - 1) / tile_of(a.N);
-  const int64_t waves = a.batch * a.G * tiles_of_group(a.channels, a.G) * waves_of(a.N);
-  auto time_of = [&](int64_t len, int64_t n) {
-    return double(len) * (waves * n <= kSimds
-                              ? 0.65 : double((waves * n + 2 * kSimds - 1) / (2 * kSimds)));
-  };
+  const int64_t waves = workgroups_of(a) * waves_of(a.N);
   Segments best = {1, tiles};
-  double least = 27.0 * time_of(tiles, 1);
+  double least = 27.0 * time_of(tiles, waves);
   for (int n = 2; n <= 64 && n * 2 <= tiles; ++n) {
     const int64_t len = (tiles + n - 1) / n;
     if ((tiles + len - 1) / len != n) continue;
-    const double t = 30.0 * time_of(len, n) + 60.0;
+    const double t = 30.0 * time_of(len, waves * n) + 60.0;
     if (t < 0.95 * least) {
       least = t;
       best = {n, len};
@@ -618,7 +611,7 @@ size_t lay_out(const SelectiveScan& a, const Segments& seg, char* base, Kept* k)
   size_t at = 0;
   auto take = [&](size_t floats) {
     float* p = reinterpret_cast<float*>(base + at);
-    at += pad256(floats * 4);
+    at += align256(floats * 4);
     return p;
   };
   const size_t tiles = size_t((a.T + tile_of(a.N) - 1) / tile_of(a.N)), batch = size_t(a.batch),
@@ -641,7 +634,7 @@ size_t lay_out(const SelectiveScan& a, const Segments& seg, char* base, Kept* k)
 template <typename T, int NW, int NS, int TL, bool GATE, bool CUT>
 void launch(const SelectiveScan& a, const SelectiveGrads& g, const Segments& seg, const Kept& kept,
             hipStream_t stream) {
-  const unsigned wgs = unsigned(a.batch * a.G * tiles_of_group(a.channels, a.G) * seg.n);
+  const unsigned wgs = unsigned(workgroups_of(a) * seg.n);
   states_kernel<T, NW, NS, TL, GATE, CUT><<<wgs, 64 * NW, 0, stream>>>(a, g.dy, seg, kept);
   if (CUT)
     join_kernel<<<unsigned(a.batch * ((a.N * a.channels + 255) / 256)), 256, 0, stream>>>(

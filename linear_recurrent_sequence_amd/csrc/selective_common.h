@@ -273,7 +273,21 @@ __device__ inline void store_kept(const SelectiveScan& a, float* x, const Channe
   }
 }
 
-inline size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
+// ---- how the work is cut, forward and backward
+
+constexpr int64_t kCUs = 256, kSimds = 4 * kCUs;
+
+// Waves of four states each (eight beyond 32)
+inline int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+inline int64_t workgroups_of(const SelectiveScan& a) {
+  return a.batch * a.G * tiles_of_group(a.channels, a.G);
+}
+
+// The time of `n` tiles of tokens of `waves` waves: a SIMD with two waves keeps its
+// vector unit three quarters busy, with one little more than half.
+inline double time_of(int64_t n, int64_t waves) {
+  return double(n) * (waves <= kSimds ? 0.65 : double((waves + 2 * kSimds - 1) / (2 * kSimds)));
+}
 
 }  // namespace selective
 }  // namespace mlstm

@@ -212,20 +212,6 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joint
   }
 }
 
-constexpr int64_t kCUs = 256, kSimds = 4 * kCUs;
-
-// Waves of four states each (eight beyond 32)
-int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
-int64_t workgroups_of(const SelectiveScan& a) {
-  return a.batch * a.G * tiles_of_group(a.channels, a.G);
-}
-
-// The time of `n` tiles of tokens of `waves` waves: a SIMD with two waves keeps its
-// vector unit three quarters busy, with one little more than half.
-double time_of(int64_t n, int64_t waves) {
-  return double(n) * (waves <= kSimds ? 0.65 : double((waves + 2 * kSimds - 1) / (2 * kSimds)));
-}
-
 // How many segments: those of a sequence run side by side, for the effect of each
 // on a state (0.8 of the scan's time) taken first.  Both sides: 1 x 16384 x 2048 in 16
 // segments 312 us, in 8 (one wave to a SIMD) 466, of one build; float32 2 x 555 x 208 in
@@ -247,7 +233,7 @@ Segments segments_of(const SelectiveScan& a) {
 }
 
 size_t state_bytes(const SelectiveScan& a, int n) {
-  return pad256(size_t(n) * size_t(a.batch * a.N * a.channels) * 4);
+  return align256(size_t(n) * size_t(a.batch * a.N * a.channels) * 4);
 }
 
 template <typename T, int NW, int NS, bool GATE>
@@ -295,7 +281,7 @@ size_t selective_fwd_workspace_bytes(const SelectiveScan& a) {
   const selective::Segments seg = selective::segments_of(a);
   if (seg.n == 1) return 0;
   return selective::state_bytes(a, seg.n) +
-         selective::pad256(size_t(seg.n) * size_t(a.batch * a.channels) * 4);
+         align256(size_t(seg.n) * size_t(a.batch * a.channels) * 4);
 }
 
 hipError_t launch_selective_fwd(const SelectiveScan& a, void* y, float* state_out, void* workspace,

@@ -303,7 +303,7 @@ __global__ __launch_bounds__(256) void conv_weight_sums_kernel(const float* part
 // of bf16: with 16 a lane needs 203 registers and two waves fill a SIMD (8 x 2048 rows
 // of 1536: 44 us, with 8 bytes 37).
 constexpr int kBwdVec = 4;
-int vec_of(int W, bool is_bf16) { return is_bf16 && W <= 4 ? 8 : 4; }
+constexpr int vec_of(int W, bool is_bf16) { return is_bf16 && W <= 4 ? 8 : 4; }
 
 // Tokens of a run: 32, fewer where that leaves less than two waves to a SIMD, but
 // no fewer than 8 (W - 1 at most are read twice).
@@ -324,12 +324,10 @@ Grid grid_of(int64_t B, int64_t C, int64_t T, int vec) {
 }
 
 template <typename T, int W>
-constexpr int kVecOf = sizeof(T) == 2 && W <= 4 ? 8 : 4;
-
-template <typename T, int W>
 void fwd(const ShortConv& a, void* y, void* state_out, const Grid& g, hipStream_t stream) {
-  conv_fwd_kernel<T, kVecOf<T, W>, W><<<unsigned(g.cols * g.spans), kLanes * kRuns, 0, stream>>>(
-      a, static_cast<T*>(y), static_cast<T*>(state_out), g.run);
+  conv_fwd_kernel<T, vec_of(W, sizeof(T) == 2), W>
+      <<<unsigned(g.cols * g.spans), kLanes * kRuns, 0, stream>>>(
+          a, static_cast<T*>(y), static_cast<T*>(state_out), g.run);
 }
 template <typename T, int W>
 void bwd(const ShortConv& a, const ShortConvGrads& gr, float* partials, const Grid& g,
