@@ -12,9 +12,9 @@ namespace rowvec {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// V neighbouring elements as they lie in memory
+// V neighbouring elements as they lie in memory, where tensors are 16-byte aligned
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Raw {
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Raw {
   unsigned w[sizeof(T) * V / 4];
 };
 

@@ -1,0 +1,80 @@
+"""Calls of the short convolution, the selective scan and the gated feed-forward at the
+ends of what their documentation allows; inputs, oracle and tolerances are those of
+test_blocks_gpu.py and test_blocks_tiles_gpu.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from linear_recurrent_sequence_amd import mlstm
+from test_blocks_gpu import (BF, DEV, FP, check_scan_grads, close, conv_inputs, ffn_inputs,
+                             scan_inputs, scan_ref)
+from test_blocks_tiles_gpu import reference
+
+pytestmark = pytest.mark.gpu
+ROWS = ("u", "dt", "B", "C", "gate")
+
+
+def _shifted(t):
+    """The same values 16 bytes behind a 256-byte border."""
+    if t is None:
+        return None
+    raw = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device=DEV)
+    out = raw[16:].view(t.dtype).view(t.shape).copy_(t)
+    assert out.data_ptr() % 256 == 16
+    return out
+
+
+def _calls(move, dtype):
+    x, w, b, st, dy, dst = map(move, conv_inputs(2, 70, 40, 4, dtype, 80))
+    kw = dict(bias=b, state=st)
+    yield mlstm.short_conv_fwd(x, w, **kw)
+    yield mlstm.short_conv_bwd(x, w, dy, dstate=dst, **kw).values()
+    x, dy, dst = scan_inputs(1, 600, 40, 12, 1, dtype, 81)
+    x, dy, dst = {k: move(v) for k, v in x.items()}, move(dy), move(dst)
+    yield mlstm.scan_fwd(**x)
+    yield mlstm.scan_bwd(**x, dy=dy, dstate=dst).values()
+    yield mlstm.scan_step(**{k: move(v[:, 0].contiguous()) if k in ROWS else v
+                             for k, v in x.items()})
+    for M in (5, 70, 300):
+        f = list(map(move, ffn_inputs(M, 72, 136, dtype, 82)))
+        yield (mlstm.gated_ffn_fwd(*f[:3]), *mlstm.gated_ffn_bwd(*f))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_tensors_that_are_aligned_to_16_bytes_and_no_more(dtype):
+    for a, b in zip(_calls(_shifted, dtype), _calls(lambda t: t, dtype)):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+# float32 sums of n terms: sqrt(n) 2^-24 of their size, three of them one after the other;
+# 2^20 terms 2^-14 and 2^-12.4, the others below
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("M,D,F", [(1 << 20, 8, 16), (70, 1 << 16, 8), (70, 8, 1 << 16),
+                                   (3, 1 << 16, 8), (3, 8, 1 << 16)])
+def test_gated_ffn_of_the_largest_sizes(M, D, F, dtype):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(83)
+    x, wg, wu, dh = (torch.randn(s, generator=gen, device=DEV)
+                     for s in ((M, D), (F, D), (F, D), (M, F)))
+    f = x.to(dtype), (wg * D ** -0.5).to(dtype), (wu * D ** -0.5).to(dtype), dh.to(dtype)
+    got = mlstm.gated_ffn_fwd(*f[:3]), *mlstm.gated_ffn_bwd(*f)
+    bf16 = 2.0 ** -8 if dtype == BF else 0.0
+    for name, a, ref, size in zip(("h", "dx", "dw_gate", "dw_up"), got, *reference(*f)):
+        err, size = (a.double() - ref).abs(), torch.maximum(ref.abs(), size)
+        assert err.norm() <= size.norm() * (2.0 ** -12.4 + bf16), name
+        assert (err <= size.square().mean().sqrt() * 2.0 ** -9.4 + ref.abs() * bf16).all(), name
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [30, 700])
+def test_scan_of_growing_states(T, dtype):
+    """A above zero: e^(A sum Delta) is at most about e^12 here."""
+    x, dy, dst = scan_inputs(2, T, 24, 6, 1, dtype, 84)
+    x["A"] = x["A"].abs().clamp(max=0.3)
+    x["dt_bias"] = x["dt_bias"].clamp(max=-3.0)  # Delta of 0.05 at most, on average
+    y, st = mlstm.scan_fwd(**x)
+    yr, sr = scan_ref(x)
+    close("y", y, yr, np.full_like(yr, np.sqrt((yr ** 2).mean())))
+    close("state", st, sr)
+    check_scan_grads(mlstm.scan_bwd(**x, dy=dy, dstate=dst), x, dy, dst)
