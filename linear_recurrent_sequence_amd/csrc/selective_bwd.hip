@@ -231,7 +231,7 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, const float*
   const int64_t b = blockIdx.x / blocks, i = (blockIdx.x % blocks) * 256 + threadIdx.x;
   if (i >= all) return;
   const int64_t c = i % a.channels, n = i / a.channels, at = (b * a.channels + c) * a.N + n;
-  const float A = a.A[c * a.N + n] * rowvec::kLog2e;
+  const float A = rate_of(a.A[c * a.N + n]);
   auto kept_at = [&](int k) { return (k * a.batch + b) * all + i; };
   constexpr int kAhead = 8;  // segments whose loads are in flight together
   // x, with each segment's share added to what is left of it, in the order of `at`
@@ -492,7 +492,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 1 : 2) void grads_kernel(Selecti
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float slope = on ? rowvec::sigmoid(pre[e] + constants.bias[v0 + e]) : 0.0f;
-        o[e] = __builtin_fmaf(uu[e], h[e], q[e]) * slope;
+        // (q of a rate near the largest number may be infinite where there is no step)
+        o[e] = slope != 0.0f ? __builtin_fmaf(uu[e], h[e], q[e]) * slope : 0.0f;
         dbias[i][e] += o[e];
       }
       store_rows<T, V>(rt, at.row[i], o);

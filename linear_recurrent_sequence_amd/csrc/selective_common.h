@@ -13,6 +13,8 @@
 // LDS to the threads that store y, rows of 64 channels at a time.
 #pragma once
 
+#include <float.h>
+
 #include "row_vec.h"
 #include "mlstm_internal.h"
 #include "scan_common.h"
@@ -29,6 +31,13 @@ constexpr int kChannels = 64;  // of a workgroup
 // log(1 + e^x); its slope is sigma(x)
 __device__ inline float softplus(float x) {
   return fmaxf(x, 0.0f) + scan::log1p_unit(rowvec::exp2_fast(-rowvec::kLog2e * fabsf(x)));
+}
+
+// A' of a rate. It stays finite, for a step of 0 to leave the state as it is: 0 times an
+// infinite one would be no number.
+__device__ inline float rate_of(float a) {
+  const float x = a * rowvec::kLog2e;
+  return fabsf(x) > FLT_MAX ? __builtin_copysignf(FLT_MAX, x) : x;
 }
 
 // The channels of a workgroup: `tile` of all groups' tiles of 64
@@ -230,7 +239,7 @@ __device__ inline void load_rates(const SelectiveScan& a, const Channels& ch, in
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
     const int64_t n = wave * NS + j;
-    A[j] = lane < ch.count && n < a.N ? a.A[(ch.first + lane) * a.N + n] * rowvec::kLog2e : 0.0f;
+    A[j] = lane < ch.count && n < a.N ? rate_of(a.A[(ch.first + lane) * a.N + n]) : 0.0f;
   }
 }
 // a state as callers keep it, [batch][channels][N]

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void join_kernel(SelectiveScan a, Joints joint
   const int64_t b = blockIdx.x / blocks, i = (blockIdx.x % blocks) * 256 + threadIdx.x;
   if (i >= all) return;
   const int64_t c = i % a.channels, n = i / a.channels;
-  const float A = a.A[c * a.N + n] * rowvec::kLog2e;
+  const float A = rate_of(a.A[c * a.N + n]);
   float s = a.state ? a.state[(b * a.channels + c) * a.N + n] : 0.0f;
   constexpr int kAhead = 8;  // segments whose loads are in flight together
   for (int k0 = 0; k0 < segments; k0 += kAhead) {

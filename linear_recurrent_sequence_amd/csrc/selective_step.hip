@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void step_kernel(SelectiveScan a, T* y, float*
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const float in = live ? v * B[e] : 0.0f;
-    s[e] = __builtin_fmaf(rowvec::exp2_fast(delta * (A[e] * rowvec::kLog2e)), s[e], in);
+    s[e] = __builtin_fmaf(rowvec::exp2_fast(delta * rate_of(A[e])), s[e], in);
     if (live && mine) p = __builtin_fmaf(C[e], s[e], p);
   }
   if (on && mine) rowvec::store(state_out + row * a.N + n, s);

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from linear_recurrent_sequence_amd import mlstm
-from test_blocks_gpu import (BF, DEV, FP, check_scan_grads, close, conv_inputs, ffn_inputs,
+from test_blocks_gpu import (BF, DEV, FP, check_scan_grads, close, conv_inputs, ffn_inputs, i32,
                              scan_inputs, scan_ref)
 from test_blocks_tiles_gpu import reference
 
@@ -78,3 +78,31 @@ def test_scan_of_growing_states(T, dtype):
     close("y", y, yr, np.full_like(yr, np.sqrt((yr ** 2).mean())))
     close("state", st, sr)
     check_scan_grads(mlstm.scan_bwd(**x, dy=dy, dstate=dst), x, dy, dst)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [40, 700])
+def test_scan_of_extreme_steps_and_rates(T, dtype):
+    """dt of the type's lowest value or minus infinity (no step), rates of float32's lowest
+    value (a state of one token), gates that are shut, and padding."""
+    x, dy, dst = scan_inputs(2, T, 24, 6, 1, dtype, 85, slow=0.1)
+    low, lengths = torch.finfo(dtype).min, [T, T // 2 + 3]
+    x["dt"][:, 3:T // 2:4], x["dt"][:, 5:T // 2:4] = low, float("-inf")
+    x["gate"][:, ::7] = low
+    x["A"][3], x["A"][4], x["A"][5, :3] = torch.finfo(FP).min, 0.0, -(2.0 ** 100)
+    y, st = mlstm.scan_fwd(**x, lengths=i32(lengths))
+    g = mlstm.scan_bwd(**x, dy=dy, dstate=dst, lengths=i32(lengths))
+    with np.errstate(over="ignore"):
+        yr, sr = scan_ref(x, lengths)
+        close("y", y, yr, np.full_like(yr, np.sqrt((yr ** 2).mean())))
+        close("state", st, sr)
+        check_scan_grads(g, x, dy, dst, lengths)
+    assert not g["ddt"][:, 3:T // 2:4].any() and not g["ddt"][:, 5:T // 2:4].any()
+    # a token of a sequence whose length is 0, and one of no step
+    one = {k: v[:, 3].contiguous() if k in ROWS else v.clone() for k, v in x.items()}
+    kept = one["state"].clone()
+    y, st = mlstm.scan_step(**one)
+    assert torch.equal(st, kept) and y.isfinite().all()
+    y, st = mlstm.scan_fwd(**{k: v[:, :1].contiguous() if k in ROWS else v for k, v in x.items()},
+                           lengths=i32([0, 0]))
+    assert torch.equal(st, kept) and not y.any()
