@@ -513,7 +513,7 @@ int mlstm_block_norm_bwd(const void* p, const void* gate, const void* residual,
  *            sequence may be NULL (zeros)
  *   lengths  [B] int32 in device memory, or NULL (T).  Sequence b has the first
  *            lengths[b] positions (kept in [0, T]); beyond them y and dx are zeros,
- *            nothing is read and the state stays as it is there
+ *            what the inputs hold is not used and the state stays as it is
  *   y        [B][NH][T][d] dtype, as the cells above read it (NH = 1: rows)
  *   W in [2, 8], d a multiple of 8, C <= 2^20.  act: a sigma(a) (MLSTM_CONV_SILU)
  * or a.  Sums are float32, and a bf16 result is rounded once.  Tensors 16-byte
@@ -559,7 +559,7 @@ int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, cons
  *   D, dt_bias     [channels] float32, or NULL (0)
  *   state          [batch][channels][N] float32; before the sequence NULL: zeros
  *   lengths        [batch] int32 in device memory, or NULL, as above: positions
- *                  beyond are not read, y and gradients there are zeros and the
+ *                  beyond are not used, y and gradients there are zeros and the
  *                  state stays as it is
  *   y              [batch][T][channels] dtype
  *   channels / G a multiple of 8, channels <= 2^20, N in [1, 64],

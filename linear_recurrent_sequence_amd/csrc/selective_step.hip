@@ -2,7 +2,7 @@
 // once, which bounds it.  A channel's states lie side by side in memory and take
 // the smallest power of two of lanes that covers them, 16 bytes (or 4, where N is
 // not a multiple of 4) to a lane; C.s is summed over those lanes.  64 x 2048 channels of
-// 16 states: 7.0 us (18 MB; 3.7 at a copy's rate and one memory latency), 7.9 with the
+// 16 states: 6.7 to 7.1 us (18 MB; 3.7 at a copy's rate and one memory latency), 7.9 with the
 // loads behind one another.
 #include "selective_common.h"
 

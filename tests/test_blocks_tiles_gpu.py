@@ -1,8 +1,8 @@
 """The gated feed-forward in every kind of tiles that its products are taken in: 256 x 256,
 128 x 256 and 128 x 128 outputs; all of them whole, all split along their sums, or both;
 one to a workgroup, or more. SIZES reach them all for each product and type
-(test_blocks_tiles_cpu.py holds them to it); results are compared with the definition in
-float64.
+(test_blocks_tiles_cpu.py holds them to it; those of test_blocks_gpu.py, many tiles among
+them, reach a part); results are compared with the definition in float64.
 
 Tolerances, by the sums' lengths: up to 16400 terms, so a float32 sum is off by up to
 sqrt(16400) 2^-24 = 2^-17 of its size (the root of the sum of the squares of its terms),
