@@ -126,7 +126,7 @@ enum {
   MLSTM_ERR_HEADS = -12,      /* NH not a multiple of NHK */
   MLSTM_ERR_NORM = -13,       /* unknown norm or gate activation, or eps not a number >= 0 */
   MLSTM_ERR_WIDTH = -14,      /* convolution width outside [2, 8], or scan states outside [1, 64] */
-  MLSTM_ERR_ROW = -15         /* a row pitch shorter than its row, or not a multiple of 8 */
+  MLSTM_ERR_ROW = -15         /* a row pitch shorter than its row, no multiple of 8, or too long */
 };
 
 /*
@@ -552,7 +552,8 @@ int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, cons
  *   y_t = (C_t . s_t + D_c u_t) z_t sigma(z_t)
  *
  *   u, dt, gate z  [batch][T] rows of `channels`, dtype, u_row, dt_row and gate_row
- *                  elements apart (multiples of 8); gate NULL: no last factor
+ *                  elements apart (multiples of 8; for T > 1 and backward all five
+ *                  pitches are at most 2^23); gate NULL: no last factor
  *   A              [channels][N] float32 (negative, as a rule; any finite value)
  *   B, C           [batch][T] rows of [G][N] dtype, B_row and C_row elements apart;
  *                  channel c reads group c / (channels / G)

@@ -17,9 +17,10 @@ using mlstm::abi::hip_status;
 
 // a launch takes fewer than 2^32 threads
 constexpr int64_t kMaxChannels = int64_t(1) << 20;
-// the byte offsets of tokens times a row's pitch stay within 62 bits
 constexpr int64_t kMaxTokens = int64_t(1) << 36;
-constexpr int64_t kMaxPitch = int64_t(1) << 23;
+constexpr int64_t kMaxElements = int64_t(1) << 58;  // byte offsets stay within 62 bits
+// 32 rows of a scan's sequence stay within a buffer's 2^30 bytes
+constexpr int64_t kMaxScanPitch = int64_t(1) << 23;
 constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
 
 bool aligned_to(const void* p, uintptr_t n) {
@@ -40,8 +41,8 @@ int check_tokens(int64_t B, int64_t T, int dtype) {
 }
 
 // rows that vectors of 16 bytes are read from
-int check_pitch(int64_t pitch, int64_t width) {
-  return pitch < width || pitch % 8 != 0 || pitch > kMaxPitch ? MLSTM_ERR_ROW : MLSTM_OK;
+int check_pitch(int64_t pitch, int64_t width, int64_t most) {
+  return pitch < width || pitch % 8 != 0 || pitch > most ? MLSTM_ERR_ROW : MLSTM_OK;
 }
 
 // ---- short convolution
@@ -85,12 +86,14 @@ int check_scan(int64_t batch, int64_t T, int64_t channels, int64_t G, int64_t N,
   return MLSTM_OK;
 }
 
-int check_scan_pitches(const SelectiveScan& a) {
-  int st = check_pitch(a.u_row, a.channels);
-  if (st == MLSTM_OK) st = check_pitch(a.dt_row, a.channels);
-  if (st == MLSTM_OK && a.gate) st = check_pitch(a.gate_row, a.channels);
-  if (st == MLSTM_OK && (a.B_row < a.G * a.N || a.C_row < a.G * a.N || a.B_row > kMaxPitch ||
-                         a.C_row > kMaxPitch))
+// (the kernel of one token takes rows that are any distance apart)
+int check_scan_pitches(const SelectiveScan& a, bool one_token) {
+  const int64_t most = one_token ? kMaxElements / a.batch : kMaxScanPitch;
+  int st = check_pitch(a.u_row, a.channels, most);
+  if (st == MLSTM_OK) st = check_pitch(a.dt_row, a.channels, most);
+  if (st == MLSTM_OK && a.gate) st = check_pitch(a.gate_row, a.channels, most);
+  if (st == MLSTM_OK &&
+      (a.B_row < a.G * a.N || a.C_row < a.G * a.N || a.B_row > most || a.C_row > most))
     st = MLSTM_ERR_ROW;
   return st;
 }
@@ -114,10 +117,10 @@ ScanBytes scan_bytes(const SelectiveScan& a, int dtype) {
 }
 
 // what is read, but for the state
-int check_scan_inputs(const SelectiveScan& a) {
+int check_scan_inputs(const SelectiveScan& a, bool one_token) {
   int st = check_given({a.u, a.dt, a.A, a.B, a.C});
   if (st != MLSTM_OK) return st;
-  if ((st = check_scan_pitches(a)) != MLSTM_OK) return st;
+  if ((st = check_scan_pitches(a, one_token)) != MLSTM_OK) return st;
   st = check_aligned({a.u, a.dt, a.gate, a.A, a.D, a.dt_bias, a.state});
   if (st != MLSTM_OK) return st;
   const uintptr_t e = a.is_bf16 ? 2 : 4;
@@ -156,7 +159,7 @@ int mlstm_short_conv_fwd(const void* x, int64_t x_row, const float* weight, cons
   if (st != MLSTM_OK) return st;
   if (!known_conv_activation(activation)) return MLSTM_ERR_ACTIVATION;
   if ((st = check_given({x, weight, y, state_out})) != MLSTM_OK) return st;
-  if ((st = check_pitch(x_row, NH * d)) != MLSTM_OK) return st;
+  if ((st = check_pitch(x_row, NH * d, kMaxElements / (B * T))) != MLSTM_OK) return st;
   st = check_aligned({x, weight, bias, state_in, y, state_out});
   if (st != MLSTM_OK) return st;
   if (!aligned_to(lengths, 4)) return MLSTM_ERR_ALIGN;
@@ -189,7 +192,7 @@ int mlstm_short_conv_bwd(const void* x, int64_t x_row, const float* weight, cons
   if (!known_conv_activation(activation)) return MLSTM_ERR_ACTIVATION;
   if ((st = check_given({x, weight, dy, dx, dweight, workspace})) != MLSTM_OK) return st;
   if ((bias == nullptr) != (dbias == nullptr)) return MLSTM_ERR_NULL;
-  if ((st = check_pitch(x_row, NH * d)) != MLSTM_OK) return st;
+  if ((st = check_pitch(x_row, NH * d, kMaxElements / (B * T))) != MLSTM_OK) return st;
   st = check_aligned({x, weight, bias, state_in, dy, dstate, dx, dweight, dbias, dstate_out});
   if (st != MLSTM_OK) return st;
   if (!aligned_to(lengths, 4) || !aligned_to(workspace, 256)) return MLSTM_ERR_ALIGN;
@@ -231,7 +234,7 @@ int mlstm_scan_fwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row,
   if (st != MLSTM_OK) return st;
   const SelectiveScan a = {u, dt, A, B, C, D, gate, dt_bias, state_in, lengths, u_row, dt_row,
                            B_row, C_row, gate_row, batch, T, channels, G, N, dtype == MLSTM_BF16};
-  if ((st = check_scan_inputs(a)) != MLSTM_OK) return st;
+  if ((st = check_scan_inputs(a, T == 1)) != MLSTM_OK) return st;
   if ((st = check_given({y, state_out})) != MLSTM_OK) return st;
   if ((st = check_aligned({y, state_out})) != MLSTM_OK) return st;
   if (!aligned_to(workspace, 256)) return MLSTM_ERR_ALIGN;
@@ -261,7 +264,7 @@ int mlstm_scan_bwd(const void* u, int64_t u_row, const void* dt, int64_t dt_row,
   if (st != MLSTM_OK) return st;
   const SelectiveScan a = {u, dt, A, B, C, D, gate, dt_bias, state_in, lengths, u_row, dt_row,
                            B_row, C_row, gate_row, batch, T, channels, G, N, dtype == MLSTM_BF16};
-  if ((st = check_scan_inputs(a)) != MLSTM_OK) return st;
+  if ((st = check_scan_inputs(a, false)) != MLSTM_OK) return st;
   if ((st = check_given({dy, du, ddt, dA, dB, dC, workspace})) != MLSTM_OK) return st;
   if ((D == nullptr) != (dD == nullptr) || (gate == nullptr) != (dgate == nullptr) ||
       (dt_bias == nullptr) != (ddt_bias == nullptr))

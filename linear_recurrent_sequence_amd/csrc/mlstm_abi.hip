@@ -469,7 +469,7 @@ const char* mlstm_strerror(int status) {
     case MLSTM_ERR_HEADS: return "the number of value heads must be a multiple of the number of key heads";
     case MLSTM_ERR_NORM: return "unknown norm or gate activation, or eps is not a number >= 0";
     case MLSTM_ERR_WIDTH: return "a convolution's width must be 2 to 8, a scan's states per channel 1 to 64";
-    case MLSTM_ERR_ROW: return "a row pitch is shorter than its row, or not a multiple of 8 elements";
+    case MLSTM_ERR_ROW: return "a row pitch is shorter than its row, not a multiple of 8 elements, or too long (2^23 elements for a scan's sequence)";
     default: return "unknown status";
   }
 }

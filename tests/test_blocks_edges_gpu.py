@@ -106,3 +106,26 @@ def test_scan_of_extreme_steps_and_rates(T, dtype):
     y, st = mlstm.scan_fwd(**{k: v[:, :1].contiguous() if k in ROWS else v for k, v in x.items()},
                            lengths=i32([0, 0]))
     assert torch.equal(st, kept) and not y.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_one_token_of_a_long_batch(dtype):
+    """Rows that are a whole sequence apart, 2^24 elements: a position of every sequence."""
+    n, pitch = 3, 1 << 24
+    wide = torch.empty(n, pitch, device=DEV, dtype=dtype)
+    x, _, _ = scan_inputs(n, 1, 40, 5, 1, dtype, 86)
+    one = {k: v[:, 0].contiguous() if k in ROWS else v for k, v in x.items()}
+    far, at = dict(one), 0
+    for k in ROWS:
+        c = one[k].flatten(1).shape[1]
+        far[k] = wide[:, at:at + c].copy_(one[k].flatten(1)).view(one[k].shape)
+        assert far[k].stride(0) == pitch
+        at += c + 8 - c % 8
+    ref, got = (mlstm.scan_step(**{**v, "state": x["state"].clone()}) for v in (one, far))
+    assert all(torch.equal(a, r) for a, r in zip(got, ref))
+    _, w, b, st, _, _ = conv_inputs(n, 1, 40, 4, dtype, 87)
+    ref, got = (mlstm.short_conv_step(u, w, st.clone(), bias=b) for u in (one["u"], far["u"]))
+    assert all(torch.equal(a, r) for a, r in zip(got, ref))
+    with pytest.raises(mlstm.MlstmError, match="pitch"):  # a sequence's rows
+        mlstm.scan_fwd(**{k: v.unsqueeze(0) if k in ROWS else v for k, v in far.items()
+                          if k != "state"})
