@@ -515,7 +515,8 @@ int mlstm_block_norm_bwd(const void* p, const void* gate, const void* residual,
  *            lengths[b] positions (kept in [0, T]); beyond them y and dx are zeros,
  *            what the inputs hold is not used and the state stays as it is
  *   y        [B][NH][T][d] dtype, as the cells above read it (NH = 1: rows)
- *   W in [2, 8], d a multiple of 8, C <= 2^20.  act: a sigma(a) (MLSTM_CONV_SILU)
+ *   W in [2, 8], d a multiple of 8, C <= 2^20, and B ceil(T / 64) ceil(C / 128) below
+ * 2^24 (a launch's workgroups).  act: a sigma(a) (MLSTM_CONV_SILU)
  * or a.  Sums are float32, and a bf16 result is rounded once.  Tensors 16-byte
  * aligned (lengths 4).  Bitwise reproducible.  T = 1 is the step of generation.
  */
